@@ -12,6 +12,14 @@
  *   kv_select_topk  budgeted per-(request, layer, KV head) selection
  *   kv_compact      ragged gather of the kept K/V rows
  *
+ * What a decoder does with the kept rows afterwards (paged cache, further down):
+ *
+ *   kv_paged_load, kv_paged_append   kept rows, then new tokens' rows, into pages
+ *   kv_paged_attention               attention of new tokens over the pages (causal,
+ *                                    optionally a sliding window with visible sinks),
+ *                                    accumulating each row's attention weight
+ *   kv_paged_evict                   eviction by accumulated attention weight
+ *
  * Definitions (the pages these steps follow):
  *
  *  - Score.  "DropKV: Decoupling Residual-Output Perturbation for Near-Optimal
@@ -352,9 +360,150 @@ kv_status kv_evict_host(const kv_problem *p, const kv_host_plan *plan, const voi
                         void *v_out_host, void *workspace, size_t workspace_bytes, void *stream,
                         int32_t *device_status);
 
+/* -------------------------------------------------------------------------
+ * Paged cache: the cache after eviction, while tokens are generated
+ * -------------------------------------------------------------------------
+ * Eviction leaves every unit (request, layer, KV head) with a length of its
+ * own, and the lengths grow again with every token, so the rows live in pages.
+ * A page holds page_size consecutive cache rows of one unit; cache row j of
+ * unit u = (r*L + l)*H + h is row j % page_size of page
+ * page_table[u][j / page_size].  Who owns which page is the caller's business:
+ * pages may lie in any order, and entries past a unit's last row are not read.
+ *
+ *   k_pages, v_pages  bf16 or fp16 [num_pages][page_size][d]
+ *   mass              f32 [num_pages][page_size]: accumulated attention weight
+ *                     of every row, or NULL where none is kept
+ *   page_table        i32 [R*L*H][max_pages]
+ *   lens              i32 [R*L*H]: rows held, 0 .. max_pages * page_size
+ *
+ * kv_paged_load and kv_paged_evict set lens (of the cache they fill).
+ * kv_paged_append and kv_paged_attention only read it: a caller raises lens by
+ * the new tokens' number once per step, before the first layer's append.
+ *
+ * Kernels size their work from lens and the token offsets in device memory, so
+ * calls captured into a CUDA graph follow the lengths of each replay; the host
+ * copy of the token offsets has to be that of the capture.
+ *
+ * Device-side conditions.  A length outside 0 .. max_pages * page_size makes
+ * its unit empty; a page index outside [0, num_pages) that holds a row in use
+ * is not followed.  kv_paged_attention and kv_paged_evict post
+ * KV_ERR_INVALID_ARG for either (a wait that expired: KV_ERR_TIMEOUT) to the
+ * workspace's status word, which each call sets anew; outputs of units so
+ * reported are unspecified.  kv_paged_append skips such rows, and
+ * kv_paged_load gives a unit that does not fit its table length -1, which the
+ * calls after it report.
+ */
+typedef enum kv_dtype {
+    KV_BF16 = 0,
+    KV_FP16 = 1
+} kv_dtype;
+
+typedef struct kv_paged {
+    int32_t num_requests;      /* R >= 0 (0: every call is a no-op) */
+    int32_t num_layers;        /* L >= 1 */
+    int32_t num_kv_heads;      /* H >= 1 */
+    int32_t num_q_heads;       /* H_q, a multiple of H; G = H_q / H */
+    int32_t head_dim;          /* d: 64 or 128 */
+    int32_t page_size;         /* rows per page: 16, 32, 64 or 128 */
+    int32_t max_pages;         /* columns of page_table */
+    int32_t dtype;             /* kv_dtype of the pools, the queries and the outputs */
+    int64_t num_pages;         /* pages in the pools; num_pages * page_size < 2^31 */
+    void *k_pages, *v_pages;
+    float *mass;
+    const int32_t *page_table;
+    int32_t *lens;
+} kv_paged;
+
+/* The new tokens of a step, packed: request r's are [tok_offsets[r], tok_offsets[r+1])
+ * (none is allowed) and are the last rows of each of its units. */
+typedef struct kv_chunk {
+    const int64_t *tok_offsets_host;   /* [R+1], non-decreasing from 0, host memory */
+    const int64_t *tok_offsets_dev;    /* the same values, device memory */
+} kv_chunk;
+
+/*
+ * New tokens' K and V rows of one layer into the cache: token i of request r
+ * (T_r new ones) becomes cache row lens[u] - T_r + i of u = (r, layer, h), for
+ * every head h, with accumulated weight 0.  k_new, v_new: [tokens][H][d] with
+ * k_stride / v_stride elements from one token to the next (a slice of a fused
+ * projection's output will do; a multiple of 8, at least H*d).  Tokens whose row
+ * would be negative (a unit shorter than the chunk) are skipped.
+ */
+kv_status kv_paged_append(const kv_paged *c, const kv_chunk *t, int32_t layer, const void *k_new,
+                          int64_t k_stride, const void *v_new, int64_t v_stride, void *stream);
+
+/*
+ * Packed ragged rows, as kv_compact writes them, into the cache: rows
+ * [offsets[u], offsets[u+1]) become cache rows 0, 1, ... of unit u and lens[u]
+ * their number.  k_rows, v_rows [total_rows][d]; offsets_dev i64 [R*L*H + 1];
+ * total_rows = offsets[R*L*H].  mass_rows: f32 [total_rows], the rows'
+ * accumulated weights so far, or NULL for 0 (ignored if the cache keeps none).
+ */
+kv_status kv_paged_load(const kv_paged *c, const void *k_rows, const void *v_rows,
+                        const float *mass_rows, const int64_t *offsets_dev, int64_t total_rows,
+                        void *stream);
+
+/* Bytes of workspace kv_paged_attention needs for this cache and chunk. */
+kv_status kv_paged_attention_workspace_size(const kv_paged *c, const kv_chunk *t,
+                                            int32_t add_mass, size_t *bytes);
+
+/*
+ * Attention of a chunk of new tokens over one layer of the cache, which already
+ * holds the chunk's own rows (kv_paged_append).  Query i of request r sits at
+ * cache row t = lens[u] - T_r + i of u = (r, layer, h) and sees the rows
+ *   j <= t  with  window == 0  or  j > t - window  or  j < num_sinks
+ * (window: rows of the sliding window, the query's own included; num_sinks: the
+ * first rows, which stay visible; ignored without a window).  For each query
+ * head of the group, over the rows seen:
+ *   s_j = softmax_scale * q.k_j,  lse = log sum e^s_j,  out = sum e^(s_j - lse) v_j;
+ * a query that sees nothing (t < 0) gets out = 0 and lse = -inf.
+ *
+ * q, out: [tokens][H_q][d] in the cache's dtype, q_stride / out_stride elements
+ * from one token to the next (multiples of 8); rows of tokens past the last
+ * request's are not touched.  lse: f32 [tokens][H_q], or NULL.  Rows that no
+ * query of the chunk sees are never used, whatever their memory holds (their
+ * pages may be gone); rows that one sees must hold finite values.  Products are
+ * taken of the stored values and summed in fp32; the softmax weights are rounded
+ * once, to the cache's dtype, before they multiply V (to two such parts where
+ * few query rows share a head's rows).
+ *
+ * add_mass != 0 adds to mass of every row j the weights e^(s_j - lse) of the
+ * chunk's queries and the group's heads (fp32, in a fixed order: the same call on
+ * the same bits gives the same bits).
+ */
+kv_status kv_paged_attention(const kv_paged *c, const kv_chunk *t, int32_t layer, int32_t window,
+                             int32_t num_sinks, float softmax_scale, const void *q,
+                             int64_t q_stride, void *out, int64_t out_stride, float *lse,
+                             int32_t add_mass, void *workspace, size_t workspace_bytes,
+                             void *stream);
+
+/* Bytes of workspace kv_paged_evict needs. */
+kv_status kv_paged_evict_workspace_size(const kv_paged *src, size_t *bytes);
+
+/*
+ * Eviction by accumulated attention weight, every unit of every layer: from
+ * src, a unit with n rows and budget b keeps all of them if n <= b, and else its
+ * first num_sinks, its last `recent`, and of the rows between those with the
+ * b - num_sinks - recent largest mass, equal weights to the lower row.  (Weights
+ * order as their fp32 bit patterns, exact for values >= 0, as in kv_select_topk.)
+ * The kept rows, in order, become rows 0, 1, ... of the same unit of dst, with
+ * their mass if dst keeps it, and dst->lens[u] is set.  kept: i32
+ * [R*L*H][kept_stride] receives the kept row indices (what else a caller
+ * keeps per row, such as positions, follows them); kept_stride >= every
+ * min(n, b).
+ * dst: the same shape and dtype as src (pages, tables and page_size may differ)
+ * in other pages than src's: the caller frees src's afterwards.  The pools may be
+ * the same memory; the tables and lens must not be.
+ * A budget below num_sinks + recent, or kept rows that exceed kept_stride or
+ * dst's table, post KV_ERR_BUDGET: that unit moves nothing and gets dst length -1.
+ */
+kv_status kv_paged_evict(const kv_paged *src, const kv_paged *dst, const int32_t *budgets_dev,
+                         int32_t num_sinks, int32_t recent, int32_t *kept, int64_t kept_stride,
+                         void *workspace, size_t workspace_bytes, void *stream);
+
 /*
  * Synchronises `stream`, then reads and clears the device status word of a
- * score or select workspace.  *device_status receives the kv_status a kernel
+ * score, select, attention or eviction workspace.  *device_status receives the kv_status a kernel
  * posted (KV_OK if none).  Returns KV_ERR_CUDA if the stream itself reports an
  * error.  It takes the workspace because the library keeps no state between
  * calls: the word lives in the caller's workspace.

@@ -8,7 +8,9 @@ if the library is missing, ``load()`` raises.
 
 Names follow the C ABI: ``kv_score``, ``kv_score_attention``,
 ``kv_score_rescore``, ``kv_make_offsets``, ``kv_select_topk``, ``kv_compact``,
-``kv_check_status``, ``kv_budgets_pyramid``, ``kv_budgets_ripple``.
+``kv_check_status``, ``kv_budgets_pyramid``, ``kv_budgets_ripple``; for the paged
+cache that holds the kept rows while tokens are generated: ``kv_paged_load``,
+``kv_paged_append``, ``kv_paged_attention``, ``kv_paged_evict``.
 """
 from __future__ import annotations
 
@@ -29,12 +31,17 @@ __all__ = ["KvError", "Problem", "load", "build", "kv_score", "kv_score_attentio
            "kv_block_scores", "kv_compact_blocks", "kv_budgets_fraction", "BlockBuffers",
            "evict_blocks", "EXPORTED_SYMBOLS", "HostPipeline", "PinnedTensor", "kv_evict_host",
            "kv_evict_host_workspace_size",
-           "evict", "KV_SCORE_DROPKV", "KV_SCORE_DROPKV_SQUARED", "KV_SCORE_ATTN_SUM"]
+           "evict", "KV_SCORE_DROPKV", "KV_SCORE_DROPKV_SQUARED", "KV_SCORE_ATTN_SUM",
+           "PagedCache", "Chunk", "kv_paged_append", "kv_paged_load", "kv_paged_attention",
+           "kv_paged_attention_workspace_size", "kv_paged_evict",
+           "kv_paged_evict_workspace_size"]
 
 KV_OK, KV_ERR_INVALID_ARG, KV_ERR_BUDGET, KV_ERR_WORKSPACE, KV_ERR_CUDA, KV_ERR_TIMEOUT, \
     KV_ERR_UNSUPPORTED = range(7)
 # kv_problem.score_rule
 KV_SCORE_DROPKV, KV_SCORE_DROPKV_SQUARED, KV_SCORE_ATTN_SUM = range(3)
+# kv_paged.dtype
+KV_BF16, KV_FP16 = range(2)
 
 EXPORTED_SYMBOLS = ("kv_score_workspace_size", "kv_score", "kv_score_attention",
                     "kv_score_rescore", "kv_make_offsets", "kv_select_workspace_size",
@@ -43,7 +50,9 @@ EXPORTED_SYMBOLS = ("kv_score_workspace_size", "kv_score", "kv_score_attention",
                     "kv_set_wait_limit_ns", "kv_get_wait_limit_ns", "kv_pool_scores",
                     "kv_head_budgets", "kv_block_scores", "kv_compact_blocks",
                     "kv_budgets_fraction", "kv_evict_fused", "kv_evict_host_workspace_size",
-                    "kv_evict_host")
+                    "kv_evict_host", "kv_paged_append", "kv_paged_load",
+                    "kv_paged_attention", "kv_paged_attention_workspace_size",
+                    "kv_paged_evict", "kv_paged_evict_workspace_size")
 
 
 class KvError(RuntimeError):
@@ -64,6 +73,21 @@ class _KvProblem(ctypes.Structure):
 class _KvHostPlan(ctypes.Structure):
     _fields_ = [("group_layers", ctypes.c_int32), ("pool_kernel", ctypes.c_int32),
                 ("head_budgets", ctypes.c_int32), ("fused", ctypes.c_int32)]
+
+
+class _KvPaged(ctypes.Structure):
+    _fields_ = [("num_requests", ctypes.c_int32), ("num_layers", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("num_pages", ctypes.c_int64), ("k_pages", ctypes.c_void_p),
+                ("v_pages", ctypes.c_void_p), ("mass", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("lens", ctypes.c_void_p)]
+
+
+class _KvChunk(ctypes.Structure):
+    _fields_ = [("tok_offsets_host", ctypes.POINTER(ctypes.c_int64)),
+                ("tok_offsets_dev", ctypes.c_void_p)]
 
 
 _lib = None
@@ -109,6 +133,7 @@ def _bind(lib):
     vp, sz, i32, i64, f64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_int64, \
         ctypes.c_double
     szp = ctypes.POINTER(ctypes.c_size_t)
+    PC, PT = ctypes.POINTER(_KvPaged), ctypes.POINTER(_KvChunk)
     sig = {
         "kv_score_workspace_size": [P, szp],
         "kv_score": [P, vp, vp, vp, vp, vp, sz, vp],
@@ -132,6 +157,13 @@ def _bind(lib):
                                          szp],
         "kv_evict_host": [P, ctypes.POINTER(_KvHostPlan), vp, vp, vp, ctypes.POINTER(i32),
                           ctypes.POINTER(i64), vp, vp, vp, vp, sz, vp, ctypes.POINTER(i32)],
+        "kv_paged_append": [PC, PT, i32, vp, i64, vp, i64, vp],
+        "kv_paged_load": [PC, vp, vp, vp, vp, i64, vp],
+        "kv_paged_attention_workspace_size": [PC, PT, i32, szp],
+        "kv_paged_attention": [PC, PT, i32, i32, i32, ctypes.c_float, vp, i64, vp, i64, vp, i32,
+                               vp, sz, vp],
+        "kv_paged_evict_workspace_size": [PC, szp],
+        "kv_paged_evict": [PC, PC, vp, i32, i32, vp, i64, vp, sz, vp],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -632,3 +664,201 @@ class HostPipeline:
         self.offsets = offsets
         n = self.total_rows
         return self.sel_host[:n], self.k_out_host[:n], self.v_out_host[:n], self.offsets
+
+
+# ---------------------------------------------------------------------------
+# paged cache: the rows kept by an eviction, while tokens are generated
+# ---------------------------------------------------------------------------
+class PagedCache:
+    """Pages, page table and lengths of a cache whose every (request, layer, KV head) has
+    a length of its own.  Views the tensors it is given.
+
+    k_pages, v_pages  bf16 or fp16 [num_pages][page_size][head_dim]
+    page_table        int32 [requests][layers][kv_heads][max_pages]
+    lens              int32 [requests][layers][kv_heads]: rows held
+    mass              float32 [num_pages][page_size] or None: accumulated attention weights
+    """
+
+    def __init__(self, k_pages, v_pages, page_table, lens, num_q_heads: int, mass=None):
+        import torch
+        if k_pages.dtype not in (torch.bfloat16, torch.float16) or k_pages.dim() != 3:
+            raise ValueError("k_pages: bf16 or fp16 [num_pages][page_size][head_dim]")
+        if v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype:
+            raise ValueError("v_pages: the shape and dtype of k_pages")
+        if page_table.dtype != torch.int32 or page_table.dim() != 4:
+            raise ValueError("page_table: int32 [requests][layers][kv_heads][max_pages]")
+        if lens.dtype != torch.int32 or lens.shape != page_table.shape[:3]:
+            raise ValueError("lens: int32 [requests][layers][kv_heads]")
+        if mass is not None and (mass.dtype != torch.float32 or mass.shape != k_pages.shape[:2]):
+            raise ValueError("mass: float32 [num_pages][page_size]")
+        for t in (k_pages, v_pages, page_table, lens, mass):
+            if t is not None and (not t.is_contiguous() or t.device != k_pages.device):
+                raise ValueError("the cache's tensors are contiguous and on one device")
+        self.k_pages, self.v_pages, self.mass = k_pages, v_pages, mass
+        self.page_table, self.lens = page_table, lens
+        self.num_requests, self.num_layers, self.num_kv_heads, self.max_pages = page_table.shape
+        self.num_q_heads = int(num_q_heads)
+        self.num_pages, self.page_size, self.head_dim = k_pages.shape
+        self.dtype, self.device = k_pages.dtype, k_pages.device
+        self._c = _KvPaged(self.num_requests, self.num_layers, self.num_kv_heads, self.num_q_heads,
+                           self.head_dim, self.page_size, self.max_pages,
+                           KV_FP16 if self.dtype == torch.float16 else KV_BF16, self.num_pages,
+                           k_pages.data_ptr(), v_pages.data_ptr(), _ptr(mass),
+                           page_table.data_ptr(), lens.data_ptr())
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def allocate(cls, num_requests: int, num_layers: int, num_kv_heads: int, num_q_heads: int,
+                 head_dim: int, max_rows: int, page_size: int = 64, dtype=None, mass: bool = False,
+                 device="cuda") -> "PagedCache":
+        """An empty cache with pages for `max_rows` rows of every unit, given out in order."""
+        import torch
+        cols = -(-max(int(max_rows), 1) // page_size)
+        pages = max(num_requests * num_layers * num_kv_heads, 1) * cols
+        pool = (pages, page_size, head_dim)
+        dtype = torch.bfloat16 if dtype is None else dtype
+        shape = (num_requests, num_layers, num_kv_heads)
+        count = num_requests * num_layers * num_kv_heads * cols
+        return cls(torch.zeros(pool, dtype=dtype, device=device),
+                   torch.zeros(pool, dtype=dtype, device=device),
+                   torch.arange(count, dtype=torch.int32, device=device).view(*shape, cols),
+                   torch.zeros(shape, dtype=torch.int32, device=device), num_q_heads,
+                   torch.zeros(pool[:2], dtype=torch.float32, device=device) if mass else None)
+
+    @property
+    def c(self):
+        return self._ref
+
+    @property
+    def num_units(self) -> int:
+        return self.num_requests * self.num_layers * self.num_kv_heads
+
+    def advance(self, chunk: "Chunk") -> None:
+        """Raises every unit's length by its request's new tokens (once a step, before the
+        first layer's kv_paged_append)."""
+        self.lens.add_(chunk.counts.view(-1, 1, 1))
+
+
+class Chunk:
+    """The new tokens of a step: `counts[r]` of request r, packed in request order."""
+
+    def __init__(self, counts: Sequence[int], device="cuda"):
+        import torch
+        host = np.asarray(list(counts), dtype=np.int64)
+        self.cu_host = np.concatenate([[0], np.cumsum(host)]).astype(np.int64)
+        self.cu_dev = torch.from_numpy(self.cu_host).to(device)
+        self.counts = torch.from_numpy(host.astype(np.int32)).to(device)
+        self.num_requests, self.tokens = len(host), int(self.cu_host[-1])
+        self._c = _KvChunk(self.cu_host.ctypes.data_as(ctypes.POINTER(ctypes.c_int64)),
+                           self.cu_dev.data_ptr())
+        self._ref = ctypes.byref(self._c)
+
+    @property
+    def c(self):
+        return self._ref
+
+
+def _on_current_device(cache: PagedCache, *others) -> None:
+    """The library works on the current device: its tensors have to be there."""
+    import torch
+    if cache.device.type == "cuda" and cache.device.index != torch.cuda.current_device():
+        raise ValueError("the cache is on %s, which is not the current device" % cache.device)
+    for t in others:
+        if t is not None and t.device != cache.device:
+            raise ValueError("a tensor is on %s, the cache on %s" % (t.device, cache.device))
+
+
+def _token_stride(cache: PagedCache, chunk: Chunk, t, heads: int, name: str) -> int:
+    """Checks t [tokens][heads][head_dim] (rows of a token contiguous); elements between tokens."""
+    if chunk.num_requests != cache.num_requests:
+        raise ValueError("the chunk has %d requests, the cache %d"
+                         % (chunk.num_requests, cache.num_requests))
+    d = cache.head_dim
+    if t.dtype != cache.dtype or tuple(t.shape) != (chunk.tokens, heads, d):
+        raise ValueError("%s: %s [%d][%d][%d]" % (name, cache.dtype, chunk.tokens, heads, d))
+    s = t.stride()
+    if chunk.tokens and (s[2] != 1 or (heads > 1 and s[1] != d)):
+        raise ValueError("%s: the heads of a token are contiguous" % name)
+    return s[0] if chunk.tokens > 1 else heads * d
+
+
+def kv_paged_append(cache: PagedCache, chunk: Chunk, layer: int, k_new, v_new, stream=None):
+    """New tokens' K and V rows [tokens][kv_heads][head_dim] of one layer into the pages."""
+    ks = _token_stride(cache, chunk, k_new, cache.num_kv_heads, "k_new")
+    vs = _token_stride(cache, chunk, v_new, cache.num_kv_heads, "v_new")
+    _on_current_device(cache, k_new, v_new, chunk.cu_dev)
+    _check(load().kv_paged_append(cache.c, chunk.c, int(layer), k_new.data_ptr(), ks,
+                                  v_new.data_ptr(), vs, _stream(stream)), "kv_paged_append")
+
+
+def kv_paged_load(cache: PagedCache, k_rows, v_rows, offsets_dev, total_rows: int, mass_rows=None,
+                  stream=None):
+    """Packed rows as kv_compact writes them into the pages; sets the cache's lens."""
+    import torch
+    n = int(total_rows)
+    for t in (k_rows, v_rows):
+        if t.dtype != cache.dtype or not t.is_contiguous() or t.numel() < n * cache.head_dim:
+            raise ValueError("k_rows, v_rows: %s [total_rows][%d]" % (cache.dtype, cache.head_dim))
+    if offsets_dev.dtype != torch.int64 or offsets_dev.numel() != cache.num_units + 1:
+        raise ValueError("offsets: int64 [units + 1]")
+    if mass_rows is not None and (mass_rows.dtype != torch.float32 or
+                                  not mass_rows.is_contiguous() or mass_rows.numel() < n):
+        raise ValueError("mass_rows: float32 [total_rows]")
+    _on_current_device(cache, k_rows, v_rows, offsets_dev, mass_rows)
+    _check(load().kv_paged_load(cache.c, _ptr(k_rows), _ptr(v_rows), _ptr(mass_rows),
+                                _ptr(offsets_dev), n, _stream(stream)), "kv_paged_load")
+
+
+def kv_paged_attention_workspace_size(cache: PagedCache, chunk: Chunk,
+                                      add_mass: bool = False) -> int:
+    n = ctypes.c_size_t()
+    _check(load().kv_paged_attention_workspace_size(cache.c, chunk.c, int(add_mass),
+                                                    ctypes.byref(n)),
+           "kv_paged_attention_workspace_size")
+    return n.value
+
+
+def kv_paged_attention(cache: PagedCache, chunk: Chunk, layer: int, q, out, workspace,
+                       window: int = 0, num_sinks: int = 0, softmax_scale: Optional[float] = None,
+                       lse=None, add_mass: bool = False, stream=None):
+    """Causal attention of a chunk of new tokens over one layer of the cache, which holds
+    their rows already; q, out [tokens][q_heads][head_dim], lse float32 [tokens][q_heads].
+    window > 0: only the last `window` rows and the first `num_sinks` are seen.
+    add_mass: adds every row's attention weights to cache.mass."""
+    import torch
+    qs = _token_stride(cache, chunk, q, cache.num_q_heads, "q")
+    os_ = _token_stride(cache, chunk, out, cache.num_q_heads, "out")
+    if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous() or
+                            tuple(lse.shape) != (chunk.tokens, cache.num_q_heads)):
+        raise ValueError("lse: float32 [%d][%d]" % (chunk.tokens, cache.num_q_heads))
+    _on_current_device(cache, q, out, lse, workspace, chunk.cu_dev)
+    scale = softmax_scale if softmax_scale is not None else 1.0 / math.sqrt(cache.head_dim)
+    _check(load().kv_paged_attention(
+        cache.c, chunk.c, int(layer), int(window), int(num_sinks), scale, q.data_ptr(), qs,
+        out.data_ptr(), os_, _ptr(lse), int(add_mass), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream(stream)), "kv_paged_attention")
+
+
+def kv_paged_evict_workspace_size(cache: PagedCache) -> int:
+    n = ctypes.c_size_t()
+    _check(load().kv_paged_evict_workspace_size(cache.c, ctypes.byref(n)),
+           "kv_paged_evict_workspace_size")
+    return n.value
+
+
+def kv_paged_evict(cache: PagedCache, into: PagedCache, budgets, num_sinks: int, recent: int, kept,
+                   workspace, stream=None):
+    """Every unit of `cache` cut to its budget by accumulated weight, its kept rows moved to
+    `into`; kept int32 [units][most rows kept] receives their indices.  budgets: int32 [units]."""
+    import torch
+    if budgets.dtype != torch.int32 or budgets.numel() != cache.num_units or \
+            not budgets.is_contiguous():
+        raise ValueError("budgets: int32 [units]")
+    if kept.dtype != torch.int32 or kept.dim() != 2 or kept.shape[0] != cache.num_units or \
+            not kept.is_contiguous():
+        raise ValueError("kept: int32 [units][most rows kept]")
+    _on_current_device(cache, into.k_pages, budgets, kept, workspace)
+    _check(load().kv_paged_evict(cache.c, into.c, _ptr(budgets), int(num_sinks), int(recent),
+                                 _ptr(kept), kept.shape[1], _ptr(workspace),
+                                 workspace.numel() * workspace.element_size(), _stream(stream)),
+           "kv_paged_evict")
