@@ -145,9 +145,9 @@ ScoreWs score_ws_layout(const DevProblem &P, void *base);
 void build_item_order(const DevProblem &P, long long block_keys, ItemOrder *O);
 // plan[u] = sum over units u' < u of ceil(n_u' / keys_per_block); plan[units] = total.
 void launch_plan(const DevProblem &P, int keys_per_block, int32_t *plan, cudaStream_t s);
-// 2-D TMA map over a row-major [rows][D] bf16 tensor: box 128 rows x 64 columns,
+// 2-D TMA map over a row-major [rows][D] 16-bit tensor: box box_rows x 64 columns,
 // 128-byte swizzle, out-of-range rows read as zero.  False if encoding fails.
-bool make_tile_map(CUtensorMap *m, const void *base, long long rows, int D);
+bool make_tile_map(CUtensorMap *m, const void *base, long long rows, int D, int box_rows = 128);
 // Total blocks of ceil(n_u / keys_per_block) over all units (host, from host_cu).
 long long total_blocks(const DevProblem &P, int keys_per_block);
 

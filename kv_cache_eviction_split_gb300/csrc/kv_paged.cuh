@@ -19,6 +19,7 @@ struct DevPaged {
     int32_t *lens;             // [units]
     void *k, *v;               // [num_pages][ps][d]
     float *mass;               // [num_pages][ps] or null
+    unsigned long long wait_ns;   // limit of the pipeline waits (kv_set_wait_limit_ns)
 };
 
 // The new tokens of a step.
@@ -75,10 +76,71 @@ cudaError_t launch_paged_evict(const DevPaged &S, const DevPaged &D, const int32
                                int sinks, int recent, int32_t *kept, long long kept_stride,
                                int *status, cudaStream_t s);
 
+// ---------------------------------------------------------------------------
+// Attention: how the work is cut
+// ---------------------------------------------------------------------------
+// A work item is the query rows of one unit that share a kernel's row tile (a row
+// is a query of the group: row i * G + g is token i, head g of the group); its work
+// is the key tiles that any of the rows sees.  All items' tiles, one after another,
+// are cut into equal runs, one per CTA, whatever the lengths: a CTA's run can end
+// inside an item.  An item that one CTA holds is finished there; of a cut item
+// every CTA writes a partial (row max, row sum, unnormalised output), and the CTA
+// that holds its last tile leaves a description for the merge.  Everything is
+// computed from device memory (lens, token offsets), so a captured call follows
+// the lengths of each replay.
+
+constexpr int kFewRows = 16;       // query rows (T * G) the few-rows kernel takes
+constexpr int kFewTile = 64;       // keys per tile there
+constexpr int kFewCtas = 2 * 152;  // two CTAs on each SM
+constexpr int kManyTile = 128;     // keys per tile of the tensor-memory kernel
+constexpr int kManyRows = 256;     // query rows per item there: two tiles of 128
+constexpr int kManyCtas = 152;
+
+// Key tiles of 2^log2 rows that the queries at cache rows t_lo .. t_hi see: the
+// sinks' tiles [0, ns), then the window's from `first` on; `total` together, at least
+// one (with t_hi < 0 nothing is seen and the one tile is empty).
+struct TileSpan {
+    int first, ns, total;
+    __device__ __forceinline__ int tile(int x) const { return x < ns ? x : first + x - ns; }
+};
+
+__host__ __device__ __forceinline__ TileSpan tile_span(const AttendMask &M, int t_lo, int t_hi,
+                                                       int log2) {
+    TileSpan s{0, 0, 1};
+    if (t_hi < 0) return s;
+    const int lo = window_lo(M, t_lo > 0 ? t_lo : 0);
+    const int sinks = M.sinks < lo ? M.sinks : lo;
+    s.first = lo >> log2;
+    s.ns = (sinks + (1 << log2) - 1) >> log2;
+    if (s.ns > s.first) s.ns = s.first;
+    s.total = s.ns + (t_hi >> log2) + 1 - s.first;
+    return s;
+}
+
+// A cut item: unit of the layer (r * H + h), first of the CTAs that hold it (the last
+// is the one whose slot this is), first query row and number of rows.
+struct CutItem {
+    int unit, cta0, row0, rows;
+};
+
+// Partials: CTA b writes slot 2 b for an item begun by an earlier CTA and 2 b + 1 for
+// one it begins and a later CTA ends.
+__device__ __forceinline__ int part_slot(int cta, bool begun_here) {
+    return 2 * cta + (begun_here ? 1 : 0);
+}
+
 // Workspace of the attention (all offsets 256-byte aligned).
 struct AttendWs {
     int *status;
-    float *lse2;               // [tokens][Hq] log2 of the softmax sums, for the mass pass
+    int *cta_status;           // [ctas] each CTA's own status word
+    CutItem *cut;              // [ctas] unit -1: no item ends here that an earlier CTA began
+    float2 *part_ml;           // [2 ctas][rows of an item] (m in log2 units, l)
+    float *part_o;             // [2 ctas][rows of an item][d]
+    float *lse2;               // [tokens][Hq] log2 of the softmax sums (add_mass)
+    // few rows with add_mass: the logits (log2 units, -inf unseen) of every tile
+    int *tiles;                // [1] tiles in all
+    int2 *tile_at;             // [tiles] unit of the layer, key tile
+    float *logits;             // [tiles][kFewRows][kFewTile]
     size_t total;
 };
 AttendWs attend_ws_layout(const DevPaged &C, const DevChunk &T, bool add_mass, void *base);
@@ -89,6 +151,7 @@ struct AttendIo {
     float *lse;                // or null
     long long q_stride, out_stride;
 };
+
 cudaError_t launch_paged_attention(const DevPaged &C, const DevChunk &T, int layer,
                                    const AttendMask &M, const AttendIo &io, bool add_mass,
                                    const AttendWs &ws, cudaStream_t s);

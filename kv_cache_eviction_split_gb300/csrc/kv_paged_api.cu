@@ -50,6 +50,7 @@ kv_status make_paged(const kv_paged *c, DevPaged *C) {
     C->k = c->k_pages;
     C->v = c->v_pages;
     C->mass = c->mass;
+    C->wait_ns = kv_get_wait_limit_ns();
     if (units > 0 && (bad_ptr(c->k_pages) || bad_ptr(c->v_pages) || bad_ptr(c->page_table) ||
                       bad_ptr(c->lens) || !aligned16(c->mass)))
         return KV_ERR_INVALID_ARG;

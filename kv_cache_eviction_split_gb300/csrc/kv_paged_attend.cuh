@@ -1,0 +1,173 @@
+// kv_paged_attend.cuh -- what the attention kernels share: dependent launches, element
+// types, the cut of the work into equal runs of key tiles, and the merge's interface.
+#pragma once
+#include <cuda_fp16.h>
+
+#include "kv_paged.cuh"
+#include "kv_sm100.cuh"
+
+namespace kvevict {
+
+// Every kernel of a call is launched as a programmatic dependent of the one before it
+// on the stream: its CTAs may be set up early, and wait here, before they touch
+// memory, until everything the earlier kernels wrote is visible.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <typename... A, typename... B>
+cudaError_t launch_dependent(void (*kernel)(A...), dim3 grid, int threads, size_t smem,
+                             cudaStream_t s, B... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<A>(args)...);
+}
+
+// 16-bit elements: packing of two fp32 values (round to nearest), the first low.
+struct Bf16 {
+    using T = __nv_bfloat16;
+    static constexpr bool kHalf = false;
+    static constexpr float kShift = 0.f;
+    static __device__ __forceinline__ uint32_t pack(float a, float b) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    static __device__ __forceinline__ float2 unpack(uint32_t w) {
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    }
+    static __device__ __forceinline__ T one(float x) { return __float2bfloat16_rn(x); }
+};
+// fp16 has a narrow exponent: weights are taken as 2^(x - m + 7), so that those down to
+// 2^-31 of the largest keep a value (a row's maximum is followed to within 2^8: at most
+// 2^15).  The factor is common to sums and products and is taken out with the maximum.
+struct Fp16 {
+    using T = __half;
+    static constexpr bool kHalf = true;
+    static constexpr float kShift = 7.f;
+    static __device__ __forceinline__ uint32_t pack(float a, float b) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    static __device__ __forceinline__ float2 unpack(uint32_t w) {
+        return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    }
+    static __device__ __forceinline__ T one(float x) { return __float2half_rn(x); }
+};
+
+constexpr float kLn2 = 0.6931471805599453f;
+// A row's running maximum is raised only when a logit exceeds it by more than this
+// (log2 units): sums and weights stay below 2^8 times the count, and the rescaling of
+// the accumulators becomes rare.
+constexpr float kLazyLog2 = 8.f;
+
+// 2^(a - b) for a running maximum b >= a; 0 when nothing was seen yet.
+__device__ __forceinline__ float shrink(float a, float b) {
+    return a == -INFINITY ? 0.f : sm100::ex2_approx(a - b);
+}
+
+// Requests and rows of unit v = r * H + h of a layer.
+struct UnitRows {
+    int r, h, n, count;        // rows held, new tokens
+    long long tok0;
+    bool ok;                   // the length is one a table can hold
+    const int32_t *table;
+};
+__device__ __forceinline__ UnitRows unit_rows(const DevPaged &C, const DevChunk &T, int layer,
+                                              int v) {
+    UnitRows U;
+    U.r = v / C.H;
+    U.h = v - U.r * C.H;
+    U.tok0 = T.off[U.r];
+    U.count = (int)(T.off[U.r + 1] - U.tok0);
+    const long long u = ((long long)U.r * C.L + layer) * C.H + U.h;
+    U.ok = unit_len(C, u, U.n);
+    U.table = C.table + u * C.max_pages;
+    return U;
+}
+
+// The run of tiles of one CTA, in the order of all units' tiles.
+struct CtaRun {
+    int begin, end, per;       // tiles [begin, end) of all; tiles per CTA
+    int unit, unit_begin;      // the unit that holds tile `begin`, and its first tile
+    int total;
+};
+
+// Cuts the tiles of all units of the layer (tiles_of(v) of unit v) into gridDim.x
+// runs of at least `least` tiles.  All kThreads threads call it.
+template <int kThreads, typename F>
+__device__ __forceinline__ CtaRun cut_run(int units, int least, F tiles_of) {
+    __shared__ int warp_sums[kThreads / 32];
+    __shared__ int found[2];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int chunk = (units + kThreads - 1) / kThreads;
+    const int v0 = min(units, tid * chunk), v1 = min(units, v0 + chunk);
+    int mine = 0;
+    for (int v = v0; v < v1; ++v) mine += tiles_of(v);
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) warp_sums[warp] = incl;
+    if (tid == 0) found[0] = units;
+    __syncthreads();
+    int before = incl - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += warp_sums[w];
+        total += warp_sums[w];
+    }
+    CtaRun R;
+    R.total = total;
+    R.per = max(least, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+    R.begin = (int)min((long long)total, (long long)blockIdx.x * R.per);
+    R.end = min(total, R.begin + R.per);
+    if (R.begin < R.end && before <= R.begin && R.begin < before + mine) {
+        int at = before;
+        for (int v = v0; v < v1; ++v) {
+            const int t = tiles_of(v);
+            if (R.begin < at + t) {
+                found[0] = v;
+                found[1] = at;
+                break;
+            }
+            at += t;
+        }
+    }
+    __syncthreads();
+    R.unit = found[0];
+    R.unit_begin = R.begin < R.end ? found[1] : R.end;
+    return R;
+}
+
+// Writes of a finished row: out = o / l is the caller's; this is its lse.
+__device__ __forceinline__ void store_lse(const DevPaged &C, const AttendIo &io, float *lse2,
+                                          long long tok, int head, float m, float l) {
+    const float z = l > 0.f ? m + __log2f(l) : -INFINITY;
+    if (io.lse) io.lse[tok * C.Hq + head] = z * kLn2;
+    if (lse2) lse2[tok * C.Hq + head] = z;
+}
+
+// Merges the partials of the items that several CTAs held and sets the call's status
+// word (first) or adds to it.  rows: row slots of a partial.
+cudaError_t launch_attend_merge(const DevPaged &C, const DevChunk &T, int layer,
+                                const AttendIo &io, float *lse2, const AttendWs &ws, int ctas,
+                                int rows, bool first, cudaStream_t s);
+cudaError_t launch_attend_few(const DevPaged &C, const DevChunk &T, int layer, const AttendMask &M,
+                              const AttendIo &io, bool add_mass, int max_rows, bool first,
+                              const AttendWs &ws, cudaStream_t s);
+cudaError_t launch_attend_many(const DevPaged &C, const DevChunk &T, int layer, const AttendMask &M,
+                               const AttendIo &io, bool add_mass, bool first, const AttendWs &ws,
+                               cudaStream_t s);
+
+}  // namespace kvevict
