@@ -1,0 +1,667 @@
+// kv_paged_many.cu -- attention over the pages for more than 16 query rows a head (prompt
+// chunks, whole prompts): bound by the tensor cores, 4 d flops per (query row, key).
+//
+// An item is 256 query rows of one unit (row i * G + g: token i, head g of the group, so
+// that a group's heads share every K and V tile) and the 128-key tiles that any of them
+// sees.  A CTA per SM works on two row tiles of 128 ("lanes"), each with S / P and O in
+// tensor memory (4 x 128 columns):
+//   S_L = Q_L K^T      128 x 128 x d, both operands in shared memory
+//   P_L = 2^(S c - m)  a thread per row, all 128 logits in its registers: row max and sum
+//                      need no exchange; P is rounded once to the pools' type and
+//                      overwrites S
+//   O_L += P_L V       P from tensor memory, V as it lies in the page
+// The issuing thread runs, per lane, P V of one tile and S of the next; while the tensor
+// cores work for one lane, the other lane's four warps take their softmax.  O is rescaled
+// only when a row's maximum rises by more than 2^8.
+//
+// One rounding of P (2^-9 relative each, random signs) adds to an output about as much as
+// its own rounding does; two parts, as in the few-rows kernel, would cost half as many
+// products again in the kernel's bottleneck.
+//
+// Warps: 0 loads K and 2 loads V (page boxes by TMA, 3- and 2-tile rings, a lane per
+// box), 1 issues the products, 4-7 and 8-11 are the lanes' rows; they also bring their Q
+// rows into shared memory and write the output.  Tiles no lane sees are skipped.
+#include "kv_paged_attend.cuh"
+
+namespace kvevict {
+namespace {
+using namespace sm100;
+
+constexpr int kThreads = 12 * 32;
+constexpr int kKWarp = 0, kMmaWarp = 1, kVWarp = 2, kSchedWarp = 3, kRowWarp = 4;
+// Registers a thread after the split, of 168 at launch (384 x 168 = 128 x 104 + 256 x 200):
+// a row thread holds its 128 logits.
+constexpr int kLoadRegs = 104, kRowRegs = 200;
+constexpr int kBlockBytes = 128 * 128;       // [128 rows][64 columns], 128 B swizzle
+constexpr uint32_t kOCol = 256;              // O of lane L at column kOCol + 128 L
+
+constexpr int kItems = 3;                    // items described ahead
+
+// Query rows of one lane in an item, and the tiles (counted as in the item's span) of
+// which it sees a key: [0, ns) and [a, b).
+struct Lane {
+    int rows;                  // 0: none
+    int t_lo, t_hi;            // cache rows of its first and last query
+    int ns, a, b;
+    __device__ __forceinline__ bool sees(int x) const { return x < ns || (x >= a && x < b); }
+};
+// An item and the part of it in this CTA's run, as the scheduler warp writes it.
+struct Item {
+    int v, h, n, count;        // unit of the layer, its head, rows held, new tokens
+    int row0, rows;            // query rows
+    int at, x0, x1;            // first tile in the order of all; this run's tiles of the item
+    TileSpan span;
+    int t_hi, lo, sinks;       // rows seen by any query: [0, sinks) and [lo, t_hi]
+    int stop;                  // 1: the run has ended, nothing else is set
+    Lane lane[2];
+    long long tok0;
+    const int32_t *table;
+};
+
+template <int D>
+struct Layout {
+    static constexpr int kOp = (D / 64) * kBlockBytes;
+    static constexpr int kKSt = 3, kVSt = 2;
+    static constexpr int kQ = 0;                          // Q of lane 0, then lane 1
+    static constexpr int kK = 2 * kOp;
+    static constexpr int kV = kK + kKSt * kOp;
+    static constexpr int kBars = kV + kVSt * kOp;
+    static constexpr int kNumBars = 2 * kKSt + 2 * kVSt + 10 + 1 + 2 * kItems;
+    static constexpr int kMisc = (kBars + kNumBars * 8 + 15) / 16 * 16;
+    static constexpr int kDesc = kMisc + 32;
+    static constexpr int kTotal = kDesc + kItems * (int)sizeof(Item);
+};
+
+struct ManyArgs {
+    int layer;
+    AttendMask M;
+    AttendIo io;
+    int *cta_status;
+    CutItem *cut;
+    float2 *part_ml;
+    float *part_o;
+    float *lse2;
+};
+
+__device__ __forceinline__ bool many_rows(const DevPaged &C, const UnitRows &U) {
+    return (long long)U.count * C.G > kFewRows;
+}
+
+__device__ __forceinline__ void make_item(Item &it, const DevPaged &C, const AttendMask &M,
+                                          const UnitRows &U, int pair) {
+    const int all = U.count * C.G, t0 = U.n - U.count;
+    it.h = U.h;
+    it.n = U.n;
+    it.count = U.count;
+    it.tok0 = U.tok0;
+    it.table = U.table;
+    it.row0 = pair * kManyRows;
+    it.rows = min(kManyRows, all - it.row0);
+    const int t_lo = t0 + it.row0 / C.G;
+    it.t_hi = t0 + (it.row0 + it.rows - 1) / C.G;
+    it.span = tile_span(M, t_lo, it.t_hi, 7);
+    it.lo = window_lo(M, max(t_lo, 0));
+    it.sinks = min(M.sinks, it.lo);
+    const TileSpan &sp = it.span;
+#pragma unroll
+    for (int L = 0; L < 2; ++L) {
+        Lane &a = it.lane[L];
+        const int row0 = it.row0 + L * 128;
+        a.rows = max(0, min(128, all - row0));
+        a.t_lo = t0 + row0 / C.G;
+        a.t_hi = a.rows ? t0 + (row0 + a.rows - 1) / C.G : -1;
+        const bool some = a.t_hi >= 0;
+        a.ns = some ? sp.ns : 0;
+        a.a = some ? sp.ns + (window_lo(M, max(a.t_lo, 0)) >> 7) - sp.first : 0;
+        a.b = some ? sp.ns + (a.t_hi >> 7) + 1 - sp.first : 0;
+    }
+}
+
+// Tiles of a unit: the sum over its items.
+__device__ __forceinline__ int unit_tiles(const DevPaged &C, const AttendMask &M,
+                                          const UnitRows &U) {
+    if (!many_rows(C, U)) return 0;
+    const int all = U.count * C.G, t0 = U.n - U.count;
+    int sum = 0;
+    for (int r0 = 0; r0 < all; r0 += kManyRows)
+        sum += tile_span(M, t0 + r0 / C.G, t0 + (min(all, r0 + kManyRows) - 1) / C.G, 7).total;
+    return sum;
+}
+
+// Bits 0 .. n-1 (none for n <= 0).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+    return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
+__device__ __forceinline__ float max32(const float (&v)[32]) {
+    float a[11];
+#pragma unroll
+    for (int i = 0; i < 10; ++i) a[i] = fmax3(v[3 * i], v[3 * i + 1], v[3 * i + 2]);
+    a[10] = fmaxf(v[30], v[31]);
+    const float b0 = fmax3(a[0], a[1], a[2]), b1 = fmax3(a[3], a[4], a[5]);
+    const float b2 = fmax3(a[6], a[7], a[8]), b3 = fmaxf(a[9], a[10]);
+    return fmaxf(fmax3(b0, b1, b2), b3);
+}
+
+template <typename E, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+            const DevPaged C, const DevChunk T, const ManyArgs A) {
+    using Ly = Layout<D>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Ly::kBars);
+    uint64_t *k_full = bars, *k_empty = k_full + Ly::kKSt;
+    uint64_t *v_full = k_empty + Ly::kKSt, *v_empty = v_full + Ly::kVSt;
+    uint64_t *q_full = v_empty + Ly::kVSt;   // [lane]: Q rows are in shared memory (4 warps)
+    uint64_t *s_full = q_full + 2;           // [lane]: S of the lane's tile is complete
+    uint64_t *p_full = s_full + 2;           // [lane]: P written (4 warps)
+    uint64_t *o_final = p_full + 2;          // [lane]: the lane's last P V of the item is done
+    uint64_t *o_empty = o_final + 2;         // [lane]: O read out (4 warps)
+    uint64_t *mma_done = o_empty + 2;
+    uint64_t *i_full = mma_done + 1, *i_empty = i_full + kItems;   // item descriptions
+    int *s_status = reinterpret_cast<int *>(smem + Ly::kMisc);
+    volatile int *s_abort = s_status + 1;
+    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(s_status + 2);
+    CutItem *s_cut = reinterpret_cast<CutItem *>(s_status + 4);
+    Item *s_item = reinterpret_cast<Item *>(smem + Ly::kDesc);
+
+    if (threadIdx.x == 0) {
+        *s_status = (smem_u32(smem) & 1023u) ? KV_ERR_UNSUPPORTED : 0;
+        *s_abort = *s_status;
+        *s_cut = CutItem{-1, 0, 0, 0};
+        for (int s = 0; s < Ly::kKSt; ++s) {
+            mbar_init(&k_full[s], 1);
+            mbar_init(&k_empty[s], 1);
+        }
+        for (int s = 0; s < Ly::kVSt; ++s) {
+            mbar_init(&v_full[s], 1);
+            mbar_init(&v_empty[s], 1);
+        }
+        for (int L = 0; L < 2; ++L) {
+            mbar_init(&q_full[L], 4);
+            mbar_init(&s_full[L], 1);
+            mbar_init(&p_full[L], 4);
+            mbar_init(&o_final[L], 1);
+            mbar_init(&o_empty[L], 4);
+        }
+        mbar_init(mma_done, 1);
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&i_full[i], 1);
+            mbar_init(&i_empty[i], 3 + 8);    // two loaders, the issuer, eight row warps
+        }
+        fence_barrier_init();
+        prefetch_tensormap(&tm_k);
+        prefetch_tensormap(&tm_v);
+    }
+    pdl_wait();
+    pdl_trigger();
+    const uint32_t tmem = tmem_acquire_all(s_tmem);
+    const CtaRun run = cut_run<kThreads>(C.R * C.H, 1, [&](int v) {
+        return unit_tiles(C, A.M, unit_rows(C, T, A.layer, v));
+    });
+    bool ok = *s_abort == 0;
+
+    // Item i of the run for the roles (one lane or a whole warp waits); null at its end or
+    // when a wait expired (ok false).
+    auto item = [&](int i, bool &fine) -> const Item * {
+        fine = fine && mbar_wait(&i_full[i % kItems], (uint32_t)((i / kItems) & 1), s_abort,
+                                 C.wait_ns);
+        if (!fine) return nullptr;
+        const Item *it = &s_item[i % kItems];
+        return it->stop ? nullptr : it;
+    };
+    if (warp >= kRowWarp) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegs));
+        // ---------------------------------------------------------------- rows
+        const int L = (warp - kRowWarp) >> 2;
+        const int quarter = warp & 3;
+        const int rr = quarter * 32 + lane;               // row of the lane = its TMEM lane
+        const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
+        const uint32_t s_base = tmem + lane_addr + 128 * L;
+        const uint32_t o_base = tmem + lane_addr + kOCol + 128 * L;
+        const float cs = A.M.scale_log2;
+        int kc = 0, sc = 0, ic = 0;
+        for (int i = 0;; ++i) {
+            const Item *w = item(i, ok);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok || !w) break;
+            const Lane me = w->lane[L], other = w->lane[1 - L];
+            const TileSpan span = w->span;
+            const int x0 = w->x0, x1 = w->x1;
+            const int row = w->row0 + L * 128 + rr;
+            const bool valid = rr < me.rows;
+            const long long tok = w->tok0 + row / C.G;
+            const int head = w->h * C.G + row % C.G;
+            const int t = valid ? w->n - w->count + row / C.G : -1;
+            // does the lane see any tile of this run?
+            const bool any = x0 < min(me.ns, x1) || max(x0, me.a) < min(x1, me.b);
+            if (any) {
+                uint8_t *qs = smem + Ly::kQ + L * Ly::kOp + rr * 128;
+                const uint4 *src = reinterpret_cast<const uint4 *>(
+                    static_cast<const typename E::T *>(A.io.q) + tok * A.io.q_stride +
+                    (long long)head * D);
+                uint4 q[D / 8];
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) q[c] = valid ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c)
+                    *reinterpret_cast<uint4 *>(qs + (c >> 3) * kBlockBytes +
+                                               (((c & 7) ^ (rr & 7)) << 4)) = q[c];
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&q_full[L]);
+            }
+            float m = -INFINITY, l = 0.f;
+            bool begun = false;
+            for (int x = x0; x < x1; ++x) {
+                const int key0 = span.tile(x) * kManyTile;
+                if (!me.sees(x)) {
+                    kc += other.sees(x);
+                    continue;
+                }
+                const int last = key0 + kManyTile - 1;
+                const bool full = last <= me.t_lo && (A.M.window == 0 ||
+                                                      key0 > me.t_hi - A.M.window ||
+                                                      last < A.M.sinks);
+                if (!full && (L == 0 || !other.sees(x)) &&
+                    (last > w->t_hi || (last >= w->sinks && key0 < w->lo))) {
+                    // V rows that no query sees may hold anything: 0 weight times NaN.  The
+                    // first lane of the tile clears them before its P goes to the products.
+                    const int s = kc % Ly::kVSt;
+                    ok = __all_sync(0xffffffffu,
+                                    mbar_wait(&v_full[s], (uint32_t)((kc / Ly::kVSt) & 1), s_abort,
+                                              C.wait_ns));
+                    if (!ok) break;
+                    const int j = key0 + rr;
+                    if (j > w->t_hi || (j >= w->sinks && j < w->lo)) {
+                        uint8_t *vr = smem + Ly::kV + s * Ly::kOp + rr * 128;
+#pragma unroll 1
+                        for (int c = 0; c < D / 8; ++c)
+                            *reinterpret_cast<uint4 *>(vr + (c >> 3) * kBlockBytes + (c & 7) * 16) =
+                                make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                }
+                ++kc;
+                ok = __all_sync(0xffffffffu, mbar_wait(&s_full[L], (uint32_t)(sc & 1), s_abort,
+                                                       C.wait_ns));
+                if (!ok) break;
+                tc_fence_after();
+                float s[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(s_base + 32 * c, s[c]);
+                tmem_ld_wait();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) reg_fence(s[c]);
+                if (!full) {
+                    const int lim = t - key0 + 1;
+                    const int wlo = A.M.window > 0 ? lim - A.M.window : -1;
+                    const int sk = A.M.sinks - key0;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t see = low_bits(lim - 32 * c) &
+                                             (~low_bits(wlo - 32 * c) | low_bits(sk - 32 * c));
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!(see >> i & 1u)) s[c][i] = -INFINITY;
+                    }
+                }
+                const float mt =
+                    fmaxf(fmaxf(max32(s[0]), max32(s[1])), fmaxf(max32(s[2]), max32(s[3]))) * cs;
+                const bool up = mt > m + kLazyLog2;
+                if (__any_sync(0xffffffffu, up)) {
+                    const float f = up ? shrink(m, mt) : 1.f;
+                    if (begun) {
+                        // O_L holds the earlier tiles' P V, complete before this S was
+#pragma unroll 1
+                        for (int c = 0; c < D / 16; ++c) {
+                            float o[16];
+                            tmem_ld16(o_base + 16 * c, o);
+                            tmem_ld_wait();
+                            reg_fence(o);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] *= f;
+                            tmem_st16(o_base + 16 * c, o);
+                        }
+                    }
+                    l *= f;
+                    if (up) m = mt;
+                }
+                begun = true;
+                // nothing seen so far: every p is 0
+                const float nm = m == -INFINITY ? 0.f : E::kShift - m;
+                const float2 cs2 = make_float2(cs, cs), nm2 = make_float2(nm, nm);
+                float2 sum[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) sum[c] = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t pw[16];
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const float2 e = __ffma2_rn(make_float2(s[c][i], s[c][i + 1]), cs2, nm2);
+                        const float2 p = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+                        sum[(i >> 1) & 3] = __fadd2_rn(sum[(i >> 1) & 3], p);
+                        pw[i >> 1] = E::pack(p.x, p.y);
+                    }
+                    tmem_st16u(s_base + 16 * c, pw);
+                }
+                const float2 a = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
+                l += a.x + a.y;
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[L]);
+                ++sc;
+            }
+            if (!ok) break;
+            // ---- the item's end: finished rows, or this run's part of them
+            const bool whole = x0 == 0 && x1 == span.total;
+            if (L == 0 && rr == 0 && x0 > 0 && x1 == span.total)
+                *s_cut = CutItem{w->v, w->at / run.per, w->row0, w->rows};
+            // the description is read
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&i_empty[i % kItems]);
+            if (begun) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&o_final[L], (uint32_t)(ic & 1), s_abort,
+                                                       C.wait_ns));
+                if (!ok) break;
+                tc_fence_after();
+                ++ic;
+            }
+            const float mm = m - E::kShift;
+            const long long prow =
+                (long long)part_slot(blockIdx.x, x0 == 0) * kManyRows + L * 128 + rr;
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            typename E::T *op = static_cast<typename E::T *>(A.io.out) + tok * A.io.out_stride +
+                                (long long)head * D;
+            float *pp = A.part_o + prow * D;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                float o[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = 0.f;
+                if (begun) {
+                    tmem_ld32(o_base + 32 * c, o);
+                    tmem_ld_wait();
+                    reg_fence(o);
+                }
+                if (!valid) continue;
+                if (whole) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8)
+                        *reinterpret_cast<uint4 *>(op + 32 * c + i) = make_uint4(
+                            E::pack(o[i] * inv, o[i + 1] * inv),
+                            E::pack(o[i + 2] * inv, o[i + 3] * inv),
+                            E::pack(o[i + 4] * inv, o[i + 5] * inv),
+                            E::pack(o[i + 6] * inv, o[i + 7] * inv));
+                } else if (begun) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        *reinterpret_cast<float4 *>(pp + 32 * c + i) =
+                            make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                }
+            }
+            if (begun) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&o_empty[L]);
+            }
+            if (valid) {
+                if (whole) store_lse(C, A.io, A.lse2, tok, head, mm, l);
+                else A.part_ml[prow] = make_float2(begun ? mm : -INFINITY, l);
+            }
+        }
+        if (!ok && lane == 0) {
+            *s_abort = 1;
+            atomicCAS(s_status, 0, KV_ERR_TIMEOUT);
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
+        if (warp == kSchedWarp) {
+            // ---------------------------------------------------------------- scheduler
+            if (lane == 0 && ok) {
+                int v = run.unit, at = run.unit_begin, i = 0;
+                for (;;) {
+                    // units from the run's first on; after the last, the end mark
+                    const bool end = at >= run.end;
+                    UnitRows U;
+                    int pairs = 1;
+                    if (!end) {
+                        U = unit_rows(C, T, A.layer, v);
+                        pairs = many_rows(C, U) ? (U.count * C.G + kManyRows - 1) / kManyRows : 0;
+                        if (pairs && !U.ok) atomicCAS(s_status, 0, KV_ERR_INVALID_ARG);
+                    }
+                    for (int pair = 0; ok && pair < pairs && (end || at < run.end); ++pair) {
+                        Item next;
+                        next.stop = end;
+                        if (!end) {
+                            make_item(next, C, A.M, U, pair);
+                            next.v = v;
+                            next.at = at;
+                            next.x0 = max(run.begin - at, 0);
+                            next.x1 = min(next.span.total, run.end - at);
+                            at += next.span.total;
+                            if (next.x0 >= next.x1) continue;
+                        }
+                        ok = mbar_wait(&i_empty[i % kItems], (uint32_t)((i / kItems) & 1) ^ 1u, s_abort,
+                                       C.wait_ns);
+                        if (!ok) break;
+                        s_item[i % kItems] = next;
+                        mbar_arrive(&i_full[i % kItems]);
+                        ++i;
+                    }
+                    if (end || !ok) break;
+                    ++v;
+                }
+                if (!ok) {
+                    *s_abort = 1;
+                    atomicCAS(s_status, 0, KV_ERR_TIMEOUT);
+                }
+            }
+        } else if (warp == kKWarp || warp == kVWarp) {
+            // ---------------------------------------------------------------- producers
+            const bool is_k = warp == kKWarp;
+            const CUtensorMap *map = is_k ? &tm_k : &tm_v;
+            uint64_t *full = is_k ? k_full : v_full, *empty = is_k ? k_empty : v_empty;
+            const int stages = is_k ? Ly::kKSt : Ly::kVSt, ring = is_k ? Ly::kK : Ly::kV;
+            const int subs = kManyTile / C.ps, boxes = subs * (D / 64);
+            const int half = lane % (D / 64), sub = lane / (D / 64);
+            int cnt = 0;
+            for (int i = 0;; ++i) {
+                const Item *w = item(i, ok);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok || !w) break;
+                const int t_hi = w->t_hi, lo = w->lo, sinks = w->sinks;
+                const int x1 = t_hi < 0 ? 0 : w->x1;              // nothing seen: nothing loaded
+                const TileSpan span = w->span;
+                const int32_t *table = w->table;
+                int base = -1, pg = -1;
+                for (int x = w->x0; x < x1; ++x) {
+                    const int key0 = span.tile(x) * kManyTile, e0 = key0 >> C.ps_log2;
+                    if ((e0 & ~31) != base) {
+                        base = e0 & ~31;
+                        pg = base + lane < C.max_pages ? table[base + lane] : -1;
+                    }
+                    const int j = key0 + sub * C.ps;
+                    const int page = __shfl_sync(0xffffffffu, pg, (j >> C.ps_log2) & 31);
+                    // a box with no row in use is not read: its page may not exist
+                    const bool use = lane < boxes && j <= t_hi && !(j >= sinks && j + C.ps <= lo);
+                    const bool bad = use && (page < 0 || page >= C.num_pages);
+                    if (bad) atomicCAS(s_status, 0, KV_ERR_INVALID_ARG);
+                    // rows past the pools' end read as zero
+                    const long long y = bad ? C.num_pages * C.ps : (long long)page << C.ps_log2;
+                    const int n_use = __popc(__ballot_sync(0xffffffffu, use));
+                    const int s = cnt % stages;
+                    ok = mbar_wait(&empty[s], (uint32_t)((cnt / stages) & 1) ^ 1u, s_abort, C.wait_ns);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        if (n_use) mbar_arrive_expect_tx(&full[s], n_use * C.ps * 128);
+                        else mbar_arrive(&full[s]);
+                    }
+                    __syncwarp();
+                    if (use)
+                        tma_load_2d(smem + ring + s * Ly::kOp + half * kBlockBytes + sub * C.ps * 128,
+                                    map, &full[s], half * 64, (int)y);
+                    ++cnt;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&i_empty[i % kItems]);
+            }
+            if (!ok && lane == 0) {
+                *s_abort = 1;
+                atomicCAS(s_status, 0, KV_ERR_TIMEOUT);
+            }
+            for (int s = 0; s < stages; ++s) {
+                const int uses = cnt / stages + (cnt % stages > s ? 1 : 0);
+                if (uses > 0) mbar_drain(&full[s], (uint32_t)((uses - 1) & 1), kDrainNs);
+            }
+        } else if (warp == kMmaWarp) {
+            // ---------------------------------------------------------------- products
+            if (lane == 0) {
+                constexpr uint32_t idesc_s = E::kHalf ? idesc_f16_f32(128, kManyTile)
+                                                      : idesc_bf16_f32(128, kManyTile);
+                constexpr uint32_t idesc_o = E::kHalf ? idesc_f16_f32_bmn(128, D)
+                                                      : idesc_bf16_f32_bmn(128, D);
+                int kc = 0;                      // tiles of the rings used so far
+                int sc[2] = {0, 0};              // P V issued per lane
+                int ic[2] = {0, 0};              // items in which the lane took part
+                const Item *w;
+                for (int i = 0; (w = item(i, ok)); ++i) {
+                    const Lane l0 = w->lane[0], l1 = w->lane[1];
+                    const int x1 = w->x1;
+                    // lane L's tile whose P V is still to be issued: its place in the rings
+                    int pend[2] = {-1, -1};
+                    bool pend_frees[2] = {false, false}, begun[2] = {false, false};
+                    for (int x = w->x0; ok && x <= x1; ++x) {
+                        const bool see[2] = {x < x1 && l0.sees(x), x < x1 && l1.sees(x)};
+    #pragma unroll
+                        for (int L = 0; L < 2; ++L) {
+                            if (ok && pend[L] >= 0) {
+                                // O_L (+)= P V of the lane's previous tile
+                                const int s = pend[L] % Ly::kVSt;
+                                const bool first = !begun[L];
+                                if (first)
+                                    ok = mbar_wait(&o_empty[L], (uint32_t)(ic[L] & 1) ^ 1u, s_abort,
+                                                   C.wait_ns);
+                                ok = ok &&
+                                     mbar_wait(&p_full[L], (uint32_t)(sc[L] & 1), s_abort, C.wait_ns) &&
+                                     mbar_wait(&v_full[s], (uint32_t)((pend[L] / Ly::kVSt) & 1), s_abort,
+                                               C.wait_ns);
+                                if (ok) {
+                                    tc_fence_after();
+                                    const uint64_t vb = sdesc_mn_sw128(
+                                        smem_u32(smem + Ly::kV + s * Ly::kOp), kBlockBytes);
+                                    const uint32_t p_col = tmem + 128 * L;
+                                    const uint32_t o_col = tmem + kOCol + 128 * L;
+    #pragma unroll
+                                    for (int q = 0; q < kManyTile / 16; ++q) {
+                                        const uint64_t bd = sdesc_add(vb, q * 16 * 128);
+                                        if (q == 0 && first)
+                                            mma_ts_c<false>(o_col, p_col, bd, idesc_o);
+                                        else
+                                            mma_ts_c<true>(o_col, p_col + q * 8, bd, idesc_o);
+                                    }
+                                    if (pend_frees[L]) mma_commit(&v_empty[s]);
+                                    begun[L] = true;
+                                    ++sc[L];
+                                }
+                                pend[L] = -1;
+                            }
+                            if (ok && see[L]) {
+                                // S_L = Q_L K^T
+                                const int s = kc % Ly::kKSt;
+                                if (!begun[L])
+                                    ok = mbar_wait(&q_full[L], (uint32_t)(ic[L] & 1), s_abort,
+                                                   C.wait_ns);
+                                ok = ok && mbar_wait(&k_full[s], (uint32_t)((kc / Ly::kKSt) & 1),
+                                                     s_abort, C.wait_ns);
+                                if (ok) {
+                                    tc_fence_after();
+                                    const uint64_t qa =
+                                        sdesc_k_sw128(smem_u32(smem + Ly::kQ + L * Ly::kOp));
+                                    const uint64_t ka =
+                                        sdesc_k_sw128(smem_u32(smem + Ly::kK + s * Ly::kOp));
+                                    const uint32_t s_col = tmem + 128 * L;
+    #pragma unroll
+                                    for (int kb = 0; kb < D / 64; ++kb)
+    #pragma unroll
+                                        for (int kk = 0; kk < 4; ++kk) {
+                                            const uint32_t o = kb * kBlockBytes + kk * 32;
+                                            if (kb | kk)
+                                                mma_ss_c<true>(s_col, sdesc_add(qa, o),
+                                                               sdesc_add(ka, o), idesc_s);
+                                            else
+                                                mma_ss_c<false>(s_col, qa, ka, idesc_s);
+                                        }
+                                    mma_commit(&s_full[L]);
+                                    if (L == 1 || !see[1]) mma_commit(&k_empty[s]);
+                                    pend[L] = kc;
+                                    pend_frees[L] = L == 1 || !see[1];
+                                }
+                            }
+                        }
+                        if (see[0] || see[1]) ++kc;
+                    }
+    #pragma unroll
+                    for (int L = 0; L < 2; ++L)
+                        if (ok && begun[L]) {
+                            mma_commit(&o_final[L]);
+                            ++ic[L];
+                        }
+                    mbar_arrive(&i_empty[i % kItems]);
+                }
+                if (!ok) {
+                    *s_abort = 1;
+                    atomicCAS(s_status, 0, KV_ERR_TIMEOUT);
+                }
+                // every product issued completes before tensor memory is freed
+                mma_commit(mma_done);
+                mbar_drain(mma_done, 0, kDrainNs);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    tmem_release_all(tmem);
+    if (threadIdx.x == 0) {
+        A.cta_status[blockIdx.x] = *s_status;
+        A.cut[blockIdx.x] = *s_cut;
+    }
+}
+
+template <typename E, int D>
+cudaError_t many(const DevPaged &C, const DevChunk &T, const ManyArgs &A, bool first,
+                 const AttendWs &ws, cudaStream_t s) {
+    using Ly = Layout<D>;
+    CUtensorMap mk, mv;
+    if (!make_tile_map(&mk, C.k, C.num_pages * C.ps, D, C.ps) ||
+        !make_tile_map(&mv, C.v, C.num_pages * C.ps, D, C.ps))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(many_kernel<E, D>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, Ly::kTotal);
+    if (e == cudaSuccess)
+        e = launch_dependent(many_kernel<E, D>, dim3(kManyCtas), kThreads, Ly::kTotal, s, mk, mv, C,
+                             T, A);
+    if (e == cudaSuccess)
+        e = launch_attend_merge(C, T, A.layer, A.io, A.lse2, ws, kManyCtas, kManyRows, first, s);
+    return e;
+}
+
+}  // namespace
+
+cudaError_t launch_attend_many(const DevPaged &C, const DevChunk &T, int layer, const AttendMask &M,
+                               const AttendIo &io, bool add_mass, bool first, const AttendWs &ws,
+                               cudaStream_t s) {
+    const ManyArgs A{layer, M, io, ws.cta_status, ws.cut, ws.part_ml, ws.part_o, ws.lse2};
+    if (C.dtype == KV_FP16)
+        return C.d == 64 ? many<Fp16, 64>(C, T, A, first, ws, s)
+                         : many<Fp16, 128>(C, T, A, first, ws, s);
+    return C.d == 64 ? many<Bf16, 64>(C, T, A, first, ws, s)
+                     : many<Bf16, 128>(C, T, A, first, ws, s);
+}
+
+}  // namespace kvevict

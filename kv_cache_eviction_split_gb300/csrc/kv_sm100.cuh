@@ -404,6 +404,13 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
            | (static_cast<uint32_t>(M >> 4) << 24);     // M / 16
 }
 
+// As idesc_bf16_f32 with fp16 A and B (type field 0).
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
+    return (1u << 4)                                    // D: f32
+           | (static_cast<uint32_t>(N >> 3) << 17)      // N / 8
+           | (static_cast<uint32_t>(M >> 4) << 24);     // M / 16
+}
+
 // Same with the B operand MN-major.
 __host__ __device__ constexpr uint32_t idesc_bf16_f32_bmn(int M, int N) {
     return idesc_bf16_f32(M, N) | (1u << 16);
