@@ -136,7 +136,10 @@ struct AttendWs {
     CutItem *cut;              // [ctas] unit -1: no item ends here that an earlier CTA began
     float2 *part_ml;           // [2 ctas][rows of an item] (m in log2 units, l)
     float *part_o;             // [2 ctas][rows of an item][d]
-    float *lse2;               // [tokens][Hq] log2 of the softmax sums (add_mass)
+    // add_mass: log2 of the softmax sums of the query rows, and the rows themselves, in
+    // packed order (packed_row)
+    float *lse2;               // [tokens * Hq]
+    void *q_packed;            // [tokens * Hq][d], of requests with more than kFewRows rows
     // few rows with add_mass: the logits (log2 units, -inf unseen) of every tile
     int *tiles;                // [1] tiles in all
     int2 *tile_at;             // [tiles] unit of the layer, key tile

@@ -94,6 +94,22 @@ __device__ __forceinline__ UnitRows unit_rows(const DevPaged &C, const DevChunk 
     return U;
 }
 
+// Whether the tensor-memory kernel takes a unit's rows (the few-rows kernel otherwise).
+__device__ __forceinline__ bool many_rows(const DevPaged &C, const UnitRows &U) {
+    return (long long)U.count * C.G > kFewRows;
+}
+
+// Bits 0 .. n-1 (none for n <= 0).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+    return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
+// Query row `row` of unit U in the workspace's packed order: units of a request one after
+// another, rows of a unit together.
+__device__ __forceinline__ long long packed_row(const DevPaged &C, const UnitRows &U, int row) {
+    return U.tok0 * C.Hq + (long long)U.h * U.count * C.G + row;
+}
+
 // The run of tiles of one CTA, in the order of all units' tiles.
 struct CtaRun {
     int begin, end, per;       // tiles [begin, end) of all; tiles per CTA
@@ -150,12 +166,9 @@ __device__ __forceinline__ CtaRun cut_run(int units, int least, F tiles_of) {
     return R;
 }
 
-// Writes of a finished row: out = o / l is the caller's; this is its lse.
-__device__ __forceinline__ void store_lse(const DevPaged &C, const AttendIo &io, float *lse2,
-                                          long long tok, int head, float m, float l) {
-    const float z = l > 0.f ? m + __log2f(l) : -INFINITY;
-    if (io.lse) io.lse[tok * C.Hq + head] = z * kLn2;
-    if (lse2) lse2[tok * C.Hq + head] = z;
+// log2 of a row's softmax sum from its maximum (log2 units) and sum.
+__device__ __forceinline__ float row_lse2(float m, float l) {
+    return l > 0.f ? m + __log2f(l) : -INFINITY;
 }
 
 // Merges the partials of the items that several CTAs held and sets the call's status
@@ -169,5 +182,8 @@ cudaError_t launch_attend_few(const DevPaged &C, const DevChunk &T, int layer, c
 cudaError_t launch_attend_many(const DevPaged &C, const DevChunk &T, int layer, const AttendMask &M,
                                const AttendIo &io, bool add_mass, bool first, const AttendWs &ws,
                                cudaStream_t s);
+// The weights of the requests launch_attend_many took, from its packed queries and lse.
+cudaError_t launch_many_mass(const DevPaged &C, const DevChunk &T, int layer, const AttendMask &M,
+                             const AttendWs &ws, cudaStream_t s);
 
 }  // namespace kvevict

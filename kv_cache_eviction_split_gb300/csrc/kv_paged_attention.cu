@@ -1,70 +1,12 @@
-// kv_paged_attention.cu -- attention of new tokens over the pages, the plain way:
-// one CTA per (token, KV head), its warps take every fourth row seen.
+// kv_paged_attention.cu -- attention of new tokens over the pages: which kernel takes a
+// request (few or many query rows a head), the merge of items that several CTAs held, and
+// the workspace they share.
 #include <algorithm>
 
 #include "kv_paged_attend.cuh"
 
 namespace kvevict {
 namespace {
-
-constexpr int kWarps = 4;
-
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
-__device__ __forceinline__ void from_f(float x, __nv_bfloat16 *y) { *y = __float2bfloat16_rn(x); }
-__device__ __forceinline__ void from_f(float x, __half *y) { *y = __float2half_rn(x); }
-
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
-}
-
-template <typename E, int D>
-__global__ void __launch_bounds__(kWarps * 32)
-mass_kernel(const DevPaged C, const DevChunk T, int layer, const AttendMask M, const AttendIo io,
-            const float *lse2, int h) {
-    constexpr int kE = D / 32;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int r = blockIdx.y;
-    const long long u = ((long long)r * C.L + layer) * C.H + h;
-    const long long t0 = T.off[r];
-    const int count = (int)(T.off[r + 1] - t0);
-    if (count * C.G <= kFewRows) return;
-    int n;
-    unit_len(C, u, n);
-    for (int j = blockIdx.x * kWarps + warp; j < n && count > 0; j += gridDim.x * kWarps) {
-        // queries that see row j
-        int first = j - (n - count), last = count - 1;
-        if (M.window > 0 && j >= M.sinks && j - (n - count) + M.window - 1 < last)
-            last = j - (n - count) + M.window - 1;
-        if (first < 0) first = 0;
-        if (first > last) continue;
-        const long long row = page_row(C, C.table + u * C.max_pages, j);
-        if (row < 0) continue;
-        float k[kE], acc = 0.f;
-        for (int e = 0; e < kE; ++e) k[e] = to_f(static_cast<const E *>(C.k)[row * D + e * 32 + lane]);
-        for (int i = first; i <= last; ++i)
-            for (int g = 0; g < C.G; ++g) {
-                const int head = h * C.G + g;
-                const E *qp = static_cast<const E *>(io.q) + (t0 + i) * io.q_stride + (long long)head * D;
-                float s = 0.f;
-                for (int e = 0; e < kE; ++e) s += k[e] * to_f(qp[e * 32 + lane]);
-                acc += exp2f(warp_sum(s) * M.scale_log2 - lse2[(t0 + i) * C.Hq + head]);
-            }
-        if (lane == 0) C.mass[row] += acc;
-    }
-}
-
-template <typename E, int D>
-cudaError_t attend(const DevPaged &C, const DevChunk &T, int layer, const AttendMask &M,
-                   const AttendIo &io, bool add_mass, const AttendWs &ws, cudaStream_t s) {
-    if (add_mass)
-        for (int h = 0; h < C.H; ++h)
-            mass_kernel<E, D><<<dim3(1024, C.R), kWarps * 32, 0, s>>>(C, T, layer, M, io, ws.lse2, h);
-    return cudaGetLastError();
-}
-
 
 // ---------------------------------------------------------------------------
 // Merge of cut items.  The CTA that held an item's last tile left its description;
@@ -144,14 +86,19 @@ merge_kernel(const DevPaged C, const DevChunk T, int layer, const AttendIo io, f
 #pragma unroll
     for (int i = 0; i < kV; i += 2)
         *reinterpret_cast<uint32_t *>(op + i) = X::pack(acc[i] * inv, acc[i + 1] * inv);
-    if (lane == 0) store_lse(C, io, lse2, tok, head, m, l);
+    if (lane == 0) {
+        const float z = row_lse2(m, l);
+        if (io.lse) io.lse[tok * C.Hq + head] = z * kLn2;
+        if (lse2) lse2[packed_row(C, U, it.row0 + row)] = z;
+    }
 }
 
 template <typename X, int D>
 cudaError_t merge(const DevPaged &C, const DevChunk &T, int layer, const AttendIo &io, float *lse2,
                   const AttendWs &ws, int ctas, int rows, bool first, cudaStream_t s) {
     if (rows == kFewRows)
-        return launch_dependent(merge_kernel<X, D, kFewRows, true>, dim3(ctas, std::min<long long>(kFewRows, (long long)T.max_t * C.G)),
+        return launch_dependent(merge_kernel<X, D, kFewRows, true>,
+                                dim3(ctas, std::min<long long>(kFewRows, (long long)T.max_t * C.G)),
                                 128, 0, s, C, T, layer, io, lse2, ws.status, ws.cta_status, ws.cut,
                                 ws.part_ml, ws.part_o, ctas, first);
     return launch_dependent(merge_kernel<X, D, kManyRows, false>, dim3(ctas, kManyRows / 4), 128, 0,
@@ -212,6 +159,7 @@ AttendWs attend_ws_layout(const DevPaged &C, const DevChunk &T, bool add_mass, v
     if (add_mass) {
         const size_t tiles = (size_t)k.few * C.H * ((C.cap + kFewTile - 1) / kFewTile);
         ws.lse2 = reinterpret_cast<float *>(take((size_t)T.tokens * C.Hq * sizeof(float)));
+        ws.q_packed = take(k.many ? (size_t)T.tokens * C.Hq * C.d * 2 : 0);
         ws.tiles = reinterpret_cast<int *>(take(sizeof(int)));
         ws.tile_at = reinterpret_cast<int2 *>(take(tiles * sizeof(int2)));
         ws.logits = reinterpret_cast<float *>(
@@ -229,12 +177,7 @@ cudaError_t launch_paged_attention(const DevPaged &C, const DevChunk &T, int lay
     if (k.few) e = launch_attend_few(C, T, layer, M, io, add_mass, k.few_rows, true, ws, s);
     if (e == cudaSuccess && k.many) {
         e = launch_attend_many(C, T, layer, M, io, add_mass, !k.few, ws, s);
-        if (e != cudaSuccess || !add_mass) return e;
-        if (C.dtype == KV_FP16)
-            return C.d == 64 ? attend<__half, 64>(C, T, layer, M, io, add_mass, ws, s)
-                             : attend<__half, 128>(C, T, layer, M, io, add_mass, ws, s);
-        return C.d == 64 ? attend<__nv_bfloat16, 64>(C, T, layer, M, io, add_mass, ws, s)
-                         : attend<__nv_bfloat16, 128>(C, T, layer, M, io, add_mass, ws, s);
+        if (e == cudaSuccess && add_mass) e = launch_many_mass(C, T, layer, M, ws, s);
     }
     return e;
 }

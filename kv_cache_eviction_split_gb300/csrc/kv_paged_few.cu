@@ -138,6 +138,7 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
 
     if (warp == kConsumers) {
         // ---------------------------------------------------------------- producer
+        fence_proxy_async_global();    // rows that earlier kernels stored, before TMA reads them
         constexpr int kParts = 2 * (D / 64);                   // K and V halves of a box
         const int box = min(C.ps, kFewTile);
         const int subs = kFewTile / box, boxes = subs * kParts;
@@ -454,7 +455,11 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
                                 op[ks * 16] = E::one(o[nt][ks][i] * inv);
                                 op[ks * 16 + 8] = E::one(o[nt][ks][i + 2] * inv);
                             }
-                            if (quad == 0) store_lse(C, A.io, A.lse2, tok, head, mm, ll);
+                            if (quad == 0) {
+                                const float z = row_lse2(mm, ll);
+                                if (A.io.lse) A.io.lse[tok * C.Hq + head] = z * kLn2;
+                                if (A.lse2) A.lse2[packed_row(C, U, row)] = z;
+                            }
                         } else {
                             const long long at_row = slot * kFewRows + row;
                             if (quad == 0) A.part_ml[at_row] = make_float2(mm, ll);
@@ -500,14 +505,14 @@ few_mass_kernel(const DevPaged C, const DevChunk T, const FewArgs A) {
         const int j = where.y * kFewTile + key, rows = U.count * C.G;
         if (j >= U.n) continue;
         const float *lg = A.logits + (long long)t * kFewRows * kFewTile + key;
+        const float *lse2 = A.lse2 + packed_row(C, U, 0);
         float acc = 0.f;
         bool seen = false;
         for (int row = 0; row < rows; ++row) {
             const float x = lg[row * kFewTile];
             if (x == -INFINITY) continue;
             seen = true;
-            const long long tok = U.tok0 + row / C.G;
-            acc += ex2_approx(x - A.lse2[tok * C.Hq + U.h * C.G + row % C.G]);
+            acc += ex2_approx(x - lse2[row]);
         }
         if (!seen) continue;
         const long long at = page_row(C, U.table, j);

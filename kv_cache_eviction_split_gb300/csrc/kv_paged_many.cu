@@ -54,7 +54,7 @@ struct Item {
     int t_hi, lo, sinks;       // rows seen by any query: [0, sinks) and [lo, t_hi]
     int stop;                  // 1: the run has ended, nothing else is set
     Lane lane[2];
-    long long tok0;
+    long long tok0, prow0;     // first token; the unit's first packed row
     const int32_t *table;
 };
 
@@ -80,12 +80,9 @@ struct ManyArgs {
     CutItem *cut;
     float2 *part_ml;
     float *part_o;
-    float *lse2;
+    float *lse2;               // null without add_mass, as is q_packed
+    void *q_packed;
 };
-
-__device__ __forceinline__ bool many_rows(const DevPaged &C, const UnitRows &U) {
-    return (long long)U.count * C.G > kFewRows;
-}
 
 __device__ __forceinline__ void make_item(Item &it, const DevPaged &C, const AttendMask &M,
                                           const UnitRows &U, int pair) {
@@ -94,6 +91,7 @@ __device__ __forceinline__ void make_item(Item &it, const DevPaged &C, const Att
     it.n = U.n;
     it.count = U.count;
     it.tok0 = U.tok0;
+    it.prow0 = packed_row(C, U, 0);
     it.table = U.table;
     it.row0 = pair * kManyRows;
     it.rows = min(kManyRows, all - it.row0);
@@ -126,11 +124,6 @@ __device__ __forceinline__ int unit_tiles(const DevPaged &C, const AttendMask &M
     for (int r0 = 0; r0 < all; r0 += kManyRows)
         sum += tile_span(M, t0 + r0 / C.G, t0 + (min(all, r0 + kManyRows) - 1) / C.G, 7).total;
     return sum;
-}
-
-// Bits 0 .. n-1 (none for n <= 0).
-__device__ __forceinline__ uint32_t low_bits(int n) {
-    return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
 }
 
 __device__ __forceinline__ float max32(const float (&v)[32]) {
@@ -234,6 +227,7 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             const long long tok = w->tok0 + row / C.G;
             const int head = w->h * C.G + row % C.G;
             const int t = valid ? w->n - w->count + row / C.G : -1;
+            const long long prow0 = w->prow0;
             // does the lane see any tile of this run?
             const bool any = x0 < min(me.ns, x1) || max(x0, me.a) < min(x1, me.b);
             if (any) {
@@ -251,6 +245,13 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&q_full[L]);
+                if (A.q_packed && valid && x0 <= (me.ns ? 0 : me.a)) {
+                    // the weights' pass takes the rows by TMA; one CTA of a cut item writes them
+                    uint4 *dst = reinterpret_cast<uint4 *>(
+                        static_cast<typename E::T *>(A.q_packed) + (prow0 + row) * D);
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) dst[c] = q[c];
+                }
             }
             float m = -INFINITY, l = 0.f;
             bool begun = false;
@@ -409,8 +410,11 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                 if (lane == 0) mbar_arrive(&o_empty[L]);
             }
             if (valid) {
-                if (whole) store_lse(C, A.io, A.lse2, tok, head, mm, l);
-                else A.part_ml[prow] = make_float2(begun ? mm : -INFINITY, l);
+                if (whole) {
+                    const float z = row_lse2(mm, l);
+                    if (A.io.lse) A.io.lse[tok * C.Hq + head] = z * kLn2;
+                    if (A.lse2) A.lse2[prow0 + row] = z;
+                } else A.part_ml[prow] = make_float2(begun ? mm : -INFINITY, l);
             }
         }
         if (!ok && lane == 0) {
@@ -462,6 +466,7 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             }
         } else if (warp == kKWarp || warp == kVWarp) {
             // ---------------------------------------------------------------- producers
+            fence_proxy_async_global();   // rows that earlier kernels stored, before TMA reads them
             const bool is_k = warp == kKWarp;
             const CUtensorMap *map = is_k ? &tm_k : &tm_v;
             uint64_t *full = is_k ? k_full : v_full, *empty = is_k ? k_empty : v_empty;
@@ -656,7 +661,8 @@ cudaError_t many(const DevPaged &C, const DevChunk &T, const ManyArgs &A, bool f
 cudaError_t launch_attend_many(const DevPaged &C, const DevChunk &T, int layer, const AttendMask &M,
                                const AttendIo &io, bool add_mass, bool first, const AttendWs &ws,
                                cudaStream_t s) {
-    const ManyArgs A{layer, M, io, ws.cta_status, ws.cut, ws.part_ml, ws.part_o, ws.lse2};
+    const ManyArgs A{layer, M, io, ws.cta_status, ws.cut, ws.part_ml, ws.part_o, ws.lse2,
+                     ws.q_packed};
     if (C.dtype == KV_FP16)
         return C.d == 64 ? many<Fp16, 64>(C, T, A, first, ws, s)
                          : many<Fp16, 128>(C, T, A, first, ws, s);

@@ -1,0 +1,450 @@
+// kv_paged_mass.cu -- accumulated attention weights of prompt chunks: for every cache row j,
+// mass_j += sum over the query rows that see it of 2^(s c - lse2), after the attention pass
+// has left each row's lse.  Bound by the powers of two (one per pair) and the K Q^T products.
+//
+// Keys are the rows of the product: S^T = K Q^T with 128 keys x 128 query rows, so that a
+// thread owns a key and adds its weights up in a register, in row order: no atomics, and
+// no exchange between threads.  An item is 256 keys (two tiles, one for each half of the key
+// warps) of one unit, against every tile of 128 query rows that sees any of them; K stays
+// in shared memory for the item (the next one's loads meanwhile), packed Q tiles stream
+// through a ring (32 KB per two products at d = 128).  The query rows that see key j are a
+// run of packed rows, [ (j - t0) G, (j + window - t0) G ), so the mask is two bounds.
+#include "kv_paged_attend.cuh"
+
+namespace kvevict {
+namespace {
+using namespace sm100;
+
+constexpr int kThreads = 12 * 32;
+constexpr int kKWarp = 0, kMmaWarp = 1, kQWarp = 2, kSchedWarp = 3, kKeyWarp = 4;
+constexpr int kBlockBytes = 128 * 128;       // [128 rows][64 columns], 128 B swizzle
+constexpr int kGroup = 2;                    // key tiles per item
+constexpr int kItems = 3;                    // items described ahead
+constexpr int kQSt = 3;                      // Q ring
+
+struct Item {
+    int stop;
+    int tile0, tiles;          // key tiles
+    int rt0, rt1;              // tiles of 128 query rows
+    int n, rows, t0;           // rows held, query rows, cache row of the first query
+    long long prow0;           // first packed row
+    const int32_t *table;
+};
+
+template <int D>
+struct Layout {
+    static constexpr int kOp = (D / 64) * kBlockBytes;
+    static constexpr int kK = 0;                          // [2 items][kGroup]
+    static constexpr int kQ = 2 * kGroup * kOp;
+    static constexpr int kLse = kQ + kQSt * kOp;          // [kQSt][128] -lse2
+    static constexpr int kBars = kLse + kQSt * 128 * 4;
+    static constexpr int kNumBars = 2 * 2 + 2 * kQSt + 2 * 4 + 1 + 2 * kItems;
+    static constexpr int kMisc = (kBars + kNumBars * 8 + 15) / 16 * 16;
+    static constexpr int kDesc = kMisc + 16;
+    static constexpr int kTotal = kDesc + kItems * (int)sizeof(Item);
+};
+
+struct MassArgs {
+    int layer;
+    AttendMask M;
+    const float *lse2;
+    int *status;
+};
+
+// Key groups of a unit, and of each the query row tiles [rt0, rt1) that see it.
+struct Groups {
+    int t0, rows, groups;
+    __device__ __forceinline__ Groups(const DevPaged &C, const UnitRows &U) {
+        rows = U.count * C.G;
+        t0 = U.n - U.count;
+        groups = many_rows(C, U) ? (U.n + kGroup * kManyTile - 1) / (kGroup * kManyTile) : 0;
+    }
+    __device__ __forceinline__ void range(const DevPaged &C, const AttendMask &M, int n, int g,
+                                          int &rt0, int &rt1) const {
+        const int key0 = g * kGroup * kManyTile, last = min(n, key0 + kGroup * kManyTile) - 1;
+        const int i0 = max(0, key0 - t0);
+        int i1 = n - 1 - t0;                       // last query
+        if (M.window > 0 && key0 >= M.sinks) i1 = min(i1, last - t0 + M.window - 1);
+        rt0 = (int)((long long)i0 * C.G >> 7);
+        rt1 = i1 < i0 ? rt0 : (int)(((long long)(i1 + 1) * C.G + 127) >> 7);
+    }
+};
+
+template <typename E, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
+            const DevPaged C, const DevChunk T, const MassArgs A) {
+    using Ly = Layout<D>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Ly::kBars);
+    uint64_t *k_full = bars, *k_empty = k_full + 2;          // [item parity]
+    uint64_t *q_full = k_empty + 2, *q_empty = q_full + kQSt;
+    uint64_t *s_full = q_empty + kQSt, *s_free = s_full + 4;  // [2 (row tile parity) + key tile]
+    uint64_t *mma_done = s_free + 4;
+    uint64_t *i_full = mma_done + 1, *i_empty = i_full + kItems;
+    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + Ly::kMisc);
+    volatile int *s_abort = reinterpret_cast<volatile int *>(s_tmem + 1);
+    Item *s_item = reinterpret_cast<Item *>(smem + Ly::kDesc);
+    float *s_lse = reinterpret_cast<float *>(smem + Ly::kLse);
+
+    if (threadIdx.x == 0) {
+        *s_abort = (smem_u32(smem) & 1023u) ? 1 : 0;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&k_full[i], 1);
+            mbar_init(&k_empty[i], 1);
+        }
+        for (int i = 0; i < kQSt; ++i) {
+            mbar_init(&q_full[i], 2);        // the copy, and the rows' lse
+            mbar_init(&q_empty[i], 1 + 8);   // the products, and the key warps (lse)
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&s_free[i], 4);
+        }
+        mbar_init(mma_done, 1);
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&i_full[i], 1);
+            mbar_init(&i_empty[i], 3 + 8);
+        }
+        fence_barrier_init();
+        prefetch_tensormap(&tm_k);
+        prefetch_tensormap(&tm_q);
+    }
+    pdl_wait();
+    pdl_trigger();
+    if (threadIdx.x == 0 && *s_abort) post_status(A.status, KV_ERR_UNSUPPORTED);
+    const uint32_t tmem = tmem_acquire_all(s_tmem);
+    // runs of equal numbers of (key group, row tile) steps; a group belongs to the run
+    // that its first step lies in
+    const CtaRun run = cut_run<kThreads>(C.R * C.H, 1, [&](int v) {
+        const UnitRows U = unit_rows(C, T, A.layer, v);
+        const Groups g(C, U);
+        int sum = 0;
+        for (int i = 0; i < g.groups; ++i) {
+            int a, b;
+            g.range(C, A.M, U.n, i, a, b);
+            sum += b - a;
+        }
+        return sum;
+    });
+    bool ok = *s_abort == 0;
+    auto item = [&](int i, bool &fine) -> const Item * {
+        fine = fine && mbar_wait(&i_full[i % kItems], (uint32_t)((i / kItems) & 1), s_abort,
+                                 C.wait_ns);
+        if (!fine) return nullptr;
+        const Item *it = &s_item[i % kItems];
+        return it->stop ? nullptr : it;
+    };
+    auto expired = [&]() {
+        *s_abort = 1;
+        post_status(A.status, KV_ERR_TIMEOUT);
+    };
+
+    if (warp == kSchedWarp) {
+        if (lane == 0 && ok) {
+            int i = 0, at = run.unit_begin;
+            auto put = [&](const Item &next) {
+                ok = mbar_wait(&i_empty[i % kItems], (uint32_t)((i / kItems) & 1) ^ 1u, s_abort,
+                               C.wait_ns);
+                if (!ok) return;
+                s_item[i % kItems] = next;
+                mbar_arrive(&i_full[i % kItems]);
+                ++i;
+            };
+            Item next;
+            next.stop = 0;
+            for (int v = run.unit; ok && at < run.end; ++v) {
+                const UnitRows U = unit_rows(C, T, A.layer, v);
+                const Groups g(C, U);
+                next.n = U.n;
+                next.rows = g.rows;
+                next.t0 = g.t0;
+                next.prow0 = packed_row(C, U, 0);
+                next.table = U.table;
+                for (int j = 0; ok && j < g.groups && at < run.end; ++j) {
+                    g.range(C, A.M, U.n, j, next.rt0, next.rt1);
+                    const int steps = next.rt1 - next.rt0;
+                    if (steps > 0 && at >= run.begin) {
+                        next.tile0 = j * kGroup;
+                        next.tiles = min(kGroup, ((U.n + kManyTile - 1) >> 7) - next.tile0);
+                        put(next);
+                    }
+                    at += steps;
+                }
+            }
+            next.stop = 1;
+            if (ok) put(next);
+            if (!ok) expired();
+        }
+    } else if (warp == kKWarp) {
+        fence_proxy_async_global();    // rows that earlier kernels stored, before TMA reads them
+        const int subs = kManyTile / C.ps, boxes = subs * (D / 64);
+        const int half = lane % (D / 64), sub = lane / (D / 64);
+        int cnt = 0;
+        for (int i = 0;; ++i) {
+            const Item *w = item(i, ok);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok || !w) break;
+            const int n = w->n, tiles = w->tiles, tile0 = w->tile0, s = i & 1;
+            const int32_t *table = w->table;
+            int y[kGroup], n_use = 0;
+            bool use[kGroup];
+#pragma unroll
+            for (int k = 0; k < kGroup; ++k) {
+                // a page that does not exist was reported by the attention pass
+                const int j = (tile0 + k) * kManyTile + sub * C.ps;
+                use[k] = k < tiles && lane < boxes && j < n;
+                const int page = use[k] ? table[j >> C.ps_log2] : -1;
+                use[k] = use[k] && page >= 0 && page < C.num_pages;
+                y[k] = page << C.ps_log2;
+                n_use += __popc(__ballot_sync(0xffffffffu, use[k]));
+            }
+            ok = mbar_wait(&k_empty[s], (uint32_t)((i >> 1) & 1) ^ 1u, s_abort, C.wait_ns);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (lane == 0) {
+                if (n_use) mbar_arrive_expect_tx(&k_full[s], n_use * C.ps * 128);
+                else mbar_arrive(&k_full[s]);
+                mbar_arrive(&i_empty[i % kItems]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < kGroup; ++k)
+                if (use[k])
+                    tma_load_2d(smem + Ly::kK + (s * kGroup + k) * Ly::kOp + half * kBlockBytes +
+                                    sub * C.ps * 128,
+                                &tm_k, &k_full[s], half * 64, y[k]);
+            ++cnt;
+        }
+        if (!ok && lane == 0) expired();
+        for (int s = 0; s < 2; ++s) {
+            const int uses = cnt / 2 + (cnt % 2 > s ? 1 : 0);
+            if (uses > 0) mbar_drain(&k_full[s], (uint32_t)((uses - 1) & 1), kDrainNs);
+        }
+    } else if (warp == kQWarp) {
+        fence_proxy_async_global();
+        int cnt = 0;
+        for (int i = 0;; ++i) {
+            const Item *w = item(i, ok);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok || !w) break;
+            const int rt0 = w->rt0, rt1 = w->rt1, rows = w->rows;
+            const long long prow0 = w->prow0;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&i_empty[i % kItems]);
+            for (int rt = rt0; rt < rt1; ++rt, ++cnt) {
+                const int s = cnt % kQSt;
+                float z[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int row = rt * 128 + lane * 4 + k;
+                    z[k] = row < rows ? -A.lse2[prow0 + row] : 0.f;
+                }
+                ok = mbar_wait(&q_empty[s], (uint32_t)((cnt / kQSt) & 1) ^ 1u, s_abort, C.wait_ns);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                *reinterpret_cast<float4 *>(s_lse + s * 128 + lane * 4) =
+                    make_float4(z[0], z[1], z[2], z[3]);
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&q_full[s]);
+                    mbar_arrive_expect_tx(&q_full[s], Ly::kOp);
+                    for (int kb = 0; kb < D / 64; ++kb)
+                        tma_load_2d(smem + Ly::kQ + s * Ly::kOp + kb * kBlockBytes, &tm_q,
+                                    &q_full[s], kb * 64, (int)(prow0 + rt * 128));
+                }
+            }
+        }
+        if (!ok && lane == 0) expired();
+        for (int s = 0; s < kQSt; ++s) {
+            const int uses = cnt / kQSt + (cnt % kQSt > s ? 1 : 0);
+            if (uses > 0) mbar_drain(&q_full[s], (uint32_t)((uses - 1) & 1), kDrainNs);
+        }
+    } else if (warp == kMmaWarp) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = E::kHalf ? idesc_f16_f32(128, 128) : idesc_bf16_f32(128, 128);
+            int rc = 0;                      // row tiles so far
+            int used[4] = {0, 0, 0, 0};      // products into each buffer
+            const Item *w;
+            for (int i = 0; (w = item(i, ok)); ++i) {
+                const int steps = w->rt1 - w->rt0, tiles = w->tiles, ks = i & 1;
+                mbar_arrive(&i_empty[i % kItems]);
+                ok = mbar_wait(&k_full[ks], (uint32_t)((i >> 1) & 1), s_abort, C.wait_ns);
+                for (int r = 0; ok && r < steps; ++r, ++rc) {
+                    const int s = rc % kQSt;
+                    ok = mbar_wait(&q_full[s], (uint32_t)((rc / kQSt) & 1), s_abort, C.wait_ns);
+#pragma unroll
+                    for (int k = 0; k < kGroup; ++k) {
+                        if (!ok || k >= tiles) continue;
+#pragma unroll
+                        for (int par = 0; par < 2; ++par) {
+                            if ((rc & 1) != par) continue;
+                            const int b = 2 * par + k;
+                            ok = mbar_wait(&s_free[b], (uint32_t)(used[b] & 1) ^ 1u, s_abort,
+                                           C.wait_ns);
+                            if (!ok) continue;
+                            ++used[b];
+                            tc_fence_after();
+                            const uint64_t ka = sdesc_k_sw128(
+                                smem_u32(smem + Ly::kK + (ks * kGroup + k) * Ly::kOp));
+                            const uint64_t qb =
+                                sdesc_k_sw128(smem_u32(smem + Ly::kQ + s * Ly::kOp));
+#pragma unroll
+                            for (int kb = 0; kb < D / 64; ++kb)
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk) {
+                                    const uint32_t o = kb * kBlockBytes + kk * 32;
+                                    if (kb | kk)
+                                        mma_ss_c<true>(tmem + 128 * b, sdesc_add(ka, o),
+                                                       sdesc_add(qb, o), idesc);
+                                    else
+                                        mma_ss_c<false>(tmem + 128 * b, ka, qb, idesc);
+                                }
+                            mma_commit(&s_full[b]);
+                        }
+                    }
+                    if (ok) mma_commit(&q_empty[s]);
+                }
+                if (ok) mma_commit(&k_empty[ks]);
+            }
+            if (!ok) expired();
+            mma_commit(mma_done);
+            mbar_drain(mma_done, 0, kDrainNs);
+        }
+    } else {
+        // ---------------------------------------------------------------- keys
+        const int k = (warp - kKeyWarp) >> 2;             // key tile of the item
+        const int quarter = warp & 3;
+        const int rr = quarter * 32 + lane;
+        const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
+        const float cs = A.M.scale_log2;
+        const float2 cs2 = make_float2(cs, cs);
+        int rc = 0, used[2] = {0, 0};
+        for (int i = 0;; ++i) {
+            const Item *w = item(i, ok);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok || !w) break;
+            const int rt0 = w->rt0, rt1 = w->rt1, rows = w->rows, n = w->n, t0 = w->t0;
+            const bool mine = k < w->tiles;
+            const int key0 = (w->tile0 + k) * kManyTile, j = key0 + rr;
+            const int32_t *table = w->table;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&i_empty[i % kItems]);
+            // the packed rows that see key j: [r_lo, r_hi); those that see every key of the
+            // tile: [a_lo, a_hi)
+            const bool held = mine && j < n;
+            const long long G = C.G;
+            const bool sink = j < A.M.sinks || A.M.window == 0;
+            const int r_lo = held ? (int)min((long long)rows, max(0ll, (j - t0) * G)) : rows;
+            const int r_hi =
+                sink ? rows
+                     : (int)min((long long)rows, max(0ll, ((long long)j + A.M.window - t0) * G));
+            const int last = key0 + kManyTile - 1;
+            const int a_lo = last < n ? (int)min((long long)rows, max(0ll, (last - t0) * G)) : rows;
+            const int a_hi =
+                last < A.M.sinks || A.M.window == 0
+                    ? rows
+                    : (int)min((long long)rows, max(0ll, ((long long)key0 + A.M.window - t0) * G));
+            float acc = 0.f;
+            for (int rt = rt0; rt < rt1; ++rt, ++rc) {
+                const int qs = rc % kQSt, par = rc & 1;
+                ok = mbar_wait(&q_full[qs], (uint32_t)((rc / kQSt) & 1), s_abort, C.wait_ns);
+                if (mine) {
+                    const int u = par ? used[1] : used[0];
+                    ok = ok && mbar_wait(&s_full[2 * par + k], (uint32_t)(u & 1), s_abort,
+                                         C.wait_ns);
+                    if (par) ++used[1]; else ++used[0];
+                }
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (mine) {
+                    tc_fence_after();
+                    const int row0 = rt * 128;
+                    const bool all = row0 >= a_lo && row0 + 128 <= a_hi;
+                    const uint32_t base = tmem + lane_addr + 128 * (2 * par + k);
+                    const float4 *lse = reinterpret_cast<const float4 *>(s_lse + qs * 128);
+                    float2 sum[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) sum[c] = make_float2(0.f, 0.f);
+                    float s[4][32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld32(base + 32 * c, s[c]);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) reg_fence(s[c]);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s_free[2 * par + k]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t see =
+                            all ? 0xffffffffu
+                                : low_bits(r_hi - row0 - 32 * c) & ~low_bits(r_lo - row0 - 32 * c);
+#pragma unroll
+                        for (int x = 0; x < 32; x += 4) {
+                            const float4 z = lse[c * 8 + x / 4];
+                            const float2 e0 = __ffma2_rn(make_float2(s[c][x], s[c][x + 1]), cs2,
+                                                         make_float2(z.x, z.y));
+                            const float2 e1 = __ffma2_rn(make_float2(s[c][x + 2], s[c][x + 3]), cs2,
+                                                         make_float2(z.z, z.w));
+                            float2 p0 = make_float2(ex2_approx(e0.x), ex2_approx(e0.y));
+                            float2 p1 = make_float2(ex2_approx(e1.x), ex2_approx(e1.y));
+                            if (!all) {
+                                if (!(see >> x & 1u)) p0.x = 0.f;
+                                if (!(see >> (x + 1) & 1u)) p0.y = 0.f;
+                                if (!(see >> (x + 2) & 1u)) p1.x = 0.f;
+                                if (!(see >> (x + 3) & 1u)) p1.y = 0.f;
+                            }
+                            sum[(x >> 1) & 3] = __fadd2_rn(sum[(x >> 1) & 3], p0);
+                            sum[((x >> 1) + 1) & 3] = __fadd2_rn(sum[((x >> 1) + 1) & 3], p1);
+                        }
+                    }
+                    const float2 a = __fadd2_rn(__fadd2_rn(sum[0], sum[1]),
+                                                __fadd2_rn(sum[2], sum[3]));
+                    acc += a.x + a.y;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&q_empty[qs]);
+            }
+            if (!ok) break;
+            if (held && r_lo < r_hi) {
+                const long long at = page_row(C, table, j);
+                if (at >= 0) C.mass[at] += acc;
+            }
+        }
+        if (!ok && lane == 0) expired();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    tmem_release_all(tmem);
+}
+
+template <typename E, int D>
+cudaError_t mass(const DevPaged &C, const DevChunk &T, const MassArgs &A, const AttendWs &ws,
+                 cudaStream_t s) {
+    using Ly = Layout<D>;
+    CUtensorMap mk, mq;
+    if (!make_tile_map(&mk, C.k, C.num_pages * C.ps, D, C.ps) ||
+        !make_tile_map(&mq, ws.q_packed, T.tokens * C.Hq, D, 128))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(mass_kernel<E, D>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, Ly::kTotal);
+    if (e == cudaSuccess)
+        e = launch_dependent(mass_kernel<E, D>, dim3(kManyCtas), kThreads, Ly::kTotal, s, mk, mq, C,
+                             T, A);
+    return e;
+}
+
+}  // namespace
+
+cudaError_t launch_many_mass(const DevPaged &C, const DevChunk &T, int layer, const AttendMask &M,
+                             const AttendWs &ws, cudaStream_t s) {
+    const MassArgs A{layer, M, ws.lse2, ws.status};
+    if (C.dtype == KV_FP16)
+        return C.d == 64 ? mass<Fp16, 64>(C, T, A, ws, s) : mass<Fp16, 128>(C, T, A, ws, s);
+    return C.d == 64 ? mass<Bf16, 64>(C, T, A, ws, s) : mass<Bf16, 128>(C, T, A, ws, s);
+}
+
+}  // namespace kvevict
