@@ -386,12 +386,17 @@ kv_status kv_evict_host(const kv_problem *p, const kv_host_plan *plan, const voi
  *
  * Device-side conditions.  A length outside 0 .. max_pages * page_size makes
  * its unit empty; a page index outside [0, num_pages) that holds a row in use
- * is not followed.  kv_paged_attention and kv_paged_evict post
- * KV_ERR_INVALID_ARG for either (a wait that expired: KV_ERR_TIMEOUT) to the
- * workspace's status word, which each call sets anew; outputs of units so
- * reported are unspecified.  kv_paged_append skips such rows, and
- * kv_paged_load gives a unit that does not fit its table length -1, which the
- * calls after it report.
+ * is not followed.  kv_paged_append and kv_paged_attention post
+ * KV_ERR_INVALID_ARG for either (an expired wait: KV_ERR_TIMEOUT) to the cache's
+ * own status word and leave the outputs of such units unspecified; a decoder
+ * makes these calls once a layer and token, so none of them spends a launch on
+ * zeroing the word: it keeps the first code until kv_check_status(c->status, ...)
+ * reads and clears it.  kv_paged_load gives a unit that does not fit its table
+ * length -1, which the calls after it post.  kv_paged_evict posts to its
+ * workspace's status word, which it zeroes first.
+ *
+ * Pages may be shared by units that only read them; a page that a call writes
+ * (rows, or weights with add_mass) belongs to one unit.
  */
 typedef enum kv_dtype {
     KV_BF16 = 0,
@@ -412,6 +417,7 @@ typedef struct kv_paged {
     float *mass;
     const int32_t *page_table;
     int32_t *lens;
+    int32_t *status;           /* the cache's status word, device memory, 0 when it is made */
 } kv_paged;
 
 /* The new tokens of a step, packed: request r's are [tok_offsets[r], tok_offsets[r+1])

@@ -82,7 +82,8 @@ class _KvPaged(ctypes.Structure):
                 ("max_pages", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("num_pages", ctypes.c_int64), ("k_pages", ctypes.c_void_p),
                 ("v_pages", ctypes.c_void_p), ("mass", ctypes.c_void_p),
-                ("page_table", ctypes.c_void_p), ("lens", ctypes.c_void_p)]
+                ("page_table", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("status", ctypes.c_void_p)]
 
 
 class _KvChunk(ctypes.Structure):
@@ -677,6 +678,10 @@ class PagedCache:
     page_table        int32 [requests][layers][kv_heads][max_pages]
     lens              int32 [requests][layers][kv_heads]: rows held
     mass              float32 [num_pages][page_size] or None: accumulated attention weights
+
+    ``status`` holds the first device-side condition that kv_paged_append or
+    kv_paged_attention met (a length or page that cannot be); kv_check_status(cache.status)
+    reads and clears it.
     """
 
     def __init__(self, k_pages, v_pages, page_table, lens, num_q_heads: int, mass=None):
@@ -700,11 +705,12 @@ class PagedCache:
         self.num_q_heads = int(num_q_heads)
         self.num_pages, self.page_size, self.head_dim = k_pages.shape
         self.dtype, self.device = k_pages.dtype, k_pages.device
+        self.status = torch.zeros(64, dtype=torch.int32, device=self.device)
         self._c = _KvPaged(self.num_requests, self.num_layers, self.num_kv_heads, self.num_q_heads,
                            self.head_dim, self.page_size, self.max_pages,
                            KV_FP16 if self.dtype == torch.float16 else KV_BF16, self.num_pages,
                            k_pages.data_ptr(), v_pages.data_ptr(), _ptr(mass),
-                           page_table.data_ptr(), lens.data_ptr())
+                           page_table.data_ptr(), lens.data_ptr(), self.status.data_ptr())
         self._ref = ctypes.byref(self._c)
 
     @classmethod

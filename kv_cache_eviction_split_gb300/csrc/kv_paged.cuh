@@ -19,6 +19,7 @@ struct DevPaged {
     int32_t *lens;             // [units]
     void *k, *v;               // [num_pages][ps][d]
     float *mass;               // [num_pages][ps] or null
+    int *status;               // the cache's status word
     unsigned long long wait_ns;   // limit of the pipeline waits (kv_set_wait_limit_ns)
 };
 
@@ -28,6 +29,7 @@ struct DevChunk {
     const long long *host_off; // host copy (host code only)
     long long tokens;          // off[R]
     int max_t;                 // most new tokens of one request
+    int few_max;               // query rows a head (T * G) that the few-rows kernels take
 };
 
 // Which cache rows a query sees, and the scale of its logits.
@@ -89,9 +91,13 @@ cudaError_t launch_paged_evict(const DevPaged &S, const DevPaged &D, const int32
 // computed from device memory (lens, token offsets), so a captured call follows
 // the lengths of each replay.
 
-constexpr int kFewRows = 16;       // query rows (T * G) the few-rows kernel takes
+constexpr int kFewRows = 16;       // most query rows of an item of the few-rows kernels
 constexpr int kFewTile = 64;       // keys per tile there
 constexpr int kFewCtas = 2 * 152;  // two CTAs on each SM
+// Tables of at most kShortRows rows take the few-rows kernel's one-launch form, which there
+// also takes up to kShortFewRows query rows, in blocks of kFewRows (without add_mass).
+constexpr int kShortRows = 4096;
+constexpr int kShortFewRows = 128;
 constexpr int kManyTile = 128;     // keys per tile of the tensor-memory kernel
 constexpr int kManyRows = 256;     // query rows per item there: two tiles of 128
 constexpr int kManyCtas = 152;
@@ -131,19 +137,16 @@ __device__ __forceinline__ int part_slot(int cta, bool begun_here) {
 
 // Workspace of the attention (all offsets 256-byte aligned).
 struct AttendWs {
-    int *status;
-    int *cta_status;           // [ctas] each CTA's own status word
     CutItem *cut;              // [ctas] unit -1: no item ends here that an earlier CTA began
     float2 *part_ml;           // [2 ctas][rows of an item] (m in log2 units, l)
     float *part_o;             // [2 ctas][rows of an item][d]
     // add_mass: log2 of the softmax sums of the query rows, and the rows themselves, in
     // packed order (packed_row)
     float *lse2;               // [tokens * Hq]
-    void *q_packed;            // [tokens * Hq][d], of requests with more than kFewRows rows
-    // few rows with add_mass: the logits (log2 units, -inf unseen) of every tile
-    int *tiles;                // [1] tiles in all
-    int2 *tile_at;             // [tiles] unit of the layer, key tile
-    float *logits;             // [tiles][kFewRows][kFewTile]
+    void *q_packed;            // [tokens * Hq][d], of the requests the many-rows kernel takes
+    // few rows with add_mass: the logits (log2 units, -inf unseen) of every tile of every
+    // unit of the layer, in its span's order
+    float *logits;             // [R * H][ceil(cap / kFewTile)][kFewRows][kFewTile]
     size_t total;
 };
 AttendWs attend_ws_layout(const DevPaged &C, const DevChunk &T, bool add_mass, void *base);

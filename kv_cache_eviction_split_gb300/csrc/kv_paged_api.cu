@@ -30,7 +30,8 @@ kv_status make_paged(const kv_paged *c, DevPaged *C) {
     const long long kRowLimit = 1LL << 31;
     const long long units = (long long)c->num_requests * c->num_layers * c->num_kv_heads;
     if (c->num_pages >= kRowLimit / c->page_size || c->max_pages >= kRowLimit / c->page_size ||
-        (long long)c->num_layers * c->num_kv_heads >= kRowLimit || units >= kRowLimit)
+        (long long)c->num_layers * c->num_kv_heads >= kRowLimit || units >= kRowLimit ||
+        (long long)c->num_requests * c->num_kv_heads >= (1 << 20))
         return KV_ERR_UNSUPPORTED;
     C->R = c->num_requests;
     C->L = c->num_layers;
@@ -50,9 +51,10 @@ kv_status make_paged(const kv_paged *c, DevPaged *C) {
     C->k = c->k_pages;
     C->v = c->v_pages;
     C->mass = c->mass;
+    C->status = c->status;
     C->wait_ns = kv_get_wait_limit_ns();
     if (units > 0 && (bad_ptr(c->k_pages) || bad_ptr(c->v_pages) || bad_ptr(c->page_table) ||
-                      bad_ptr(c->lens) || !aligned16(c->mass)))
+                      bad_ptr(c->lens) || bad_ptr(c->status) || !aligned16(c->mass)))
         return KV_ERR_INVALID_ARG;
     return KV_OK;
 }

@@ -16,20 +16,29 @@ __device__ __forceinline__ void pdl_trigger() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// cluster > 1: blocks in clusters of that many along x.
 template <typename... A, typename... B>
-cudaError_t launch_dependent(void (*kernel)(A...), dim3 grid, int threads, size_t smem,
-                             cudaStream_t s, B... args) {
+cudaError_t launch_cluster_dependent(void (*kernel)(A...), int cluster, dim3 grid, int threads,
+                                     size_t smem, cudaStream_t s, B... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<A>(args)...);
+}
+template <typename... A, typename... B>
+cudaError_t launch_dependent(void (*kernel)(A...), dim3 grid, int threads, size_t smem,
+                             cudaStream_t s, B... args) {
+    return launch_cluster_dependent(kernel, 1, grid, threads, smem, s, args...);
 }
 
 // 16-bit elements: packing of two fp32 values (round to nearest), the first low.
@@ -94,9 +103,10 @@ __device__ __forceinline__ UnitRows unit_rows(const DevPaged &C, const DevChunk 
     return U;
 }
 
-// Whether the tensor-memory kernel takes a unit's rows (the few-rows kernel otherwise).
-__device__ __forceinline__ bool many_rows(const DevPaged &C, const UnitRows &U) {
-    return (long long)U.count * C.G > kFewRows;
+// Whether the tensor-memory kernel takes a unit's rows (the few-rows kernels otherwise).
+__device__ __forceinline__ bool many_rows(const DevPaged &C, const DevChunk &T,
+                                          const UnitRows &U) {
+    return (long long)U.count * C.G > T.few_max;
 }
 
 // Bits 0 .. n-1 (none for n <= 0).
@@ -171,18 +181,20 @@ __device__ __forceinline__ float row_lse2(float m, float l) {
     return l > 0.f ? m + __log2f(l) : -INFINITY;
 }
 
-// Merges the partials of the items that several CTAs held and sets the call's status
-// word (first) or adds to it.  rows: row slots of a partial.
+// Merges the partials of the items that several CTAs held.  rows: row slots of a partial.
 cudaError_t launch_attend_merge(const DevPaged &C, const DevChunk &T, int layer,
                                 const AttendIo &io, float *lse2, const AttendWs &ws, int ctas,
-                                int rows, bool first, cudaStream_t s);
+                                int rows, cudaStream_t s);
+// Requests of at most T.few_max query rows a head: `items` items of at most kFewRows rows
+// in all, the largest with max_rows, `blocks` of them at most to a unit.
 cudaError_t launch_attend_few(const DevPaged &C, const DevChunk &T, int layer, const AttendMask &M,
-                              const AttendIo &io, bool add_mass, int max_rows, bool first,
-                              const AttendWs &ws, cudaStream_t s);
+                              const AttendIo &io, bool add_mass, long long items, int max_rows,
+                              int blocks, const AttendWs &ws, cudaStream_t s);
+// The others.
 cudaError_t launch_attend_many(const DevPaged &C, const DevChunk &T, int layer, const AttendMask &M,
-                               const AttendIo &io, bool add_mass, bool first, const AttendWs &ws,
+                               const AttendIo &io, bool add_mass, const AttendWs &ws,
                                cudaStream_t s);
-// The weights of the requests launch_attend_many took, from its packed queries and lse.
+// Their weights, from its packed queries and lse.
 cudaError_t launch_many_mass(const DevPaged &C, const DevChunk &T, int layer, const AttendMask &M,
                              const AttendWs &ws, cudaStream_t s);
 

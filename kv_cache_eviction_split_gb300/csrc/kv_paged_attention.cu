@@ -17,27 +17,14 @@ namespace {
 template <typename X, int D, int kRowSlots, bool kSplit>
 __global__ void __launch_bounds__(128)
 merge_kernel(const DevPaged C, const DevChunk T, int layer, const AttendIo io, float *lse2,
-             int *status, const int *__restrict__ cta_status, const CutItem *__restrict__ cut,
-             const float2 *__restrict__ part_ml, const float *__restrict__ part_o, int ctas,
-             bool first) {
+             const CutItem *__restrict__ cut, const float2 *__restrict__ part_ml,
+             const float *__restrict__ part_o) {
     constexpr int kV = D / 32;
-    __shared__ float sm_o[4][D], sm_l[4];
+    constexpr int kMost = kSplit ? kFewCtas : kManyCtas;      // partials of an item
+    __shared__ float sm_o[4][D], sm_w[kSplit ? 1 : 4][kMost], sm_l[4];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
     pdl_trigger();
-    if (blockIdx.x == 0 && blockIdx.y == 0) {
-        int code = 0;
-        for (int i = threadIdx.x; i < ctas; i += 128) code = max(code, cta_status[i]);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) code = max(code, __shfl_xor_sync(0xffffffffu, code, o));
-        if (lane == 0) sm_l[warp] = __int_as_float(code);
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            for (int w = 1; w < 4; ++w) code = max(code, __float_as_int(sm_l[w]));
-            if (first || *status == 0) *status = code;
-        }
-        __syncthreads();
-    }
     const CutItem it = cut[blockIdx.x];
     if (it.unit < 0) return;
     const int row = kSplit ? (int)blockIdx.y : (int)blockIdx.y * 4 + warp;
@@ -46,35 +33,48 @@ merge_kernel(const DevPaged C, const DevChunk T, int layer, const AttendIo io, f
     auto slot_row = [&](int p) {
         return (long long)part_slot(it.cta0 + p, p == 0) * kRowSlots + row;
     };
-    float m = -INFINITY;
+    // the partials' weights 2^(m_p - m) (0 where nothing was seen: no output was written)
+    float *w = sm_w[kSplit ? 0 : warp];
+    const int step = kSplit ? 128 : 32, i0 = kSplit ? threadIdx.x : lane;
+    float m = -INFINITY, l = 0.f;
     for (int p = lane; p < parts; p += 32) m = fmaxf(m, part_ml[slot_row(p)].x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float l = 0.f, acc[kV] = {};
-    constexpr int kStep = kSplit ? 4 : 1;
-#pragma unroll 4
-    for (int p = kSplit ? warp : 0; p < parts; p += kStep) {
-        const long long at = slot_row(p);
-        const float2 ml = part_ml[at];
-        if (ml.x == -INFINITY) continue;   // nothing seen: its output was not written
-        const float w = shrink(ml.x, m);
-        l += ml.y * w;
-        const float *src = part_o + at * D + lane * kV;
+    for (int p = i0; p < parts; p += step) {
+        const float2 ml = part_ml[slot_row(p)];
+        w[p] = shrink(ml.x, m);
+        l += ml.y * w[p];
+    }
 #pragma unroll
-        for (int i = 0; i < kV; ++i) acc[i] += src[i] * w;
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (kSplit) {
+        if (lane == 0) sm_l[warp] = l;
+        __syncthreads();
+        l = (sm_l[0] + sm_l[1]) + (sm_l[2] + sm_l[3]);
+    } else {
+        __syncwarp();
+    }
+    float acc[kV] = {};
+    constexpr int kStep = kSplit ? 4 : 1;
+#pragma unroll 8
+    for (int p = kSplit ? warp : 0; p < parts; p += kStep) {
+        const float f = w[p];
+        const float *src = part_o + slot_row(p) * D + lane * kV;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            const float x = src[i];
+            acc[i] += f == 0.f ? 0.f : x * f;
+        }
     }
     if (kSplit) {
 #pragma unroll
         for (int i = 0; i < kV; ++i) sm_o[warp][lane * kV + i] = acc[i];
-        if (lane == 0) sm_l[warp] = l;
         __syncthreads();
         if (warp) return;
 #pragma unroll
-        for (int w = 1; w < 4; ++w) {
-            l += sm_l[w];
+        for (int k = 1; k < 4; ++k)
 #pragma unroll
-            for (int i = 0; i < kV; ++i) acc[i] += sm_o[w][lane * kV + i];
-        }
+            for (int i = 0; i < kV; ++i) acc[i] += sm_o[k][lane * kV + i];
     }
     const UnitRows U = unit_rows(C, T, layer, it.unit);
     const long long tok = U.tok0 + (it.row0 + row) / C.G;
@@ -95,43 +95,49 @@ merge_kernel(const DevPaged C, const DevChunk T, int layer, const AttendIo io, f
 
 template <typename X, int D>
 cudaError_t merge(const DevPaged &C, const DevChunk &T, int layer, const AttendIo &io, float *lse2,
-                  const AttendWs &ws, int ctas, int rows, bool first, cudaStream_t s) {
+                  const AttendWs &ws, int ctas, int rows, cudaStream_t s) {
     if (rows == kFewRows)
         return launch_dependent(merge_kernel<X, D, kFewRows, true>,
                                 dim3(ctas, std::min<long long>(kFewRows, (long long)T.max_t * C.G)),
-                                128, 0, s, C, T, layer, io, lse2, ws.status, ws.cta_status, ws.cut,
-                                ws.part_ml, ws.part_o, ctas, first);
+                                128, 0, s, C, T, layer, io, lse2, ws.cut, ws.part_ml, ws.part_o);
     return launch_dependent(merge_kernel<X, D, kManyRows, false>, dim3(ctas, kManyRows / 4), 128, 0,
-                            s, C, T, layer, io, lse2, ws.status, ws.cta_status, ws.cut, ws.part_ml,
-                            ws.part_o, ctas, first);
+                            s, C, T, layer, io, lse2, ws.cut, ws.part_ml, ws.part_o);
 }
 
 }  // namespace
 
 cudaError_t launch_attend_merge(const DevPaged &C, const DevChunk &T, int layer,
                                 const AttendIo &io, float *lse2, const AttendWs &ws, int ctas,
-                                int rows, bool first, cudaStream_t s) {
+                                int rows, cudaStream_t s) {
     if (C.dtype == KV_FP16)
-        return C.d == 64 ? merge<Fp16, 64>(C, T, layer, io, lse2, ws, ctas, rows, first, s)
-                         : merge<Fp16, 128>(C, T, layer, io, lse2, ws, ctas, rows, first, s);
-    return C.d == 64 ? merge<Bf16, 64>(C, T, layer, io, lse2, ws, ctas, rows, first, s)
-                     : merge<Bf16, 128>(C, T, layer, io, lse2, ws, ctas, rows, first, s);
+        return C.d == 64 ? merge<Fp16, 64>(C, T, layer, io, lse2, ws, ctas, rows, s)
+                         : merge<Fp16, 128>(C, T, layer, io, lse2, ws, ctas, rows, s);
+    return C.d == 64 ? merge<Bf16, 64>(C, T, layer, io, lse2, ws, ctas, rows, s)
+                     : merge<Bf16, 128>(C, T, layer, io, lse2, ws, ctas, rows, s);
 }
 
 namespace {
-// Requests of the step whose query rows a head fit the few-rows kernel, and the others.
+// Which kernels take the step's requests.
 struct Classes {
-    int few, few_rows, many;
+    int few_max;               // most query rows a head of the few-rows kernels
+    int few_requests, max_rows, blocks;   // rows and row blocks of the largest of them
+    long long items;           // their items
+    int many;                  // the others
 };
-Classes classify(const DevPaged &C, const DevChunk &T) {
-    Classes k{0, 0, 0};
+Classes classify(const DevPaged &C, const DevChunk &T, bool add_mass) {
+    Classes k{};
+    k.few_max = C.cap <= kShortRows && !add_mass ? kShortFewRows : kFewRows;
+    k.blocks = 1;
     for (int r = 0; r < C.R; ++r) {
         const long long rows = (T.host_off[r + 1] - T.host_off[r]) * C.G;
-        if (rows > kFewRows) {
+        if (rows > k.few_max) {
             ++k.many;
         } else if (rows > 0) {
-            ++k.few;
-            k.few_rows = std::max(k.few_rows, (int)rows);
+            const int blocks = (int)(rows + kFewRows - 1) / kFewRows;
+            ++k.few_requests;
+            k.max_rows = std::max(k.max_rows, (int)rows);
+            k.blocks = std::max(k.blocks, blocks);
+            k.items += (long long)blocks * C.H;
         }
     }
     return k;
@@ -147,36 +153,36 @@ AttendWs attend_ws_layout(const DevPaged &C, const DevChunk &T, bool add_mass, v
         off = (off + bytes + 255) / 256 * 256;
         return p;
     };
-    const Classes k = classify(C, T);
+    const Classes k = classify(C, T, add_mass);
     // the two kernels run one after the other: they share the partials
-    const size_t slots = std::max<size_t>(k.few ? 2 * kFewCtas * (size_t)kFewRows : 0,
+    const bool cut_few = k.few_requests && C.cap > kShortRows;
+    const size_t slots = std::max<size_t>(cut_few ? 2 * kFewCtas * (size_t)kFewRows : 0,
                                           k.many ? 2 * kManyCtas * (size_t)kManyRows : 0);
-    ws.status = reinterpret_cast<int *>(take(kHeaderBytes));
-    ws.cta_status = reinterpret_cast<int *>(take(kFewCtas * sizeof(int)));
     ws.cut = reinterpret_cast<CutItem *>(take(kFewCtas * sizeof(CutItem)));
     ws.part_ml = reinterpret_cast<float2 *>(take(slots * sizeof(float2)));
     ws.part_o = reinterpret_cast<float *>(take(slots * C.d * sizeof(float)));
     if (add_mass) {
-        const size_t tiles = (size_t)k.few * C.H * ((C.cap + kFewTile - 1) / kFewTile);
+        const size_t tiles = (size_t)C.R * C.H * ((C.cap + kFewTile - 1) / kFewTile);
         ws.lse2 = reinterpret_cast<float *>(take((size_t)T.tokens * C.Hq * sizeof(float)));
         ws.q_packed = take(k.many ? (size_t)T.tokens * C.Hq * C.d * 2 : 0);
-        ws.tiles = reinterpret_cast<int *>(take(sizeof(int)));
-        ws.tile_at = reinterpret_cast<int2 *>(take(tiles * sizeof(int2)));
         ws.logits = reinterpret_cast<float *>(
-            take(tiles * kFewRows * kFewTile * sizeof(float)));
+            take(k.few_requests ? tiles * kFewRows * kFewTile * sizeof(float) : 0));
     }
     ws.total = off;
     return ws;
 }
 
-cudaError_t launch_paged_attention(const DevPaged &C, const DevChunk &T, int layer,
+cudaError_t launch_paged_attention(const DevPaged &C, const DevChunk &T0, int layer,
                                    const AttendMask &M, const AttendIo &io, bool add_mass,
                                    const AttendWs &ws, cudaStream_t s) {
-    const Classes k = classify(C, T);
+    const Classes k = classify(C, T0, add_mass);
+    DevChunk T = T0;
+    T.few_max = k.few_max;
     cudaError_t e = cudaSuccess;
-    if (k.few) e = launch_attend_few(C, T, layer, M, io, add_mass, k.few_rows, true, ws, s);
+    if (k.few_requests)
+        e = launch_attend_few(C, T, layer, M, io, add_mass, k.items, k.max_rows, k.blocks, ws, s);
     if (e == cudaSuccess && k.many) {
-        e = launch_attend_many(C, T, layer, M, io, add_mass, !k.few, ws, s);
+        e = launch_attend_many(C, T, layer, M, io, add_mass, ws, s);
         if (e == cudaSuccess && add_mass) e = launch_many_mass(C, T, layer, M, ws, s);
     }
     return e;

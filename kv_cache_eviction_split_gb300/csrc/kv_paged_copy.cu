@@ -47,11 +47,14 @@ append_kernel(const DevPaged C, const DevChunk T, int layer, const uint4 *__rest
     if (tok >= T.off[C.R]) return;
     const long long u = ((long long)r * C.L + layer) * C.H + h;
     int n;
-    if (!unit_len(C, u, n)) return;
+    const bool ok = unit_len(C, u, n);
     const long long j = n - (T.off[r + 1] - tok);
-    if (j < 0) return;
-    const long long row = page_row(C, C.table + u * C.max_pages, (int)j);
-    if (row < 0) return;
+    if (ok && j < 0) return;
+    const long long row = ok ? page_row(C, C.table + u * C.max_pages, (int)j) : -1;
+    if (row < 0) {
+        post_status(C.status, KV_ERR_INVALID_ARG);
+        return;
+    }
     reinterpret_cast<uint4 *>(p.which ? C.v : C.k)[row * Part::kVecs + p.ch] = val;
     if (C.mass && p.which == 0 && p.ch == 0) C.mass[row] = 0.f;
 }

@@ -17,11 +17,22 @@
 // of tiles by TMA (3 x 32 KB at d = 128): its lanes hold 32 page-table entries and issue
 // one box each.  Two CTAs an SM keep ~190 KB in flight.  The consumers merge through
 // shared memory once per item.
+//
+// Two forms.  Long tables (kCluster = 0): all items' tiles cut into 304 equal runs, cut items
+// merged by a second kernel (kv_paged_attention.cu).  Short tables (kCluster = 1 .. 8): a
+// cluster per item, each CTA a part of its tiles, merged through distributed shared
+// memory: one launch, which is what a short call costs; there an item's row block may also
+// be one of several of a unit (up to kShortFewRows rows), each reading K and V again.
+#include <algorithm>
+
+#include <cooperative_groups.h>
+
 #include "kv_paged_attend.cuh"
 
 namespace kvevict {
 namespace {
 using namespace sm100;
+namespace cg = cooperative_groups;
 
 constexpr int kConsumers = 4;
 constexpr int kThreads = (kConsumers + 1) * 32;
@@ -92,31 +103,50 @@ struct FewArgs {
     int layer;
     AttendMask M;
     AttendIo io;
-    int *cta_status;
     CutItem *cut;
     float2 *part_ml;
     float *part_o;
     float *lse2;
-    int *tiles;
-    int2 *tile_at;
     float *logits;             // null without add_mass
+    int unit_tiles;            // tiles of the logits to a unit
+    int blocks;                // kCluster > 0: row blocks to a unit
 };
 
-template <typename E, int D, int NT>
+// At most NT * 8 query rows of a unit, and the tiles they see.
+struct FewItem {
+    int row0, rows, t_lo, t_hi, lo, sinks;
+    TileSpan span;
+    __device__ __forceinline__ FewItem(const DevPaged &C, const AttendMask &M, const UnitRows &U,
+                                       int block, int most) {
+        row0 = block * most;
+        rows = min(most, U.count * C.G - row0);
+        t_lo = U.n - U.count + row0 / C.G;
+        t_hi = U.n - U.count + (row0 + rows - 1) / C.G;
+        lo = window_lo(M, max(t_lo, 0));
+        sinks = min(M.sinks, lo);
+        span = tile_span(M, t_lo, t_hi, 6);
+    }
+};
+
+// Whether the few-rows kernels take a unit's rows.
+__device__ __forceinline__ bool few_rows(const DevPaged &C, const DevChunk &T, const UnitRows &U) {
+    return U.count > 0 && !many_rows(C, T, U);
+}
+
+template <typename E, int D, int NT, int kCluster>
 __global__ void __launch_bounds__(kThreads, 2)
 few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
            const DevPaged C, const DevChunk T, const FewArgs A) {
     using Ly = Layout<D, NT>;
-    constexpr int kSt = Ly::kStages;
+    constexpr int kSt = Ly::kStages, kRows = NT * 8;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + Ly::kBars), *empty = full + kSt;
-    int *s_status = reinterpret_cast<int *>(empty + kSt);
-    volatile int *s_abort = s_status + 1;
-    CutItem *s_cut = reinterpret_cast<CutItem *>(s_status + 4);
+    volatile int *s_abort = reinterpret_cast<volatile int *>(empty + kSt);
+    CutItem *s_cut = reinterpret_cast<CutItem *>(empty + kSt + 2);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        *s_status = (smem_u32(smem) & 1023u) ? KV_ERR_UNSUPPORTED : 0;
-        *s_abort = *s_status;
+        *s_abort = (smem_u32(smem) & 1023u) ? 1 : 0;
+        if (*s_abort) post_status(C.status, KV_ERR_UNSUPPORTED);
         *s_cut = CutItem{-1, 0, 0, 0};
         for (int s = 0; s < kSt; ++s) {
             mbar_init(&full[s], 1);
@@ -129,12 +159,31 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
     pdl_wait();
     pdl_trigger();
     const int units = C.R * C.H;
-    const CtaRun run = cut_run<kThreads>(units, 1, [&](int v) {
-        const UnitRows U = unit_rows(C, T, A.layer, v);
-        if (U.count <= 0 || (long long)U.count * C.G > NT * 8) return 0;
-        return tile_span(A.M, U.n - U.count, U.n - 1, 6).total;
-    });
+    CtaRun run;
+    int rank = 0, block = 0;
+    if constexpr (kCluster == 0) {
+        run = cut_run<kThreads>(units, 1, [&](int v) {
+            const UnitRows U = unit_rows(C, T, A.layer, v);
+            return few_rows(C, T, U) ? FewItem(C, A.M, U, 0, kRows).span.total : 0;
+        });
+    } else {
+        // one item a cluster: its tiles are the whole order, each CTA's run a part of them
+        rank = (int)(blockIdx.x % kCluster);
+        const int i = (int)(blockIdx.x / kCluster);
+        run.unit = i / A.blocks;
+        block = i % A.blocks;
+        const UnitRows U = unit_rows(C, T, A.layer, run.unit);
+        if (!few_rows(C, T, U) || block * kRows >= U.count * C.G) return;   // a whole cluster
+        run.total = FewItem(C, A.M, U, block, kRows).span.total;
+        run.per = (run.total + kCluster - 1) / kCluster;
+        run.begin = min(run.total, rank * run.per);
+        run.end = min(run.total, run.begin + run.per);
+        run.unit_begin = 0;
+        __syncthreads();
+    }
     const bool go = *s_abort == 0;
+    // the loop over items ends after the run's last tile, or after the cluster's one item
+    auto more = [&](int at) { return kCluster > 0 ? at == 0 : at < run.end; };
 
     if (warp == kConsumers) {
         // ---------------------------------------------------------------- producer
@@ -146,18 +195,15 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
         const CUtensorMap *map = kv ? &tm_v : &tm_k;
         int cnt = 0;
         bool ok = go;
-        int v = run.unit, at = run.unit_begin;
-        while (ok && at < run.end) {
+        for (int v = run.unit, at = run.unit_begin; ok && more(at); ++v) {
             const UnitRows U = unit_rows(C, T, A.layer, v);
-            const bool mine = U.count > 0 && (long long)U.count * C.G <= NT * 8;
-            const TileSpan span = tile_span(A.M, U.n - U.count, U.n - 1, 6);
-            const int total = mine ? span.total : 0;
-            if (total && !U.ok && lane == 0) atomicCAS(s_status, 0, KV_ERR_INVALID_ARG);
-            const int lo = window_lo(A.M, max(U.n - U.count, 0)), sinks = min(A.M.sinks, lo);
-            const int x1 = min(total, run.end - at);
+            if (!few_rows(C, T, U)) continue;
+            const FewItem it(C, A.M, U, block, kRows);
+            if (!U.ok && lane == 0) post_status(C.status, KV_ERR_INVALID_ARG);
+            const int x1 = min(it.span.total, run.end - at);
             int base = -1, pg = -1;
-            for (int x = max(run.begin - at, 0); ok && x < x1; ++x) {
-                const int key0 = span.tile(x) * kFewTile;
+            for (int x = max(run.begin - at, 0); x < x1; ++x) {
+                const int key0 = it.span.tile(x) * kFewTile;
                 const int e0 = key0 >> C.ps_log2;
                 if ((e0 & ~31) != base) {
                     base = e0 & ~31;
@@ -166,9 +212,9 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
                 const int j = key0 + sub * box;
                 const int page = __shfl_sync(0xffffffffu, pg, (j >> C.ps_log2) & 31);
                 // a box with no row in use is not read: its page may not exist
-                const bool use = lane < boxes && j < U.n && !(j >= sinks && j + box <= lo);
+                const bool use = lane < boxes && j <= it.t_hi && !(j >= it.sinks && j + box <= it.lo);
                 const bool bad = use && (page < 0 || page >= C.num_pages);
-                if (bad) atomicCAS(s_status, 0, KV_ERR_INVALID_ARG);
+                if (bad) post_status(C.status, KV_ERR_INVALID_ARG);
                 // rows past the pools' end read as zero
                 const long long y = bad ? C.num_pages * C.ps
                                         : ((long long)page << C.ps_log2) + (j & (C.ps - 1));
@@ -188,12 +234,11 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
                                 map, &full[s], half * 64, (int)y);
                 ++cnt;
             }
-            at += total;
-            ++v;
+            at += it.span.total;
         }
         if (!ok && lane == 0) {
             *s_abort = 1;
-            atomicCAS(s_status, 0, KV_ERR_TIMEOUT);
+            post_status(C.status, KV_ERR_TIMEOUT);
         }
         // the last load into every stage lands before the CTA exits
         for (int s = 0; s < kSt; ++s) {
@@ -206,30 +251,25 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
         const float cs = A.M.scale_log2;
         int cnt = 0;
         bool ok = go;
-        int v = run.unit, at = run.unit_begin;
-        while (ok && at < run.end) {
+        for (int v = run.unit, at = run.unit_begin; ok && more(at); ++v) {
             const UnitRows U = unit_rows(C, T, A.layer, v);
-            const int rows = U.count * C.G;
-            const bool mine = U.count > 0 && (long long)U.count * C.G <= NT * 8;
-            const int t_lo = U.n - U.count, t_hi = U.n - 1;
-            const TileSpan span = tile_span(A.M, t_lo, t_hi, 6);
-            const int total = mine ? span.total : 0;
+            if (!few_rows(C, T, U)) continue;
+            const FewItem it(C, A.M, U, block, kRows);
+            const int rows = it.rows, t_lo = it.t_lo, t_hi = it.t_hi, total = it.span.total;
             const int x0 = max(run.begin - at, 0), x1 = min(total, run.end - at);
-            if (x0 >= x1) {
+            if (kCluster == 0 && x0 >= x1) {
                 at += total;
-                ++v;
                 continue;
             }
-            const int lo = window_lo(A.M, max(t_lo, 0)), sinks = min(A.M.sinks, lo);
             // Q^T: columns are query rows (those past the last are zero)
             uint32_t qf[NT][D / 16][2];
             float m[NT][2], l[NT][2], o[NT][D / 16][4];
             int t_row[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const int row = nt * 8 + quad;
+                const int row = it.row0 + nt * 8 + quad;
                 const uint32_t *qp = nullptr;
-                if (row < rows)
+                if (nt * 8 + quad < rows)
                     qp = reinterpret_cast<const uint32_t *>(
                         static_cast<const typename E::T *>(A.io.q) +
                         (U.tok0 + row / C.G) * A.io.q_stride +
@@ -245,12 +285,12 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
                 for (int i = 0; i < 2; ++i) {
                     m[nt][i] = -INFINITY;
                     l[nt][i] = 0.f;
-                    const int row2 = nt * 8 + pair + i;
-                    t_row[nt][i] = row2 < rows ? t_lo + row2 / C.G : -1;
+                    const int r2 = nt * 8 + pair + i;
+                    t_row[nt][i] = r2 < rows ? U.n - U.count + (it.row0 + r2) / C.G : -1;
                 }
             }
             for (int x = x0; x < x1; ++x) {
-                const int tile = span.tile(x), key0 = tile * kFewTile;
+                const int key0 = it.span.tile(x) * kFewTile;
                 const int s = cnt % kSt;
                 ok = __all_sync(0xffffffffu, mbar_wait(&full[s], (uint32_t)((cnt / kSt) & 1),
                                                        s_abort, C.wait_ns));
@@ -300,7 +340,7 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
 #pragma unroll 1
                     for (int c = lane; c < 16 * (D / 8); c += 32) {
                         const int kr = wk + c / (D / 8), ch = c % (D / 8), j = key0 + kr;
-                        if (j > t_hi || (j >= sinks && j < lo))
+                        if (j > t_hi || (j >= it.sinks && j < it.lo))
                             *reinterpret_cast<uint4 *>(vt + (ch >> 3) * kHalfBytes + kr * 128 +
                                                        (((ch & 7) ^ (kr & 7)) << 4)) =
                                 make_uint4(0, 0, 0, 0);
@@ -309,15 +349,14 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
                     __syncwarp();
                 }
                 if (A.logits) {
-                    float *lg = A.logits + ((long long)(at + x) * kFewRows) * kFewTile;
+                    float *lg = A.logits +
+                                ((long long)v * A.unit_tiles + x) * (kFewRows * kFewTile) + wk + quad;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             if (nt * 8 + pair + (i & 1) < rows)
-                                lg[(nt * 8 + pair + (i & 1)) * kFewTile + wk + quad + (i >> 1) * 8] =
-                                    sc[nt][i];
-                    if (warp == 0 && lane == 0) A.tile_at[at + x] = make_int2(v, tile);
+                                lg[(nt * 8 + pair + (i & 1)) * kFewTile + (i >> 1) * 8] = sc[nt][i];
                 }
                 bool up = false;
 #pragma unroll
@@ -432,19 +471,21 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
                     }
                 }
             }
+            if (kCluster > 1) bar_consumers();                   // the buffers are read
             if (warp == 0) {
-                const bool whole = x0 == 0 && x1 == total;
+                const bool whole = kCluster == 1 || (kCluster == 0 && x0 == 0 && x1 == total);
                 const long long slot = part_slot(blockIdx.x, x0 == 0);
-                if (lane == 0 && x0 > 0 && x1 == total)
+                if (kCluster == 0 && lane == 0 && x0 > 0 && x1 == total)
                     *s_cut = CutItem{v, at / run.per, 0, rows};
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const int row = nt * 8 + pair + i;
-                        if (row >= rows) continue;
+                        const int r2 = nt * 8 + pair + i;
+                        if (r2 >= rows) continue;
                         const float mm = m[nt][i] - E::kShift, ll = l[nt][i];
                         if (whole) {
+                            const int row = it.row0 + r2;
                             const long long tok = U.tok0 + row / C.G;
                             const int head = U.h * C.G + row % C.G;
                             const float inv = ll > 0.f ? 1.f / ll : 0.f;
@@ -461,9 +502,17 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
                                 if (A.lse2) A.lse2[packed_row(C, U, row)] = z;
                             }
                         } else {
-                            const long long at_row = slot * kFewRows + row;
-                            if (quad == 0) A.part_ml[at_row] = make_float2(mm, ll);
-                            float *op = A.part_o + at_row * D + quad;
+                            // this CTA's part: in its shared memory, or the workspace
+                            float *ml = kCluster > 1
+                                            ? buf + 2 * r2
+                                            : reinterpret_cast<float *>(A.part_ml +
+                                                                        slot * kFewRows + r2);
+                            float *op = kCluster > 1 ? buf + 2 * kRows + r2 * D + quad
+                                                     : A.part_o + (slot * kFewRows + r2) * D + quad;
+                            if (quad == 0) {
+                                ml[0] = mm;
+                                ml[1] = ll;
+                            }
 #pragma unroll
                             for (int ks = 0; ks < D / 16; ++ks) {
                                 op[ks * 16] = o[nt][ks][i];
@@ -473,95 +522,159 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
                     }
             }
             at += total;
-            ++v;
         }
         if (!ok && lane == 0) {
             *s_abort = 1;
-            atomicCAS(s_status, 0, KV_ERR_TIMEOUT);
+            post_status(C.status, KV_ERR_TIMEOUT);
         }
     }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        A.cta_status[blockIdx.x] = *s_status;
-        A.cut[blockIdx.x] = *s_cut;
-        if (blockIdx.x == 0 && A.logits) *A.tiles = run.total;
+    if constexpr (kCluster > 1) {
+        // the cluster's parts of the item: CTA `rank` merges every kCluster-th row
+        static_assert((2 + D) * kRows * 4 <= 2 * Ly::kBufBytes, "a part fits the merge buffers");
+        cg::cluster_group cl = cg::this_cluster();
+        cl.sync();
+        const UnitRows U = unit_rows(C, T, A.layer, run.unit);
+        const FewItem it(C, A.M, U, block, kRows);
+        float *buf = reinterpret_cast<float *>(smem + Ly::kBuf);
+        const float *part[kCluster];
+#pragma unroll
+        for (int r = 0; r < kCluster; ++r) part[r] = cl.map_shared_rank(buf, r);
+        constexpr int kAtOnce = 128 / D;                     // rows of 128 threads
+        for (int r2 = rank + kCluster * (threadIdx.x / D); threadIdx.x < 128 && r2 < it.rows;
+             r2 += kCluster * kAtOnce) {
+            const int e = threadIdx.x % D;
+            float mr[kCluster], lr[kCluster], mm = -INFINITY, ll = 0.f, acc = 0.f;
+#pragma unroll
+            for (int r = 0; r < kCluster; ++r) {
+                mr[r] = part[r][2 * r2];
+                lr[r] = part[r][2 * r2 + 1];
+            }
+#pragma unroll
+            for (int r = 0; r < kCluster; ++r) mm = fmaxf(mm, mr[r]);
+#pragma unroll
+            for (int r = 0; r < kCluster; ++r) {
+                const float w = shrink(mr[r], mm);
+                ll += lr[r] * w;
+                acc += part[r][2 * kRows + r2 * D + e] * w;
+            }
+            const int row = it.row0 + r2;
+            const long long tok = U.tok0 + row / C.G;
+            const int head = U.h * C.G + row % C.G;
+            static_cast<typename E::T *>(A.io.out)[tok * A.io.out_stride + (long long)head * D + e] =
+                E::one(ll > 0.f ? acc / ll : 0.f);
+            if (e == 0) {
+                const float z = row_lse2(mm, ll);
+                if (A.io.lse) A.io.lse[tok * C.Hq + head] = z * kLn2;
+                if (A.lse2) A.lse2[packed_row(C, U, row)] = z;
+            }
+        }
+        cl.sync();                                           // no CTA leaves while it is read
+    } else if constexpr (kCluster == 0) {
+        __syncthreads();
+        if (threadIdx.x == 0) A.cut[blockIdx.x] = *s_cut;
     }
 }
 
 // mass of the rows of every tile: sum over the unit's query rows of 2^(logit - lse), in
-// row order.  One 64-thread group per tile, a thread per key.
+// row order.  64 threads a tile, a thread a key.
 constexpr int kMassThreads = 256;
 __global__ void __launch_bounds__(kMassThreads)
 few_mass_kernel(const DevPaged C, const DevChunk T, const FewArgs A) {
     pdl_wait();
     pdl_trigger();
-    const int tiles = *A.tiles;
     constexpr int kGroups = kMassThreads / kFewTile;
+    const long long tiles = (long long)C.R * C.H * A.unit_tiles;
     const int key = threadIdx.x % kFewTile;
-    for (int t = blockIdx.x * kGroups + threadIdx.x / kFewTile; t < tiles;
-         t += gridDim.x * kGroups) {
-        const int2 where = A.tile_at[t];
-        const UnitRows U = unit_rows(C, T, A.layer, where.x);
-        const int j = where.y * kFewTile + key, rows = U.count * C.G;
-        if (j >= U.n) continue;
-        const float *lg = A.logits + (long long)t * kFewRows * kFewTile + key;
+    for (long long t = (long long)blockIdx.x * kGroups + threadIdx.x / kFewTile; t < tiles;
+         t += (long long)gridDim.x * kGroups) {
+        const int v = (int)(t / A.unit_tiles), x = (int)(t - (long long)v * A.unit_tiles);
+        const UnitRows U = unit_rows(C, T, A.layer, v);
+        if (!few_rows(C, T, U)) continue;
+        const FewItem it(C, A.M, U, 0, kFewRows);
+        const int j = it.span.tile(x) * kFewTile + key;
+        if (x >= it.span.total || j > it.t_hi) continue;
+        const float *lg = A.logits + t * (kFewRows * kFewTile) + key;
         const float *lse2 = A.lse2 + packed_row(C, U, 0);
+        const long long at = page_row(C, U.table, j);
         float acc = 0.f;
         bool seen = false;
-        for (int row = 0; row < rows; ++row) {
-            const float x = lg[row * kFewTile];
-            if (x == -INFINITY) continue;
+#pragma unroll 8
+        for (int row = 0; row < it.rows; ++row) {
+            const float z = lg[row * kFewTile];
+            if (z == -INFINITY) continue;
             seen = true;
-            acc += ex2_approx(x - lse2[row]);
+            acc += ex2_approx(z - lse2[row]);
         }
-        if (!seen) continue;
-        const long long at = page_row(C, U.table, j);
-        if (at >= 0) C.mass[at] += acc;
+        if (seen && at >= 0) C.mass[at] += acc;
     }
 }
 
-template <typename E, int D, int NT>
-cudaError_t few(const DevPaged &C, const DevChunk &T, const FewArgs &A, bool first,
-                const AttendWs &ws, cudaStream_t s) {
+template <typename E, int D, int NT, int kCluster>
+cudaError_t few(const DevPaged &C, const DevChunk &T, const FewArgs &A, const AttendWs &ws,
+                cudaStream_t s) {
     using Ly = Layout<D, NT>;
     CUtensorMap mk, mv;
     const int box = C.ps < kFewTile ? C.ps : kFewTile;
     if (!make_tile_map(&mk, C.k, C.num_pages * C.ps, D, box) ||
         !make_tile_map(&mv, C.v, C.num_pages * C.ps, D, box))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(few_kernel<E, D, NT>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, Ly::kTotal);
+    auto kernel = few_kernel<E, D, NT, kCluster>;
+    cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Ly::kTotal);
+    const unsigned grid = kCluster == 0 ? kFewCtas : (unsigned)(C.R * C.H * A.blocks * kCluster);
     if (e == cudaSuccess)
-        e = launch_dependent(few_kernel<E, D, NT>, dim3(kFewCtas), kThreads, Ly::kTotal, s, mk, mv,
-                             C, T, A);
-    if (e == cudaSuccess)
-        e = launch_attend_merge(C, T, A.layer, A.io, A.lse2, ws, kFewCtas, kFewRows, first, s);
-    if (e == cudaSuccess && A.logits)
-        e = launch_dependent(few_mass_kernel, dim3(kFewCtas), kMassThreads, 0, s, C, T, A);
+        e = launch_cluster_dependent(kernel, kCluster, dim3(grid), kThreads, Ly::kTotal, s, mk, mv, C,
+                                     T, A);
+    if (e == cudaSuccess && kCluster == 0)
+        e = launch_attend_merge(C, T, A.layer, A.io, A.lse2, ws, kFewCtas, kFewRows, s);
+    if (e == cudaSuccess && A.logits) {
+        const long long groups = ((long long)C.R * C.H * A.unit_tiles + 3) / 4;
+        e = launch_dependent(few_mass_kernel, dim3((unsigned)std::min<long long>(groups, 16 * 152)),
+                             kMassThreads, 0, s, C, T, A);
+    }
     return e;
+}
+
+template <typename E, int D, int NT>
+cudaError_t few_form(const DevPaged &C, const DevChunk &T, const FewArgs &A, int cluster,
+                     const AttendWs &ws, cudaStream_t s) {
+    switch (cluster) {
+        case 0: return few<E, D, NT, 0>(C, T, A, ws, s);
+        case 1: return few<E, D, NT, 1>(C, T, A, ws, s);
+        case 2: return few<E, D, NT, 2>(C, T, A, ws, s);
+        case 4: return few<E, D, NT, 4>(C, T, A, ws, s);
+        default: return few<E, D, NT, 8>(C, T, A, ws, s);
+    }
 }
 
 }  // namespace
 
 cudaError_t launch_attend_few(const DevPaged &C, const DevChunk &T, int layer, const AttendMask &M,
-                              const AttendIo &io, bool add_mass, int max_rows, bool first,
-                              const AttendWs &ws, cudaStream_t s) {
-    const FewArgs A{layer,      M,       io,       ws.cta_status, ws.cut,
-                    ws.part_ml, ws.part_o, ws.lse2, ws.tiles,      ws.tile_at,
-                    add_mass ? ws.logits : nullptr};
+                              const AttendIo &io, bool add_mass, long long items, int max_rows,
+                              int blocks, const AttendWs &ws, cudaStream_t s) {
+    const FewArgs A{layer,      M,         io,      ws.cut,
+                    ws.part_ml, ws.part_o, ws.lse2, add_mass ? ws.logits : nullptr,
+                    (C.cap + kFewTile - 1) / kFewTile, blocks};
+    // short tables: the largest cluster that leaves every CTA a tile and the GPU in one round
+    int cluster = 0;
+    if (C.cap <= kShortRows) {
+        cluster = 8;
+        while (cluster > 1 && (cluster * kFewTile > C.cap || items * cluster > kFewCtas))
+            cluster /= 2;
+    }
     const int nt = max_rows <= 8 ? 1 : 2;
     if (C.dtype == KV_FP16) {
         if (C.d == 64)
-            return nt == 1 ? few<Fp16, 64, 1>(C, T, A, first, ws, s)
-                           : few<Fp16, 64, 2>(C, T, A, first, ws, s);
-        return nt == 1 ? few<Fp16, 128, 1>(C, T, A, first, ws, s)
-                       : few<Fp16, 128, 2>(C, T, A, first, ws, s);
+            return nt == 1 ? few_form<Fp16, 64, 1>(C, T, A, cluster, ws, s)
+                           : few_form<Fp16, 64, 2>(C, T, A, cluster, ws, s);
+        return nt == 1 ? few_form<Fp16, 128, 1>(C, T, A, cluster, ws, s)
+                       : few_form<Fp16, 128, 2>(C, T, A, cluster, ws, s);
     }
     if (C.d == 64)
-        return nt == 1 ? few<Bf16, 64, 1>(C, T, A, first, ws, s)
-                       : few<Bf16, 64, 2>(C, T, A, first, ws, s);
-    return nt == 1 ? few<Bf16, 128, 1>(C, T, A, first, ws, s)
-                   : few<Bf16, 128, 2>(C, T, A, first, ws, s);
+        return nt == 1 ? few_form<Bf16, 64, 1>(C, T, A, cluster, ws, s)
+                       : few_form<Bf16, 64, 2>(C, T, A, cluster, ws, s);
+    return nt == 1 ? few_form<Bf16, 128, 1>(C, T, A, cluster, ws, s)
+                   : few_form<Bf16, 128, 2>(C, T, A, cluster, ws, s);
 }
 
 }  // namespace kvevict

@@ -76,7 +76,6 @@ struct ManyArgs {
     int layer;
     AttendMask M;
     AttendIo io;
-    int *cta_status;
     CutItem *cut;
     float2 *part_ml;
     float *part_o;
@@ -116,9 +115,9 @@ __device__ __forceinline__ void make_item(Item &it, const DevPaged &C, const Att
 }
 
 // Tiles of a unit: the sum over its items.
-__device__ __forceinline__ int unit_tiles(const DevPaged &C, const AttendMask &M,
-                                          const UnitRows &U) {
-    if (!many_rows(C, U)) return 0;
+__device__ __forceinline__ int unit_tiles(const DevPaged &C, const DevChunk &T,
+                                          const AttendMask &M, const UnitRows &U) {
+    if (!many_rows(C, T, U)) return 0;
     const int all = U.count * C.G, t0 = U.n - U.count;
     int sum = 0;
     for (int r0 = 0; r0 < all; r0 += kManyRows)
@@ -153,15 +152,14 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     uint64_t *o_empty = o_final + 2;         // [lane]: O read out (4 warps)
     uint64_t *mma_done = o_empty + 2;
     uint64_t *i_full = mma_done + 1, *i_empty = i_full + kItems;   // item descriptions
-    int *s_status = reinterpret_cast<int *>(smem + Ly::kMisc);
-    volatile int *s_abort = s_status + 1;
-    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(s_status + 2);
-    CutItem *s_cut = reinterpret_cast<CutItem *>(s_status + 4);
+    volatile int *s_abort = reinterpret_cast<volatile int *>(smem + Ly::kMisc);
+    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + Ly::kMisc + 4);
+    CutItem *s_cut = reinterpret_cast<CutItem *>(smem + Ly::kMisc + 16);
     Item *s_item = reinterpret_cast<Item *>(smem + Ly::kDesc);
 
     if (threadIdx.x == 0) {
-        *s_status = (smem_u32(smem) & 1023u) ? KV_ERR_UNSUPPORTED : 0;
-        *s_abort = *s_status;
+        *s_abort = (smem_u32(smem) & 1023u) ? 1 : 0;
+        if (*s_abort) post_status(C.status, KV_ERR_UNSUPPORTED);
         *s_cut = CutItem{-1, 0, 0, 0};
         for (int s = 0; s < Ly::kKSt; ++s) {
             mbar_init(&k_full[s], 1);
@@ -191,7 +189,7 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     pdl_trigger();
     const uint32_t tmem = tmem_acquire_all(s_tmem);
     const CtaRun run = cut_run<kThreads>(C.R * C.H, 1, [&](int v) {
-        return unit_tiles(C, A.M, unit_rows(C, T, A.layer, v));
+        return unit_tiles(C, T, A.M, unit_rows(C, T, A.layer, v));
     });
     bool ok = *s_abort == 0;
 
@@ -419,7 +417,7 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         }
         if (!ok && lane == 0) {
             *s_abort = 1;
-            atomicCAS(s_status, 0, KV_ERR_TIMEOUT);
+            post_status(C.status, KV_ERR_TIMEOUT);
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
@@ -434,8 +432,8 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                     int pairs = 1;
                     if (!end) {
                         U = unit_rows(C, T, A.layer, v);
-                        pairs = many_rows(C, U) ? (U.count * C.G + kManyRows - 1) / kManyRows : 0;
-                        if (pairs && !U.ok) atomicCAS(s_status, 0, KV_ERR_INVALID_ARG);
+                        pairs = many_rows(C, T, U) ? (U.count * C.G + kManyRows - 1) / kManyRows : 0;
+                        if (pairs && !U.ok) post_status(C.status, KV_ERR_INVALID_ARG);
                     }
                     for (int pair = 0; ok && pair < pairs && (end || at < run.end); ++pair) {
                         Item next;
@@ -461,7 +459,7 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                 }
                 if (!ok) {
                     *s_abort = 1;
-                    atomicCAS(s_status, 0, KV_ERR_TIMEOUT);
+                    post_status(C.status, KV_ERR_TIMEOUT);
                 }
             }
         } else if (warp == kKWarp || warp == kVWarp) {
@@ -494,7 +492,7 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                     // a box with no row in use is not read: its page may not exist
                     const bool use = lane < boxes && j <= t_hi && !(j >= sinks && j + C.ps <= lo);
                     const bool bad = use && (page < 0 || page >= C.num_pages);
-                    if (bad) atomicCAS(s_status, 0, KV_ERR_INVALID_ARG);
+                    if (bad) post_status(C.status, KV_ERR_INVALID_ARG);
                     // rows past the pools' end read as zero
                     const long long y = bad ? C.num_pages * C.ps : (long long)page << C.ps_log2;
                     const int n_use = __popc(__ballot_sync(0xffffffffu, use));
@@ -517,7 +515,7 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             }
             if (!ok && lane == 0) {
                 *s_abort = 1;
-                atomicCAS(s_status, 0, KV_ERR_TIMEOUT);
+                post_status(C.status, KV_ERR_TIMEOUT);
             }
             for (int s = 0; s < stages; ++s) {
                 const int uses = cnt / stages + (cnt % stages > s ? 1 : 0);
@@ -620,7 +618,7 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                 }
                 if (!ok) {
                     *s_abort = 1;
-                    atomicCAS(s_status, 0, KV_ERR_TIMEOUT);
+                    post_status(C.status, KV_ERR_TIMEOUT);
                 }
                 // every product issued completes before tensor memory is freed
                 mma_commit(mma_done);
@@ -632,15 +630,11 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     __syncthreads();
     tc_fence_after();
     tmem_release_all(tmem);
-    if (threadIdx.x == 0) {
-        A.cta_status[blockIdx.x] = *s_status;
-        A.cut[blockIdx.x] = *s_cut;
-    }
+    if (threadIdx.x == 0) A.cut[blockIdx.x] = *s_cut;
 }
 
 template <typename E, int D>
-cudaError_t many(const DevPaged &C, const DevChunk &T, const ManyArgs &A, bool first,
-                 const AttendWs &ws, cudaStream_t s) {
+cudaError_t many(const DevPaged &C, const DevChunk &T, const ManyArgs &A, const AttendWs &ws, cudaStream_t s) {
     using Ly = Layout<D>;
     CUtensorMap mk, mv;
     if (!make_tile_map(&mk, C.k, C.num_pages * C.ps, D, C.ps) ||
@@ -652,22 +646,21 @@ cudaError_t many(const DevPaged &C, const DevChunk &T, const ManyArgs &A, bool f
         e = launch_dependent(many_kernel<E, D>, dim3(kManyCtas), kThreads, Ly::kTotal, s, mk, mv, C,
                              T, A);
     if (e == cudaSuccess)
-        e = launch_attend_merge(C, T, A.layer, A.io, A.lse2, ws, kManyCtas, kManyRows, first, s);
+        e = launch_attend_merge(C, T, A.layer, A.io, A.lse2, ws, kManyCtas, kManyRows, s);
     return e;
 }
 
 }  // namespace
 
 cudaError_t launch_attend_many(const DevPaged &C, const DevChunk &T, int layer, const AttendMask &M,
-                               const AttendIo &io, bool add_mass, bool first, const AttendWs &ws,
+                               const AttendIo &io, bool add_mass, const AttendWs &ws,
                                cudaStream_t s) {
-    const ManyArgs A{layer, M, io, ws.cta_status, ws.cut, ws.part_ml, ws.part_o, ws.lse2,
-                     ws.q_packed};
+    const ManyArgs A{layer, M, io, ws.cut, ws.part_ml, ws.part_o, ws.lse2, ws.q_packed};
     if (C.dtype == KV_FP16)
-        return C.d == 64 ? many<Fp16, 64>(C, T, A, first, ws, s)
-                         : many<Fp16, 128>(C, T, A, first, ws, s);
-    return C.d == 64 ? many<Bf16, 64>(C, T, A, first, ws, s)
-                     : many<Bf16, 128>(C, T, A, first, ws, s);
+        return C.d == 64 ? many<Fp16, 64>(C, T, A, ws, s)
+                         : many<Fp16, 128>(C, T, A, ws, s);
+    return C.d == 64 ? many<Bf16, 64>(C, T, A, ws, s)
+                     : many<Bf16, 128>(C, T, A, ws, s);
 }
 
 }  // namespace kvevict

@@ -48,16 +48,15 @@ struct MassArgs {
     int layer;
     AttendMask M;
     const float *lse2;
-    int *status;
 };
 
 // Key groups of a unit, and of each the query row tiles [rt0, rt1) that see it.
 struct Groups {
     int t0, rows, groups;
-    __device__ __forceinline__ Groups(const DevPaged &C, const UnitRows &U) {
+    __device__ __forceinline__ Groups(const DevPaged &C, const DevChunk &T, const UnitRows &U) {
         rows = U.count * C.G;
         t0 = U.n - U.count;
-        groups = many_rows(C, U) ? (U.n + kGroup * kManyTile - 1) / (kGroup * kManyTile) : 0;
+        groups = many_rows(C, T, U) ? (U.n + kGroup * kManyTile - 1) / (kGroup * kManyTile) : 0;
     }
     __device__ __forceinline__ void range(const DevPaged &C, const AttendMask &M, int n, int g,
                                           int &rt0, int &rt1) const {
@@ -113,13 +112,13 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     }
     pdl_wait();
     pdl_trigger();
-    if (threadIdx.x == 0 && *s_abort) post_status(A.status, KV_ERR_UNSUPPORTED);
+    if (threadIdx.x == 0 && *s_abort) post_status(C.status, KV_ERR_UNSUPPORTED);
     const uint32_t tmem = tmem_acquire_all(s_tmem);
     // runs of equal numbers of (key group, row tile) steps; a group belongs to the run
     // that its first step lies in
     const CtaRun run = cut_run<kThreads>(C.R * C.H, 1, [&](int v) {
         const UnitRows U = unit_rows(C, T, A.layer, v);
-        const Groups g(C, U);
+        const Groups g(C, T, U);
         int sum = 0;
         for (int i = 0; i < g.groups; ++i) {
             int a, b;
@@ -138,7 +137,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     };
     auto expired = [&]() {
         *s_abort = 1;
-        post_status(A.status, KV_ERR_TIMEOUT);
+        post_status(C.status, KV_ERR_TIMEOUT);
     };
 
     if (warp == kSchedWarp) {
@@ -156,7 +155,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             next.stop = 0;
             for (int v = run.unit; ok && at < run.end; ++v) {
                 const UnitRows U = unit_rows(C, T, A.layer, v);
-                const Groups g(C, U);
+                const Groups g(C, T, U);
                 next.n = U.n;
                 next.rows = g.rows;
                 next.t0 = g.t0;
@@ -441,7 +440,7 @@ cudaError_t mass(const DevPaged &C, const DevChunk &T, const MassArgs &A, const 
 
 cudaError_t launch_many_mass(const DevPaged &C, const DevChunk &T, int layer, const AttendMask &M,
                              const AttendWs &ws, cudaStream_t s) {
-    const MassArgs A{layer, M, ws.lse2, ws.status};
+    const MassArgs A{layer, M, ws.lse2};
     if (C.dtype == KV_FP16)
         return C.d == 64 ? mass<Fp16, 64>(C, T, A, ws, s) : mass<Fp16, 128>(C, T, A, ws, s);
     return C.d == 64 ? mass<Bf16, 64>(C, T, A, ws, s) : mass<Bf16, 128>(C, T, A, ws, s);

@@ -36,7 +36,7 @@ def _run(kv, made, counts, q, out, layer=0, window=0, sinks=0, mass=False, scale
                     dtype=torch.uint8, device="cuda")
     kv.kv_paged_attention(c, chunk, layer, q, out, ws, window=window, num_sinks=sinks, lse=lse,
                           add_mass=mass, softmax_scale=scale, stream=stream)
-    return lse, kv.kv_check_status(ws, stream)
+    return lse, kv.kv_check_status(c.status, stream)
 
 
 def _check(made, counts, q, out, lse, layer=0, window=0, sinks=0, mass=False, scale=None):
@@ -102,6 +102,14 @@ CASES = {
     "prompt": (2, 8, 128, 64, "bf16", [513], 513, 513, 0, 0, True, False),
     "prompt_window": (1, 4, 128, 64, "fp16", [700], 700, 700, 129, 1, True, True),
     "long": (1, 4, 128, 64, "bf16", [1], 20011, 20011, 0, 0, True, False),
+    # short tables: blocks of query rows, one launch
+    "short_64_rows": (2, 8, 128, 64, "bf16", [16, 9, 0, 1], 16, 900, 0, 0, False, True),
+    "short_128_rows": (1, 4, 64, 16, "fp16", [32, 31], 33, 2047, 0, 0, False, False),
+    "short_g7": (2, 14, 128, 32, "bf16", [18, 2], 40, 3000, 0, 0, False, False),
+    "short_window": (2, 8, 128, 64, "bf16", [20, 5], 300, 1500, 70, 5, False, True),
+    "short_empty_rows": (1, 8, 128, 16, "bf16", [9, 5], 0, 4, 0, 0, False, False),
+    "short_and_long_chunks": (2, 8, 64, 64, "bf16", [16, 200, 1], 201, 900, 0, 0, False, False),
+    "many_requests": (2, 8, 128, 64, "bf16", [1] * 40, 1, 260, 0, 0, True, False),
     "long_chunk": (1, 8, 128, 64, "bf16", [96], 12345, 12345, 0, 0, True, False),
 }
 
@@ -232,6 +240,7 @@ def test_bad_lengths_and_pages_are_reported(cuda_lib, counts):
             made.cache.lens[0, 0, 1] = -1 if what == "negative" else made.cache.max_pages * 64 + 1
         lse, status = _run(kv, made, counts, q, out)
         assert status == kv.KV_ERR_INVALID_ARG
+        assert kv.kv_check_status(made.cache.status) == 0       # read and cleared
         # the other request is untouched by it
         t0 = counts[0]
         rest = paged.Made(kv, _spread(2, 1, 2, 200, 300), 8, 128, 64, seed=8)
@@ -271,7 +280,7 @@ def test_graph_replays_follow_lengths_and_tables(cuda_lib, counts):
         call()
     g.replay()
     torch.cuda.synchronize()
-    assert kv.kv_check_status(ws) == 0
+    assert kv.kv_check_status(c.status) == 0
     _check(a, counts, q, out, lse, mass=True)
     c.k_pages.copy_(b.cache.k_pages)
     c.v_pages.copy_(b.cache.v_pages)
@@ -282,7 +291,7 @@ def test_graph_replays_follow_lengths_and_tables(cuda_lib, counts):
     a.K, a.V, a.lens_host, a.mass0 = b.K, b.V, b.lens_host, b.mass0
     g.replay()
     torch.cuda.synchronize()
-    assert kv.kv_check_status(ws) == 0
+    assert kv.kv_check_status(c.status) == 0
     _check(a, counts, q, out, lse, mass=True)
 
 
@@ -306,5 +315,5 @@ def test_two_streams_at_once(cuda_lib):
         kv.kv_paged_attention(made.cache, chunk, 0, q, out, ws, lse=lse, add_mass=True, stream=s)
     torch.cuda.synchronize()
     for made, counts, q, out, chunk, ws, lse, s in sets:
-        assert kv.kv_check_status(ws, s) == 0
+        assert kv.kv_check_status(made.cache.status, s) == 0
         _check(made, counts, q, out, lse, mass=True)

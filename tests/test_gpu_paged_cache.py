@@ -51,6 +51,7 @@ def test_append_writes_the_last_rows(cuda_lib, d, page, dtype, counts, lo, hi, s
     torch.cuda.synchronize()
     for a, b in ((c.k_pages, k), (c.v_pages, v), (c.mass, mass)):
         assert torch.equal(_bits(a), _bits(b))
+    assert kv.kv_check_status(c.status) == 0
 
 
 def test_append_skips_pages_that_do_not_exist(cuda_lib):
@@ -68,6 +69,7 @@ def test_append_skips_pages_that_do_not_exist(cuda_lib):
     kv.kv_paged_append(c, kv.Chunk([1, 1]), 0, new, new)
     torch.cuda.synchronize()
     assert torch.equal(_bits(c.k_pages), _bits(want))
+    assert kv.kv_check_status(c.status) == kv.KV_ERR_INVALID_ARG
 
 
 @pytest.mark.parametrize("d,page,dtype,lo,hi", [(128, 64, "bf16", 0, 200), (64, 16, "fp16", 1, 33),
@@ -118,7 +120,7 @@ def test_load_refuses_a_unit_that_does_not_fit(cuda_lib):
     chunk = kv.Chunk([1])
     ws = torch.empty(kv.kv_paged_attention_workspace_size(c, chunk), dtype=torch.uint8, device="cuda")
     kv.kv_paged_attention(c, chunk, 0, q, torch.empty_like(q), ws)
-    assert kv.kv_check_status(ws) == kv.KV_ERR_INVALID_ARG
+    assert kv.kv_check_status(c.status) == kv.KV_ERR_INVALID_ARG
 
 
 def _evict(kv, made, into, budgets, sinks, recent, stride):
@@ -248,7 +250,7 @@ def test_from_prefill_eviction_to_decoding(cuda_lib, page):
             out = torch.empty((chunk.tokens, Hq, d), dtype=torch.bfloat16, device="cuda")
             kv.kv_paged_attention(cache, chunk, layer, q, out, ws, window=window, num_sinks=sinks,
                                   add_mass=True)
-            assert kv.kv_check_status(ws) == 0
+            assert kv.kv_check_status(cache.status) == 0
             t0 = 0
             for r, count in enumerate(counts):
                 for h in range(H):

@@ -42,7 +42,8 @@ def test_workspace_sizes_and_shape_checks(kv):
                                ("num_pages", 1 << 25, kv.KV_ERR_UNSUPPORTED),
                                ("max_pages", 1 << 25, kv.KV_ERR_UNSUPPORTED),
                                ("k_pages", None, kv.KV_ERR_INVALID_ARG),
-                               ("lens", c.lens.data_ptr() + 4, kv.KV_ERR_INVALID_ARG)]:
+                               ("lens", c.lens.data_ptr() + 4, kv.KV_ERR_INVALID_ARG),
+                               ("status", None, kv.KV_ERR_INVALID_ARG)]:
         old = getattr(c._c, field)
         setattr(c._c, field, value)
         for call in (lambda: kv.kv_paged_attention_workspace_size(c, t),
@@ -161,4 +162,4 @@ def test_advance_raises_every_units_length(kv):
     c.advance(kv.Chunk([1, 5], device="cpu"))
     assert c.lens[0].tolist() == [[1, 1], [1, 8], [1, 1]] and c.lens[1].eq(5).all()
     assert np.array_equal(kv.Chunk([1, 0, 5], device="cpu").cu_host, [0, 1, 1, 6])
-    assert ctypes.sizeof(kv._KvPaged) == 80
+    assert ctypes.sizeof(kv._KvPaged) == 88
