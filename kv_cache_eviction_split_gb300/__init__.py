@@ -197,6 +197,10 @@ def _ptr(t) -> Optional[int]:
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
+        # the handle alone, where torch offers it: a Stream object costs as much as a launch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:
+            return raw(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     return getattr(stream, "cuda_stream", stream)
 
@@ -706,6 +710,8 @@ class PagedCache:
         self.num_pages, self.page_size, self.head_dim = k_pages.shape
         self.dtype, self.device = k_pages.dtype, k_pages.device
         self.status = torch.zeros(64, dtype=torch.int32, device=self.device)
+        self._index = k_pages.get_device()          # -1 on the CPU
+        self._scale = 1.0 / math.sqrt(self.head_dim)
         self._c = _KvPaged(self.num_requests, self.num_layers, self.num_kv_heads, self.num_q_heads,
                            self.head_dim, self.page_size, self.max_pages,
                            KV_FP16 if self.dtype == torch.float16 else KV_BF16, self.num_pages,
@@ -767,29 +773,34 @@ class Chunk:
 def _on_current_device(cache: PagedCache, *others) -> None:
     """The library works on the current device: its tensors have to be there."""
     import torch
-    if cache.device.type == "cuda" and cache.device.index != torch.cuda.current_device():
+    index = cache._index
+    if index >= 0 and index != torch.cuda.current_device():
         raise ValueError("the cache is on %s, which is not the current device" % cache.device)
     for t in others:
-        if t is not None and t.device != cache.device:
+        if t is not None and t.get_device() != index:
             raise ValueError("a tensor is on %s, the cache on %s" % (t.device, cache.device))
 
 
 def _token_stride(cache: PagedCache, chunk: Chunk, t, heads: int, name: str) -> int:
     """Checks t [tokens][heads][head_dim] (rows of a token contiguous); elements between tokens."""
+    d, n = cache.head_dim, chunk.tokens
+    if t.dtype is not cache.dtype or t.shape != (n, heads, d):
+        raise ValueError("%s: %s [%d][%d][%d]" % (name, cache.dtype, n, heads, d))
+    s0, s1, s2 = t.stride()
+    if n and (s2 != 1 or (heads > 1 and s1 != d)):
+        raise ValueError("%s: the heads of a token are contiguous" % name)
+    return s0 if n > 1 else heads * d
+
+
+def _same_requests(cache: PagedCache, chunk: Chunk) -> None:
     if chunk.num_requests != cache.num_requests:
         raise ValueError("the chunk has %d requests, the cache %d"
                          % (chunk.num_requests, cache.num_requests))
-    d = cache.head_dim
-    if t.dtype != cache.dtype or tuple(t.shape) != (chunk.tokens, heads, d):
-        raise ValueError("%s: %s [%d][%d][%d]" % (name, cache.dtype, chunk.tokens, heads, d))
-    s = t.stride()
-    if chunk.tokens and (s[2] != 1 or (heads > 1 and s[1] != d)):
-        raise ValueError("%s: the heads of a token are contiguous" % name)
-    return s[0] if chunk.tokens > 1 else heads * d
 
 
 def kv_paged_append(cache: PagedCache, chunk: Chunk, layer: int, k_new, v_new, stream=None):
     """New tokens' K and V rows [tokens][kv_heads][head_dim] of one layer into the pages."""
+    _same_requests(cache, chunk)
     ks = _token_stride(cache, chunk, k_new, cache.num_kv_heads, "k_new")
     vs = _token_stride(cache, chunk, v_new, cache.num_kv_heads, "v_new")
     _on_current_device(cache, k_new, v_new, chunk.cu_dev)
@@ -832,17 +843,21 @@ def kv_paged_attention(cache: PagedCache, chunk: Chunk, layer: int, q, out, work
     window > 0: only the last `window` rows and the first `num_sinks` are seen.
     add_mass: adds every row's attention weights to cache.mass."""
     import torch
-    qs = _token_stride(cache, chunk, q, cache.num_q_heads, "q")
-    os_ = _token_stride(cache, chunk, out, cache.num_q_heads, "out")
-    if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous() or
-                            tuple(lse.shape) != (chunk.tokens, cache.num_q_heads)):
-        raise ValueError("lse: float32 [%d][%d]" % (chunk.tokens, cache.num_q_heads))
+    heads = cache.num_q_heads
+    _same_requests(cache, chunk)
+    qs = _token_stride(cache, chunk, q, heads, "q")
+    os_ = _token_stride(cache, chunk, out, heads, "out")
+    if lse is not None and (lse.dtype is not torch.float32 or not lse.is_contiguous() or
+                            lse.shape != (chunk.tokens, heads)):
+        raise ValueError("lse: float32 [%d][%d]" % (chunk.tokens, heads))
     _on_current_device(cache, q, out, lse, workspace, chunk.cu_dev)
-    scale = softmax_scale if softmax_scale is not None else 1.0 / math.sqrt(cache.head_dim)
-    _check(load().kv_paged_attention(
-        cache.c, chunk.c, int(layer), int(window), int(num_sinks), scale, q.data_ptr(), qs,
-        out.data_ptr(), os_, _ptr(lse), int(add_mass), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream(stream)), "kv_paged_attention")
+    code = load().kv_paged_attention(
+        cache._ref, chunk._ref, layer, window, num_sinks,
+        cache._scale if softmax_scale is None else softmax_scale, q.data_ptr(), qs,
+        out.data_ptr(), os_, _ptr(lse), int(add_mass), workspace.data_ptr(), workspace.nbytes,
+        _stream(stream))
+    if code:
+        raise KvError(code, "kv_paged_attention")
 
 
 def kv_paged_evict_workspace_size(cache: PagedCache) -> int:
