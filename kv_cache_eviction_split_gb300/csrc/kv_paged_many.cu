@@ -141,7 +141,8 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             const DevPaged C, const DevChunk T, const ManyArgs A) {
     using Ly = Layout<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);   // uniform
+    const int lane = threadIdx.x & 31;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Ly::kBars);
     uint64_t *k_full = bars, *k_empty = k_full + Ly::kKSt;
     uint64_t *v_full = k_empty + Ly::kKSt, *v_empty = v_full + Ly::kVSt;
@@ -523,7 +524,15 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             }
         } else if (warp == kMmaWarp) {
             // ---------------------------------------------------------------- products
-            if (lane == 0) {
+            // The whole warp walks the loop with uniform operands and one lane issues.
+            {
+                const uint32_t el = elect_one();
+                auto uni = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+                auto wait = [&](uint64_t *bar, int count) {
+                    return __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)(count & 1), s_abort,
+                                                             C.wait_ns)) != 0;
+                };
+                const uint32_t tm = (uint32_t)uni((int)tmem);
                 constexpr uint32_t idesc_s = E::kHalf ? idesc_f16_f32(128, kManyTile)
                                                       : idesc_bf16_f32(128, kManyTile);
                 constexpr uint32_t idesc_o = E::kHalf ? idesc_f16_f32_bmn(128, D)
@@ -531,14 +540,22 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                 int kc = 0;                      // tiles of the rings used so far
                 int sc[2] = {0, 0};              // P V issued per lane
                 int ic[2] = {0, 0};              // items in which the lane took part
-                const Item *w;
-                for (int i = 0; (w = item(i, ok)); ++i) {
-                    const Lane l0 = w->lane[0], l1 = w->lane[1];
-                    const int x1 = w->x1;
+                for (int i = 0;; ++i) {
+                    const Item *w = item(i, ok);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok || uni(w == nullptr)) break;
+                    auto lane_of = [&](int L) {
+                        const Lane &a = w->lane[L];
+                        return Lane{0, 0, 0, uni(a.ns), uni(a.a), uni(a.b)};
+                    };
+                    const Lane l0 = lane_of(0), l1 = lane_of(1);
+                    const int x0 = uni(w->x0), x1 = uni(w->x1);
+                    __syncwarp();
+                    if (el) mbar_arrive(&i_empty[i % kItems]);
                     // lane L's tile whose P V is still to be issued: its place in the rings
                     int pend[2] = {-1, -1};
                     bool pend_frees[2] = {false, false}, begun[2] = {false, false};
-                    for (int x = w->x0; ok && x <= x1; ++x) {
+                    for (int x = x0; ok && x <= x1; ++x) {
                         const bool see[2] = {x < x1 && l0.sees(x), x < x1 && l1.sees(x)};
     #pragma unroll
                         for (int L = 0; L < 2; ++L) {
@@ -547,27 +564,24 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                                 const int s = pend[L] % Ly::kVSt;
                                 const bool first = !begun[L];
                                 if (first)
-                                    ok = mbar_wait(&o_empty[L], (uint32_t)(ic[L] & 1) ^ 1u, s_abort,
-                                                   C.wait_ns);
-                                ok = ok &&
-                                     mbar_wait(&p_full[L], (uint32_t)(sc[L] & 1), s_abort, C.wait_ns) &&
-                                     mbar_wait(&v_full[s], (uint32_t)((pend[L] / Ly::kVSt) & 1), s_abort,
-                                               C.wait_ns);
+                                    ok = wait(&o_empty[L], ic[L] + 1);
+                                ok = ok && wait(&p_full[L], sc[L]) &&
+                                     wait(&v_full[s], pend[L] / Ly::kVSt);
                                 if (ok) {
                                     tc_fence_after();
                                     const uint64_t vb = sdesc_mn_sw128(
                                         smem_u32(smem + Ly::kV + s * Ly::kOp), kBlockBytes);
-                                    const uint32_t p_col = tmem + 128 * L;
-                                    const uint32_t o_col = tmem + kOCol + 128 * L;
+                                    const uint32_t p_col = tm + 128 * L;
+                                    const uint32_t o_col = tm + kOCol + 128 * L;
     #pragma unroll
                                     for (int q = 0; q < kManyTile / 16; ++q) {
                                         const uint64_t bd = sdesc_add(vb, q * 16 * 128);
                                         if (q == 0 && first)
-                                            mma_ts_c<false>(o_col, p_col, bd, idesc_o);
+                                            mma_ts_e<false>(o_col, p_col, bd, idesc_o, el);
                                         else
-                                            mma_ts_c<true>(o_col, p_col + q * 8, bd, idesc_o);
+                                            mma_ts_e<true>(o_col, p_col + q * 8, bd, idesc_o, el);
                                     }
-                                    if (pend_frees[L]) mma_commit(&v_empty[s]);
+                                    if (pend_frees[L]) mma_commit_e(&v_empty[s], el);
                                     begun[L] = true;
                                     ++sc[L];
                                 }
@@ -577,30 +591,28 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                                 // S_L = Q_L K^T
                                 const int s = kc % Ly::kKSt;
                                 if (!begun[L])
-                                    ok = mbar_wait(&q_full[L], (uint32_t)(ic[L] & 1), s_abort,
-                                                   C.wait_ns);
-                                ok = ok && mbar_wait(&k_full[s], (uint32_t)((kc / Ly::kKSt) & 1),
-                                                     s_abort, C.wait_ns);
+                                    ok = wait(&q_full[L], ic[L]);
+                                ok = ok && wait(&k_full[s], kc / Ly::kKSt);
                                 if (ok) {
                                     tc_fence_after();
                                     const uint64_t qa =
                                         sdesc_k_sw128(smem_u32(smem + Ly::kQ + L * Ly::kOp));
                                     const uint64_t ka =
                                         sdesc_k_sw128(smem_u32(smem + Ly::kK + s * Ly::kOp));
-                                    const uint32_t s_col = tmem + 128 * L;
+                                    const uint32_t s_col = tm + 128 * L;
     #pragma unroll
                                     for (int kb = 0; kb < D / 64; ++kb)
     #pragma unroll
                                         for (int kk = 0; kk < 4; ++kk) {
                                             const uint32_t o = kb * kBlockBytes + kk * 32;
                                             if (kb | kk)
-                                                mma_ss_c<true>(s_col, sdesc_add(qa, o),
-                                                               sdesc_add(ka, o), idesc_s);
+                                                mma_ss_e<true>(s_col, sdesc_add(qa, o),
+                                                               sdesc_add(ka, o), idesc_s, el);
                                             else
-                                                mma_ss_c<false>(s_col, qa, ka, idesc_s);
+                                                mma_ss_e<false>(s_col, qa, ka, idesc_s, el);
                                         }
-                                    mma_commit(&s_full[L]);
-                                    if (L == 1 || !see[1]) mma_commit(&k_empty[s]);
+                                    mma_commit_e(&s_full[L], el);
+                                    if (L == 1 || !see[1]) mma_commit_e(&k_empty[s], el);
                                     pend[L] = kc;
                                     pend_frees[L] = L == 1 || !see[1];
                                 }
@@ -611,17 +623,16 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     #pragma unroll
                     for (int L = 0; L < 2; ++L)
                         if (ok && begun[L]) {
-                            mma_commit(&o_final[L]);
+                            mma_commit_e(&o_final[L], el);
                             ++ic[L];
                         }
-                    mbar_arrive(&i_empty[i % kItems]);
                 }
-                if (!ok) {
+                if (!ok && el) {
                     *s_abort = 1;
                     post_status(C.status, KV_ERR_TIMEOUT);
                 }
                 // every product issued completes before tensor memory is freed
-                mma_commit(mma_done);
+                mma_commit_e(mma_done, el);
                 mbar_drain(mma_done, 0, kDrainNs);
             }
         }

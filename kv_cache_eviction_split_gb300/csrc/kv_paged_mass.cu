@@ -75,7 +75,8 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             const DevPaged C, const DevChunk T, const MassArgs A) {
     using Ly = Layout<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);   // uniform
+    const int lane = threadIdx.x & 31;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Ly::kBars);
     uint64_t *k_full = bars, *k_empty = k_full + 2;          // [item parity]
     uint64_t *q_full = k_empty + 2, *q_empty = q_full + kQSt;
@@ -261,18 +262,29 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             if (uses > 0) mbar_drain(&q_full[s], (uint32_t)((uses - 1) & 1), kDrainNs);
         }
     } else if (warp == kMmaWarp) {
-        if (lane == 0) {
+        // the whole warp walks the loop with uniform operands and one lane issues
+        {
+            const uint32_t el = elect_one();
+            auto uni = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+            auto wait = [&](uint64_t *bar, int count) {
+                return __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)(count & 1), s_abort,
+                                                         C.wait_ns)) != 0;
+            };
+            const uint32_t tm = (uint32_t)uni((int)tmem);
             constexpr uint32_t idesc = E::kHalf ? idesc_f16_f32(128, 128) : idesc_bf16_f32(128, 128);
             int rc = 0;                      // row tiles so far
             int used[4] = {0, 0, 0, 0};      // products into each buffer
-            const Item *w;
-            for (int i = 0; (w = item(i, ok)); ++i) {
-                const int steps = w->rt1 - w->rt0, tiles = w->tiles, ks = i & 1;
-                mbar_arrive(&i_empty[i % kItems]);
-                ok = mbar_wait(&k_full[ks], (uint32_t)((i >> 1) & 1), s_abort, C.wait_ns);
+            for (int i = 0;; ++i) {
+                const Item *w = item(i, ok);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok || uni(w == nullptr)) break;
+                const int steps = uni(w->rt1 - w->rt0), tiles = uni(w->tiles), ks = i & 1;
+                __syncwarp();
+                if (el) mbar_arrive(&i_empty[i % kItems]);
+                ok = wait(&k_full[ks], i >> 1);
                 for (int r = 0; ok && r < steps; ++r, ++rc) {
                     const int s = rc % kQSt;
-                    ok = mbar_wait(&q_full[s], (uint32_t)((rc / kQSt) & 1), s_abort, C.wait_ns);
+                    ok = wait(&q_full[s], rc / kQSt);
 #pragma unroll
                     for (int k = 0; k < kGroup; ++k) {
                         if (!ok || k >= tiles) continue;
@@ -280,8 +292,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                         for (int par = 0; par < 2; ++par) {
                             if ((rc & 1) != par) continue;
                             const int b = 2 * par + k;
-                            ok = mbar_wait(&s_free[b], (uint32_t)(used[b] & 1) ^ 1u, s_abort,
-                                           C.wait_ns);
+                            ok = wait(&s_free[b], used[b] + 1);
                             if (!ok) continue;
                             ++used[b];
                             tc_fence_after();
@@ -295,20 +306,20 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                                 for (int kk = 0; kk < 4; ++kk) {
                                     const uint32_t o = kb * kBlockBytes + kk * 32;
                                     if (kb | kk)
-                                        mma_ss_c<true>(tmem + 128 * b, sdesc_add(ka, o),
-                                                       sdesc_add(qb, o), idesc);
+                                        mma_ss_e<true>(tm + 128 * b, sdesc_add(ka, o),
+                                                       sdesc_add(qb, o), idesc, el);
                                     else
-                                        mma_ss_c<false>(tmem + 128 * b, ka, qb, idesc);
+                                        mma_ss_e<false>(tm + 128 * b, ka, qb, idesc, el);
                                 }
-                            mma_commit(&s_full[b]);
+                            mma_commit_e(&s_full[b], el);
                         }
                     }
-                    if (ok) mma_commit(&q_empty[s]);
+                    if (ok) mma_commit_e(&q_empty[s], el);
                 }
-                if (ok) mma_commit(&k_empty[ks]);
+                if (ok) mma_commit_e(&k_empty[ks], el);
             }
-            if (!ok) expired();
-            mma_commit(mma_done);
+            if (!ok && el) expired();
+            mma_commit_e(mma_done, el);
             mbar_drain(mma_done, 0, kDrainNs);
         }
     } else {
