@@ -120,24 +120,48 @@ __device__ __forceinline__ long long packed_row(const DevPaged &C, const UnitRow
     return U.tok0 * C.Hq + (long long)U.h * U.count * C.G + row;
 }
 
-// The run of tiles of one CTA, in the order of all units' tiles.
+// The run of tiles of one CTA, in the order of all units' parts' tiles.
 struct CtaRun {
     int begin, end, per;       // tiles [begin, end) of all; tiles per CTA
-    int unit, unit_begin;      // the unit that holds tile `begin`, and its first tile
+    int unit, part;            // the part that holds tile `begin`, and its first tile
+    int part_begin;
     int total;
 };
 
-// Cuts the tiles of all units of the layer (tiles_of(v) of unit v) into gridDim.x
-// runs of at least `least` tiles.  All kThreads threads call it.
-template <int kThreads, typename F>
-__device__ __forceinline__ CtaRun cut_run(int units, int least, F tiles_of) {
-    __shared__ int warp_sums[kThreads / 32];
-    __shared__ int found[2];
+// Cuts the tiles of all units of the layer into gridDim.x equal runs.  A unit v consists
+// of parts_of(v) parts and part i of tiles_of(v, i) tiles.  All kThreads threads call it:
+// a warp sums up a unit (a thread, where there are more units than threads), and a warp
+// finds the run's first part.  s_tiles: kThreads words of shared memory (TMA may write
+// there afterwards).
+template <int kThreads, typename P, typename F>
+__device__ __forceinline__ CtaRun cut_run(int units, int *s_tiles, P parts_of, F tiles_of) {
+    constexpr int kWarps = kThreads / 32;
+    __shared__ int warp_sums[kWarps];
+    __shared__ int found[3];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int chunk = (units + kThreads - 1) / kThreads;
     const int v0 = min(units, tid * chunk), v1 = min(units, v0 + chunk);
+    auto unit_tiles = [&](int v) {
+        int sum = 0;
+        const int n = parts_of(v);
+        for (int i = 0; i < n; ++i) sum += tiles_of(v, i);
+        return sum;
+    };
     int mine = 0;
-    for (int v = v0; v < v1; ++v) mine += tiles_of(v);
+    if (chunk <= 1) {
+        for (int v = warp; v < units; v += kWarps) {
+            int sum = 0;
+            const int n = parts_of(v);
+            for (int i = lane; i < n; i += 32) sum += tiles_of(v, i);
+            sum = __reduce_add_sync(0xffffffffu, sum);
+            if (lane == 0) s_tiles[v] = sum;
+        }
+        __syncthreads();
+        mine = tid < units ? s_tiles[tid] : 0;
+        sm100::fence_proxy_async_smem();
+    } else {
+        for (int v = v0; v < v1; ++v) mine += unit_tiles(v);
+    }
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -145,34 +169,59 @@ __device__ __forceinline__ CtaRun cut_run(int units, int least, F tiles_of) {
         if (lane >= o) incl += y;
     }
     if (lane == 31) warp_sums[warp] = incl;
-    if (tid == 0) found[0] = units;
     __syncthreads();
     int before = incl - mine, total = 0;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
         if (w < warp) before += warp_sums[w];
         total += warp_sums[w];
     }
     CtaRun R;
     R.total = total;
-    R.per = max(least, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+    R.per = max(1, (total + (int)gridDim.x - 1) / (int)gridDim.x);
     R.begin = (int)min((long long)total, (long long)blockIdx.x * R.per);
     R.end = min(total, R.begin + R.per);
     if (R.begin < R.end && before <= R.begin && R.begin < before + mine) {
-        int at = before;
-        for (int v = v0; v < v1; ++v) {
-            const int t = tiles_of(v);
-            if (R.begin < at + t) {
-                found[0] = v;
-                found[1] = at;
-                break;
-            }
-            at += t;
-        }
+        int at = before, v = v0;
+        if (chunk > 1)
+            for (int t; at + (t = unit_tiles(v)) <= R.begin; ++v) at += t;
+        found[0] = v;
+        found[2] = at;
     }
     __syncthreads();
+    if (R.begin >= R.end) {
+        R.unit = units;
+        R.part = 0;
+        R.part_begin = R.end;
+        return R;
+    }
     R.unit = found[0];
-    R.unit_begin = R.begin < R.end ? found[1] : R.end;
+    if (warp == 0) {
+        const int n = parts_of(R.unit);
+        int at = found[2];
+        for (int i0 = 0; i0 < n; i0 += 32) {
+            const int t = i0 + lane < n ? tiles_of(R.unit, i0 + lane) : 0;
+            int x = t;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            const unsigned past = __ballot_sync(0xffffffffu, at + x > R.begin);
+            if (past) {
+                if (lane == __ffs(past) - 1) {
+                    found[1] = i0 + lane;
+                    found[2] = at + x - t;
+                }
+                break;
+            }
+            at += __shfl_sync(0xffffffffu, x, 31);
+        }
+        __syncwarp();
+    }
+    __syncthreads();
+    R.part = found[1];
+    R.part_begin = found[2];
     return R;
 }
 

@@ -162,10 +162,12 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
     CtaRun run;
     int rank = 0, block = 0;
     if constexpr (kCluster == 0) {
-        run = cut_run<kThreads>(units, 1, [&](int v) {
-            const UnitRows U = unit_rows(C, T, A.layer, v);
-            return few_rows(C, T, U) ? FewItem(C, A.M, U, 0, kRows).span.total : 0;
-        });
+        run = cut_run<kThreads>(
+            units, reinterpret_cast<int *>(smem),
+            [&](int v) { return (int)few_rows(C, T, unit_rows(C, T, A.layer, v)); },
+            [&](int v, int) {
+                return FewItem(C, A.M, unit_rows(C, T, A.layer, v), 0, kRows).span.total;
+            });
     } else {
         // one item a cluster: its tiles are the whole order, each CTA's run a part of them
         rank = (int)(blockIdx.x % kCluster);
@@ -178,7 +180,7 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
         run.per = (run.total + kCluster - 1) / kCluster;
         run.begin = min(run.total, rank * run.per);
         run.end = min(run.total, run.begin + run.per);
-        run.unit_begin = 0;
+        run.part_begin = 0;
         __syncthreads();
     }
     const bool go = *s_abort == 0;
@@ -195,7 +197,7 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
         const CUtensorMap *map = kv ? &tm_v : &tm_k;
         int cnt = 0;
         bool ok = go;
-        for (int v = run.unit, at = run.unit_begin; ok && more(at); ++v) {
+        for (int v = run.unit, at = run.part_begin; ok && more(at); ++v) {
             const UnitRows U = unit_rows(C, T, A.layer, v);
             if (!few_rows(C, T, U)) continue;
             const FewItem it(C, A.M, U, block, kRows);
@@ -251,7 +253,7 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
         const float cs = A.M.scale_log2;
         int cnt = 0;
         bool ok = go;
-        for (int v = run.unit, at = run.unit_begin; ok && more(at); ++v) {
+        for (int v = run.unit, at = run.part_begin; ok && more(at); ++v) {
             const UnitRows U = unit_rows(C, T, A.layer, v);
             if (!few_rows(C, T, U)) continue;
             const FewItem it(C, A.M, U, block, kRows);

@@ -70,6 +70,7 @@ struct Layout {
     static constexpr int kMisc = (kBars + kNumBars * 8 + 15) / 16 * 16;
     static constexpr int kDesc = kMisc + 32;
     static constexpr int kTotal = kDesc + kItems * (int)sizeof(Item);
+    static_assert(kTotal + 1024 <= 227 * 1024, "with cut_run's and TMEM's few static words");
 };
 
 struct ManyArgs {
@@ -114,15 +115,14 @@ __device__ __forceinline__ void make_item(Item &it, const DevPaged &C, const Att
     }
 }
 
-// Tiles of a unit: the sum over its items.
-__device__ __forceinline__ int unit_tiles(const DevPaged &C, const DevChunk &T,
-                                          const AttendMask &M, const UnitRows &U) {
-    if (!many_rows(C, T, U)) return 0;
-    const int all = U.count * C.G, t0 = U.n - U.count;
-    int sum = 0;
-    for (int r0 = 0; r0 < all; r0 += kManyRows)
-        sum += tile_span(M, t0 + r0 / C.G, t0 + (min(all, r0 + kManyRows) - 1) / C.G, 7).total;
-    return sum;
+// Items of a unit, and the tiles of one of them.
+__device__ __forceinline__ int unit_items(const DevPaged &C, const DevChunk &T, const UnitRows &U) {
+    return many_rows(C, T, U) ? (U.count * C.G + kManyRows - 1) / kManyRows : 0;
+}
+__device__ __forceinline__ int item_tiles(const DevPaged &C, const AttendMask &M, const UnitRows &U,
+                                          int pair) {
+    const int all = U.count * C.G, t0 = U.n - U.count, r0 = pair * kManyRows;
+    return tile_span(M, t0 + r0 / C.G, t0 + (min(all, r0 + kManyRows) - 1) / C.G, 7).total;
 }
 
 __device__ __forceinline__ float max32(const float (&v)[32]) {
@@ -189,9 +189,10 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     pdl_wait();
     pdl_trigger();
     const uint32_t tmem = tmem_acquire_all(s_tmem);
-    const CtaRun run = cut_run<kThreads>(C.R * C.H, 1, [&](int v) {
-        return unit_tiles(C, T, A.M, unit_rows(C, T, A.layer, v));
-    });
+    const CtaRun run = cut_run<kThreads>(
+        C.R * C.H, reinterpret_cast<int *>(smem),
+        [&](int v) { return unit_items(C, T, unit_rows(C, T, A.layer, v)); },
+        [&](int v, int i) { return item_tiles(C, A.M, unit_rows(C, T, A.layer, v), i); });
     bool ok = *s_abort == 0;
 
     // Item i of the run for the roles (one lane or a whole warp waits); null at its end or
@@ -425,18 +426,18 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         if (warp == kSchedWarp) {
             // ---------------------------------------------------------------- scheduler
             if (lane == 0 && ok) {
-                int v = run.unit, at = run.unit_begin, i = 0;
+                int v = run.unit, at = run.part_begin, i = 0, pair = run.part;
                 for (;;) {
-                    // units from the run's first on; after the last, the end mark
+                    // units from the run's first part on; after the last, the end mark
                     const bool end = at >= run.end;
                     UnitRows U;
-                    int pairs = 1;
+                    int pairs = pair + 1;
                     if (!end) {
                         U = unit_rows(C, T, A.layer, v);
-                        pairs = many_rows(C, T, U) ? (U.count * C.G + kManyRows - 1) / kManyRows : 0;
+                        pairs = unit_items(C, T, U);
                         if (pairs && !U.ok) post_status(C.status, KV_ERR_INVALID_ARG);
                     }
-                    for (int pair = 0; ok && pair < pairs && (end || at < run.end); ++pair) {
+                    for (; ok && pair < pairs && (end || at < run.end); ++pair) {
                         Item next;
                         next.stop = end;
                         if (!end) {
@@ -456,6 +457,7 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                         ++i;
                     }
                     if (end || !ok) break;
+                    pair = 0;
                     ++v;
                 }
                 if (!ok) {
@@ -527,16 +529,16 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             // The whole warp walks the loop with uniform operands and one lane issues.
             {
                 const uint32_t el = elect_one();
-                auto uni = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+                constexpr uint32_t idesc_s = E::kHalf ? idesc_f16_f32(128, kManyTile)
+                                                      : idesc_bf16_f32(128, kManyTile);
+                constexpr uint32_t idesc_o = E::kHalf ? idesc_f16_f32_bmn(128, D)
+                                                      : idesc_bf16_f32_bmn(128, D);
+                auto uni = [](int x) { return __reduce_max_sync(0xffffffffu, x); };
                 auto wait = [&](uint64_t *bar, int count) {
                     return __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)(count & 1), s_abort,
                                                              C.wait_ns)) != 0;
                 };
                 const uint32_t tm = (uint32_t)uni((int)tmem);
-                constexpr uint32_t idesc_s = E::kHalf ? idesc_f16_f32(128, kManyTile)
-                                                      : idesc_bf16_f32(128, kManyTile);
-                constexpr uint32_t idesc_o = E::kHalf ? idesc_f16_f32_bmn(128, D)
-                                                      : idesc_bf16_f32_bmn(128, D);
                 int kc = 0;                      // tiles of the rings used so far
                 int sc[2] = {0, 0};              // P V issued per lane
                 int ic[2] = {0, 0};              // items in which the lane took part
@@ -549,78 +551,72 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                         return Lane{0, 0, 0, uni(a.ns), uni(a.a), uni(a.b)};
                     };
                     const Lane l0 = lane_of(0), l1 = lane_of(1);
-                    const int x0 = uni(w->x0), x1 = uni(w->x1);
+                    const int x0 = uni(w->x0), x1 = uni(w->x1), w_seen = w->t_hi >= 0;
                     __syncwarp();
                     if (el) mbar_arrive(&i_empty[i % kItems]);
-                    // lane L's tile whose P V is still to be issued: its place in the rings
-                    int pend[2] = {-1, -1};
-                    bool pend_frees[2] = {false, false}, begun[2] = {false, false};
-                    for (int x = x0; ok && x <= x1; ++x) {
-                        const bool see[2] = {x < x1 && l0.sees(x), x < x1 && l1.sees(x)};
-    #pragma unroll
+                    // Slot x: P V of the lanes' tiles of slot x - 1, then S of tile x.  Their
+                    // K and V are waited for once, before the lanes' P, so that nothing
+                    // lies between a lane's P and its sixteen products.  Every tile of a
+                    // run is loaded and seen by a lane, unless the item sees nothing.
+                    bool pend[2] = {false, false}, begun[2] = {false, false};
+                    const int slots = uni(w_seen) ? x1 - x0 : 0;
+                    for (int i = 0; ok && i < slots + 1; ++i) {
+                        const int x = x0 + i;
+                        const bool see[2] = {i < slots && l0.sees(x), i < slots && l1.sees(x)};
+                        const int ks = (kc + i) % Ly::kKSt, vs = (kc + i + 1) % Ly::kVSt;
+                        if (i < slots) ok = wait(&k_full[ks], (kc + i) / Ly::kKSt);
+                        if (ok && i > 0) ok = wait(&v_full[vs], (kc + i - 1) / Ly::kVSt);
+                        const bool two = pend[1];        // lane 1's P V is the tile's last
+                        const uint64_t vb =
+                            sdesc_mn_sw128(smem_u32(smem + Ly::kV) + vs * Ly::kOp, kBlockBytes);
+                        const uint64_t ka = sdesc_k_sw128(smem_u32(smem + Ly::kK) + ks * Ly::kOp);
+#pragma unroll
                         for (int L = 0; L < 2; ++L) {
-                            if (ok && pend[L] >= 0) {
+                            const uint32_t s_col = tm + 128 * L, o_col = tm + kOCol + 128 * L;
+                            if (ok && !begun[L] && see[L]) ok = wait(&q_full[L], ic[L]);
+                            if (ok && pend[L]) {
                                 // O_L (+)= P V of the lane's previous tile
-                                const int s = pend[L] % Ly::kVSt;
                                 const bool first = !begun[L];
-                                if (first)
-                                    ok = wait(&o_empty[L], ic[L] + 1);
-                                ok = ok && wait(&p_full[L], sc[L]) &&
-                                     wait(&v_full[s], pend[L] / Ly::kVSt);
+                                if (first) ok = wait(&o_empty[L], ic[L] + 1);
+                                ok = ok && wait(&p_full[L], sc[L]);
                                 if (ok) {
                                     tc_fence_after();
-                                    const uint64_t vb = sdesc_mn_sw128(
-                                        smem_u32(smem + Ly::kV + s * Ly::kOp), kBlockBytes);
-                                    const uint32_t p_col = tm + 128 * L;
-                                    const uint32_t o_col = tm + kOCol + 128 * L;
-    #pragma unroll
-                                    for (int q = 0; q < kManyTile / 16; ++q) {
-                                        const uint64_t bd = sdesc_add(vb, q * 16 * 128);
-                                        if (q == 0 && first)
-                                            mma_ts_e<false>(o_col, p_col, bd, idesc_o, el);
-                                        else
-                                            mma_ts_e<true>(o_col, p_col + q * 8, bd, idesc_o, el);
-                                    }
-                                    if (pend_frees[L]) mma_commit_e(&v_empty[s], el);
+                                    if (first)
+                                        mma_ts_e<false>(o_col, s_col, vb, idesc_o, el);
+                                    else
+                                        mma_ts_e<true>(o_col, s_col, vb, idesc_o, el);
+#pragma unroll
+                                    for (int q = 1; q < kManyTile / 16; ++q)
+                                        mma_ts_e<true>(o_col, s_col + q * 8,
+                                                       sdesc_at(vb, q * 16 * 128), idesc_o, el);
+                                    if (L == 1 || !two) mma_commit_e(&v_empty[vs], el);
                                     begun[L] = true;
                                     ++sc[L];
                                 }
-                                pend[L] = -1;
+                                pend[L] = false;
                             }
                             if (ok && see[L]) {
                                 // S_L = Q_L K^T
-                                const int s = kc % Ly::kKSt;
-                                if (!begun[L])
-                                    ok = wait(&q_full[L], ic[L]);
-                                ok = ok && wait(&k_full[s], kc / Ly::kKSt);
-                                if (ok) {
-                                    tc_fence_after();
-                                    const uint64_t qa =
-                                        sdesc_k_sw128(smem_u32(smem + Ly::kQ + L * Ly::kOp));
-                                    const uint64_t ka =
-                                        sdesc_k_sw128(smem_u32(smem + Ly::kK + s * Ly::kOp));
-                                    const uint32_t s_col = tm + 128 * L;
-    #pragma unroll
-                                    for (int kb = 0; kb < D / 64; ++kb)
-    #pragma unroll
-                                        for (int kk = 0; kk < 4; ++kk) {
-                                            const uint32_t o = kb * kBlockBytes + kk * 32;
-                                            if (kb | kk)
-                                                mma_ss_e<true>(s_col, sdesc_add(qa, o),
-                                                               sdesc_add(ka, o), idesc_s, el);
-                                            else
-                                                mma_ss_e<false>(s_col, qa, ka, idesc_s, el);
-                                        }
-                                    mma_commit_e(&s_full[L], el);
-                                    if (L == 1 || !see[1]) mma_commit_e(&k_empty[s], el);
-                                    pend[L] = kc;
-                                    pend_frees[L] = L == 1 || !see[1];
+                                tc_fence_after();
+                                const uint64_t qa =
+                                    sdesc_k_sw128(smem_u32(smem + Ly::kQ + L * Ly::kOp));
+#pragma unroll
+                                for (int k = 0; k < D / 16; ++k) {
+                                    const uint32_t o = (k >> 2) * kBlockBytes + (k & 3) * 32;
+                                    if (k)
+                                        mma_ss_e<true>(s_col, sdesc_at(qa, o), sdesc_at(ka, o),
+                                                       idesc_s, el);
+                                    else
+                                        mma_ss_e<false>(s_col, qa, ka, idesc_s, el);
                                 }
+                                mma_commit_e(&s_full[L], el);
+                                if (L == 1 || !see[1]) mma_commit_e(&k_empty[ks], el);
+                                pend[L] = true;
                             }
                         }
-                        if (see[0] || see[1]) ++kc;
                     }
-    #pragma unroll
+                    kc += slots;
+#pragma unroll
                     for (int L = 0; L < 2; ++L)
                         if (ok && begun[L]) {
                             mma_commit_e(&o_final[L], el);

@@ -9,6 +9,8 @@
 // in shared memory for the item (the next one's loads meanwhile), packed Q tiles stream
 // through a ring (32 KB per two products at d = 128).  The query rows that see key j are a
 // run of packed rows, [ (j - t0) G, (j + window - t0) G ), so the mask is two bounds.
+#include <type_traits>
+
 #include "kv_paged_attend.cuh"
 
 namespace kvevict {
@@ -17,6 +19,10 @@ using namespace sm100;
 
 constexpr int kThreads = 12 * 32;
 constexpr int kKWarp = 0, kMmaWarp = 1, kQWarp = 2, kSchedWarp = 3, kKeyWarp = 4;
+// Registers a thread after the split, of 168 at launch (384 x 168 = 128 x 104 + 256 x 200):
+// a key thread holds its 128 logits and the rows' lse read ahead (at 168 it read them just
+// before use, and the exponentials took 1500 clocks a tile).
+constexpr int kLoadRegs = 104, kKeyRegs = 200;
 constexpr int kBlockBytes = 128 * 128;       // [128 rows][64 columns], 128 B swizzle
 constexpr int kGroup = 2;                    // key tiles per item
 constexpr int kItems = 3;                    // items described ahead
@@ -42,6 +48,7 @@ struct Layout {
     static constexpr int kMisc = (kBars + kNumBars * 8 + 15) / 16 * 16;
     static constexpr int kDesc = kMisc + 16;
     static constexpr int kTotal = kDesc + kItems * (int)sizeof(Item);
+    static_assert(kTotal + 1024 <= 227 * 1024, "with cut_run's and TMEM's few static words");
 };
 
 struct MassArgs {
@@ -117,17 +124,15 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     const uint32_t tmem = tmem_acquire_all(s_tmem);
     // runs of equal numbers of (key group, row tile) steps; a group belongs to the run
     // that its first step lies in
-    const CtaRun run = cut_run<kThreads>(C.R * C.H, 1, [&](int v) {
-        const UnitRows U = unit_rows(C, T, A.layer, v);
-        const Groups g(C, T, U);
-        int sum = 0;
-        for (int i = 0; i < g.groups; ++i) {
-            int a, b;
-            g.range(C, A.M, U.n, i, a, b);
-            sum += b - a;
-        }
-        return sum;
-    });
+    const CtaRun run = cut_run<kThreads>(
+        C.R * C.H, reinterpret_cast<int *>(smem),
+        [&](int v) { return Groups(C, T, unit_rows(C, T, A.layer, v)).groups; },
+        [&](int v, int i) {
+            const UnitRows U = unit_rows(C, T, A.layer, v);
+            int r0, r1;
+            Groups(C, T, U).range(C, A.M, U.n, i, r0, r1);
+            return r1 - r0;
+        });
     bool ok = *s_abort == 0;
     auto item = [&](int i, bool &fine) -> const Item * {
         fine = fine && mbar_wait(&i_full[i % kItems], (uint32_t)((i / kItems) & 1), s_abort,
@@ -141,188 +146,8 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         post_status(C.status, KV_ERR_TIMEOUT);
     };
 
-    if (warp == kSchedWarp) {
-        if (lane == 0 && ok) {
-            int i = 0, at = run.unit_begin;
-            auto put = [&](const Item &next) {
-                ok = mbar_wait(&i_empty[i % kItems], (uint32_t)((i / kItems) & 1) ^ 1u, s_abort,
-                               C.wait_ns);
-                if (!ok) return;
-                s_item[i % kItems] = next;
-                mbar_arrive(&i_full[i % kItems]);
-                ++i;
-            };
-            Item next;
-            next.stop = 0;
-            for (int v = run.unit; ok && at < run.end; ++v) {
-                const UnitRows U = unit_rows(C, T, A.layer, v);
-                const Groups g(C, T, U);
-                next.n = U.n;
-                next.rows = g.rows;
-                next.t0 = g.t0;
-                next.prow0 = packed_row(C, U, 0);
-                next.table = U.table;
-                for (int j = 0; ok && j < g.groups && at < run.end; ++j) {
-                    g.range(C, A.M, U.n, j, next.rt0, next.rt1);
-                    const int steps = next.rt1 - next.rt0;
-                    if (steps > 0 && at >= run.begin) {
-                        next.tile0 = j * kGroup;
-                        next.tiles = min(kGroup, ((U.n + kManyTile - 1) >> 7) - next.tile0);
-                        put(next);
-                    }
-                    at += steps;
-                }
-            }
-            next.stop = 1;
-            if (ok) put(next);
-            if (!ok) expired();
-        }
-    } else if (warp == kKWarp) {
-        fence_proxy_async_global();    // rows that earlier kernels stored, before TMA reads them
-        const int subs = kManyTile / C.ps, boxes = subs * (D / 64);
-        const int half = lane % (D / 64), sub = lane / (D / 64);
-        int cnt = 0;
-        for (int i = 0;; ++i) {
-            const Item *w = item(i, ok);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok || !w) break;
-            const int n = w->n, tiles = w->tiles, tile0 = w->tile0, s = i & 1;
-            const int32_t *table = w->table;
-            int y[kGroup], n_use = 0;
-            bool use[kGroup];
-#pragma unroll
-            for (int k = 0; k < kGroup; ++k) {
-                // a page that does not exist was reported by the attention pass
-                const int j = (tile0 + k) * kManyTile + sub * C.ps;
-                use[k] = k < tiles && lane < boxes && j < n;
-                const int page = use[k] ? table[j >> C.ps_log2] : -1;
-                use[k] = use[k] && page >= 0 && page < C.num_pages;
-                y[k] = page << C.ps_log2;
-                n_use += __popc(__ballot_sync(0xffffffffu, use[k]));
-            }
-            ok = mbar_wait(&k_empty[s], (uint32_t)((i >> 1) & 1) ^ 1u, s_abort, C.wait_ns);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            if (lane == 0) {
-                if (n_use) mbar_arrive_expect_tx(&k_full[s], n_use * C.ps * 128);
-                else mbar_arrive(&k_full[s]);
-                mbar_arrive(&i_empty[i % kItems]);
-            }
-            __syncwarp();
-#pragma unroll
-            for (int k = 0; k < kGroup; ++k)
-                if (use[k])
-                    tma_load_2d(smem + Ly::kK + (s * kGroup + k) * Ly::kOp + half * kBlockBytes +
-                                    sub * C.ps * 128,
-                                &tm_k, &k_full[s], half * 64, y[k]);
-            ++cnt;
-        }
-        if (!ok && lane == 0) expired();
-        for (int s = 0; s < 2; ++s) {
-            const int uses = cnt / 2 + (cnt % 2 > s ? 1 : 0);
-            if (uses > 0) mbar_drain(&k_full[s], (uint32_t)((uses - 1) & 1), kDrainNs);
-        }
-    } else if (warp == kQWarp) {
-        fence_proxy_async_global();
-        int cnt = 0;
-        for (int i = 0;; ++i) {
-            const Item *w = item(i, ok);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok || !w) break;
-            const int rt0 = w->rt0, rt1 = w->rt1, rows = w->rows;
-            const long long prow0 = w->prow0;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&i_empty[i % kItems]);
-            for (int rt = rt0; rt < rt1; ++rt, ++cnt) {
-                const int s = cnt % kQSt;
-                float z[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int row = rt * 128 + lane * 4 + k;
-                    z[k] = row < rows ? -A.lse2[prow0 + row] : 0.f;
-                }
-                ok = mbar_wait(&q_empty[s], (uint32_t)((cnt / kQSt) & 1) ^ 1u, s_abort, C.wait_ns);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                *reinterpret_cast<float4 *>(s_lse + s * 128 + lane * 4) =
-                    make_float4(z[0], z[1], z[2], z[3]);
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&q_full[s]);
-                    mbar_arrive_expect_tx(&q_full[s], Ly::kOp);
-                    for (int kb = 0; kb < D / 64; ++kb)
-                        tma_load_2d(smem + Ly::kQ + s * Ly::kOp + kb * kBlockBytes, &tm_q,
-                                    &q_full[s], kb * 64, (int)(prow0 + rt * 128));
-                }
-            }
-        }
-        if (!ok && lane == 0) expired();
-        for (int s = 0; s < kQSt; ++s) {
-            const int uses = cnt / kQSt + (cnt % kQSt > s ? 1 : 0);
-            if (uses > 0) mbar_drain(&q_full[s], (uint32_t)((uses - 1) & 1), kDrainNs);
-        }
-    } else if (warp == kMmaWarp) {
-        // the whole warp walks the loop with uniform operands and one lane issues
-        {
-            const uint32_t el = elect_one();
-            auto uni = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
-            auto wait = [&](uint64_t *bar, int count) {
-                return __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)(count & 1), s_abort,
-                                                         C.wait_ns)) != 0;
-            };
-            const uint32_t tm = (uint32_t)uni((int)tmem);
-            constexpr uint32_t idesc = E::kHalf ? idesc_f16_f32(128, 128) : idesc_bf16_f32(128, 128);
-            int rc = 0;                      // row tiles so far
-            int used[4] = {0, 0, 0, 0};      // products into each buffer
-            for (int i = 0;; ++i) {
-                const Item *w = item(i, ok);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok || uni(w == nullptr)) break;
-                const int steps = uni(w->rt1 - w->rt0), tiles = uni(w->tiles), ks = i & 1;
-                __syncwarp();
-                if (el) mbar_arrive(&i_empty[i % kItems]);
-                ok = wait(&k_full[ks], i >> 1);
-                for (int r = 0; ok && r < steps; ++r, ++rc) {
-                    const int s = rc % kQSt;
-                    ok = wait(&q_full[s], rc / kQSt);
-#pragma unroll
-                    for (int k = 0; k < kGroup; ++k) {
-                        if (!ok || k >= tiles) continue;
-#pragma unroll
-                        for (int par = 0; par < 2; ++par) {
-                            if ((rc & 1) != par) continue;
-                            const int b = 2 * par + k;
-                            ok = wait(&s_free[b], used[b] + 1);
-                            if (!ok) continue;
-                            ++used[b];
-                            tc_fence_after();
-                            const uint64_t ka = sdesc_k_sw128(
-                                smem_u32(smem + Ly::kK + (ks * kGroup + k) * Ly::kOp));
-                            const uint64_t qb =
-                                sdesc_k_sw128(smem_u32(smem + Ly::kQ + s * Ly::kOp));
-#pragma unroll
-                            for (int kb = 0; kb < D / 64; ++kb)
-#pragma unroll
-                                for (int kk = 0; kk < 4; ++kk) {
-                                    const uint32_t o = kb * kBlockBytes + kk * 32;
-                                    if (kb | kk)
-                                        mma_ss_e<true>(tm + 128 * b, sdesc_add(ka, o),
-                                                       sdesc_add(qb, o), idesc, el);
-                                    else
-                                        mma_ss_e<false>(tm + 128 * b, ka, qb, idesc, el);
-                                }
-                            mma_commit_e(&s_full[b], el);
-                        }
-                    }
-                    if (ok) mma_commit_e(&q_empty[s], el);
-                }
-                if (ok) mma_commit_e(&k_empty[ks], el);
-            }
-            if (!ok && el) expired();
-            mma_commit_e(mma_done, el);
-            mbar_drain(mma_done, 0, kDrainNs);
-        }
-    } else {
+    if (warp >= kKeyWarp) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kKeyRegs));
         // ---------------------------------------------------------------- keys
         const int k = (warp - kKeyWarp) >> 2;             // key tile of the item
         const int quarter = warp & 3;
@@ -386,30 +211,38 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&s_free[2 * par + k]);
+// every row of the tile sees the thread's key, or a run of its bits does
+                    auto add = [&](auto masked) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const uint32_t see =
-                            all ? 0xffffffffu
-                                : low_bits(r_hi - row0 - 32 * c) & ~low_bits(r_lo - row0 - 32 * c);
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t see = 0;
+                            if (masked)
+                                see = low_bits(r_hi - row0 - 32 * c) &
+                                      ~low_bits(r_lo - row0 - 32 * c);
 #pragma unroll
-                        for (int x = 0; x < 32; x += 4) {
-                            const float4 z = lse[c * 8 + x / 4];
-                            const float2 e0 = __ffma2_rn(make_float2(s[c][x], s[c][x + 1]), cs2,
-                                                         make_float2(z.x, z.y));
-                            const float2 e1 = __ffma2_rn(make_float2(s[c][x + 2], s[c][x + 3]), cs2,
-                                                         make_float2(z.z, z.w));
-                            float2 p0 = make_float2(ex2_approx(e0.x), ex2_approx(e0.y));
-                            float2 p1 = make_float2(ex2_approx(e1.x), ex2_approx(e1.y));
-                            if (!all) {
-                                if (!(see >> x & 1u)) p0.x = 0.f;
-                                if (!(see >> (x + 1) & 1u)) p0.y = 0.f;
-                                if (!(see >> (x + 2) & 1u)) p1.x = 0.f;
-                                if (!(see >> (x + 3) & 1u)) p1.y = 0.f;
+                            for (int x = 0; x < 32; x += 4) {
+                                const float4 z = lse[c * 8 + x / 4];
+                                const float2 e0 =
+                                    __ffma2_rn(make_float2(s[c][x], s[c][x + 1]), cs2,
+                                               make_float2(z.x, z.y));
+                                const float2 e1 =
+                                    __ffma2_rn(make_float2(s[c][x + 2], s[c][x + 3]), cs2,
+                                               make_float2(z.z, z.w));
+                                float2 p0 = make_float2(ex2_approx(e0.x), ex2_approx(e0.y));
+                                float2 p1 = make_float2(ex2_approx(e1.x), ex2_approx(e1.y));
+                                if (masked) {
+                                    if (!(see >> x & 1u)) p0.x = 0.f;
+                                    if (!(see >> (x + 1) & 1u)) p0.y = 0.f;
+                                    if (!(see >> (x + 2) & 1u)) p1.x = 0.f;
+                                    if (!(see >> (x + 3) & 1u)) p1.y = 0.f;
+                                }
+                                sum[(x >> 1) & 3] = __fadd2_rn(sum[(x >> 1) & 3], p0);
+                                sum[((x >> 1) + 1) & 3] = __fadd2_rn(sum[((x >> 1) + 1) & 3], p1);
                             }
-                            sum[(x >> 1) & 3] = __fadd2_rn(sum[(x >> 1) & 3], p0);
-                            sum[((x >> 1) + 1) & 3] = __fadd2_rn(sum[((x >> 1) + 1) & 3], p1);
                         }
-                    }
+                    };
+                    if (all) add(std::false_type{});
+                    else add(std::true_type{});
                     const float2 a = __fadd2_rn(__fadd2_rn(sum[0], sum[1]),
                                                 __fadd2_rn(sum[2], sum[3]));
                     acc += a.x + a.y;
@@ -424,6 +257,191 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             }
         }
         if (!ok && lane == 0) expired();
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
+        if (warp == kSchedWarp) {
+            if (lane == 0 && ok) {
+                int i = 0, at = run.part_begin, j = run.part;
+                auto put = [&](const Item &next) {
+                    ok = mbar_wait(&i_empty[i % kItems], (uint32_t)((i / kItems) & 1) ^ 1u, s_abort,
+                                   C.wait_ns);
+                    if (!ok) return;
+                    s_item[i % kItems] = next;
+                    mbar_arrive(&i_full[i % kItems]);
+                    ++i;
+                };
+                Item next;
+                next.stop = 0;
+                for (int v = run.unit; ok && at < run.end; ++v) {
+                    const UnitRows U = unit_rows(C, T, A.layer, v);
+                    const Groups g(C, T, U);
+                    next.n = U.n;
+                    next.rows = g.rows;
+                    next.t0 = g.t0;
+                    next.prow0 = packed_row(C, U, 0);
+                    next.table = U.table;
+                    for (; ok && j < g.groups && at < run.end; ++j) {
+                        g.range(C, A.M, U.n, j, next.rt0, next.rt1);
+                        const int steps = next.rt1 - next.rt0;
+                        if (steps > 0 && at >= run.begin) {
+                            next.tile0 = j * kGroup;
+                            next.tiles = min(kGroup, ((U.n + kManyTile - 1) >> 7) - next.tile0);
+                            put(next);
+                        }
+                        at += steps;
+                    }
+                    j = 0;
+                }
+                next.stop = 1;
+                if (ok) put(next);
+                if (!ok) expired();
+            }
+        } else if (warp == kKWarp) {
+            fence_proxy_async_global();    // rows that earlier kernels stored, before TMA reads them
+            const int subs = kManyTile / C.ps, boxes = subs * (D / 64);
+            const int half = lane % (D / 64), sub = lane / (D / 64);
+            int cnt = 0;
+            for (int i = 0;; ++i) {
+                const Item *w = item(i, ok);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok || !w) break;
+                const int n = w->n, tiles = w->tiles, tile0 = w->tile0, s = i & 1;
+                const int32_t *table = w->table;
+                int y[kGroup], n_use = 0;
+                bool use[kGroup];
+#pragma unroll
+                for (int k = 0; k < kGroup; ++k) {
+                    // a page that does not exist was reported by the attention pass
+                    const int j = (tile0 + k) * kManyTile + sub * C.ps;
+                    use[k] = k < tiles && lane < boxes && j < n;
+                    const int page = use[k] ? table[j >> C.ps_log2] : -1;
+                    use[k] = use[k] && page >= 0 && page < C.num_pages;
+                    y[k] = page << C.ps_log2;
+                    n_use += __popc(__ballot_sync(0xffffffffu, use[k]));
+                }
+                ok = mbar_wait(&k_empty[s], (uint32_t)((i >> 1) & 1) ^ 1u, s_abort, C.wait_ns);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (lane == 0) {
+                    if (n_use) mbar_arrive_expect_tx(&k_full[s], n_use * C.ps * 128);
+                    else mbar_arrive(&k_full[s]);
+                    mbar_arrive(&i_empty[i % kItems]);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < kGroup; ++k)
+                    if (use[k])
+                        tma_load_2d(smem + Ly::kK + (s * kGroup + k) * Ly::kOp + half * kBlockBytes +
+                                        sub * C.ps * 128,
+                                    &tm_k, &k_full[s], half * 64, y[k]);
+                ++cnt;
+            }
+            if (!ok && lane == 0) expired();
+            for (int s = 0; s < 2; ++s) {
+                const int uses = cnt / 2 + (cnt % 2 > s ? 1 : 0);
+                if (uses > 0) mbar_drain(&k_full[s], (uint32_t)((uses - 1) & 1), kDrainNs);
+            }
+        } else if (warp == kQWarp) {
+            fence_proxy_async_global();
+            int cnt = 0;
+            for (int i = 0;; ++i) {
+                const Item *w = item(i, ok);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok || !w) break;
+                const int rt0 = w->rt0, rt1 = w->rt1, rows = w->rows;
+                const long long prow0 = w->prow0;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&i_empty[i % kItems]);
+                for (int rt = rt0; rt < rt1; ++rt, ++cnt) {
+                    const int s = cnt % kQSt;
+                    float z[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int row = rt * 128 + lane * 4 + k;
+                        z[k] = row < rows ? -A.lse2[prow0 + row] : 0.f;
+                    }
+                    ok = mbar_wait(&q_empty[s], (uint32_t)((cnt / kQSt) & 1) ^ 1u, s_abort, C.wait_ns);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    *reinterpret_cast<float4 *>(s_lse + s * 128 + lane * 4) =
+                        make_float4(z[0], z[1], z[2], z[3]);
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&q_full[s]);
+                        mbar_arrive_expect_tx(&q_full[s], Ly::kOp);
+                        for (int kb = 0; kb < D / 64; ++kb)
+                            tma_load_2d(smem + Ly::kQ + s * Ly::kOp + kb * kBlockBytes, &tm_q,
+                                        &q_full[s], kb * 64, (int)(prow0 + rt * 128));
+                    }
+                }
+            }
+            if (!ok && lane == 0) expired();
+            for (int s = 0; s < kQSt; ++s) {
+                const int uses = cnt / kQSt + (cnt % kQSt > s ? 1 : 0);
+                if (uses > 0) mbar_drain(&q_full[s], (uint32_t)((uses - 1) & 1), kDrainNs);
+            }
+        } else if (warp == kMmaWarp) {
+            // the whole warp walks the loop with uniform operands and one lane issues
+            {
+                const uint32_t el = elect_one();
+                auto uni = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+                auto wait = [&](uint64_t *bar, int count) {
+                    return __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)(count & 1), s_abort,
+                                                             C.wait_ns)) != 0;
+                };
+                const uint32_t tm = (uint32_t)uni((int)tmem);
+                constexpr uint32_t idesc = E::kHalf ? idesc_f16_f32(128, 128) : idesc_bf16_f32(128, 128);
+                int rc = 0;                      // row tiles so far
+                int used[4] = {0, 0, 0, 0};      // products into each buffer
+                for (int i = 0;; ++i) {
+                    const Item *w = item(i, ok);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok || uni(w == nullptr)) break;
+                    const int steps = uni(w->rt1 - w->rt0), tiles = uni(w->tiles), ks = i & 1;
+                    __syncwarp();
+                    if (el) mbar_arrive(&i_empty[i % kItems]);
+                    ok = wait(&k_full[ks], i >> 1);
+                    for (int r = 0; ok && r < steps; ++r, ++rc) {
+                        const int s = rc % kQSt;
+                        ok = wait(&q_full[s], rc / kQSt);
+#pragma unroll
+                        for (int k = 0; k < kGroup; ++k) {
+                            if (!ok || k >= tiles) continue;
+#pragma unroll
+                            for (int par = 0; par < 2; ++par) {
+                                if ((rc & 1) != par) continue;
+                                const int b = 2 * par + k;
+                                ok = wait(&s_free[b], used[b] + 1);
+                                if (!ok) continue;
+                                ++used[b];
+                                tc_fence_after();
+                                const uint64_t ka = sdesc_k_sw128(
+                                    smem_u32(smem + Ly::kK + (ks * kGroup + k) * Ly::kOp));
+                                const uint64_t qb =
+                                    sdesc_k_sw128(smem_u32(smem + Ly::kQ + s * Ly::kOp));
+#pragma unroll
+                                for (int kb = 0; kb < D / 64; ++kb)
+#pragma unroll
+                                    for (int kk = 0; kk < 4; ++kk) {
+                                        const uint32_t o = kb * kBlockBytes + kk * 32;
+                                        if (kb | kk)
+                                            mma_ss_e<true>(tm + 128 * b, sdesc_add(ka, o),
+                                                           sdesc_add(qb, o), idesc, el);
+                                        else
+                                            mma_ss_e<false>(tm + 128 * b, ka, qb, idesc, el);
+                                    }
+                                mma_commit_e(&s_full[b], el);
+                            }
+                        }
+                        if (ok) mma_commit_e(&q_empty[s], el);
+                    }
+                    if (ok) mma_commit_e(&k_empty[ks], el);
+                }
+                if (!ok && el) expired();
+                mma_commit_e(mma_done, el);
+                mbar_drain(mma_done, 0, kDrainNs);
+            }
+        }
     }
     tc_fence_before();
     __syncthreads();

@@ -322,6 +322,13 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
     return d;
 }
 
+// A descriptor whose start address is `bytes` past that of `desc`, for operands known at
+// compile time: the low word alone changes (no carry), the high word stays a constant.
+__device__ __forceinline__ uint64_t sdesc_at(uint64_t desc, uint32_t bytes) {
+    const uint32_t lo = static_cast<uint32_t>(desc) + (bytes >> 4);
+    return (desc & 0xFFFFFFFF00000000ull) | lo;
+}
+
 // Descriptor of the same operand `bytes` further on (the start-address field
 // holds address / 16 in bits 0-13 and cannot carry within shared memory).
 __device__ __forceinline__ uint64_t sdesc_add(uint64_t desc, uint32_t bytes) {
