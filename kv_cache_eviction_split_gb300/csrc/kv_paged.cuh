@@ -101,6 +101,18 @@ constexpr int kShortFewRows = 128;
 constexpr int kManyTile = 128;     // keys per tile of the tensor-memory kernel
 constexpr int kManyRows = 256;     // query rows per item there: two tiles of 128
 constexpr int kManyCtas = 152;
+// The many-rows kernel takes the units in up to kMaxPhases groups, one after another, each
+// cut into runs over all CTAs: a group's rows (kPhaseBytes, where that gives few enough
+// groups) stay in L2 while all its items read them.
+constexpr int kMaxPhases = 4;
+// A phase is worth its merge (~10 us) from kPhaseTiles tiles a CTA on (~200 us).
+constexpr long long kPhaseBytes = 64ll << 20;
+constexpr int kPhaseTiles = 128;
+inline int many_phases(const DevPaged &C) {
+    const long long bytes = (long long)C.R * C.H * C.cap * C.d * 4;
+    const long long n = (bytes + kPhaseBytes - 1) / kPhaseBytes;
+    return (int)(n < 1 ? 1 : n < kMaxPhases ? n : kMaxPhases);
+}
 
 // Key tiles of 2^log2 rows that the queries at cache rows t_lo .. t_hi see: the
 // sinks' tiles [0, ns), then the window's from `first` on; `total` together, at least
@@ -129,7 +141,7 @@ struct CutItem {
     int unit, cta0, row0, rows;
 };
 
-// Partials: CTA b writes slot 2 b for an item begun by an earlier CTA and 2 b + 1 for
+// Partials: CTA b (counted on through the phases) writes slot 2 b for an item begun by an earlier CTA and 2 b + 1 for
 // one it begins and a later CTA ends.
 __device__ __forceinline__ int part_slot(int cta, bool begun_here) {
     return 2 * cta + (begun_here ? 1 : 0);
@@ -137,7 +149,7 @@ __device__ __forceinline__ int part_slot(int cta, bool begun_here) {
 
 // Workspace of the attention (all offsets 256-byte aligned).
 struct AttendWs {
-    CutItem *cut;              // [ctas] unit -1: no item ends here that an earlier CTA began
+    CutItem *cut;              // [ctas] (a set for each phase) unit -1: no item ends here that an earlier CTA began
     float2 *part_ml;           // [2 ctas][rows of an item] (m in log2 units, l)
     float *part_o;             // [2 ctas][rows of an item][d]
     // add_mass: log2 of the softmax sums of the query rows, and the rows themselves, in

@@ -225,12 +225,62 @@ __device__ __forceinline__ CtaRun cut_run(int units, int *s_tiles, P parts_of, F
     return R;
 }
 
+// Cuts the units, in order, into groups of equal rows (rows_of(v) of unit v), at least
+// `rows` each and no more groups than `phases`, or than leave each `work` (work_of(v) of
+// unit v).  Group g is units [first[g], first[g + 1]) (shared memory, phases + 1 words).
+// All kThreads threads call it.
+template <int kThreads, typename F, typename W>
+__device__ __forceinline__ void cut_units(int units, int phases, long long rows, long long work,
+                                          int *first, F rows_of, W work_of) {
+    constexpr int kWarps = kThreads / 32;
+    __shared__ long long warp_sums[kWarps], warp_work[kWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid <= phases) first[tid] = tid ? units : 0;
+    __syncthreads();
+    if (phases == 1) return;
+    const int chunk = (units + kThreads - 1) / kThreads;
+    const int v0 = min(units, tid * chunk), v1 = min(units, v0 + chunk);
+    long long mine = 0, load = 0;
+    for (int v = v0; v < v1; ++v) {
+        mine += rows_of(v);
+        load += work_of(v);
+    }
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+        load += __shfl_xor_sync(0xffffffffu, load, o);
+    }
+    if (lane == 31) {
+        warp_sums[warp] = incl;
+        warp_work[warp] = load;
+    }
+    __syncthreads();
+    long long at = incl - mine, total = 0, all = 0;
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) at += warp_sums[w];
+        total += warp_sums[w];
+        all += warp_work[w];
+    }
+    const long long groups = max(1ll, min((long long)phases, all / work));
+    const long long quota = max(rows, (total + groups - 1) / groups);
+    for (int v = v0; v < v1; ++v) {
+        const long long to = at + rows_of(v);
+        for (int g = 1; g < groups; ++g)
+            if (at < g * quota && g * quota <= to) first[g] = v + 1;
+        at = to;
+    }
+    __syncthreads();
+}
+
 // log2 of a row's softmax sum from its maximum (log2 units) and sum.
 __device__ __forceinline__ float row_lse2(float m, float l) {
     return l > 0.f ? m + __log2f(l) : -INFINITY;
 }
 
 // Merges the partials of the items that several CTAs held.  rows: row slots of a partial.
+// ctas: CTAs of the launch that left them, times its phases.
 cudaError_t launch_attend_merge(const DevPaged &C, const DevChunk &T, int layer,
                                 const AttendIo &io, float *lse2, const AttendWs &ws, int ctas,
                                 int rows, cudaStream_t s);

@@ -29,9 +29,9 @@ using namespace sm100;
 
 constexpr int kThreads = 12 * 32;
 constexpr int kKWarp = 0, kMmaWarp = 1, kVWarp = 2, kSchedWarp = 3, kRowWarp = 4;
-// Registers a thread after the split, of 168 at launch (384 x 168 = 128 x 104 + 256 x 200):
+// Registers a thread after the split, of 168 at launch (384 x 168 = 128 x 72 + 256 x 216):
 // a row thread holds its 128 logits.
-constexpr int kLoadRegs = 104, kRowRegs = 200;
+constexpr int kLoadRegs = 72, kRowRegs = 216;
 constexpr int kBlockBytes = 128 * 128;       // [128 rows][64 columns], 128 B swizzle
 constexpr uint32_t kOCol = 256;              // O of lane L at column kOCol + 128 L
 
@@ -47,9 +47,11 @@ struct Lane {
 };
 // An item and the part of it in this CTA's run, as the scheduler warp writes it.
 struct Item {
+    int cta;                   // this CTA, counted on through the phases
+    int cta0;                  // and the one that holds the item's first tile
     int v, h, n, count;        // unit of the layer, its head, rows held, new tokens
     int row0, rows;            // query rows
-    int at, x0, x1;            // first tile in the order of all; this run's tiles of the item
+    int x0, x1;                // this run's tiles of the item
     TileSpan span;
     int t_hi, lo, sinks;       // rows seen by any query: [0, sinks) and [lo, t_hi]
     int stop;                  // 1: the run has ended, nothing else is set
@@ -68,7 +70,10 @@ struct Layout {
     static constexpr int kBars = kV + kVSt * kOp;
     static constexpr int kNumBars = 2 * kKSt + 2 * kVSt + 10 + 1 + 2 * kItems;
     static constexpr int kMisc = (kBars + kNumBars * 8 + 15) / 16 * 16;
-    static constexpr int kDesc = kMisc + 32;
+    static constexpr int kCut = kMisc + 32;               // [kMaxPhases] CutItem
+    static constexpr int kRuns = kCut + kMaxPhases * (int)sizeof(CutItem);
+    static constexpr int kFirst = kRuns + (kMaxPhases * (int)sizeof(CtaRun) + 15) / 16 * 16;
+    static constexpr int kDesc = kFirst + 32;
     static constexpr int kTotal = kDesc + kItems * (int)sizeof(Item);
     static_assert(kTotal + 1024 <= 227 * 1024, "with cut_run's and TMEM's few static words");
 };
@@ -82,6 +87,7 @@ struct ManyArgs {
     float *part_o;
     float *lse2;               // null without add_mass, as is q_packed
     void *q_packed;
+    int phases;
 };
 
 __device__ __forceinline__ void make_item(Item &it, const DevPaged &C, const AttendMask &M,
@@ -155,13 +161,15 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     uint64_t *i_full = mma_done + 1, *i_empty = i_full + kItems;   // item descriptions
     volatile int *s_abort = reinterpret_cast<volatile int *>(smem + Ly::kMisc);
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + Ly::kMisc + 4);
-    CutItem *s_cut = reinterpret_cast<CutItem *>(smem + Ly::kMisc + 16);
+    CutItem *s_cut = reinterpret_cast<CutItem *>(smem + Ly::kCut);
+    CtaRun *s_run = reinterpret_cast<CtaRun *>(smem + Ly::kRuns);
+    int *s_first = reinterpret_cast<int *>(smem + Ly::kFirst);
     Item *s_item = reinterpret_cast<Item *>(smem + Ly::kDesc);
 
     if (threadIdx.x == 0) {
         *s_abort = (smem_u32(smem) & 1023u) ? 1 : 0;
         if (*s_abort) post_status(C.status, KV_ERR_UNSUPPORTED);
-        *s_cut = CutItem{-1, 0, 0, 0};
+        for (int g = 0; g < kMaxPhases; ++g) s_cut[g] = CutItem{-1, 0, 0, 0};
         for (int s = 0; s < Ly::kKSt; ++s) {
             mbar_init(&k_full[s], 1);
             mbar_init(&k_empty[s], 1);
@@ -189,10 +197,31 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     pdl_wait();
     pdl_trigger();
     const uint32_t tmem = tmem_acquire_all(s_tmem);
-    const CtaRun run = cut_run<kThreads>(
-        C.R * C.H, reinterpret_cast<int *>(smem),
-        [&](int v) { return unit_items(C, T, unit_rows(C, T, A.layer, v)); },
-        [&](int v, int i) { return item_tiles(C, A.M, unit_rows(C, T, A.layer, v), i); });
+    // the phases' units, and this CTA's run in each
+    cut_units<kThreads>(
+        C.R * C.H, A.phases, kPhaseBytes / (D * 4), (long long)kManyCtas * kPhaseTiles, s_first,
+        [&](int v) {
+            const UnitRows U = unit_rows(C, T, A.layer, v);
+            return many_rows(C, T, U) ? U.n : 0;
+        },
+        [&](int v) {
+            const UnitRows U = unit_rows(C, T, A.layer, v);
+            const int items = unit_items(C, T, U);
+            return items ? (long long)items * item_tiles(C, A.M, U, items / 2) : 0ll;
+        });
+    for (int g = 0; g < A.phases; ++g) {
+        const int u0 = s_first[g], units = s_first[g + 1] - u0;
+        CtaRun run{};
+        if (units > 0)
+            run = cut_run<kThreads>(
+                units, reinterpret_cast<int *>(smem),
+                [&](int v) { return unit_items(C, T, unit_rows(C, T, A.layer, u0 + v)); },
+                [&](int v, int i) {
+                    return item_tiles(C, A.M, unit_rows(C, T, A.layer, u0 + v), i);
+                });
+        if (threadIdx.x == 0) s_run[g] = run;
+        __syncthreads();
+    }
     bool ok = *s_abort == 0;
 
     // Item i of the run for the roles (one lane or a whole warp waits); null at its end or
@@ -215,44 +244,65 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         const uint32_t o_base = tmem + lane_addr + kOCol + 128 * L;
         const float cs = A.M.scale_log2;
         int kc = 0, sc = 0, ic = 0;
-        for (int i = 0;; ++i) {
-            const Item *w = item(i, ok);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok || !w) break;
+        // This thread's row of an item.
+        struct Row {
+            bool valid, any;           // a row of the lane; the lane sees a tile of the run
+            int t, head, row;          // its query's cache row, query head, row of the unit
+            long long tok, prow0;
+        };
+        auto row_of = [&](const Item *w) {
+            Row r;
+            const int ns = w->lane[L].ns, x0 = w->x0, x1 = w->x1;
+            r.row = w->row0 + L * 128 + rr;
+            r.valid = rr < w->lane[L].rows;
+            const int token = r.row / C.G;
+            r.tok = w->tok0 + token;
+            r.head = w->h * C.G + r.row - token * C.G;
+            r.t = r.valid ? w->n - w->count + token : -1;
+            r.prow0 = w->prow0;
+            r.any = x0 < min(ns, x1) || max(x0, w->lane[L].a) < min(x1, w->lane[L].b);
+            return r;
+        };
+        auto load_q = [&](const Row &r, uint4 (&q)[D / 8]) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(
+                static_cast<const typename E::T *>(A.io.q) + r.tok * A.io.q_stride +
+                (long long)r.head * D);
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) q[c] = r.valid ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+        };
+        // Q into shared memory for the products, once those of the item before are done
+        auto store_q = [&](const Row &r, const Item *w, const uint4 (&q)[D / 8]) {
+            uint8_t *qs = smem + Ly::kQ + L * Ly::kOp + rr * 128;
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c)
+                *reinterpret_cast<uint4 *>(qs + (c >> 3) * kBlockBytes +
+                                           (((c & 7) ^ (rr & 7)) << 4)) = q[c];
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_full[L]);
+            if (A.q_packed && r.valid && w->x0 <= (w->lane[L].ns ? 0 : w->lane[L].a)) {
+                // the weights' pass takes the rows by TMA; one CTA of a cut item writes them
+                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<typename E::T *>(A.q_packed) +
+                                                       (r.prow0 + r.row) * D);
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) dst[c] = q[c];
+            }
+        };
+        const Item *w = item(0, ok);
+        ok = __all_sync(0xffffffffu, ok);
+        Row cur{}, nxt{};
+        if (ok && w) {
+            cur = row_of(w);
+            if (cur.any) {
+                uint4 q[D / 8];
+                load_q(cur, q);
+                store_q(cur, w, q);
+            }
+        }
+        for (int i = 0; ok && w; ++i) {
             const Lane me = w->lane[L], other = w->lane[1 - L];
             const TileSpan span = w->span;
-            const int x0 = w->x0, x1 = w->x1;
-            const int row = w->row0 + L * 128 + rr;
-            const bool valid = rr < me.rows;
-            const long long tok = w->tok0 + row / C.G;
-            const int head = w->h * C.G + row % C.G;
-            const int t = valid ? w->n - w->count + row / C.G : -1;
-            const long long prow0 = w->prow0;
-            // does the lane see any tile of this run?
-            const bool any = x0 < min(me.ns, x1) || max(x0, me.a) < min(x1, me.b);
-            if (any) {
-                uint8_t *qs = smem + Ly::kQ + L * Ly::kOp + rr * 128;
-                const uint4 *src = reinterpret_cast<const uint4 *>(
-                    static_cast<const typename E::T *>(A.io.q) + tok * A.io.q_stride +
-                    (long long)head * D);
-                uint4 q[D / 8];
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c) q[c] = valid ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c)
-                    *reinterpret_cast<uint4 *>(qs + (c >> 3) * kBlockBytes +
-                                               (((c & 7) ^ (rr & 7)) << 4)) = q[c];
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&q_full[L]);
-                if (A.q_packed && valid && x0 <= (me.ns ? 0 : me.a)) {
-                    // the weights' pass takes the rows by TMA; one CTA of a cut item writes them
-                    uint4 *dst = reinterpret_cast<uint4 *>(
-                        static_cast<typename E::T *>(A.q_packed) + (prow0 + row) * D);
-#pragma unroll
-                    for (int c = 0; c < D / 8; ++c) dst[c] = q[c];
-                }
-            }
+            const int x0 = w->x0, x1 = w->x1, cta = w->cta, t = cur.t;
             float m = -INFINITY, l = 0.f;
             bool begun = false;
             for (int x = x0; x < x1; ++x) {
@@ -360,10 +410,21 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             // ---- the item's end: finished rows, or this run's part of them
             const bool whole = x0 == 0 && x1 == span.total;
             if (L == 0 && rr == 0 && x0 > 0 && x1 == span.total)
-                *s_cut = CutItem{w->v, w->at / run.per, w->row0, w->rows};
+                s_cut[cta / kManyCtas] = CutItem{w->v, w->cta0, w->row0, w->rows};
             // the description is read
             __syncwarp();
             if (lane == 0) mbar_arrive(&i_empty[i % kItems]);
+            // The next item's Q is read from memory while this one's last products run, and
+            // handed over before this one's output is written.
+            w = item(i + 1, ok);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            uint4 q[D / 8];
+            nxt.any = false;
+            if (w) {
+                nxt = row_of(w);
+                if (nxt.any) load_q(nxt, q);
+            }
             if (begun) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&o_final[L], (uint32_t)(ic & 1), s_abort,
                                                        C.wait_ns));
@@ -371,12 +432,13 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                 tc_fence_after();
                 ++ic;
             }
+            if (nxt.any) store_q(nxt, w, q);
             const float mm = m - E::kShift;
             const long long prow =
-                (long long)part_slot(blockIdx.x, x0 == 0) * kManyRows + L * 128 + rr;
+                (long long)part_slot(cta, x0 == 0) * kManyRows + L * 128 + rr;
             const float inv = l > 0.f ? 1.f / l : 0.f;
-            typename E::T *op = static_cast<typename E::T *>(A.io.out) + tok * A.io.out_stride +
-                                (long long)head * D;
+            typename E::T *op = static_cast<typename E::T *>(A.io.out) + cur.tok * A.io.out_stride +
+                                (long long)cur.head * D;
             float *pp = A.part_o + prow * D;
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
@@ -388,7 +450,7 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                     tmem_ld_wait();
                     reg_fence(o);
                 }
-                if (!valid) continue;
+                if (!cur.valid) continue;
                 if (whole) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 8)
@@ -409,13 +471,14 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&o_empty[L]);
             }
-            if (valid) {
+            if (cur.valid) {
                 if (whole) {
                     const float z = row_lse2(mm, l);
-                    if (A.io.lse) A.io.lse[tok * C.Hq + head] = z * kLn2;
-                    if (A.lse2) A.lse2[prow0 + row] = z;
+                    if (A.io.lse) A.io.lse[cur.tok * C.Hq + cur.head] = z * kLn2;
+                    if (A.lse2) A.lse2[cur.prow0 + cur.row] = z;
                 } else A.part_ml[prow] = make_float2(begun ? mm : -INFINITY, l);
             }
+            cur = nxt;
         }
         if (!ok && lane == 0) {
             *s_abort = 1;
@@ -426,40 +489,38 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         if (warp == kSchedWarp) {
             // ---------------------------------------------------------------- scheduler
             if (lane == 0 && ok) {
-                int v = run.unit, at = run.part_begin, i = 0, pair = run.part;
-                for (;;) {
-                    // units from the run's first part on; after the last, the end mark
-                    const bool end = at >= run.end;
-                    UnitRows U;
-                    int pairs = pair + 1;
-                    if (!end) {
-                        U = unit_rows(C, T, A.layer, v);
-                        pairs = unit_items(C, T, U);
+                int i = 0;
+                auto put = [&](const Item &next) {
+                    ok = mbar_wait(&i_empty[i % kItems], (uint32_t)((i / kItems) & 1) ^ 1u, s_abort,
+                                   C.wait_ns);
+                    if (!ok) return;
+                    s_item[i % kItems] = next;
+                    mbar_arrive(&i_full[i % kItems]);
+                    ++i;
+                };
+                Item next;
+                next.stop = 0;
+                for (int g = 0; ok && g < A.phases; ++g) {
+                    const CtaRun run = s_run[g];
+                    int at = run.part_begin, pair = run.part;
+                    for (int v = s_first[g] + run.unit; ok && at < run.end; ++v, pair = 0) {
+                        const UnitRows U = unit_rows(C, T, A.layer, v);
+                        const int pairs = unit_items(C, T, U);
                         if (pairs && !U.ok) post_status(C.status, KV_ERR_INVALID_ARG);
-                    }
-                    for (; ok && pair < pairs && (end || at < run.end); ++pair) {
-                        Item next;
-                        next.stop = end;
-                        if (!end) {
+                        for (; ok && pair < pairs && at < run.end; ++pair) {
                             make_item(next, C, A.M, U, pair);
                             next.v = v;
-                            next.at = at;
+                            next.cta = g * kManyCtas + blockIdx.x;
+                            next.cta0 = g * kManyCtas + at / run.per;
                             next.x0 = max(run.begin - at, 0);
                             next.x1 = min(next.span.total, run.end - at);
                             at += next.span.total;
-                            if (next.x0 >= next.x1) continue;
+                            put(next);
                         }
-                        ok = mbar_wait(&i_empty[i % kItems], (uint32_t)((i / kItems) & 1) ^ 1u, s_abort,
-                                       C.wait_ns);
-                        if (!ok) break;
-                        s_item[i % kItems] = next;
-                        mbar_arrive(&i_full[i % kItems]);
-                        ++i;
                     }
-                    if (end || !ok) break;
-                    pair = 0;
-                    ++v;
                 }
+                next.stop = 1;
+                if (ok) put(next);
                 if (!ok) {
                     *s_abort = 1;
                     post_status(C.status, KV_ERR_TIMEOUT);
@@ -637,7 +698,7 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     __syncthreads();
     tc_fence_after();
     tmem_release_all(tmem);
-    if (threadIdx.x == 0) A.cut[blockIdx.x] = *s_cut;
+    if (threadIdx.x < A.phases) A.cut[threadIdx.x * kManyCtas + blockIdx.x] = s_cut[threadIdx.x];
 }
 
 template <typename E, int D>
@@ -653,7 +714,8 @@ cudaError_t many(const DevPaged &C, const DevChunk &T, const ManyArgs &A, const 
         e = launch_dependent(many_kernel<E, D>, dim3(kManyCtas), kThreads, Ly::kTotal, s, mk, mv, C,
                              T, A);
     if (e == cudaSuccess)
-        e = launch_attend_merge(C, T, A.layer, A.io, A.lse2, ws, kManyCtas, kManyRows, s);
+        e = launch_attend_merge(C, T, A.layer, A.io, A.lse2, ws, kManyCtas * A.phases, kManyRows,
+                                s);
     return e;
 }
 
@@ -662,7 +724,8 @@ cudaError_t many(const DevPaged &C, const DevChunk &T, const ManyArgs &A, const 
 cudaError_t launch_attend_many(const DevPaged &C, const DevChunk &T, int layer, const AttendMask &M,
                                const AttendIo &io, bool add_mass, const AttendWs &ws,
                                cudaStream_t s) {
-    const ManyArgs A{layer, M, io, ws.cut, ws.part_ml, ws.part_o, ws.lse2, ws.q_packed};
+    const ManyArgs A{layer, M, io, ws.cut, ws.part_ml, ws.part_o, ws.lse2, ws.q_packed,
+                     many_phases(C)};
     if (C.dtype == KV_FP16)
         return C.d == 64 ? many<Fp16, 64>(C, T, A, ws, s)
                          : many<Fp16, 128>(C, T, A, ws, s);
