@@ -128,13 +128,14 @@ struct CtaRun {
     int total;
 };
 
-// Cuts the tiles of all units of the layer into gridDim.x equal runs.  A unit v consists
-// of parts_of(v) parts and part i of tiles_of(v, i) tiles.  All kThreads threads call it:
-// a warp sums up a unit (a thread, where there are more units than threads), and a warp
-// finds the run's first part.  s_tiles: kThreads words of shared memory (TMA may write
-// there afterwards).
-template <int kThreads, typename P, typename F>
-__device__ __forceinline__ CtaRun cut_run(int units, int *s_tiles, P parts_of, F tiles_of) {
+// Cuts the tiles of all units of the layer into gridDim.x equal runs.  unit(v) reads what
+// is needed of unit v; it consists of parts_of(unit) parts, part i of tiles_of(unit, i)
+// tiles.  All kThreads threads call it: a thread sums up its units, or a warp one unit
+// where there are few, and a warp finds the run's first part.  s_tiles: kThreads words of
+// shared memory (TMA may write there afterwards).
+template <int kThreads, typename U, typename P, typename F>
+__device__ __forceinline__ CtaRun cut_run(int units, int *s_tiles, U unit, P parts_of,
+                                          F tiles_of) {
     constexpr int kWarps = kThreads / 32;
     __shared__ int warp_sums[kWarps];
     __shared__ int found[3];
@@ -143,16 +144,18 @@ __device__ __forceinline__ CtaRun cut_run(int units, int *s_tiles, P parts_of, F
     const int v0 = min(units, tid * chunk), v1 = min(units, v0 + chunk);
     auto unit_tiles = [&](int v) {
         int sum = 0;
-        const int n = parts_of(v);
-        for (int i = 0; i < n; ++i) sum += tiles_of(v, i);
+        const auto u = unit(v);
+        const int n = parts_of(u);
+        for (int i = 0; i < n; ++i) sum += tiles_of(u, i);
         return sum;
     };
     int mine = 0;
-    if (chunk <= 1) {
+    if (units <= 2 * kWarps) {
         for (int v = warp; v < units; v += kWarps) {
             int sum = 0;
-            const int n = parts_of(v);
-            for (int i = lane; i < n; i += 32) sum += tiles_of(v, i);
+            const auto u = unit(v);
+            const int n = parts_of(u);
+            for (int i = lane; i < n; i += 32) sum += tiles_of(u, i);
             sum = __reduce_add_sync(0xffffffffu, sum);
             if (lane == 0) s_tiles[v] = sum;
         }
@@ -197,10 +200,11 @@ __device__ __forceinline__ CtaRun cut_run(int units, int *s_tiles, P parts_of, F
     }
     R.unit = found[0];
     if (warp == 0) {
-        const int n = parts_of(R.unit);
+        const auto u = unit(R.unit);
+        const int n = parts_of(u);
         int at = found[2];
         for (int i0 = 0; i0 < n; i0 += 32) {
-            const int t = i0 + lane < n ? tiles_of(R.unit, i0 + lane) : 0;
+            const int t = i0 + lane < n ? tiles_of(u, i0 + lane) : 0;
             int x = t;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {

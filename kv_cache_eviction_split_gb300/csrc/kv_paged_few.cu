@@ -164,10 +164,9 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
     if constexpr (kCluster == 0) {
         run = cut_run<kThreads>(
             units, reinterpret_cast<int *>(smem),
-            [&](int v) { return (int)few_rows(C, T, unit_rows(C, T, A.layer, v)); },
-            [&](int v, int) {
-                return FewItem(C, A.M, unit_rows(C, T, A.layer, v), 0, kRows).span.total;
-            });
+            [&](int v) { return unit_rows(C, T, A.layer, v); },
+            [&](const UnitRows &U) { return (int)few_rows(C, T, U); },
+            [&](const UnitRows &U, int) { return FewItem(C, A.M, U, 0, kRows).span.total; });
     } else {
         // one item a cluster: its tiles are the whole order, each CTA's run a part of them
         rank = (int)(blockIdx.x % kCluster);

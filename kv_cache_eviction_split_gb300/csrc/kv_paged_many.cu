@@ -215,10 +215,9 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         if (units > 0)
             run = cut_run<kThreads>(
                 units, reinterpret_cast<int *>(smem),
-                [&](int v) { return unit_items(C, T, unit_rows(C, T, A.layer, u0 + v)); },
-                [&](int v, int i) {
-                    return item_tiles(C, A.M, unit_rows(C, T, A.layer, u0 + v), i);
-                });
+                [&](int v) { return unit_rows(C, T, A.layer, u0 + v); },
+                [&](const UnitRows &U) { return unit_items(C, T, U); },
+                [&](const UnitRows &U, int i) { return item_tiles(C, A.M, U, i); });
         if (threadIdx.x == 0) s_run[g] = run;
         __syncthreads();
     }

@@ -126,9 +126,9 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     // that its first step lies in
     const CtaRun run = cut_run<kThreads>(
         C.R * C.H, reinterpret_cast<int *>(smem),
-        [&](int v) { return Groups(C, T, unit_rows(C, T, A.layer, v)).groups; },
-        [&](int v, int i) {
-            const UnitRows U = unit_rows(C, T, A.layer, v);
+        [&](int v) { return unit_rows(C, T, A.layer, v); },
+        [&](const UnitRows &U) { return Groups(C, T, U).groups; },
+        [&](const UnitRows &U, int i) {
             int r0, r1;
             Groups(C, T, U).range(C, A.M, U.n, i, r0, r1);
             return r1 - r0;
