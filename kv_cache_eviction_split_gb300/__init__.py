@@ -194,14 +194,29 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+_raw = None
+
+
+def _raw_calls():
+    """(current device, handle of its current stream) as functions: torch's own, without the
+    Stream object, which costs as much as a launch."""
+    global _raw
+    if _raw is None:
+        import torch
+        handle = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        device = getattr(torch._C, "_cuda_getDevice", None)
+        if handle is None or device is None:
+            handle = lambda index: torch.cuda.current_stream(index).cuda_stream  # noqa: E731
+            device = torch.cuda.current_device
+        torch.cuda.current_device()              # initialises CUDA
+        _raw = device, handle
+    return _raw
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        # the handle alone, where torch offers it: a Stream object costs as much as a launch
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is not None:
-            return raw(torch.cuda.current_device())
-        return torch.cuda.current_stream().cuda_stream
+        device, handle = _raw or _raw_calls()
+        return handle(device())
     return getattr(stream, "cuda_stream", stream)
 
 
@@ -761,6 +776,7 @@ class Chunk:
         self.cu_dev = torch.from_numpy(self.cu_host).to(device)
         self.counts = torch.from_numpy(host.astype(np.int32)).to(device)
         self.num_requests, self.tokens = len(host), int(self.cu_host[-1])
+        self._index = self.cu_dev.get_device()
         self._c = _KvChunk(self.cu_host.ctypes.data_as(ctypes.POINTER(ctypes.c_int64)),
                            self.cu_dev.data_ptr())
         self._ref = ctypes.byref(self._c)
@@ -772,9 +788,8 @@ class Chunk:
 
 def _on_current_device(cache: PagedCache, *others) -> None:
     """The library works on the current device: its tensors have to be there."""
-    import torch
     index = cache._index
-    if index >= 0 and index != torch.cuda.current_device():
+    if index >= 0 and index != (_raw or _raw_calls())[0]():
         raise ValueError("the cache is on %s, which is not the current device" % cache.device)
     for t in others:
         if t is not None and t.get_device() != index:
@@ -792,20 +807,24 @@ def _token_stride(cache: PagedCache, chunk: Chunk, t, heads: int, name: str) -> 
     return s0 if n > 1 else heads * d
 
 
-def _same_requests(cache: PagedCache, chunk: Chunk) -> None:
+def _check_chunk(cache: PagedCache, chunk: Chunk) -> None:
     if chunk.num_requests != cache.num_requests:
         raise ValueError("the chunk has %d requests, the cache %d"
                          % (chunk.num_requests, cache.num_requests))
+    if chunk._index != cache._index:
+        raise ValueError("the chunk is on %s, the cache on %s" % (chunk.cu_dev.device, cache.device))
 
 
 def kv_paged_append(cache: PagedCache, chunk: Chunk, layer: int, k_new, v_new, stream=None):
     """New tokens' K and V rows [tokens][kv_heads][head_dim] of one layer into the pages."""
-    _same_requests(cache, chunk)
+    _check_chunk(cache, chunk)
     ks = _token_stride(cache, chunk, k_new, cache.num_kv_heads, "k_new")
     vs = _token_stride(cache, chunk, v_new, cache.num_kv_heads, "v_new")
-    _on_current_device(cache, k_new, v_new, chunk.cu_dev)
-    _check(load().kv_paged_append(cache.c, chunk.c, int(layer), k_new.data_ptr(), ks,
-                                  v_new.data_ptr(), vs, _stream(stream)), "kv_paged_append")
+    _on_current_device(cache, k_new, v_new)
+    code = (_lib or load()).kv_paged_append(cache._ref, chunk._ref, layer, k_new.data_ptr(), ks,
+                                            v_new.data_ptr(), vs, _stream(stream))
+    if code:
+        raise KvError(code, "kv_paged_append")
 
 
 def kv_paged_load(cache: PagedCache, k_rows, v_rows, offsets_dev, total_rows: int, mass_rows=None,
@@ -844,14 +863,14 @@ def kv_paged_attention(cache: PagedCache, chunk: Chunk, layer: int, q, out, work
     add_mass: adds every row's attention weights to cache.mass."""
     import torch
     heads = cache.num_q_heads
-    _same_requests(cache, chunk)
+    _check_chunk(cache, chunk)
     qs = _token_stride(cache, chunk, q, heads, "q")
     os_ = _token_stride(cache, chunk, out, heads, "out")
     if lse is not None and (lse.dtype is not torch.float32 or not lse.is_contiguous() or
                             lse.shape != (chunk.tokens, heads)):
         raise ValueError("lse: float32 [%d][%d]" % (chunk.tokens, heads))
-    _on_current_device(cache, q, out, lse, workspace, chunk.cu_dev)
-    code = load().kv_paged_attention(
+    _on_current_device(cache, q, out, lse, workspace)
+    code = (_lib or load()).kv_paged_attention(
         cache._ref, chunk._ref, layer, window, num_sinks,
         cache._scale if softmax_scale is None else softmax_scale, q.data_ptr(), qs,
         out.data_ptr(), os_, _ptr(lse), int(add_mass), workspace.data_ptr(), workspace.nbytes,
