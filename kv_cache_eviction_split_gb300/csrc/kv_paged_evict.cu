@@ -9,9 +9,8 @@
 // of a cluster of 8 (up to 131072 rows; longer slices are re-read), and the three digit
 // passes (11, 11 and 10 bits) count from there; a cluster's counts are added bin range by
 // bin range through distributed shared memory.  The passes are bound by latencies
-// (cluster barriers, remote reads), the gather by HBM: with clusters a block moves its own
-// kept rows, so that one cluster's passes overlap the copies of the others on its SMs;
-// with one block a unit, a second kernel spreads the rows evenly over the SMs.
+// (cluster barriers, remote reads), the gather by HBM: it is a kernel of its own, which
+// spreads the rows evenly over the SMs.
 #include <cooperative_groups.h>
 
 #include "kv_compact.cuh"
@@ -93,11 +92,10 @@ __device__ __forceinline__ void gather_rows(const DevPaged &S, const DevPaged &Q
     }
 }
 
-// One unit by a block of kT threads (kCluster = 1) or a cluster of such blocks, which also
-// move their rows (D: head dim; 0 leaves them to evict_gather_kernel).  Rows are dealt to
-// blocks in equal consecutive slices, which a block walks in rounds of kT * kKeys rows (one,
-// where the slice fits: its keys are loaded once).
-template <int kT, int kKeys, int kCluster, int D>
+// One unit by a block of kT threads (kCluster = 1) or a cluster of such blocks.  Rows are
+// dealt to blocks in equal consecutive slices, which a block walks in rounds of kT * kKeys
+// rows (one, where the slice fits: its keys are loaded once).
+template <int kT, int kKeys, int kCluster>
 __global__ void __launch_bounds__(kT, kCluster > 1 ? 2 : 1)
 evict_select_kernel(const DevPaged S, const DevPaged Q, const EvictArgs A) {
     constexpr int kRound = kT * kKeys;
@@ -111,9 +109,6 @@ evict_select_kernel(const DevPaged S, const DevPaged Q, const EvictArgs A) {
     auto sync_all = [&]() {
         if constexpr (kCluster > 1) cg::this_cluster().sync();
         else __syncthreads();
-    };
-    auto gather = [&](int i0, int i1) {
-        if constexpr (D > 0) gather_rows<D, kT / 32>(S, Q, A, u, i0, i1);
     };
     int n;
     const bool len_ok = unit_len(S, u, n);
@@ -136,8 +131,6 @@ evict_select_kernel(const DevPaged S, const DevPaged Q, const EvictArgs A) {
         const int part = ((int)keep + kCluster - 1) / kCluster;
         const int i0 = min((int)keep, rank * part), i1 = min((int)keep, i0 + part);
         for (int i = i0 + tid; i < i1; i += kT) out[i] = n <= b || i < A.sinks ? i : n - (int)b + i;
-        __syncthreads();
-        gather(i0, i1);
         return;
     }
     if (rank == 0)
@@ -308,7 +301,6 @@ evict_select_kernel(const DevPaged S, const DevPaged Q, const EvictArgs A) {
         eq = __reduce_add_sync(0xffffffffu, eq);
         at = x0 + min(eq, need);
     }
-    const unsigned at0 = at;
     for (int r0 = lo; r0 < hi; r0 += kRound) {
         if (!held) {
             load(r0);
@@ -333,12 +325,7 @@ evict_select_kernel(const DevPaged S, const DevPaged Q, const EvictArgs A) {
         at += (total & 0xffffu) + min(total >> 16, left);
         eq += total >> 16;
     }
-    if constexpr (kCluster > 1) {
-        sync_all();                               // no block leaves while its counts are read
-        // this block's kept rows, and the pinned ones beside them
-        gather(rank == 0 ? 0 : first + (int)min(at0, k),
-               rank == kCluster - 1 ? (int)b : first + (int)min(at, k));
-    }
+    if constexpr (kCluster > 1) sync_all();       // no block leaves while its counts are read
 }
 
 constexpr int kWarps = 8;
@@ -352,12 +339,12 @@ evict_gather_kernel(const DevPaged S, const DevPaged Q, const EvictArgs A, long 
     gather_rows<D, kWarps>(S, Q, A, u, i0, min(Q.lens[u], i0 + kWarps * 32));
 }
 
-template <int kT, int kKeys, int kCluster, int D>
+template <int kT, int kKeys, int kCluster>
 cudaError_t launch_select(const DevPaged &S, const DevPaged &Q, const EvictArgs &A,
                           cudaStream_t s) {
     constexpr int kSmem = (kT * kKeys + kT * kKeys / 32 + kT) * 4;   // keys, a word a thread
     static_assert(kT * kKeys <= 32768, "counts of a round are 16-bit");
-    auto kernel = evict_select_kernel<kT, kKeys, kCluster, D>;
+    auto kernel = evict_select_kernel<kT, kKeys, kCluster>;
     cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
@@ -382,11 +369,9 @@ cudaError_t launch_paged_evict(const DevPaged &S, const DevPaged &D, const int32
                                int *status, cudaStream_t s) {
     const EvictArgs A{budgets, sinks, recent, kept, kept_stride, status};
     // the smallest shape that holds the longest possible unit in shared memory
-    if (S.cap > 16384)
-        return S.d == 64 ? launch_select<512, 32, 8, 64>(S, D, A, s)
-                         : launch_select<512, 32, 8, 128>(S, D, A, s);
-    cudaError_t e = S.cap <= 4096 ? launch_select<256, 16, 1, 0>(S, D, A, s)
-                                  : launch_select<512, 32, 1, 0>(S, D, A, s);
+    cudaError_t e = S.cap <= 4096    ? launch_select<256, 16, 1>(S, D, A, s)
+                    : S.cap <= 16384 ? launch_select<512, 32, 1>(S, D, A, s)
+                                     : launch_select<512, 32, 8>(S, D, A, s);
     const long long most = kept_stride < D.cap ? kept_stride : D.cap;
     const unsigned gx = (unsigned)((most + kWarps * 32 - 1) / (kWarps * 32));
     // grid.y is limited to 65535 units a launch
