@@ -150,6 +150,7 @@ __device__ __forceinline__ int part_slot(int cta, bool begun_here) {
 // Workspace of the attention (all offsets 256-byte aligned).
 struct AttendWs {
     CutItem *cut;              // [ctas] (a set for each phase) unit -1: no item ends here that an earlier CTA began
+    int *unit_cut;             // [R * H] few rows: the CTA whose `cut` is the unit's, or -1
     float2 *part_ml;           // [2 ctas][rows of an item] (m in log2 units, l)
     float *part_o;             // [2 ctas][rows of an item][d]
     // add_mass: log2 of the softmax sums of the query rows, and the rows themselves, in

@@ -283,11 +283,34 @@ __device__ __forceinline__ float row_lse2(float m, float l) {
     return l > 0.f ? m + __log2f(l) : -INFINITY;
 }
 
-// Merges the partials of the items that several CTAs held.  rows: row slots of a partial.
-// ctas: CTAs of the launch that left them, times its phases.
-cudaError_t launch_attend_merge(const DevPaged &C, const DevChunk &T, int layer,
-                                const AttendIo &io, float *lse2, const AttendWs &ws, int ctas,
-                                int rows, cudaStream_t s);
+// Writes a merged row of an item (a warp, D / 32 elements of the sum a lane).
+template <typename X, int D>
+__device__ __forceinline__ void store_merged(const DevPaged &C, const DevChunk &T, int layer,
+                                             const AttendIo &io, float *lse2, const CutItem &it,
+                                             int row, float m, float l, const float (&acc)[D / 32]) {
+    constexpr int kV = D / 32;
+    const int lane = threadIdx.x & 31;
+    const UnitRows U = unit_rows(C, T, layer, it.unit);
+    const long long tok = U.tok0 + (it.row0 + row) / C.G;
+    const int head = U.h * C.G + (it.row0 + row) % C.G;
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    typename X::T *op = static_cast<typename X::T *>(io.out) + tok * io.out_stride +
+                        (long long)head * D + lane * kV;
+    static_assert(kV == 2 || kV == 4, "two or four elements a lane");
+#pragma unroll
+    for (int i = 0; i < kV; i += 2)
+        *reinterpret_cast<uint32_t *>(op + i) = X::pack(acc[i] * inv, acc[i + 1] * inv);
+    if (lane == 0) {
+        const float z = row_lse2(m, l);
+        if (io.lse) io.lse[tok * C.Hq + head] = z * kLn2;
+        if (lse2) lse2[packed_row(C, U, it.row0 + row)] = z;
+    }
+}
+
+// Merges the many-rows kernel's partials of the items that several CTAs held.  ctas: CTAs
+// of the launch that left them, times its phases.
+cudaError_t launch_many_merge(const DevPaged &C, const DevChunk &T, int layer, const AttendIo &io,
+                              float *lse2, const AttendWs &ws, int ctas, cudaStream_t s);
 // Requests of at most T.few_max query rows a head: `items` items of at most kFewRows rows
 // in all, the largest with max_rows, `blocks` of them at most to a unit.
 cudaError_t launch_attend_few(const DevPaged &C, const DevChunk &T, int layer, const AttendMask &M,

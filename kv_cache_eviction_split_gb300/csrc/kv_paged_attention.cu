@@ -9,88 +9,11 @@ namespace kvevict {
 namespace {
 
 // ---------------------------------------------------------------------------
-// Merge of cut items.  The CTA that held an item's last tile left its description; block
-// (b, y) merges rows of the item of slot b.  Partials are added in order: the result does
-// not depend on timing.  A partial that saw nothing (m = -inf) has no output written.
+// Merge of the many-rows kernel's cut items.  The CTA that held an item's last tile left
+// its description; block (b, y) merges rows of the item of slot b.  Partials are added in
+// order: the result does not depend on timing.  A partial that saw nothing (m = -inf) has
+// no output written.
 // ---------------------------------------------------------------------------
-template <typename X, int D>
-__device__ __forceinline__ void store_merged(const DevPaged &C, const DevChunk &T, int layer,
-                                             const AttendIo &io, float *lse2, const CutItem &it,
-                                             int row, float m, float l, const float (&acc)[D / 32]) {
-    constexpr int kV = D / 32;
-    const int lane = threadIdx.x & 31;
-    const UnitRows U = unit_rows(C, T, layer, it.unit);
-    const long long tok = U.tok0 + (it.row0 + row) / C.G;
-    const int head = U.h * C.G + (it.row0 + row) % C.G;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    typename X::T *op = static_cast<typename X::T *>(io.out) + tok * io.out_stride +
-                        (long long)head * D + lane * kV;
-    static_assert(kV == 2 || kV == 4, "two or four elements a lane");
-#pragma unroll
-    for (int i = 0; i < kV; i += 2)
-        *reinterpret_cast<uint32_t *>(op + i) = X::pack(acc[i] * inv, acc[i + 1] * inv);
-    if (lane == 0) {
-        const float z = row_lse2(m, l);
-        if (io.lse) io.lse[tok * C.Hq + head] = z * kLn2;
-        if (lse2) lse2[packed_row(C, U, it.row0 + row)] = z;
-    }
-}
-
-// Few rows, up to 304 partials: a row a block, its warps taking every fourth partial.
-template <typename X, int D>
-__global__ void __launch_bounds__(128)
-merge_few_kernel(const DevPaged C, const DevChunk T, int layer, const AttendIo io, float *lse2,
-                 const CutItem *__restrict__ cut, const float2 *__restrict__ part_ml,
-                 const float *__restrict__ part_o) {
-    constexpr int kV = D / 32;
-    __shared__ float sm_o[4][D], sm_w[kFewCtas], sm_l[4];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    pdl_wait();
-    pdl_trigger();
-    const CutItem it = cut[blockIdx.x];
-    const int row = blockIdx.y;
-    if (it.unit < 0 || row >= it.rows) return;
-    const int parts = (int)blockIdx.x - it.cta0 + 1;
-    auto slot_row = [&](int p) {
-        return (long long)part_slot(it.cta0 + p, p == 0) * kFewRows + row;
-    };
-    // the partials' weights 2^(m_p - m)
-    float m = -INFINITY, l = 0.f;
-    for (int p = lane; p < parts; p += 32) m = fmaxf(m, part_ml[slot_row(p)].x);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    for (int p = threadIdx.x; p < parts; p += 128) {
-        const float2 ml = part_ml[slot_row(p)];
-        sm_w[p] = shrink(ml.x, m);
-        l += ml.y * sm_w[p];
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if (lane == 0) sm_l[warp] = l;
-    __syncthreads();
-    l = (sm_l[0] + sm_l[1]) + (sm_l[2] + sm_l[3]);
-    float acc[kV] = {};
-#pragma unroll 8
-    for (int p = warp; p < parts; p += 4) {
-        const float f = sm_w[p];
-        const float *src = part_o + slot_row(p) * D + lane * kV;
-#pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            const float x = src[i];
-            acc[i] += f == 0.f ? 0.f : x * f;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < kV; ++i) sm_o[warp][lane * kV + i] = acc[i];
-    __syncthreads();
-    if (warp) return;
-#pragma unroll
-    for (int k = 1; k < 4; ++k)
-#pragma unroll
-        for (int i = 0; i < kV; ++i) acc[i] += sm_o[k][lane * kV + i];
-    store_merged<X, D>(C, T, layer, io, lse2, it, row, m, l, acc);
-}
-
 // Up to 256 rows, few partials: kMergeRows rows a warp, their loads together.
 constexpr int kMergeRows = 4;
 template <typename X, int D>
@@ -143,25 +66,20 @@ merge_many_kernel(const DevPaged C, const DevChunk T, int layer, const AttendIo 
 
 template <typename X, int D>
 cudaError_t merge(const DevPaged &C, const DevChunk &T, int layer, const AttendIo &io, float *lse2,
-                  const AttendWs &ws, int ctas, int rows, cudaStream_t s) {
-    if (rows == kFewRows)
-        return launch_dependent(merge_few_kernel<X, D>,
-                                dim3(ctas, std::min<long long>(kFewRows, (long long)T.max_t * C.G)),
-                                128, 0, s, C, T, layer, io, lse2, ws.cut, ws.part_ml, ws.part_o);
+                  const AttendWs &ws, int ctas, cudaStream_t s) {
     return launch_dependent(merge_many_kernel<X, D>, dim3(ctas, kManyRows / (4 * kMergeRows)), 128, 0,
                             s, C, T, layer, io, lse2, ws.cut, ws.part_ml, ws.part_o);
 }
 
 }  // namespace
 
-cudaError_t launch_attend_merge(const DevPaged &C, const DevChunk &T, int layer,
-                                const AttendIo &io, float *lse2, const AttendWs &ws, int ctas,
-                                int rows, cudaStream_t s) {
+cudaError_t launch_many_merge(const DevPaged &C, const DevChunk &T, int layer, const AttendIo &io,
+                              float *lse2, const AttendWs &ws, int ctas, cudaStream_t s) {
     if (C.dtype == KV_FP16)
-        return C.d == 64 ? merge<Fp16, 64>(C, T, layer, io, lse2, ws, ctas, rows, s)
-                         : merge<Fp16, 128>(C, T, layer, io, lse2, ws, ctas, rows, s);
-    return C.d == 64 ? merge<Bf16, 64>(C, T, layer, io, lse2, ws, ctas, rows, s)
-                     : merge<Bf16, 128>(C, T, layer, io, lse2, ws, ctas, rows, s);
+        return C.d == 64 ? merge<Fp16, 64>(C, T, layer, io, lse2, ws, ctas, s)
+                         : merge<Fp16, 128>(C, T, layer, io, lse2, ws, ctas, s);
+    return C.d == 64 ? merge<Bf16, 64>(C, T, layer, io, lse2, ws, ctas, s)
+                     : merge<Bf16, 128>(C, T, layer, io, lse2, ws, ctas, s);
 }
 
 namespace {
@@ -207,6 +125,7 @@ AttendWs attend_ws_layout(const DevPaged &C, const DevChunk &T, bool add_mass, v
     const size_t slots = std::max<size_t>(cut_few ? 2 * kFewCtas * (size_t)kFewRows : 0,
                                           k.many ? 2 * (size_t)many_phases(C) * kManyCtas * kManyRows : 0);
     ws.cut = reinterpret_cast<CutItem *>(take(std::max(kFewCtas, kManyCtas * kMaxPhases) * sizeof(CutItem)));
+    ws.unit_cut = reinterpret_cast<int *>(take((size_t)C.R * C.H * sizeof(int)));
     ws.part_ml = reinterpret_cast<float2 *>(take(slots * sizeof(float2)));
     ws.part_o = reinterpret_cast<float *>(take(slots * C.d * sizeof(float)));
     if (add_mass) {

@@ -104,6 +104,7 @@ struct FewArgs {
     AttendMask M;
     AttendIo io;
     CutItem *cut;
+    int *unit_cut;
     float2 *part_ml;
     float *part_o;
     float *lse2;
@@ -476,8 +477,10 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
             if (warp == 0) {
                 const bool whole = kCluster == 1 || (kCluster == 0 && x0 == 0 && x1 == total);
                 const long long slot = part_slot(blockIdx.x, x0 == 0);
-                if (kCluster == 0 && lane == 0 && x0 > 0 && x1 == total)
-                    *s_cut = CutItem{v, at / run.per, 0, rows};
+                if (kCluster == 0 && lane == 0 && x1 == total) {
+                    if (x0 > 0) *s_cut = CutItem{v, at / run.per, 0, rows};
+                    A.unit_cut[v] = x0 > 0 ? (int)blockIdx.x : -1;
+                }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -576,43 +579,163 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
     }
 }
 
-// mass of the rows of every tile: sum over the unit's query rows of 2^(logit - lse), in
-// row order.  64 threads a tile, a thread a key.
-constexpr int kMassThreads = 256;
-__global__ void __launch_bounds__(kMassThreads)
-few_mass_kernel(const DevPaged C, const DevChunk T, const FewArgs A) {
-    pdl_wait();
-    pdl_trigger();
-    constexpr int kGroups = kMassThreads / kFewTile;
-    const long long tiles = (long long)C.R * C.H * A.unit_tiles;
-    const int key = threadIdx.x % kFewTile;
-    for (long long t = (long long)blockIdx.x * kGroups + threadIdx.x / kFewTile; t < tiles;
-         t += (long long)gridDim.x * kGroups) {
-        const int v = (int)(t / A.unit_tiles), x = (int)(t - (long long)v * A.unit_tiles);
+// ---------------------------------------------------------------------------
+// What is left after the tiles: cut items merged, weights added.  Two kinds of block in
+// one launch, neither waiting for the other: the first merge_rows * units blocks merge a row
+// each; the rest add the weights, whose normaliser they merge for themselves (the partials'
+// maxima and sums are a few KB; as a launch after the merge they cost 8 us more).
+// ---------------------------------------------------------------------------
+constexpr int kFinishThreads = 256;
+
+// The cut item of unit v and the CTA that held its last tile; false if one CTA held it all
+// (or, after an expired wait, if nothing valid was left).
+__device__ __forceinline__ bool cut_of(const FewArgs &A, int v, CutItem &it, int &last) {
+    last = A.unit_cut[v];
+    if (last < 0 || last >= kFewCtas) return false;
+    it = A.cut[last];
+    return it.unit == v && it.cta0 >= 0 && it.cta0 <= last;
+}
+
+// One row of a cut item: the partials' weights 2^(m_p - m), then their outputs, every
+// eighth to a warp, added up in order.
+template <typename E, int D>
+__device__ __forceinline__ void merge_row(const DevPaged &C, const DevChunk &T, const FewArgs &A,
+                                          const CutItem &it, int last_cta, int row) {
+    constexpr int kV = D / 32, kW = kFinishThreads / 32;
+    __shared__ float sm_o[kW][D], sm_w[kFewCtas], sm_l[kW];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int parts = last_cta - it.cta0 + 1;
+    auto slot_row = [&](int p) {
+        return (long long)part_slot(it.cta0 + p, p == 0) * kFewRows + row;
+    };
+    float m = -INFINITY, l = 0.f;
+    for (int p = lane; p < parts; p += 32) m = fmaxf(m, A.part_ml[slot_row(p)].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int p = threadIdx.x; p < parts; p += kFinishThreads) {
+        const float2 ml = A.part_ml[slot_row(p)];
+        sm_w[p] = shrink(ml.x, m);
+        l += ml.y * sm_w[p];
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) sm_l[warp] = l;
+    __syncthreads();
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kW; ++w) l += sm_l[w];
+    float acc[kV] = {};
+#pragma unroll 8
+    for (int p = warp; p < parts; p += kW) {
+        const float f = sm_w[p];
+        const float *src = A.part_o + slot_row(p) * D + lane * kV;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) acc[i] += src[i] * f;
+    }
+#pragma unroll
+    for (int i = 0; i < kV; ++i) sm_o[warp][lane * kV + i] = acc[i];
+    __syncthreads();
+    if (warp) return;
+#pragma unroll
+    for (int k = 1; k < kW; ++k)
+#pragma unroll
+        for (int i = 0; i < kV; ++i) acc[i] += sm_o[k][lane * kV + i];
+    store_merged<E, D>(C, T, A.layer, A.io, A.lse2, it, row, m, l, acc);
+}
+
+// Weights of tiles [t0, t1): sums over the unit's query rows of 2^(logit - lse), in row
+// order, 64 threads a tile, a thread a key.  Unit by unit: the block first finds the rows'
+// lse, of a cut item from its partials.
+__device__ __forceinline__ void add_weights(const DevPaged &C, const DevChunk &T, const FewArgs &A,
+                                            bool cut, long long t0, long long t1) {
+    constexpr int kK = kFinishThreads / kFewRows;
+    __shared__ float sm_m[kK][kFewRows], sm_l[kK][kFewRows], sm_z[kFewRows];
+    const int key = threadIdx.x & 63, group = threadIdx.x >> 6;
+    for (long long t = t0; t < t1;) {
+        const int v = (int)(t / A.unit_tiles);
+        const long long base = (long long)v * A.unit_tiles, end = min(t1, base + A.unit_tiles);
         const UnitRows U = unit_rows(C, T, A.layer, v);
+        const int x0 = (int)(t - base);
+        t = end;
         if (!few_rows(C, T, U)) continue;
         const FewItem it(C, A.M, U, 0, kFewRows);
-        const int j = it.span.tile(x) * kFewTile + key;
-        if (x >= it.span.total || j > it.t_hi) continue;
-        const float *lg = A.logits + t * (kFewRows * kFewTile) + key;
-        const float *lse2 = A.lse2 + packed_row(C, U, 0);
-        const long long at = page_row(C, U.table, j);
-        float acc = 0.f;
-        bool seen = false;
-#pragma unroll 8
-        for (int row = 0; row < it.rows; ++row) {
-            const float z = lg[row * kFewTile];
-            if (z == -INFINITY) continue;
-            seen = true;
-            acc += ex2_approx(z - lse2[row]);
+        const int x1 = min((int)(end - base), it.span.total);
+        if (x0 >= x1) continue;
+        CutItem item;
+        int last;
+        if (!cut || !cut_of(A, v, item, last)) {
+            if (threadIdx.x < it.rows) sm_z[threadIdx.x] = A.lse2[packed_row(C, U, threadIdx.x)];
+        } else {
+            const int row = threadIdx.x % kFewRows, k = threadIdx.x / kFewRows;
+            const int first = item.cta0 + k, n = row < it.rows ? last + 1 : 0;
+            auto part = [&](int c) {
+                return A.part_ml[(long long)part_slot(c, c == item.cta0) * kFewRows + row];
+            };
+            float m = -INFINITY, l = 0.f;
+#pragma unroll 4
+            for (int c = first; c < n; c += kK) m = fmaxf(m, part(c).x);
+#pragma unroll 4
+            for (int c = first; c < n; c += kK) {
+                const float2 ml = part(c);
+                l += ml.y * shrink(ml.x, m);
+            }
+            sm_m[k][row] = m;
+            sm_l[k][row] = l;
+            __syncthreads();
+            if (k == 0) {
+                float mm = -INFINITY, ll = 0.f;
+#pragma unroll
+                for (int i = 0; i < kK; ++i) mm = fmaxf(mm, sm_m[i][row]);
+#pragma unroll
+                for (int i = 0; i < kK; ++i) ll += sm_l[i][row] * shrink(sm_m[i][row], mm);
+                sm_z[row] = row_lse2(mm, ll);
+            }
         }
-        if (seen && at >= 0) C.mass[at] += acc;
+        __syncthreads();
+        for (int x = x0 + group; x < x1; x += 4) {
+            const int j = it.span.tile(x) * kFewTile + key;
+            const bool in = j <= it.t_hi;
+            const long long at = in ? page_row(C, U.table, j) : -1;
+            const float *lg = A.logits + (base + x) * (kFewRows * kFewTile) + key;
+            float acc = 0.f;
+            bool seen = false;
+#pragma unroll 8
+            for (int row = 0; row < it.rows; ++row) {
+                const float z = lg[row * kFewTile];
+                const bool see = in && z != -INFINITY;
+                seen |= see;
+                acc += see ? ex2_approx(z - sm_z[row]) : 0.f;
+            }
+            if (seen && at >= 0) C.mass[at] += acc;
+        }
+        __syncthreads();                             // sm_z is read
     }
 }
 
+// cut: whether the tiles came from the cut form (else every unit's lse2 is written).
+template <typename E, int D>
+__global__ void __launch_bounds__(kFinishThreads)
+few_finish_kernel(const DevPaged C, const DevChunk T, const FewArgs A, int merge_rows, bool cut) {
+    pdl_wait();
+    pdl_trigger();
+    const int units = C.R * C.H, merges = cut ? units * merge_rows : 0;
+    if ((int)blockIdx.x < merges) {
+        const int v = blockIdx.x / merge_rows, row = blockIdx.x % merge_rows;
+        const UnitRows U = unit_rows(C, T, A.layer, v);
+        if (!few_rows(C, T, U) || row >= U.count * C.G) return;
+        CutItem it;
+        int last;
+        if (cut_of(A, v, it, last)) merge_row<E, D>(C, T, A, it, last, row);
+        return;
+    }
+    const long long tiles = (long long)units * A.unit_tiles;
+    const int blocks = (int)gridDim.x - merges;
+    const long long per = (tiles + blocks - 1) / blocks, t0 = ((int)blockIdx.x - merges) * per;
+    add_weights(C, T, A, cut, min(tiles, t0), min(tiles, t0 + per));
+}
+
 template <typename E, int D, int NT, int kCluster>
-cudaError_t few(const DevPaged &C, const DevChunk &T, const FewArgs &A, const AttendWs &ws,
-                cudaStream_t s) {
+cudaError_t few(const DevPaged &C, const DevChunk &T, const FewArgs &A, cudaStream_t s) {
     using Ly = Layout<D, NT>;
     CUtensorMap mk, mv;
     const int box = C.ps < kFewTile ? C.ps : kFewTile;
@@ -626,25 +749,27 @@ cudaError_t few(const DevPaged &C, const DevChunk &T, const FewArgs &A, const At
     if (e == cudaSuccess)
         e = launch_cluster_dependent(kernel, kCluster, dim3(grid), kThreads, Ly::kTotal, s, mk, mv, C,
                                      T, A);
-    if (e == cudaSuccess && kCluster == 0)
-        e = launch_attend_merge(C, T, A.layer, A.io, A.lse2, ws, kFewCtas, kFewRows, s);
-    if (e == cudaSuccess && A.logits) {
-        const long long groups = ((long long)C.R * C.H * A.unit_tiles + 3) / 4;
-        e = launch_dependent(few_mass_kernel, dim3((unsigned)std::min<long long>(groups, 16 * 152)),
-                             kMassThreads, 0, s, C, T, A);
+    if (e == cudaSuccess && (kCluster == 0 || A.logits)) {
+        const int rows = NT * 8 < T.max_t * (long long)C.G ? NT * 8 : T.max_t * C.G;
+        const long long merges = kCluster == 0 ? (long long)C.R * C.H * rows : 0;
+        // eight tiles a block, while that fills the SMs at most once
+        const long long tiles = A.logits ? (long long)C.R * C.H * A.unit_tiles : 0;
+        const long long adds = std::min<long long>((tiles + 7) / 8, 8 * 152);
+        e = launch_dependent(few_finish_kernel<E, D>, dim3((unsigned)(merges + adds)),
+                             kFinishThreads, 0, s, C, T, A, rows, kCluster == 0);
     }
     return e;
 }
 
 template <typename E, int D, int NT>
 cudaError_t few_form(const DevPaged &C, const DevChunk &T, const FewArgs &A, int cluster,
-                     const AttendWs &ws, cudaStream_t s) {
+                     cudaStream_t s) {
     switch (cluster) {
-        case 0: return few<E, D, NT, 0>(C, T, A, ws, s);
-        case 1: return few<E, D, NT, 1>(C, T, A, ws, s);
-        case 2: return few<E, D, NT, 2>(C, T, A, ws, s);
-        case 4: return few<E, D, NT, 4>(C, T, A, ws, s);
-        default: return few<E, D, NT, 8>(C, T, A, ws, s);
+        case 0: return few<E, D, NT, 0>(C, T, A, s);
+        case 1: return few<E, D, NT, 1>(C, T, A, s);
+        case 2: return few<E, D, NT, 2>(C, T, A, s);
+        case 4: return few<E, D, NT, 4>(C, T, A, s);
+        default: return few<E, D, NT, 8>(C, T, A, s);
     }
 }
 
@@ -654,7 +779,7 @@ cudaError_t launch_attend_few(const DevPaged &C, const DevChunk &T, int layer, c
                               const AttendIo &io, bool add_mass, long long items, int max_rows,
                               int blocks, const AttendWs &ws, cudaStream_t s) {
     const FewArgs A{layer,      M,         io,      ws.cut,
-                    ws.part_ml, ws.part_o, ws.lse2, add_mass ? ws.logits : nullptr,
+                    ws.unit_cut, ws.part_ml, ws.part_o, ws.lse2, add_mass ? ws.logits : nullptr,
                     (C.cap + kFewTile - 1) / kFewTile, blocks};
     // short tables: the largest cluster that leaves every CTA a tile and the GPU in one round
     int cluster = 0;
@@ -666,16 +791,16 @@ cudaError_t launch_attend_few(const DevPaged &C, const DevChunk &T, int layer, c
     const int nt = max_rows <= 8 ? 1 : 2;
     if (C.dtype == KV_FP16) {
         if (C.d == 64)
-            return nt == 1 ? few_form<Fp16, 64, 1>(C, T, A, cluster, ws, s)
-                           : few_form<Fp16, 64, 2>(C, T, A, cluster, ws, s);
-        return nt == 1 ? few_form<Fp16, 128, 1>(C, T, A, cluster, ws, s)
-                       : few_form<Fp16, 128, 2>(C, T, A, cluster, ws, s);
+            return nt == 1 ? few_form<Fp16, 64, 1>(C, T, A, cluster, s)
+                           : few_form<Fp16, 64, 2>(C, T, A, cluster, s);
+        return nt == 1 ? few_form<Fp16, 128, 1>(C, T, A, cluster, s)
+                       : few_form<Fp16, 128, 2>(C, T, A, cluster, s);
     }
     if (C.d == 64)
-        return nt == 1 ? few_form<Bf16, 64, 1>(C, T, A, cluster, ws, s)
-                       : few_form<Bf16, 64, 2>(C, T, A, cluster, ws, s);
-    return nt == 1 ? few_form<Bf16, 128, 1>(C, T, A, cluster, ws, s)
-                   : few_form<Bf16, 128, 2>(C, T, A, cluster, ws, s);
+        return nt == 1 ? few_form<Bf16, 64, 1>(C, T, A, cluster, s)
+                       : few_form<Bf16, 64, 2>(C, T, A, cluster, s);
+    return nt == 1 ? few_form<Bf16, 128, 1>(C, T, A, cluster, s)
+                   : few_form<Bf16, 128, 2>(C, T, A, cluster, s);
 }
 
 }  // namespace kvevict

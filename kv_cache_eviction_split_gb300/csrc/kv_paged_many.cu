@@ -713,8 +713,7 @@ cudaError_t many(const DevPaged &C, const DevChunk &T, const ManyArgs &A, const 
         e = launch_dependent(many_kernel<E, D>, dim3(kManyCtas), kThreads, Ly::kTotal, s, mk, mv, C,
                              T, A);
     if (e == cudaSuccess)
-        e = launch_attend_merge(C, T, A.layer, A.io, A.lse2, ws, kManyCtas * A.phases, kManyRows,
-                                s);
+        e = launch_many_merge(C, T, A.layer, A.io, A.lse2, ws, kManyCtas * A.phases, s);
     return e;
 }
 

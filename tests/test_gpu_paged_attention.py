@@ -295,6 +295,32 @@ def test_graph_replays_follow_lengths_and_tables(cuda_lib, counts):
     _check(a, counts, q, out, lse, mass=True)
 
 
+@pytest.mark.parametrize("counts,hi", [([1, 1], 900), ([1, 1], 9000), ([90, 40], 900)])
+def test_an_expired_wait_is_reported(cuda_lib, counts, hi):
+    """With a wait limit of 0 a wait that is not satisfied at once gives up: the call posts
+    KV_ERR_TIMEOUT and returns (or none had to wait, and it is right); the next call with the
+    usual limit is right."""
+    from tests import paged
+    kv = cuda_lib
+    made = paged.Made(kv, _spread(2, 1, 2, 200, hi), 8, 128, 64, seed=8, mass=True)
+    q, out = _chunk_inputs(made, counts, 8, False, 8)
+    limit = kv.kv_get_wait_limit_ns()
+    try:
+        kv.kv_set_wait_limit_ns(0)
+        for _ in range(5):
+            made.cache.mass.copy_(made.mass0)
+            lse, status = _run(kv, made, counts, q, out, mass=True)
+            assert status in (kv.KV_OK, kv.KV_ERR_TIMEOUT)
+            if status == kv.KV_OK:
+                _check(made, counts, q, out, lse, mass=True)
+    finally:
+        kv.kv_set_wait_limit_ns(limit)
+    made.cache.mass.copy_(made.mass0)
+    lse, status = _run(kv, made, counts, q, out, mass=True)
+    assert status == 0
+    _check(made, counts, q, out, lse, mass=True)
+
+
 def test_two_streams_at_once(cuda_lib):
     """Two calls with their own workspaces on two streams, while a third runs on the default."""
     import torch
