@@ -94,6 +94,7 @@ cudaError_t launch_paged_evict(const DevPaged &S, const DevPaged &D, const int32
 constexpr int kFewRows = 16;       // most query rows of an item of the few-rows kernels
 constexpr int kFewTile = 64;       // keys per tile there
 constexpr int kFewCtas = 2 * 152;  // two CTAs on each SM
+constexpr int kFewCost = 3;        // an item's own cost in tiles
 // Tables of at most kShortRows rows take the few-rows kernel's one-launch form, which there
 // also takes up to kShortFewRows query rows, in blocks of kFewRows (without add_mass).
 constexpr int kShortRows = 4096;
@@ -101,6 +102,7 @@ constexpr int kShortFewRows = 128;
 constexpr int kManyTile = 128;     // keys per tile of the tensor-memory kernel
 constexpr int kManyRows = 256;     // query rows per item there: two tiles of 128
 constexpr int kManyCtas = 152;
+constexpr int kManyCost = 4;
 // The many-rows kernel takes the units in up to kMaxPhases groups, one after another, each
 // cut into runs over all CTAs: a group's rows (kPhaseBytes, where that gives few enough
 // groups) stay in L2 while all its items read them.

@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
            const DevPaged C, const DevChunk T, const FewArgs A) {
     using Ly = Layout<D, NT>;
-    constexpr int kSt = Ly::kStages, kRows = NT * 8;
+    constexpr int kSt = Ly::kStages, kRows = NT * 8, kCost = kCluster == 0 ? kFewCost : 0;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + Ly::kBars), *empty = full + kSt;
     volatile int *s_abort = reinterpret_cast<volatile int *>(empty + kSt);
@@ -167,7 +167,9 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
             units, reinterpret_cast<int *>(smem),
             [&](int v) { return unit_rows(C, T, A.layer, v); },
             [&](const UnitRows &U) { return (int)few_rows(C, T, U); },
-            [&](const UnitRows &U, int) { return FewItem(C, A.M, U, 0, kRows).span.total; });
+            [&](const UnitRows &U, int) { 
+                return kCost + FewItem(C, A.M, U, 0, kRows).span.total;
+            });
     } else {
         // one item a cluster: its tiles are the whole order, each CTA's run a part of them
         rank = (int)(blockIdx.x % kCluster);
@@ -202,9 +204,9 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
             if (!few_rows(C, T, U)) continue;
             const FewItem it(C, A.M, U, block, kRows);
             if (!U.ok && lane == 0) post_status(C.status, KV_ERR_INVALID_ARG);
-            const int x1 = min(it.span.total, run.end - at);
+            const int x1 = min(it.span.total, run.end - at - kCost);
             int base = -1, pg = -1;
-            for (int x = max(run.begin - at, 0); x < x1; ++x) {
+            for (int x = max(run.begin - at - kCost, 0); x < x1; ++x) {
                 const int key0 = it.span.tile(x) * kFewTile;
                 const int e0 = key0 >> C.ps_log2;
                 if ((e0 & ~31) != base) {
@@ -236,7 +238,7 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
                                 map, &full[s], half * 64, (int)y);
                 ++cnt;
             }
-            at += it.span.total;
+            at += kCost + it.span.total;
         }
         if (!ok && lane == 0) {
             *s_abort = 1;
@@ -258,9 +260,9 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
             if (!few_rows(C, T, U)) continue;
             const FewItem it(C, A.M, U, block, kRows);
             const int rows = it.rows, t_lo = it.t_lo, t_hi = it.t_hi, total = it.span.total;
-            const int x0 = max(run.begin - at, 0), x1 = min(total, run.end - at);
+            const int x0 = max(run.begin - at - kCost, 0), x1 = min(total, run.end - at - kCost);
             if (kCluster == 0 && x0 >= x1) {
-                at += total;
+                at += kCost + total;
                 continue;
             }
             // Q^T: columns are query rows (those past the last are zero)
@@ -478,7 +480,7 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
                 const bool whole = kCluster == 1 || (kCluster == 0 && x0 == 0 && x1 == total);
                 const long long slot = part_slot(blockIdx.x, x0 == 0);
                 if (kCluster == 0 && lane == 0 && x1 == total) {
-                    if (x0 > 0) *s_cut = CutItem{v, at / run.per, 0, rows};
+                    if (x0 > 0) *s_cut = CutItem{v, (at + kCost) / run.per, 0, rows};
                     A.unit_cut[v] = x0 > 0 ? (int)blockIdx.x : -1;
                 }
 #pragma unroll
@@ -525,7 +527,7 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
                         }
                     }
             }
-            at += total;
+            at += kCost + total;
         }
         if (!ok && lane == 0) {
             *s_abort = 1;

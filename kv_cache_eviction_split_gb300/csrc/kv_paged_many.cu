@@ -217,7 +217,7 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                 units, reinterpret_cast<int *>(smem),
                 [&](int v) { return unit_rows(C, T, A.layer, u0 + v); },
                 [&](const UnitRows &U) { return unit_items(C, T, U); },
-                [&](const UnitRows &U, int i) { return item_tiles(C, A.M, U, i); });
+                [&](const UnitRows &U, int i) { return kManyCost + item_tiles(C, A.M, U, i); });
         if (threadIdx.x == 0) s_run[g] = run;
         __syncthreads();
     }
@@ -510,11 +510,12 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                             make_item(next, C, A.M, U, pair);
                             next.v = v;
                             next.cta = g * kManyCtas + blockIdx.x;
+                            at += kManyCost;
                             next.cta0 = g * kManyCtas + at / run.per;
                             next.x0 = max(run.begin - at, 0);
                             next.x1 = min(next.span.total, run.end - at);
                             at += next.span.total;
-                            put(next);
+                            if (next.x0 < next.x1) put(next);
                         }
                     }
                 }

@@ -25,6 +25,7 @@ constexpr int kKWarp = 0, kMmaWarp = 1, kQWarp = 2, kSchedWarp = 3, kKeyWarp = 4
 constexpr int kLoadRegs = 104, kKeyRegs = 200;
 constexpr int kBlockBytes = 128 * 128;       // [128 rows][64 columns], 128 B swizzle
 constexpr int kGroup = 2;                    // key tiles per item
+constexpr int kGroupCost = 2;                // an item's own cost in row tiles
 constexpr int kItems = 3;                    // items described ahead
 constexpr int kQSt = 3;                      // Q ring
 
@@ -131,7 +132,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         [&](const UnitRows &U, int i) {
             int r0, r1;
             Groups(C, T, U).range(C, A.M, U.n, i, r0, r1);
-            return r1 - r0;
+            return r1 > r0 ? r1 - r0 + kGroupCost : 0;
         });
     bool ok = *s_abort == 0;
     auto item = [&](int i, bool &fine) -> const Item * {
@@ -288,7 +289,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                             next.tiles = min(kGroup, ((U.n + kManyTile - 1) >> 7) - next.tile0);
                             put(next);
                         }
-                        at += steps;
+                        at += steps > 0 ? steps + kGroupCost : 0;
                     }
                     j = 0;
                 }
