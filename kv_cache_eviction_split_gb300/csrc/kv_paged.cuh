@@ -95,10 +95,20 @@ constexpr int kFewRows = 16;       // most query rows of an item of the few-rows
 constexpr int kFewTile = 64;       // keys per tile there
 constexpr int kFewCtas = 2 * 152;  // two CTAs on each SM
 constexpr int kFewCost = 3;        // an item's own cost in tiles
-// Tables of at most kShortRows rows take the few-rows kernel's one-launch form, which there
-// also takes up to kShortFewRows query rows, in blocks of kFewRows (without add_mass).
-constexpr int kShortRows = 4096;
-constexpr int kShortFewRows = 128;
+// Tables of at most kShortRows rows take the few-rows kernel's one-launch form.  One new
+// token, 8 KV heads of 4 query heads, d = 128, GPU time in us one-launch / cut and merged:
+//   1 request   1024 rows 5.6 / 10.6   4096 8.0 / 11.3   8192 11.7 / 12.6   16384 18.5 / 16.8
+//   64 requests 1024 rows 44 / 52      4096 148 / 161    8192 288 / 308
+// Longer tables are cut: lengths that differ (30% of 16384 .. 131072 rows, 8 requests) then
+// cost nothing.
+constexpr int kShortRows = 8192;
+// There the kernel also takes up to kShortFewRows query rows a head, in blocks of kFewRows
+// that each read the keys again, while a step has no more than kFewCtas such items and
+// kShortVisits key tiles over all of them (without add_mass).  In us, this / the many-rows
+// kernel:  1 request   64 rows on 1024 keys 9.9 / 23.0   256 on 4096 35 / 44   512 on 4096 57 / 37
+//          16 requests 64 rows on 1024 keys 38 / 28 (512 items)
+constexpr int kShortFewRows = 512;
+constexpr int kShortVisits = 8192;
 constexpr int kManyTile = 128;     // keys per tile of the tensor-memory kernel
 constexpr int kManyRows = 256;     // query rows per item there: two tiles of 128
 constexpr int kManyCtas = 152;

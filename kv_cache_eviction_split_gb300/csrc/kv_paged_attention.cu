@@ -91,22 +91,30 @@ struct Classes {
     int many;                  // the others
 };
 Classes classify(const DevPaged &C, const DevChunk &T, bool add_mass) {
-    Classes k{};
-    k.few_max = C.cap <= kShortRows && !add_mass ? kShortFewRows : kFewRows;
-    k.blocks = 1;
-    for (int r = 0; r < C.R; ++r) {
-        const long long rows = (T.host_off[r + 1] - T.host_off[r]) * C.G;
-        if (rows > k.few_max) {
-            ++k.many;
-        } else if (rows > 0) {
-            const int blocks = (int)(rows + kFewRows - 1) / kFewRows;
-            ++k.few_requests;
-            k.max_rows = std::max(k.max_rows, (int)rows);
-            k.blocks = std::max(k.blocks, blocks);
-            k.items += (long long)blocks * C.H;
+    auto with = [&](int few_max) {
+        Classes k{};
+        k.few_max = few_max;
+        k.blocks = 1;
+        for (int r = 0; r < C.R; ++r) {
+            const long long rows = (T.host_off[r + 1] - T.host_off[r]) * C.G;
+            if (rows > few_max) {
+                ++k.many;
+            } else if (rows > 0) {
+                const int blocks = (int)(rows + kFewRows - 1) / kFewRows;
+                ++k.few_requests;
+                k.max_rows = std::max(k.max_rows, (int)rows);
+                k.blocks = std::max(k.blocks, blocks);
+                k.items += (long long)blocks * C.H;
+            }
         }
+        return k;
+    };
+    if (C.cap <= kShortRows && !add_mass) {
+        const Classes k = with(kShortFewRows);
+        if (k.items <= kFewCtas && k.items * ((C.cap + kFewTile - 1) / kFewTile) <= kShortVisits)
+            return k;
     }
-    return k;
+    return with(kFewRows);
 }
 }  // namespace
 

@@ -22,7 +22,7 @@
 // merged by a second kernel (kv_paged_attention.cu).  Short tables (kCluster = 1 .. 8): a
 // cluster per item, each CTA a part of its tiles, merged through distributed shared
 // memory: one launch, which is what a short call costs; there an item's row block may also
-// be one of several of a unit (up to kShortFewRows rows), each reading K and V again.
+// be one of several of a unit, each reading K and V again.  kv_paged.cuh has the rules.
 #include <algorithm>
 
 #include <cooperative_groups.h>

@@ -109,6 +109,10 @@ CASES = {
     "short_window": (2, 8, 128, 64, "bf16", [20, 5], 300, 1500, 70, 5, False, True),
     "short_empty_rows": (1, 8, 128, 16, "bf16", [9, 5], 0, 4, 0, 0, False, False),
     "short_and_long_chunks": (2, 8, 64, 64, "bf16", [16, 200, 1], 201, 900, 0, 0, False, False),
+    "short_512_rows": (1, 4, 128, 64, "bf16", [128], 700, 700, 0, 0, False, False),
+    "short_too_many_items": (2, 8, 128, 64, "bf16", [30] * 30, 40, 300, 0, 0, False, False),
+    "long_few_tokens": (2, 8, 128, 32, "bf16", [4, 1, 2], 300, 9001, 0, 0, True, False),
+    "long_few_tokens_window": (2, 8, 64, 16, "fp16", [4, 1], 8000, 9001, 3001, 7, True, False),
     "many_requests": (2, 8, 128, 64, "bf16", [1] * 40, 1, 260, 0, 0, True, False),
     "long_chunk": (1, 8, 128, 64, "bf16", [96], 12345, 12345, 0, 0, True, False),
 }
