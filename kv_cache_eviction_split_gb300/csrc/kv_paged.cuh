@@ -95,7 +95,8 @@ constexpr int kFewRows = 16;       // most query rows of an item of the few-rows
 constexpr int kFewTile = 64;       // keys per tile there
 constexpr int kFewCtas = 2 * 152;  // two CTAs on each SM
 constexpr int kFewCost = 3;        // an item's own cost in tiles
-// Tables of at most kShortRows rows take the few-rows kernel's one-launch form.  One new
+// Tables of at most kShortRows rows, and windows that see no more of longer ones, take the
+// few-rows kernel's one-launch form.  One new
 // token, 8 KV heads of 4 query heads, d = 128, GPU time in us one-launch / cut and merged:
 //   1 request   1024 rows 5.6 / 10.6   4096 8.0 / 11.3   8192 11.7 / 12.6   16384 18.5 / 16.8
 //   64 requests 1024 rows 44 / 52      4096 148 / 161    8192 288 / 308

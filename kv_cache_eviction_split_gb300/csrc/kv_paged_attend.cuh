@@ -312,10 +312,11 @@ __device__ __forceinline__ void store_merged(const DevPaged &C, const DevChunk &
 cudaError_t launch_many_merge(const DevPaged &C, const DevChunk &T, int layer, const AttendIo &io,
                               float *lse2, const AttendWs &ws, int ctas, cudaStream_t s);
 // Requests of at most T.few_max query rows a head: `items` items of at most kFewRows rows
-// in all, the largest with max_rows, `blocks` of them at most to a unit.
+// in all, the largest with max_rows, `blocks` of them at most to a unit, which sees at
+// most `seen` rows of it.
 cudaError_t launch_attend_few(const DevPaged &C, const DevChunk &T, int layer, const AttendMask &M,
-                              const AttendIo &io, bool add_mass, long long items, int max_rows,
-                              int blocks, const AttendWs &ws, cudaStream_t s);
+                              const AttendIo &io, bool add_mass, long long seen, long long items,
+                              int max_rows, int blocks, const AttendWs &ws, cudaStream_t s);
 // The others.
 cudaError_t launch_attend_many(const DevPaged &C, const DevChunk &T, int layer, const AttendMask &M,
                                const AttendIo &io, bool add_mass, const AttendWs &ws,

@@ -90,7 +90,8 @@ struct Classes {
     long long items;           // their items
     int many;                  // the others
 };
-Classes classify(const DevPaged &C, const DevChunk &T, bool add_mass) {
+// seen: most rows of a unit that the step's queries see.
+Classes classify(const DevPaged &C, const DevChunk &T, long long seen, bool add_mass) {
     auto with = [&](int few_max) {
         Classes k{};
         k.few_max = few_max;
@@ -109,9 +110,9 @@ Classes classify(const DevPaged &C, const DevChunk &T, bool add_mass) {
         }
         return k;
     };
-    if (C.cap <= kShortRows && !add_mass) {
+    if (seen <= kShortRows && !add_mass) {
         const Classes k = with(kShortFewRows);
-        if (k.items <= kFewCtas && k.items * ((C.cap + kFewTile - 1) / kFewTile) <= kShortVisits)
+        if (k.items <= kFewCtas && k.items * ((seen + kFewTile - 1) / kFewTile) <= kShortVisits)
             return k;
     }
     return with(kFewRows);
@@ -127,7 +128,8 @@ AttendWs attend_ws_layout(const DevPaged &C, const DevChunk &T, bool add_mass, v
         off = (off + bytes + 255) / 256 * 256;
         return p;
     };
-    const Classes k = classify(C, T, add_mass);
+    // whatever the window: a call without one needs most
+    const Classes k = classify(C, T, C.cap, add_mass);
     // the two kernels run one after the other: they share the partials
     const bool cut_few = k.few_requests && C.cap > kShortRows;
     const size_t slots = std::max<size_t>(cut_few ? 2 * kFewCtas * (size_t)kFewRows : 0,
@@ -150,12 +152,18 @@ AttendWs attend_ws_layout(const DevPaged &C, const DevChunk &T, bool add_mass, v
 cudaError_t launch_paged_attention(const DevPaged &C, const DevChunk &T0, int layer,
                                    const AttendMask &M, const AttendIo &io, bool add_mass,
                                    const AttendWs &ws, cudaStream_t s) {
-    const Classes k = classify(C, T0, add_mass);
+    // a window's rows and the sinks' may begin and end inside a tile
+    const long long seen =
+        M.window > 0 ? std::min<long long>(C.cap, (long long)M.window + M.sinks + T0.max_t +
+                                                      2 * kFewTile)
+                     : C.cap;
+    const Classes k = classify(C, T0, seen, add_mass);
     DevChunk T = T0;
     T.few_max = k.few_max;
     cudaError_t e = cudaSuccess;
     if (k.few_requests)
-        e = launch_attend_few(C, T, layer, M, io, add_mass, k.items, k.max_rows, k.blocks, ws, s);
+        e = launch_attend_few(C, T, layer, M, io, add_mass, seen, k.items, k.max_rows, k.blocks, ws,
+                              s);
     if (e == cudaSuccess && k.many) {
         e = launch_attend_many(C, T, layer, M, io, add_mass, ws, s);
         if (e == cudaSuccess && add_mass) e = launch_many_mass(C, T, layer, M, ws, s);

@@ -778,16 +778,16 @@ cudaError_t few_form(const DevPaged &C, const DevChunk &T, const FewArgs &A, int
 }  // namespace
 
 cudaError_t launch_attend_few(const DevPaged &C, const DevChunk &T, int layer, const AttendMask &M,
-                              const AttendIo &io, bool add_mass, long long items, int max_rows,
-                              int blocks, const AttendWs &ws, cudaStream_t s) {
+                              const AttendIo &io, bool add_mass, long long seen, long long items,
+                              int max_rows, int blocks, const AttendWs &ws, cudaStream_t s) {
     const FewArgs A{layer,      M,         io,      ws.cut,
                     ws.unit_cut, ws.part_ml, ws.part_o, ws.lse2, add_mass ? ws.logits : nullptr,
                     (C.cap + kFewTile - 1) / kFewTile, blocks};
-    // short tables: the largest cluster that leaves every CTA a tile and the GPU in one round
+    // short: the largest cluster that leaves every CTA a tile and the GPU in one round
     int cluster = 0;
-    if (C.cap <= kShortRows) {
+    if (seen <= kShortRows) {
         cluster = 8;
-        while (cluster > 1 && (cluster * kFewTile > C.cap || items * cluster > kFewCtas))
+        while (cluster > 1 && (cluster * kFewTile > seen || items * cluster > kFewCtas))
             cluster /= 2;
     }
     const int nt = max_rows <= 8 ? 1 : 2;
