@@ -98,6 +98,10 @@ CASES = {
     "chunk_window_small": (1, 4, 64, 16, "bf16", [200], 900, 900, 5, 2, True, False),
     "chunk_window_wide": (1, 4, 128, 32, "bf16", [130], 300, 300, 5000, 4, True, False),
     "chunk_sinks_in_window": (1, 4, 128, 64, "bf16", [140], 140, 140, 64, 100, True, False),
+    # sinks that end behind the windows' begin, in a tile that only some rows' windows reach
+    "chunk_sinks_past_window": (1, 1, 128, 64, "bf16", [700], 1500, 1500, 200, 1000, True, False),
+    "chunk_sinks_past_window_g4": (2, 8, 64, 32, "fp16", [150], 900, 1300, 40, 777, True, False),
+    "decode_sinks_past_window": (1, 4, 128, 64, "bf16", [3], 700, 700, 40, 690, True, False),
     "chunk_longer_than_rows": (1, 4, 128, 64, "bf16", [150], 90, 90, 0, 0, True, False),
     "prompt": (2, 8, 128, 64, "bf16", [513], 513, 513, 0, 0, True, False),
     "prompt_window": (1, 4, 128, 64, "fp16", [700], 700, 700, 129, 1, True, True),
