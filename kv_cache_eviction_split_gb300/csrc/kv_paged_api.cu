@@ -158,7 +158,9 @@ kv_status kv_paged_attention(const kv_paged *c, const kv_chunk *t, int32_t layer
         return KV_ERR_INVALID_ARG;
     const AttendWs ws = attend_ws_layout(C, T, add_mass != 0, workspace);
     if (workspace_bytes < ws.total) return KV_ERR_WORKSPACE;
-    const AttendMask M{window, window > 0 ? num_sinks : 0, softmax_scale * 1.4426950408889634f};
+    // a window of the table's length or more hides nothing
+    const int w = window >= C.cap ? 0 : window;
+    const AttendMask M{w, w > 0 ? num_sinks : 0, softmax_scale * 1.4426950408889634f};
     const AttendIo io{q, out, lse, q_stride, out_stride};
     return map_cuda(launch_paged_attention(C, T, layer, M, io, add_mass != 0, ws,
                                            (cudaStream_t)stream));

@@ -71,7 +71,8 @@ struct Groups {
         const int key0 = g * kGroup * kManyTile, last = min(n, key0 + kGroup * kManyTile) - 1;
         const int i0 = max(0, key0 - t0);
         int i1 = n - 1 - t0;                       // last query
-        if (M.window > 0 && key0 >= M.sinks) i1 = min(i1, last - t0 + M.window - 1);
+        if (M.window > 0 && key0 >= M.sinks)
+            i1 = (int)min((long long)i1, (long long)last - t0 + M.window - 1);
         rt0 = (int)((long long)i0 * C.G >> 7);
         rt1 = i1 < i0 ? rt0 : (int)(((long long)(i1 + 1) * C.G + 127) >> 7);
     }

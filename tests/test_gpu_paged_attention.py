@@ -102,6 +102,9 @@ CASES = {
     "chunk_sinks_past_window": (1, 1, 128, 64, "bf16", [700], 1500, 1500, 200, 1000, True, False),
     "chunk_sinks_past_window_g4": (2, 8, 64, 32, "fp16", [150], 900, 1300, 40, 777, True, False),
     "decode_sinks_past_window": (1, 4, 128, 64, "bf16", [3], 700, 700, 40, 690, True, False),
+    "chunk_window_largest": (1, 4, 128, 64, "bf16", [150], 600, 600, 2 ** 31 - 1, 2 ** 31 - 1, True,
+                             False),
+    "decode_window_largest": (1, 4, 128, 64, "bf16", [1, 3], 500, 9000, 2 ** 31 - 1, 4, True, False),
     "chunk_longer_than_rows": (1, 4, 128, 64, "bf16", [150], 90, 90, 0, 0, True, False),
     "prompt": (2, 8, 128, 64, "bf16", [513], 513, 513, 0, 0, True, False),
     "prompt_window": (1, 4, 128, 64, "fp16", [700], 700, 700, 129, 1, True, True),
