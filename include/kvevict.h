@@ -476,6 +476,11 @@ kv_status kv_paged_attention_workspace_size(const kv_paged *c, const kv_chunk *t
  * add_mass != 0 adds to mass of every row j the weights e^(s_j - lse) of the
  * chunk's queries and the group's heads (fp32, in a fixed order: the same call on
  * the same bits gives the same bits).
+ *
+ * KV_ERR_UNSUPPORTED: a step whose (query row block, key tile) pairs could pass 2^31,
+ * counted for units as long as their tables (256 query rows of a head by 128 keys;
+ * with add_mass also 128 by 256), about a million new tokens of 32 query heads
+ * over as many rows; give it in shorter chunks.
  */
 kv_status kv_paged_attention(const kv_paged *c, const kv_chunk *t, int32_t layer, int32_t window,
                              int32_t num_sinks, float softmax_scale, const void *q,
@@ -509,7 +514,8 @@ kv_status kv_paged_evict(const kv_paged *src, const kv_paged *dst, const int32_t
 
 /*
  * Synchronises `stream`, then reads and clears the device status word of a
- * score, select, attention or eviction workspace.  *device_status receives the kv_status a kernel
+ * score, select or eviction workspace, or a paged cache's own (its status
+ * member in place of the workspace).  *device_status receives the kv_status a kernel
  * posted (KV_OK if none).  Returns KV_ERR_CUDA if the stream itself reports an
  * error.  It takes the workspace because the library keeps no state between
  * calls: the word lives in the caller's workspace.

@@ -789,7 +789,9 @@ class Chunk:
 def _on_current_device(cache: PagedCache, *others) -> None:
     """The library works on the current device: its tensors have to be there."""
     index = cache._index
-    if index >= 0 and index != (_raw or _raw_calls())[0]():
+    if index < 0:
+        raise ValueError("the cache's tensors are not on a CUDA device")
+    if index != (_raw or _raw_calls())[0]():
         raise ValueError("the cache is on %s, which is not the current device" % cache.device)
     for t in others:
         if t is not None and t.get_device() != index:
@@ -835,7 +837,8 @@ def kv_paged_load(cache: PagedCache, k_rows, v_rows, offsets_dev, total_rows: in
     for t in (k_rows, v_rows):
         if t.dtype != cache.dtype or not t.is_contiguous() or t.numel() < n * cache.head_dim:
             raise ValueError("k_rows, v_rows: %s [total_rows][%d]" % (cache.dtype, cache.head_dim))
-    if offsets_dev.dtype != torch.int64 or offsets_dev.numel() != cache.num_units + 1:
+    if offsets_dev.dtype != torch.int64 or offsets_dev.numel() != cache.num_units + 1 or \
+            not offsets_dev.is_contiguous():
         raise ValueError("offsets: int64 [units + 1]")
     if mass_rows is not None and (mass_rows.dtype != torch.float32 or
                                   not mass_rows.is_contiguous() or mass_rows.numel() < n):
@@ -869,6 +872,8 @@ def kv_paged_attention(cache: PagedCache, chunk: Chunk, layer: int, q, out, work
     if lse is not None and (lse.dtype is not torch.float32 or not lse.is_contiguous() or
                             lse.shape != (chunk.tokens, heads)):
         raise ValueError("lse: float32 [%d][%d]" % (chunk.tokens, heads))
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: contiguous")
     _on_current_device(cache, q, out, lse, workspace)
     code = (_lib or load()).kv_paged_attention(
         cache._ref, chunk._ref, layer, window, num_sinks,
@@ -897,6 +902,8 @@ def kv_paged_evict(cache: PagedCache, into: PagedCache, budgets, num_sinks: int,
     if kept.dtype != torch.int32 or kept.dim() != 2 or kept.shape[0] != cache.num_units or \
             not kept.is_contiguous():
         raise ValueError("kept: int32 [units][most rows kept]")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: contiguous")
     _on_current_device(cache, into.k_pages, budgets, kept, workspace)
     _check(load().kv_paged_evict(cache.c, into.c, _ptr(budgets), int(num_sinks), int(recent),
                                  _ptr(kept), kept.shape[1], _ptr(workspace),

@@ -184,6 +184,9 @@ struct AttendIo {
     long long q_stride, out_stride;
 };
 
+// Whether every kernel's count of tiles (as above, for units as long as their tables) fits
+// in 32 bits.
+bool attend_tiles_fit(const DevPaged &C, const DevChunk &T, const AttendMask &M, bool add_mass);
 cudaError_t launch_paged_attention(const DevPaged &C, const DevChunk &T, int layer,
                                    const AttendMask &M, const AttendIo &io, bool add_mass,
                                    const AttendWs &ws, cudaStream_t s);

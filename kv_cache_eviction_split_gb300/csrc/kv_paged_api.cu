@@ -161,6 +161,7 @@ kv_status kv_paged_attention(const kv_paged *c, const kv_chunk *t, int32_t layer
     // a window of the table's length or more hides nothing
     const int w = window >= C.cap ? 0 : window;
     const AttendMask M{w, w > 0 ? num_sinks : 0, softmax_scale * 1.4426950408889634f};
+    if (!attend_tiles_fit(C, T, M, add_mass != 0)) return KV_ERR_UNSUPPORTED;
     const AttendIo io{q, out, lse, q_stride, out_stride};
     return map_cuda(launch_paged_attention(C, T, layer, M, io, add_mass != 0, ws,
                                            (cudaStream_t)stream));

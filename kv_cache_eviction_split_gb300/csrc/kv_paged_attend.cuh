@@ -183,7 +183,7 @@ __device__ __forceinline__ CtaRun cut_run(int units, int *s_tiles, U unit, P par
     R.total = total;
     R.per = max(1, (total + (int)gridDim.x - 1) / (int)gridDim.x);
     R.begin = (int)min((long long)total, (long long)blockIdx.x * R.per);
-    R.end = min(total, R.begin + R.per);
+    R.end = (int)min((long long)total, (long long)R.begin + R.per);
     if (R.begin < R.end && before <= R.begin && R.begin < before + mine) {
         int at = before, v = v0;
         if (chunk > 1)

@@ -149,14 +149,36 @@ AttendWs attend_ws_layout(const DevPaged &C, const DevChunk &T, bool add_mass, v
     return ws;
 }
 
+namespace {
+// Most rows of a unit that a step's queries see; a window's rows and the sinks' may begin and
+// end inside a tile.
+long long rows_seen(const DevPaged &C, const DevChunk &T, const AttendMask &M) {
+    return M.window > 0 ? std::min<long long>(C.cap, (long long)M.window + M.sinks + T.max_t +
+                                                         2 * kFewTile)
+                        : C.cap;
+}
+}  // namespace
+
+bool attend_tiles_fit(const DevPaged &C, const DevChunk &T, const AttendMask &M, bool add_mass) {
+    const long long seen = rows_seen(C, T, M), few_tiles = seen / kFewTile + 2;
+    const long long many_tiles = seen / kManyTile + 2;
+    const long long groups = C.cap / (2 * kManyTile) + 1;      // of the weights' pass
+    double few = 0, many = 0, weights = 0;
+    for (int r = 0; r < C.R; ++r) {
+        const long long rows = (T.host_off[r + 1] - T.host_off[r]) * C.G;
+        if (rows == 0) continue;
+        few += (double)C.H * (few_tiles + kFewCost);
+        many += (double)C.H * (rows / kManyRows + 1) * (many_tiles + kManyCost);
+        weights += (double)C.H * groups * (rows / 128 + 1 + kManyCost);
+    }
+    const double most = 2147483647.0;
+    return few <= most && many <= most && (!add_mass || weights <= most);
+}
+
 cudaError_t launch_paged_attention(const DevPaged &C, const DevChunk &T0, int layer,
                                    const AttendMask &M, const AttendIo &io, bool add_mass,
                                    const AttendWs &ws, cudaStream_t s) {
-    // a window's rows and the sinks' may begin and end inside a tile
-    const long long seen =
-        M.window > 0 ? std::min<long long>(C.cap, (long long)M.window + M.sinks + T0.max_t +
-                                                      2 * kFewTile)
-                     : C.cap;
+    const long long seen = rows_seen(C, T0, M);
     const Classes k = classify(C, T0, seen, add_mass);
     DevChunk T = T0;
     T.few_max = k.few_max;

@@ -82,6 +82,42 @@ def test_attention_argument_checks(kv):
                                   None) == kv.KV_OK
 
 
+def test_attention_refuses_more_tiles_than_it_counts(kv):
+    lib, c = kv.load(), _cache(kv)
+    t = kv.Chunk([1, 1 << 21], device="cpu")
+    c._c.max_pages = 1 << 15                                    # tables of 2^21 rows
+    args = [c.c, t.c, 1, 0, 0, 0.1, F, 1024, F, 1024, F, 0, F, 1 << 62, None]
+    # 2 heads x 2^23 / 256 row blocks x 2^21 / 128 key tiles: 2^30
+    t.cu_host[2] = 1 << 22                                      # twice that, and the items' costs
+    assert lib.kv_paged_attention(*args) == kv.KV_ERR_UNSUPPORTED
+    args[11] = 1
+    t.cu_host[2] = 1 << 22
+    args[3] = 4096                                # a window: few tiles, but the weights' count
+    assert lib.kv_paged_attention(*args) == kv.KV_ERR_UNSUPPORTED
+
+
+def test_binding_refuses_tensors_the_gpu_cannot_take(kv):
+    import torch
+    c, t = _cache(kv), kv.Chunk([1, 5], device="cpu")
+    ws = torch.empty(1 << 24, dtype=torch.uint8)
+    q, k = (torch.zeros((6, h, 128), dtype=torch.bfloat16) for h in (8, 2))
+    rows, off = torch.zeros((4, 128), dtype=torch.bfloat16), torch.zeros(c.num_units + 1).long()
+    kept = torch.zeros((c.num_units, 50), dtype=torch.int32)
+    for call in (lambda: kv.kv_paged_attention(c, t, 0, q, torch.empty_like(q), ws),
+                 lambda: kv.kv_paged_append(c, t, 0, k, k),
+                 lambda: kv.kv_paged_load(c, rows, rows, off, 4),
+                 lambda: kv.kv_paged_evict(c, _cache(kv), kept[:, 0].contiguous(), 4, 16, kept, ws)):
+        with pytest.raises(ValueError, match="CUDA device"):
+            call()
+    # views that lie apart
+    with pytest.raises(ValueError, match="workspace"):
+        kv.kv_paged_attention(c, t, 0, q, torch.empty_like(q), ws[::2])
+    with pytest.raises(ValueError, match="workspace"):
+        kv.kv_paged_evict(c, _cache(kv), kept[:, 0].contiguous(), 4, 16, kept, ws[::2])
+    with pytest.raises(ValueError, match="offsets"):
+        kv.kv_paged_load(c, rows, rows, torch.zeros(2 * c.num_units + 2).long()[::2], 4)
+
+
 def test_append_load_evict_argument_checks(kv):
     lib, c, t = kv.load(), _cache(kv), kv.Chunk([1, 5], device="cpu")
     good = [c.c, t.c, 0, F, 256, F, 256, None]
