@@ -395,6 +395,9 @@ kv_status kv_evict_host(const kv_problem *p, const kv_host_plan *plan, const voi
  * length -1, which the calls after it post.  kv_paged_evict posts to its
  * workspace's status word, which it zeroes first.
  *
+ * A workspace serves one call at a time: calls, or graphs of them, that may run
+ * side by side need workspaces of their own.
+ *
  * Pages may be shared by units that only read them; a page that a call writes
  * (rows, or weights with add_mass) belongs to one unit.
  */

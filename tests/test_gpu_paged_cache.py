@@ -139,7 +139,10 @@ def _evict(kv, made, into, budgets, sinks, recent, stride):
     (128, 32, 16, "bf16", 1, 60, 30, 30, 2, 28, 1),         # all weights equal; pinned rows only
     (64, 128, 32, "bf16", 0, 300, 1, 299, 1, 0, 3),
     (128, 64, 64, "bf16", 9000, 20000, 1000, 9000, 4, 64, 4096),
-    (64, 64, 64, "bf16", 33000, 70000, 3000, 65000, 4, 64, 0)])
+    (64, 64, 64, "bf16", 33000, 70000, 3000, 65000, 4, 64, 0),
+    # more rows than a cluster's shared memory holds, and just as many
+    (64, 64, 128, "fp16", 131072 + 68, 300000, 3000, 140000, 4, 64, 0),
+    (64, 128, 64, "bf16", 131072 + 67, 200000, 5, 200, 2, 1, 600)])
 def test_evict_keeps_the_largest_weights(cuda_lib, d, page, page2, dtype, lo, hi, blo, bhi, sinks,
                                          recent, levels):
     import torch
