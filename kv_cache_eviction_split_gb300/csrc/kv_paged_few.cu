@@ -647,12 +647,12 @@ __device__ __forceinline__ void merge_row(const DevPaged &C, const DevChunk &T, 
 
 // Weights of tiles [t0, t1): sums over the unit's query rows of 2^(logit - lse), in row
 // order, 64 threads a tile, a thread a key.  Unit by unit: the block first finds the rows'
-// lse, of a cut item from its partials.
+// lse, of a cut item from its partials, while its first tiles' logits and weights arrive.
 __device__ __forceinline__ void add_weights(const DevPaged &C, const DevChunk &T, const FewArgs &A,
                                             bool cut, long long t0, long long t1) {
-    constexpr int kK = kFinishThreads / kFewRows;
+    constexpr int kK = kFinishThreads / kFewRows, kTiles = kFinishThreads / kFewTile;
     __shared__ float sm_m[kK][kFewRows], sm_l[kK][kFewRows], sm_z[kFewRows];
-    const int key = threadIdx.x & 63, group = threadIdx.x >> 6;
+    const int key = threadIdx.x % kFewTile, group = threadIdx.x / kFewTile;
     for (long long t = t0; t < t1;) {
         const int v = (int)(t / A.unit_tiles);
         const long long base = (long long)v * A.unit_tiles, end = min(t1, base + A.unit_tiles);
@@ -663,23 +663,37 @@ __device__ __forceinline__ void add_weights(const DevPaged &C, const DevChunk &T
         const FewItem it(C, A.M, U, 0, kFewRows);
         const int x1 = min((int)(end - base), it.span.total);
         if (x0 >= x1) continue;
+        // what a thread needs of its key in a tile: the rows' logits (-inf past the last or
+        // unseen) and the weight so far
+        float lg[kFewRows], old = 0.f;
+        long long at = -1;
+        auto fetch = [&](int x) {
+            const int j = it.span.tile(x) * kFewTile + key;
+            const float *src = A.logits + (base + x) * (kFewRows * kFewTile) + key;
+#pragma unroll
+            for (int row = 0; row < kFewRows; ++row)
+                lg[row] = row < it.rows ? src[row * kFewTile] : -INFINITY;
+            at = j <= it.t_hi ? page_row(C, U.table, j) : -1;
+            old = at >= 0 ? C.mass[at] : 0.f;
+        };
+        int x = x0 + group;
+        if (x < x1) fetch(x);
         CutItem item;
         int last;
         if (!cut || !cut_of(A, v, item, last)) {
             if (threadIdx.x < it.rows) sm_z[threadIdx.x] = A.lse2[packed_row(C, U, threadIdx.x)];
         } else {
             const int row = threadIdx.x % kFewRows, k = threadIdx.x / kFewRows;
-            const int first = item.cta0 + k, n = row < it.rows ? last + 1 : 0;
-            auto part = [&](int c) {
-                return A.part_ml[(long long)part_slot(c, c == item.cta0) * kFewRows + row];
-            };
             float m = -INFINITY, l = 0.f;
+            if (row < it.rows) {
 #pragma unroll 4
-            for (int c = first; c < n; c += kK) m = fmaxf(m, part(c).x);
-#pragma unroll 4
-            for (int c = first; c < n; c += kK) {
-                const float2 ml = part(c);
-                l += ml.y * shrink(ml.x, m);
+                for (int c = item.cta0 + k; c <= last; c += kK) {
+                    const float2 ml =
+                        A.part_ml[(long long)part_slot(c, c == item.cta0) * kFewRows + row];
+                    const float mm = fmaxf(m, ml.x);
+                    l = l * shrink(m, mm) + ml.y * shrink(ml.x, mm);
+                    m = mm;
+                }
             }
             sm_m[k][row] = m;
             sm_l[k][row] = l;
@@ -694,21 +708,18 @@ __device__ __forceinline__ void add_weights(const DevPaged &C, const DevChunk &T
             }
         }
         __syncthreads();
-        for (int x = x0 + group; x < x1; x += 4) {
-            const int j = it.span.tile(x) * kFewTile + key;
-            const bool in = j <= it.t_hi;
-            const long long at = in ? page_row(C, U.table, j) : -1;
-            const float *lg = A.logits + (base + x) * (kFewRows * kFewTile) + key;
+        while (x < x1) {
             float acc = 0.f;
             bool seen = false;
-#pragma unroll 8
-            for (int row = 0; row < it.rows; ++row) {
-                const float z = lg[row * kFewTile];
-                const bool see = in && z != -INFINITY;
+#pragma unroll
+            for (int row = 0; row < kFewRows; ++row) {
+                const bool see = lg[row] != -INFINITY;
                 seen |= see;
-                acc += see ? ex2_approx(z - sm_z[row]) : 0.f;
+                acc += see ? ex2_approx(lg[row] - sm_z[row]) : 0.f;
             }
-            if (seen && at >= 0) C.mass[at] += acc;
+            if (seen && at >= 0) C.mass[at] = old + acc;
+            x += kTiles;
+            if (x < x1) fetch(x);
         }
         __syncthreads();                             // sm_z is read
     }
