@@ -307,10 +307,9 @@ __device__ __forceinline__ void store_merged(const DevPaged &C, const DevChunk &
     }
 }
 
-// Merges the many-rows kernel's partials of the items that several CTAs held.  ctas: CTAs
-// of the launch that left them, times its phases.
+// Merges the many-rows kernel's partials of the items that several CTAs held.
 cudaError_t launch_many_merge(const DevPaged &C, const DevChunk &T, int layer, const AttendIo &io,
-                              float *lse2, const AttendWs &ws, int ctas, cudaStream_t s);
+                              float *lse2, const AttendWs &ws, int phases, cudaStream_t s);
 // Requests of at most T.few_max query rows a head: `items` items of at most kFewRows rows
 // in all, the largest with max_rows, `blocks` of them at most to a unit, which sees at
 // most `seen` rows of it.

@@ -10,9 +10,9 @@ namespace {
 
 // ---------------------------------------------------------------------------
 // Merge of the many-rows kernel's cut items.  The CTA that held an item's last tile left
-// its description; block (b, y) merges rows of the item of slot b.  Partials are added in
-// order: the result does not depend on timing.  A partial that saw nothing (m = -inf) has
-// no output written.
+// its description; block (b, y) merges rows of CTA b's item of every phase.  Partials are
+// added in order: the result does not depend on timing.  A partial that saw nothing
+// (m = -inf) has no output written.
 // ---------------------------------------------------------------------------
 // Up to 256 rows, few partials: kMergeRows rows a warp, their loads together.
 constexpr int kMergeRows = 4;
@@ -20,66 +20,74 @@ template <typename X, int D>
 __global__ void __launch_bounds__(128)
 merge_many_kernel(const DevPaged C, const DevChunk T, int layer, const AttendIo io, float *lse2,
                   const CutItem *__restrict__ cut, const float2 *__restrict__ part_ml,
-                  const float *__restrict__ part_o) {
+                  const float *__restrict__ part_o, int phases) {
     constexpr int kV = D / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
     pdl_trigger();
-    const CutItem it = cut[blockIdx.x];
     const int row0 = ((int)blockIdx.y * 4 + warp) * kMergeRows;
-    if (it.unit < 0 || row0 >= it.rows) return;
-    const int parts = (int)blockIdx.x - it.cta0 + 1;
-    auto slot_row = [&](int p, int r) {
-        return (long long)part_slot(it.cta0 + p, p == 0) * kManyRows + min(row0 + r, it.rows - 1);
-    };
-    float m[kMergeRows], l[kMergeRows], acc[kMergeRows][kV];
-#pragma unroll
-    for (int r = 0; r < kMergeRows; ++r) {
-        m[r] = -INFINITY;
-        l[r] = 0.f;
-#pragma unroll
-        for (int i = 0; i < kV; ++i) acc[r][i] = 0.f;
-    }
-    for (int p = 0; p < parts; ++p)
-#pragma unroll
-        for (int r = 0; r < kMergeRows; ++r) m[r] = fmaxf(m[r], part_ml[slot_row(p, r)].x);
-#pragma unroll 2
-    for (int p = 0; p < parts; ++p)
+    for (int g = 0; g < phases; ++g) {
+        const int last = g * kManyCtas + (int)blockIdx.x;
+        const CutItem it = cut[last];
+        if (it.unit < 0 || row0 >= it.rows) continue;
+        const int parts = last - it.cta0 + 1;
+        auto slot_row = [&](int p, int r) {
+            return (long long)part_slot(it.cta0 + p, p == 0) * kManyRows +
+                   min(row0 + r, it.rows - 1);
+        };
+        float m[kMergeRows], l[kMergeRows], acc[kMergeRows][kV];
 #pragma unroll
         for (int r = 0; r < kMergeRows; ++r) {
-            const long long at = slot_row(p, r);
-            const float2 ml = part_ml[at];
-            const float f = shrink(ml.x, m[r]);
-            l[r] += ml.y * f;
-            const float *src = part_o + at * D + lane * kV;
+            m[r] = -INFINITY;
+            l[r] = 0.f;
 #pragma unroll
-            for (int i = 0; i < kV; ++i) {
-                const float x = src[i];
-                acc[r][i] += f == 0.f ? 0.f : x * f;
-            }
+            for (int i = 0; i < kV; ++i) acc[r][i] = 0.f;
         }
+        for (int p = 0; p < parts; ++p)
 #pragma unroll
-    for (int r = 0; r < kMergeRows; ++r)
-        if (row0 + r < it.rows)
-            store_merged<X, D>(C, T, layer, io, lse2, it, row0 + r, m[r], l[r], acc[r]);
+            for (int r = 0; r < kMergeRows; ++r) m[r] = fmaxf(m[r], part_ml[slot_row(p, r)].x);
+#pragma unroll 2
+        for (int p = 0; p < parts; ++p)
+#pragma unroll
+            for (int r = 0; r < kMergeRows; ++r) {
+                const long long at = slot_row(p, r);
+                const float2 ml = part_ml[at];
+                const float f = shrink(ml.x, m[r]);
+                l[r] += ml.y * f;
+                float x[kV];
+                if constexpr (kV == 4)
+                    *reinterpret_cast<float4 *>(x) =
+                        *reinterpret_cast<const float4 *>(part_o + at * D + lane * kV);
+                else
+                    *reinterpret_cast<float2 *>(x) =
+                        *reinterpret_cast<const float2 *>(part_o + at * D + lane * kV);
+#pragma unroll
+                for (int i = 0; i < kV; ++i) acc[r][i] += f == 0.f ? 0.f : x[i] * f;
+            }
+#pragma unroll
+        for (int r = 0; r < kMergeRows; ++r)
+            if (row0 + r < it.rows)
+                store_merged<X, D>(C, T, layer, io, lse2, it, row0 + r, m[r], l[r], acc[r]);
+    }
 }
 
 template <typename X, int D>
 cudaError_t merge(const DevPaged &C, const DevChunk &T, int layer, const AttendIo &io, float *lse2,
-                  const AttendWs &ws, int ctas, cudaStream_t s) {
-    return launch_dependent(merge_many_kernel<X, D>, dim3(ctas, kManyRows / (4 * kMergeRows)), 128, 0,
-                            s, C, T, layer, io, lse2, ws.cut, ws.part_ml, ws.part_o);
+                  const AttendWs &ws, int phases, cudaStream_t s) {
+    return launch_dependent(merge_many_kernel<X, D>,
+                            dim3(kManyCtas, kManyRows / (4 * kMergeRows)), 128, 0, s, C, T, layer,
+                            io, lse2, ws.cut, ws.part_ml, ws.part_o, phases);
 }
 
 }  // namespace
 
 cudaError_t launch_many_merge(const DevPaged &C, const DevChunk &T, int layer, const AttendIo &io,
-                              float *lse2, const AttendWs &ws, int ctas, cudaStream_t s) {
+                              float *lse2, const AttendWs &ws, int phases, cudaStream_t s) {
     if (C.dtype == KV_FP16)
-        return C.d == 64 ? merge<Fp16, 64>(C, T, layer, io, lse2, ws, ctas, s)
-                         : merge<Fp16, 128>(C, T, layer, io, lse2, ws, ctas, s);
-    return C.d == 64 ? merge<Bf16, 64>(C, T, layer, io, lse2, ws, ctas, s)
-                     : merge<Bf16, 128>(C, T, layer, io, lse2, ws, ctas, s);
+        return C.d == 64 ? merge<Fp16, 64>(C, T, layer, io, lse2, ws, phases, s)
+                         : merge<Fp16, 128>(C, T, layer, io, lse2, ws, phases, s);
+    return C.d == 64 ? merge<Bf16, 64>(C, T, layer, io, lse2, ws, phases, s)
+                     : merge<Bf16, 128>(C, T, layer, io, lse2, ws, phases, s);
 }
 
 namespace {

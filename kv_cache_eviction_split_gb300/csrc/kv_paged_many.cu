@@ -716,7 +716,7 @@ cudaError_t many(const DevPaged &C, const DevChunk &T, const ManyArgs &A, const 
         e = launch_dependent(many_kernel<E, D>, dim3(kManyCtas), kThreads, Ly::kTotal, s, mk, mv, C,
                              T, A);
     if (e == cudaSuccess)
-        e = launch_many_merge(C, T, A.layer, A.io, A.lse2, ws, kManyCtas * A.phases, s);
+        e = launch_many_merge(C, T, A.layer, A.io, A.lse2, ws, A.phases, s);
     return e;
 }
 
