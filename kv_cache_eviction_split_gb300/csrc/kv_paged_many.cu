@@ -14,7 +14,7 @@
 // cores work for one lane, the other lane's four warps take their softmax.  O is rescaled
 // only when a row's maximum rises by more than 2^8.
 //
-// One rounding of P (2^-9 relative each, random signs) adds to an output about as much as
+// One rounding of P (at most 2^-8 relative in bf16, random signs) adds to an output about as much as
 // its own rounding does; two parts, as in the few-rows kernel, would cost half as many
 // products again in the kernel's bottleneck.
 //
@@ -415,16 +415,19 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             // the description is read
             __syncwarp();
             if (lane == 0) mbar_arrive(&i_empty[i % kItems]);
-            // The next item's Q is read from memory while this one's last products run, and
-            // handed over before this one's output is written.
+            // The next item's Q goes to shared memory beside this one's last P V (its last
+            // S is complete), so that S of the next follows at once.
             w = item(i + 1, ok);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            uint4 q[D / 8];
             nxt.any = false;
             if (w) {
                 nxt = row_of(w);
-                if (nxt.any) load_q(nxt, q);
+                if (nxt.any) {
+                    uint4 q[D / 8];
+                    load_q(nxt, q);
+                    store_q(nxt, w, q);
+                }
             }
             if (begun) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&o_final[L], (uint32_t)(ic & 1), s_abort,
@@ -433,7 +436,6 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                 tc_fence_after();
                 ++ic;
             }
-            if (nxt.any) store_q(nxt, w, q);
             const float mm = m - E::kShift;
             const long long prow =
                 (long long)part_slot(cta, x0 == 0) * kManyRows + L * 128 + rr;
