@@ -1,14 +1,25 @@
 // kv_paged_mass.cu -- accumulated attention weights of prompt chunks: for every cache row j,
 // mass_j += sum over the query rows that see it of 2^(s c - lse2), after the attention pass
-// has left each row's lse.  Bound by the powers of two (one per pair) and the K Q^T products.
+// has left each row's lse.
 //
 // Keys are the rows of the product: S^T = K Q^T with 128 keys x 128 query rows, so that a
 // thread owns a key and adds its weights up in a register, in row order: no atomics, and
-// no exchange between threads.  An item is 256 keys (two tiles, one for each half of the key
-// warps) of one unit, against every tile of 128 query rows that sees any of them; K stays
-// in shared memory for the item (the next one's loads meanwhile), packed Q tiles stream
-// through a ring (32 KB per two products at d = 128).  The query rows that see key j are a
-// run of packed rows, [ (j - t0) G, (j + window - t0) G ), so the mask is two bounds.
+// no exchange between threads but one.  An item is 256 keys (two tiles) of one unit, against
+// every tile of 128 query rows that sees any of them; K stays in shared memory for the item
+// (the next one's loads meanwhile), packed Q tiles stream through a ring (32 KB per two
+// products at d = 128).  Four groups of four warps take the two key tiles' products, of even
+// and odd row tiles, each from a tensor-memory buffer of its own: four warps a scheduler hide
+// each other's waits and loads.  At the item's end the odd rows' sums go to the even rows'
+// threads.  The query rows that see key j are a run of packed rows,
+// [ (j - t0) G, (j + window - t0) G ), so the mask is two bounds.
+//
+// Measured (2 requests, 301 .. 511 new tokens of 32 query heads over 8 x 13107 .. 32768 rows,
+// d = 128, bf16): 168 us of the call's 447, where the products alone would take 90.  Both
+// operands of a product come from shared memory, as much of its bandwidth as of the tensor
+// cores' time, which the Q tiles' arrival and the rows' lse share.  Without the exponentials
+// 25 us less, with half the products 20 us less, with half the Q traffic the same.  Eight
+// key warps were as fast until the two tiles' products were issued after one wait (178 us);
+// an issuing warp for each tile was slower (172 us).
 #include <type_traits>
 
 #include "kv_paged_attend.cuh"
@@ -17,17 +28,16 @@ namespace kvevict {
 namespace {
 using namespace sm100;
 
-constexpr int kThreads = 12 * 32;
+constexpr int kThreads = 20 * 32;
 constexpr int kKWarp = 0, kMmaWarp = 1, kQWarp = 2, kSchedWarp = 3, kKeyWarp = 4;
-// Registers a thread after the split, of 168 at launch (384 x 168 = 128 x 104 + 256 x 200):
-// a key thread holds its 128 logits and the rows' lse read ahead (at 168 it read them just
-// before use, and the exponentials took 1500 clocks a tile).
-constexpr int kLoadRegs = 104, kKeyRegs = 200;
+// Registers a thread after the split, of 96 at launch (640 x 96 = 128 x 64 + 512 x 104).
+constexpr int kLoadRegs = 64, kKeyRegs = 104;
 constexpr int kBlockBytes = 128 * 128;       // [128 rows][64 columns], 128 B swizzle
 constexpr int kGroup = 2;                    // key tiles per item
 constexpr int kGroupCost = 2;                // an item's own cost in row tiles
 constexpr int kItems = 3;                    // items described ahead
 constexpr int kQSt = 3;                      // Q ring
+constexpr int kLSt = 2;                      // ring of the rows' lse: even, a warp sees every other step
 
 struct Item {
     int stop;
@@ -43,13 +53,11 @@ struct Layout {
     static constexpr int kOp = (D / 64) * kBlockBytes;
     static constexpr int kK = 0;                          // [2 items][kGroup]
     static constexpr int kQ = 2 * kGroup * kOp;
-    static constexpr int kLse = kQ + kQSt * kOp;          // [kQSt][128] -lse2
-    static constexpr int kBars = kLse + kQSt * 128 * 4;
-    static constexpr int kNumBars = 2 * 2 + 2 * kQSt + 2 * 4 + 1 + 2 * kItems;
-    static constexpr int kMisc = (kBars + kNumBars * 8 + 15) / 16 * 16;
-    static constexpr int kDesc = kMisc + 16;
-    static constexpr int kTotal = kDesc + kItems * (int)sizeof(Item);
-    static_assert(kTotal + 1024 <= 227 * 1024, "with cut_run's and TMEM's few static words");
+    static constexpr int kLse = kQ + kQSt * kOp;          // [kLSt][128] -lse2
+    static constexpr int kAcc = kLse + kLSt * 128 * 4;    // [kGroup][128] sums of odd row tiles
+    static constexpr int kTotal = kAcc + kGroup * 128 * 4;
+    // the static words lie below the first 1024 bytes' end
+    static_assert(kTotal + 1024 <= 227 * 1024, "fits with the static words");
 };
 
 struct MassArgs {
@@ -86,16 +94,17 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);   // uniform
     const int lane = threadIdx.x & 31;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Ly::kBars);
-    uint64_t *k_full = bars, *k_empty = k_full + 2;          // [item parity]
-    uint64_t *q_full = k_empty + 2, *q_empty = q_full + kQSt;
-    uint64_t *s_full = q_empty + kQSt, *s_free = s_full + 4;  // [2 (row tile parity) + key tile]
-    uint64_t *mma_done = s_free + 4;
-    uint64_t *i_full = mma_done + 1, *i_empty = i_full + kItems;
-    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + Ly::kMisc);
-    volatile int *s_abort = reinterpret_cast<volatile int *>(s_tmem + 1);
-    Item *s_item = reinterpret_cast<Item *>(smem + Ly::kDesc);
+    __shared__ uint64_t k_full[2], k_empty[2];               // [item parity]
+    __shared__ uint64_t q_full[kQSt], q_empty[kQSt], l_full[kLSt], l_empty[kLSt];
+    __shared__ uint64_t s_full[2], s_free[2];                // [row tile parity]
+    __shared__ uint64_t a_full[kGroup], a_empty[kGroup];     // the odd row tiles' sums
+    __shared__ uint64_t mma_done[1], i_full[kItems], i_empty[kItems];
+    __shared__ Item s_item[kItems];
+    __shared__ uint32_t s_tmem[1];
+    __shared__ int s_abort_word;
+    volatile int *s_abort = &s_abort_word;
     float *s_lse = reinterpret_cast<float *>(smem + Ly::kLse);
+    float *s_acc = reinterpret_cast<float *>(smem + Ly::kAcc);
 
     if (threadIdx.x == 0) {
         *s_abort = (smem_u32(smem) & 1023u) ? 1 : 0;
@@ -104,17 +113,25 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             mbar_init(&k_empty[i], 1);
         }
         for (int i = 0; i < kQSt; ++i) {
-            mbar_init(&q_full[i], 2);        // the copy, and the rows' lse
-            mbar_init(&q_empty[i], 1 + 8);   // the products, and the key warps (lse)
+            mbar_init(&q_full[i], 1);
+            mbar_init(&q_empty[i], 1);
         }
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kLSt; ++i) {
+            mbar_init(&l_full[i], 1);
+            mbar_init(&l_empty[i], 8);       // the warps of the row tile's parity
+        }
+        for (int i = 0; i < kGroup; ++i) {
+            mbar_init(&a_full[i], 4);
+            mbar_init(&a_empty[i], 4);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&s_free[i], 4);
+            mbar_init(&s_free[i], 8);
         }
         mbar_init(mma_done, 1);
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&i_full[i], 1);
-            mbar_init(&i_empty[i], 3 + 8);
+            mbar_init(&i_empty[i], 3 + 16);
         }
         fence_barrier_init();
         prefetch_tensormap(&tm_k);
@@ -151,13 +168,14 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     if (warp >= kKeyWarp) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kKeyRegs));
         // ---------------------------------------------------------------- keys
-        const int k = (warp - kKeyWarp) >> 2;             // key tile of the item
+        const int b = (warp - kKeyWarp) >> 2;             // tensor-memory buffer
+        const int k = b & 1, par = b >> 1;                // key tile of the item, row tiles' parity
         const int quarter = warp & 3;
         const int rr = quarter * 32 + lane;
         const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
         const float cs = A.M.scale_log2;
         const float2 cs2 = make_float2(cs, cs);
-        int rc = 0, used[2] = {0, 0};
+        int rc = 0, summed = 0;
         for (int i = 0;; ++i) {
             const Item *w = item(i, ok);
             ok = __all_sync(0xffffffffu, ok);
@@ -183,40 +201,47 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                 last < A.M.sinks || A.M.window == 0
                     ? rows
                     : (int)min((long long)rows, max(0ll, ((long long)key0 + A.M.window - t0) * G));
-            float acc = 0.f;
-            for (int rt = rt0; rt < rt1; ++rt, ++rc) {
-                const int qs = rc % kQSt, par = rc & 1;
-                ok = mbar_wait(&q_full[qs], (uint32_t)((rc / kQSt) & 1), s_abort, C.wait_ns);
-                if (mine) {
-                    const int u = par ? used[1] : used[0];
-                    ok = ok && mbar_wait(&s_full[2 * par + k], (uint32_t)(u & 1), s_abort,
-                                         C.wait_ns);
-                    if (par) ++used[1]; else ++used[0];
+            // the key's weight so far is looked up beside the first steps: its page here, its
+            // value after the first
+            const int page = par == 0 && held && r_lo < r_hi ? table[j >> C.ps_log2] : -1;
+            float *to = nullptr;
+            float acc = 0.f, old = 0.f;
+            auto find = [&]() {
+                if (to == nullptr && page >= 0 && page < C.num_pages) {
+                    to = C.mass + ((long long)page << C.ps_log2) + (j & (C.ps - 1));
+                    old = *to;
                 }
+            };
+            const int step0 = rc - rt0;
+            rc += rt1 - rt0;
+            for (int rt = rt0 + ((step0 + rt0 + par) & 1); rt < rt1; rt += 2) {
+                const int step = step0 + rt, ls = step % kLSt;
+                ok = mbar_wait(&l_full[ls], (uint32_t)((step / kLSt) & 1), s_abort, C.wait_ns);
+                ok = ok && mbar_wait(&s_full[par], (uint32_t)((step >> 1) & 1), s_abort, C.wait_ns);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 if (mine) {
                     tc_fence_after();
                     const int row0 = rt * 128;
                     const bool all = row0 >= a_lo && row0 + 128 <= a_hi;
-                    const uint32_t base = tmem + lane_addr + 128 * (2 * par + k);
-                    const float4 *lse = reinterpret_cast<const float4 *>(s_lse + qs * 128);
+                    const uint32_t base = tmem + lane_addr + 128 * b;
+                    const float4 *lse = reinterpret_cast<const float4 *>(s_lse + ls * 128);
                     float2 sum[4];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) sum[c] = make_float2(0.f, 0.f);
-                    float s[4][32];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld32(base + 32 * c, s[c]);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) reg_fence(s[c]);
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&s_free[2 * par + k]);
-// every row of the tile sees the thread's key, or a run of its bits does
+                    // every row of the tile sees the thread's key, or a run of its bits does
                     auto add = [&](auto masked) {
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
+                            float s[32];
+                            tmem_ld32(base + 32 * c, s);
+                            tmem_ld_wait();
+                            reg_fence(s);
+                            if (c == 3) {
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(&s_free[par]);
+                            }
                             uint32_t see = 0;
                             if (masked)
                                 see = low_bits(r_hi - row0 - 32 * c) &
@@ -224,12 +249,10 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
 #pragma unroll
                             for (int x = 0; x < 32; x += 4) {
                                 const float4 z = lse[c * 8 + x / 4];
-                                const float2 e0 =
-                                    __ffma2_rn(make_float2(s[c][x], s[c][x + 1]), cs2,
-                                               make_float2(z.x, z.y));
-                                const float2 e1 =
-                                    __ffma2_rn(make_float2(s[c][x + 2], s[c][x + 3]), cs2,
-                                               make_float2(z.z, z.w));
+                                const float2 e0 = __ffma2_rn(make_float2(s[x], s[x + 1]), cs2,
+                                                             make_float2(z.x, z.y));
+                                const float2 e1 = __ffma2_rn(make_float2(s[x + 2], s[x + 3]), cs2,
+                                                             make_float2(z.z, z.w));
                                 float2 p0 = make_float2(ex2_approx(e0.x), ex2_approx(e0.y));
                                 float2 p1 = make_float2(ex2_approx(e1.x), ex2_approx(e1.y));
                                 if (masked) {
@@ -243,20 +266,33 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                             }
                         }
                     };
-                    if (all) add(std::false_type{});
+                    if (__all_sync(0xffffffffu, all)) add(std::false_type{});
                     else add(std::true_type{});
                     const float2 a = __fadd2_rn(__fadd2_rn(sum[0], sum[1]),
                                                 __fadd2_rn(sum[2], sum[3]));
                     acc += a.x + a.y;
+                } else if (lane == 0) {
+                    mbar_arrive(&s_free[par]);
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&q_empty[qs]);
+                if (lane == 0) mbar_arrive(&l_empty[ls]);
+                find();
             }
             if (!ok) break;
-            if (held && r_lo < r_hi) {
-                const long long at = page_row(C, table, j);
-                if (at >= 0) C.mass[at] += acc;
-            }
+            if (!mine) continue;
+            // the odd row tiles' sums to the even ones' threads
+            float *part = s_acc + k * 128 + rr;
+            ok = __all_sync(0xffffffffu,
+                            par ? mbar_wait(&a_empty[k], (uint32_t)(summed & 1) ^ 1u, s_abort, C.wait_ns)
+                                : mbar_wait(&a_full[k], (uint32_t)(summed & 1), s_abort, C.wait_ns));
+            if (!ok) break;
+            ++summed;
+            if (par) *part = acc;
+            else acc += *part;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(par ? &a_full[k] : &a_empty[k]);
+            find();
+            if (to) *to = old + acc;
         }
         if (!ok && lane == 0) expired();
     } else {
@@ -354,27 +390,40 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                 const long long prow0 = w->prow0;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&i_empty[i % kItems]);
-                for (int rt = rt0; rt < rt1; ++rt, ++cnt) {
-                    const int s = cnt % kQSt;
-                    float z[4];
+                // the rows' lse are read a step ahead: their latency is about a step's products
+                float z[4];
+                auto fetch = [&](int rt) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int row = rt * 128 + lane * 4 + k;
                         z[k] = row < rows ? -A.lse2[prow0 + row] : 0.f;
                     }
+                };
+                fetch(rt0);
+                for (int rt = rt0; rt < rt1; ++rt, ++cnt) {
+                    const int s = cnt % kQSt;
+                    const int ls = cnt % kLSt;
                     ok = mbar_wait(&q_empty[s], (uint32_t)((cnt / kQSt) & 1) ^ 1u, s_abort, C.wait_ns);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
-                    *reinterpret_cast<float4 *>(s_lse + s * 128 + lane * 4) =
-                        make_float4(z[0], z[1], z[2], z[3]);
-                    __syncwarp();
                     if (lane == 0) {
-                        mbar_arrive(&q_full[s]);
                         mbar_arrive_expect_tx(&q_full[s], Ly::kOp);
                         for (int kb = 0; kb < D / 64; ++kb)
                             tma_load_2d(smem + Ly::kQ + s * Ly::kOp + kb * kBlockBytes, &tm_q,
                                         &q_full[s], kb * 64, (int)(prow0 + rt * 128));
                     }
+                    __syncwarp();
+                    ok = mbar_wait(&l_empty[ls], (uint32_t)((cnt / kLSt) & 1) ^ 1u, s_abort, C.wait_ns);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) {
+                        ++cnt;                       // its copy is drained below
+                        break;
+                    }
+                    *reinterpret_cast<float4 *>(s_lse + ls * 128 + lane * 4) =
+                        make_float4(z[0], z[1], z[2], z[3]);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&l_full[ls]);
+                    if (rt + 1 < rt1) fetch(rt + 1);
                 }
             }
             if (!ok && lane == 0) expired();
@@ -393,8 +442,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                 };
                 const uint32_t tm = (uint32_t)uni((int)tmem);
                 constexpr uint32_t idesc = E::kHalf ? idesc_f16_f32(128, 128) : idesc_bf16_f32(128, 128);
-                int rc = 0;                      // row tiles so far
-                int used[4] = {0, 0, 0, 0};      // products into each buffer
+                int rc = 0, s = 0, turn = 0;     // row tiles so far, Q slot, its round
                 for (int i = 0;; ++i) {
                     const Item *w = item(i, ok);
                     ok = __all_sync(0xffffffffu, ok);
@@ -403,39 +451,33 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                     __syncwarp();
                     if (el) mbar_arrive(&i_empty[i % kItems]);
                     ok = wait(&k_full[ks], i >> 1);
+                    const uint64_t ka = sdesc_k_sw128(smem_u32(smem + Ly::kK) + ks * kGroup * Ly::kOp);
                     for (int r = 0; ok && r < steps; ++r, ++rc) {
-                        const int s = rc % kQSt;
-                        ok = wait(&q_full[s], rc / kQSt);
+                        const int par = rc & 1;
+                        ok = wait(&q_full[s], turn) && wait(&s_free[par], (rc >> 1) + 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t qb = sdesc_k_sw128(smem_u32(smem + Ly::kQ) + s * Ly::kOp);
 #pragma unroll
                         for (int k = 0; k < kGroup; ++k) {
-                            if (!ok || k >= tiles) continue;
+                            if (k >= tiles) continue;
+                            const uint32_t col = tm + 256 * par + 128 * k;
 #pragma unroll
-                            for (int par = 0; par < 2; ++par) {
-                                if ((rc & 1) != par) continue;
-                                const int b = 2 * par + k;
-                                ok = wait(&s_free[b], used[b] + 1);
-                                if (!ok) continue;
-                                ++used[b];
-                                tc_fence_after();
-                                const uint64_t ka = sdesc_k_sw128(
-                                    smem_u32(smem + Ly::kK + (ks * kGroup + k) * Ly::kOp));
-                                const uint64_t qb =
-                                    sdesc_k_sw128(smem_u32(smem + Ly::kQ + s * Ly::kOp));
-#pragma unroll
-                                for (int kb = 0; kb < D / 64; ++kb)
-#pragma unroll
-                                    for (int kk = 0; kk < 4; ++kk) {
-                                        const uint32_t o = kb * kBlockBytes + kk * 32;
-                                        if (kb | kk)
-                                            mma_ss_e<true>(tm + 128 * b, sdesc_add(ka, o),
-                                                           sdesc_add(qb, o), idesc, el);
-                                        else
-                                            mma_ss_e<false>(tm + 128 * b, ka, qb, idesc, el);
-                                    }
-                                mma_commit_e(&s_full[b], el);
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                const uint32_t o = (kk >> 2) * kBlockBytes + (kk & 3) * 32;
+                                if (kk)
+                                    mma_ss_e<true>(col, sdesc_at(ka, k * Ly::kOp + o),
+                                                   sdesc_at(qb, o), idesc, el);
+                                else
+                                    mma_ss_e<false>(col, sdesc_at(ka, k * Ly::kOp), qb, idesc, el);
                             }
                         }
-                        if (ok) mma_commit_e(&q_empty[s], el);
+                        mma_commit_e(&s_full[par], el);
+                        mma_commit_e(&q_empty[s], el);
+                        if (++s == kQSt) {
+                            s = 0;
+                            turn ^= 1;
+                        }
                     }
                     if (ok) mma_commit_e(&k_empty[ks], el);
                 }
