@@ -23,9 +23,9 @@
 // they also bring their Q rows into shared memory and write the output.  Tiles no lane sees
 // are skipped.
 //
-// Measured (32 query heads on 8, d = 128, bf16): 2048 tokens over 67584 rows 1.48 ms, 1.51
+// Measured (32 query heads on 8, d = 128, bf16): 2048 tokens over 67584 rows 1.46 ms, 1.52
 // PFLOP/s, where the card's sustained library rate is 1.72 (it holds the clock to ~1.7 GHz);
-// a prompt of 8192 tokens, window 4096, 347 us, 1.19 PFLOP/s: 6.7 items a CTA, whose ends
+// a prompt of 8192 tokens, window 4096, 340 us, 1.21 PFLOP/s: 6.7 items a CTA, whose ends
 // cost about four tiles each (the last products, the output's stores: 12 us in all, the
 // first softmax) and the masked halves of the tiles at the window's and diagonal's edges.
 #include "kv_paged_attend.cuh"
@@ -43,6 +43,9 @@ constexpr int kBlockBytes = 128 * 128;       // [128 rows][64 columns], 128 B sw
 constexpr uint32_t kOCol = 256;              // O of lane L at column kOCol + 128 L
 
 constexpr int kItems = 3;                    // items described ahead
+// P V of a tile begins when P of its first kPFirst keys is written, beside the exponentials
+// of the others (8192 tokens, window 4096, in us: 32 keys 344, 64 339, 96 343, all 128 346).
+constexpr int kPFirst = 64;
 
 // Query rows of one lane in an item, and the tiles (counted as in the item's span) of
 // which it sees a key: [0, ns) and [a, b).
@@ -75,7 +78,7 @@ struct Layout {
     static constexpr int kK = 2 * kOp;
     static constexpr int kV = kK + kKSt * kOp;
     static constexpr int kBars = kV + kVSt * kOp;
-    static constexpr int kNumBars = 2 * kKSt + 2 * kVSt + 10 + 1 + 2 * kItems;
+    static constexpr int kNumBars = 2 * kKSt + 2 * kVSt + 12 + 1 + 2 * kItems;
     static constexpr int kMisc = (kBars + kNumBars * 8 + 15) / 16 * 16;
     static constexpr int kCut = kMisc + 32;               // [kMaxPhases] CutItem
     static constexpr int kRuns = kCut + kMaxPhases * (int)sizeof(CutItem);
@@ -163,8 +166,9 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     uint64_t *v_full = k_empty + Ly::kKSt, *v_empty = v_full + Ly::kVSt;
     uint64_t *q_full = v_empty + Ly::kVSt;   // [lane]: Q rows are in shared memory (4 warps)
     uint64_t *s_full = q_full + 2;           // [lane]: S of the lane's tile is complete
-    uint64_t *p_full = s_full + 2;           // [lane]: P written (4 warps)
-    uint64_t *o_final = p_full + 2;          // [lane]: the lane's last P V of the item is done
+    uint64_t *p_full = s_full + 2;           // [lane]: P of the first kPFirst keys written (4 warps)
+    uint64_t *p_rest = p_full + 2;           // [lane]: all of P
+    uint64_t *o_final = p_rest + 2;          // [lane]: the lane's last P V of the item is done
     uint64_t *o_empty = o_final + 2;         // [lane]: O read out (4 warps)
     uint64_t *mma_done = o_empty + 2;
     uint64_t *i_full = mma_done + 1, *i_empty = i_full + kItems;   // item descriptions
@@ -191,6 +195,7 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             mbar_init(&q_full[L], 4);
             mbar_init(&s_full[L], 1);
             mbar_init(&p_full[L], 4);
+            mbar_init(&p_rest[L], 4);
             mbar_init(&o_final[L], 1);
             mbar_init(&o_empty[L], 4);
         }
@@ -405,13 +410,19 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                         pw[i >> 1] = E::pack(p.x, p.y);
                     }
                     tmem_st16u(s_base + 16 * c, pw);
+                    if (c == kPFirst / 32 - 1) {
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&p_full[L]);
+                    }
                 }
                 const float2 a = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
                 l += a.x + a.y;
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[L]);
+                if (lane == 0) mbar_arrive(&p_rest[L]);
                 ++sc;
             }
             if (!ok) break;
@@ -658,7 +669,15 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                                     else
                                         mma_ts_e<true>(o_col, s_col, vb, idesc_o, el);
 #pragma unroll
-                                    for (int q = 1; q < kManyTile / 16; ++q)
+                                    for (int q = 1; q < kPFirst / 16; ++q)
+                                        mma_ts_e<true>(o_col, s_col + q * 8,
+                                                       sdesc_at(vb, q * 16 * 128), idesc_o, el);
+                                    ok = wait(&p_rest[L], sc[L]);
+                                }
+                                if (ok) {
+                                    tc_fence_after();
+#pragma unroll
+                                    for (int q = kPFirst / 16; q < kManyTile / 16; ++q)
                                         mma_ts_e<true>(o_col, s_col + q * 8,
                                                        sdesc_at(vb, q * 16 * 128), idesc_o, el);
                                     if (L == 1 || !two) mma_commit_e(&v_empty[vs], el);
