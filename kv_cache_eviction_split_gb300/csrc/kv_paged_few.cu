@@ -26,8 +26,8 @@
 // kv_paged.cuh has the rules and what both forms take.
 //
 // Measured (d = 128, bf16, one layer's call).  HBM-bound: 8 requests of 4915 .. 39321 rows
-// in 8 heads each 116 us (6.3 TB/s); 4 heads of 131072 rows, weights added, 68 us of which
-// the tiles 47 (5.7 TB/s) and the finish 12.5; 16 requests, window 4096 of longer tables,
+// in 8 heads each 116 us (6.3 TB/s); 4 heads of 131072 rows, weights added, 67 us of which
+// the tiles 47 (5.7 TB/s) and the finish 12; 16 requests, window 4096 of longer tables,
 // 48 us (5.6 TB/s).  Latency-bound: 8 heads of 1638 rows 6.4 us on the GPU.  As products of
 // 128-row tiles in tensor memory the same work would be padded 32 times over.
 #include <algorithm>
@@ -655,6 +655,7 @@ __device__ __forceinline__ void merge_row(const DevPaged &C, const DevChunk &T, 
 // Weights of tiles [t0, t1): sums over the unit's query rows of 2^(logit - lse), in row
 // order, 64 threads a tile, a thread a key.  Unit by unit: the block first finds the rows'
 // lse, of a cut item from its partials, while its first tiles' logits and weights arrive.
+template <int kRows>
 __device__ __forceinline__ void add_weights(const DevPaged &C, const DevChunk &T, const FewArgs &A,
                                             bool cut, long long t0, long long t1) {
     constexpr int kK = kFinishThreads / kFewRows, kTiles = kFinishThreads / kFewTile;
@@ -672,15 +673,15 @@ __device__ __forceinline__ void add_weights(const DevPaged &C, const DevChunk &T
         if (x0 >= x1) continue;
         // what a thread needs of its key in a tile: the rows' logits (-inf past the last or
         // unseen) and the weight so far
-        float lg[kFewRows], old = 0.f;
-        long long at = -1;
+        float lg[kRows], old = 0.f;
+        int at = -1;                                 // pool rows are counted in 31 bits
         auto fetch = [&](int x) {
             const int j = it.span.tile(x) * kFewTile + key;
             const float *src = A.logits + (base + x) * (kFewRows * kFewTile) + key;
 #pragma unroll
-            for (int row = 0; row < kFewRows; ++row)
+            for (int row = 0; row < kRows; ++row)
                 lg[row] = row < it.rows ? src[row * kFewTile] : -INFINITY;
-            at = j <= it.t_hi ? page_row(C, U.table, j) : -1;
+            at = j <= it.t_hi ? (int)page_row(C, U.table, j) : -1;
             old = at >= 0 ? C.mass[at] : 0.f;
         };
         int x = x0 + group;
@@ -719,7 +720,7 @@ __device__ __forceinline__ void add_weights(const DevPaged &C, const DevChunk &T
             float acc = 0.f;
             bool seen = false;
 #pragma unroll
-            for (int row = 0; row < kFewRows; ++row) {
+            for (int row = 0; row < kRows; ++row) {
                 const bool see = lg[row] != -INFINITY;
                 seen |= see;
                 acc += see ? ex2_approx(lg[row] - sm_z[row]) : 0.f;
@@ -733,8 +734,8 @@ __device__ __forceinline__ void add_weights(const DevPaged &C, const DevChunk &T
 }
 
 // cut: whether the tiles came from the cut form (else every unit's lse2 is written).
-template <typename E, int D>
-__global__ void __launch_bounds__(kFinishThreads)
+template <typename E, int D, int NT>
+__global__ void __launch_bounds__(kFinishThreads, NT == 1 ? 6 : 5)
 few_finish_kernel(const DevPaged C, const DevChunk T, const FewArgs A, int merge_rows, bool cut) {
     pdl_wait();
     pdl_trigger();
@@ -751,7 +752,7 @@ few_finish_kernel(const DevPaged C, const DevChunk T, const FewArgs A, int merge
     const long long tiles = (long long)units * A.unit_tiles;
     const int blocks = (int)gridDim.x - merges;
     const long long per = (tiles + blocks - 1) / blocks, t0 = ((int)blockIdx.x - merges) * per;
-    add_weights(C, T, A, cut, min(tiles, t0), min(tiles, t0 + per));
+    add_weights<NT * 8>(C, T, A, cut, min(tiles, t0), min(tiles, t0 + per));
 }
 
 template <typename E, int D, int NT, int kCluster>
@@ -772,10 +773,11 @@ cudaError_t few(const DevPaged &C, const DevChunk &T, const FewArgs &A, cudaStre
     if (e == cudaSuccess && (kCluster == 0 || A.logits)) {
         const int rows = NT * 8 < T.max_t * (long long)C.G ? NT * 8 : T.max_t * C.G;
         const long long merges = kCluster == 0 ? (long long)C.R * C.H * rows : 0;
-        // eight tiles a block, while that fills the SMs at most once
+        // eight tiles a block, or what one round of blocks (six an SM) needs (4 heads of 131072
+        // rows, in us: 4 tiles 68.2, 8 66.5, 12 66.4, 16 67.5)
         const long long tiles = A.logits ? (long long)C.R * C.H * A.unit_tiles : 0;
-        const long long adds = std::min<long long>((tiles + 7) / 8, 8 * 152);
-        e = launch_dependent(few_finish_kernel<E, D>, dim3((unsigned)(merges + adds)),
+        const long long adds = std::min<long long>((tiles + 7) / 8, 6 * 152);
+        e = launch_dependent(few_finish_kernel<E, D, NT>, dim3((unsigned)(merges + adds)),
                              kFinishThreads, 0, s, C, T, A, rows, kCluster == 0);
     }
     return e;
