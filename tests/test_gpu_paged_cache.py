@@ -140,6 +140,7 @@ def _evict(kv, made, into, budgets, sinks, recent, stride):
     (64, 128, 32, "bf16", 0, 300, 1, 299, 1, 0, 3),
     (128, 64, 64, "bf16", 9000, 20000, 1000, 9000, 4, 64, 4096),
     (64, 64, 64, "bf16", 33000, 70000, 3000, 65000, 4, 64, 0),
+    (64, 32, 64, "bf16", 17000, 17500, 100, 1500, 3, 9, 2000),
     # more rows than a cluster's shared memory holds, and just as many
     (64, 64, 128, "fp16", 131072 + 68, 300000, 3000, 140000, 4, 64, 0),
     (64, 128, 64, "bf16", 131072 + 67, 200000, 5, 200, 2, 1, 600)])
@@ -149,6 +150,8 @@ def test_evict_keeps_the_largest_weights(cuda_lib, d, page, page2, dtype, lo, hi
     from tests import paged
     kv = cuda_lib
     R, L, H = (2, 2, 2) if hi < 30000 else (1, 1, 3)
+    if lo == 17000:                                          # more clusters than run at once
+        R, L, H = 2, 3, 17
     lens = _spread(R, L, H, lo, hi)
     made = paged.Made(kv, lens, 2 * H, d, page, dtype, mass=True, seed=5)
     if levels:
