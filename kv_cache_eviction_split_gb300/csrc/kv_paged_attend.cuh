@@ -318,8 +318,7 @@ cudaError_t launch_attend_few(const DevPaged &C, const DevChunk &T, int layer, c
                               int max_rows, int blocks, const AttendWs &ws, cudaStream_t s);
 // The others.
 cudaError_t launch_attend_many(const DevPaged &C, const DevChunk &T, int layer, const AttendMask &M,
-                               const AttendIo &io, bool add_mass, const AttendWs &ws,
-                               cudaStream_t s);
+                               const AttendIo &io, const AttendWs &ws, cudaStream_t s);
 // Their weights, from its packed queries and lse.
 cudaError_t launch_many_mass(const DevPaged &C, const DevChunk &T, int layer, const AttendMask &M,
                              const AttendWs &ws, cudaStream_t s);

@@ -197,7 +197,7 @@ cudaError_t launch_paged_attention(const DevPaged &C, const DevChunk &T0, int la
         e = launch_attend_few(C, T, layer, M, io, add_mass, seen, k.items, k.max_rows, k.blocks, ws,
                               s);
     if (e == cudaSuccess && k.many) {
-        e = launch_attend_many(C, T, layer, M, io, add_mass, ws, s);
+        e = launch_attend_many(C, T, layer, M, io, ws, s);
         if (e == cudaSuccess && add_mass) e = launch_many_mass(C, T, layer, M, ws, s);
     }
     return e;

@@ -751,8 +751,7 @@ cudaError_t many(const DevPaged &C, const DevChunk &T, const ManyArgs &A, const 
 }  // namespace
 
 cudaError_t launch_attend_many(const DevPaged &C, const DevChunk &T, int layer, const AttendMask &M,
-                               const AttendIo &io, bool add_mass, const AttendWs &ws,
-                               cudaStream_t s) {
+                               const AttendIo &io, const AttendWs &ws, cudaStream_t s) {
     const ManyArgs A{layer, M, io, ws.cut, ws.part_ml, ws.part_o, ws.lse2, ws.q_packed,
                      many_phases(C)};
     if (C.dtype == KV_FP16)
