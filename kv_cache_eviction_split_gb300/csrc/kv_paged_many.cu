@@ -126,8 +126,9 @@ __device__ __forceinline__ void make_item(Item &it, const DevPaged &C, const Att
         a.t_hi = a.rows ? t0 + (row0 + a.rows - 1) / C.G : -1;
         const bool some = a.t_hi >= 0;
         a.ns = some ? sp.ns : 0;
-        // sinks that reach past the item's window begin: the lane sees them before its own
-        const int from = M.sinks > it.lo ? it.lo : window_lo(M, max(a.t_lo, 0));
+        // Sinks that reach into the tile where the item's window begins, or past it, are not
+        // among the span's first `ns` tiles: the lane sees them before its own window.
+        const int from = M.sinks > sp.first << 7 ? it.lo : window_lo(M, max(a.t_lo, 0));
         a.a = some ? sp.ns + (from >> 7) - sp.first : 0;
         a.b = some ? sp.ns + (a.t_hi >> 7) + 1 - sp.first : 0;
     }

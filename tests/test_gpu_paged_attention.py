@@ -354,3 +354,26 @@ def test_two_streams_at_once(cuda_lib):
     for made, counts, q, out, chunk, ws, lse, s in sets:
         assert kv.kv_check_status(made.cache.status, s) == 0
         _check(made, counts, q, out, lse, mass=True)
+
+
+# Sinks that end in the very tile of 128 keys where an item's window begins: of the item's two
+# blocks of 128 query rows, the second one's windows begin in a later tile, and it still sees them.
+SINKS_AT_WINDOW = {
+    "g4_lo97": (1, 4, 128, 64, "bf16", [300], 300, 300, 96, 4),
+    "g4_lo98": (1, 4, 128, 64, "bf16", [300], 300, 300, 95, 4),
+    "second_tile": (1, 1, 128, 64, "bf16", [600], 600, 600, 100, 150),
+    "g7_ragged": (2, 14, 64, 16, "fp16", [400, 333], 400, 700, 260, 8),
+    "window_4000": (1, 4, 128, 128, "bf16", [200], 4300, 4300, 4000, 4),
+}
+
+
+@pytest.mark.parametrize("name", SINKS_AT_WINDOW)
+def test_sinks_in_the_tile_where_the_window_begins(cuda_lib, name):
+    from tests import paged
+    H, Hq, d, page, dtype, counts, lo, hi, window, sinks = SINKS_AT_WINDOW[name]
+    made = paged.Made(cuda_lib, _spread(len(counts), 1, H, lo, hi), Hq, d, page, dtype, mass=True,
+                      max_rows=hi + page, seed=41)
+    q, out = _chunk_inputs(made, counts, Hq, False, 41)
+    lse, status = _run(cuda_lib, made, counts, q, out, 0, window, sinks, True)
+    assert status == 0
+    _check(made, counts, q, out, lse, 0, window, sinks, True)
