@@ -698,7 +698,7 @@ class PagedCache:
     lens              int32 [requests][layers][kv_heads]: rows held
     mass              float32 [num_pages][page_size] or None: accumulated attention weights
 
-    ``status`` holds the first device-side condition that kv_paged_append or
+    ``status`` holds the first device-side condition that kv_paged_load, kv_paged_append or
     kv_paged_attention met (a length or page that cannot be); kv_check_status(cache.status)
     reads and clears it.
     """

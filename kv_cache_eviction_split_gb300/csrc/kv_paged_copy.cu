@@ -113,6 +113,7 @@ load_kernel(const DevPaged C, const uint4 *__restrict__ k_rows, const uint4 *__r
             const long long j = row - u0;
             if (row >= u1 || j < 0 || u1 - u0 > C.cap) continue;
             to[i] = page_row(C, C.table + u * C.max_pages, (int)j);
+            if (to[i] < 0 && p.which == 0 && p.ch == 0) post_status(C.status, KV_ERR_INVALID_ARG);
         }
 #pragma unroll
         for (int i = 0; i < kLoadUnroll; ++i) {

@@ -293,3 +293,31 @@ def test_from_prefill_eviction_to_decoding(cuda_lib, page):
         idx = torch.as_tensor(want, device="cuda")
         ref[x] = [K[idx], V[idx], have[idx]]
     step(into, [1, 5])
+
+
+def test_load_reports_rows_that_it_could_not_write(cuda_lib):
+    """A page that does not exist holds rows in use: they cannot be written, which is said."""
+    import torch
+    from tests import paged
+    kv = cuda_lib
+    for bad in (lambda c: c.num_pages, lambda c: -1):
+        made = paged.Made(kv, _spread(1, 1, 3, 40, 40), 3, 64, 16, seed=13, mass=True)
+        c = made.cache
+        page = bad(c)
+        want = [c.k_pages.clone(), c.v_pages.clone()]
+        x = torch.randn((120, 64), device="cuda").to(made.dtype)
+        for h in range(3):
+            rows = made.rows(0, 0, h)
+            j = torch.arange(40, device="cuda")
+            if h == 1:
+                rows, j = rows[j // 16 != 1], j[j // 16 != 1]
+            want[0].view(-1, 64)[rows] = x[40 * h + j]
+            want[1].view(-1, 64)[rows] = x[40 * h + j]
+        c.page_table[0, 0, 1, 1] = page
+        offsets = torch.tensor([0, 40, 80, 120], device="cuda")
+        kv.kv_paged_load(c, x, x, offsets, 120)
+        assert kv.kv_check_status(c.status) == kv.KV_ERR_INVALID_ARG
+        assert c.lens.view(-1).tolist() == [40, 40, 40]
+        for a, b in zip((c.k_pages, c.v_pages), want):
+            assert torch.equal(_bits(a), _bits(b))
+        assert kv.kv_check_status(c.status) == 0
