@@ -119,3 +119,23 @@ def evict_unit(mass, n, b, sinks, recent):
     mid = sorted(range(sinks, n - recent), key=lambda j: (-float(mass[j]), j))
     mid = sorted(mid[:b - sinks - recent])
     return list(range(sinks)) + mid + list(range(n - recent, n))
+
+
+def cancelling(n, new, d, dtype, seed, device="cpu"):
+    """A query, n + new keys and values (in `dtype`) whose softmax average is all but zero while
+    sum p |v| is not: the output's own rounding then hides nothing of an error in the weights.
+    The last `new` rows have values 0, so queries that see different numbers of them agree up to
+    a factor.  Returns (q [d], K [n + new][d], V [n + new][d], softmax scale)."""
+    g = torch.Generator(device=device).manual_seed(seed)
+    q, K, V = (torch.zeros(s, dtype=torch.float64, device=device)
+               for s in ((d,), (n + new, d), (n + new, d)))
+    scale = 1 / math.sqrt(d)
+    q[0] = 0.5 / scale
+    q = q.to(dtype)
+    # logits in -0.5 .. 0.5: one product each
+    K[:n, 0] = torch.rand(n, generator=g, device=device, dtype=torch.float64) * 2 - 1
+    K = K.to(dtype)
+    p = torch.exp(scale * (K[:n].double() @ q.double()))
+    v = torch.randn((n, d), generator=g, device=device, dtype=torch.float64)
+    V[:n] = v - torch.outer(p, (p @ v) / (p @ p))
+    return q, K, V.to(dtype), scale

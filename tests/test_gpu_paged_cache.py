@@ -295,6 +295,52 @@ def test_from_prefill_eviction_to_decoding(cuda_lib, page):
     step(into, [1, 5])
 
 
+@pytest.mark.parametrize("d,H,counts", [(128, 8, [3001, 0, 5, 2000]), (64, 3, [4097])])
+def test_append_of_a_prompts_rows(cuda_lib, d, H, counts):
+    import torch
+    from tests import paged
+    kv = cuda_lib
+    made = paged.Made(kv, _spread(len(counts), 2, H, 3100, 4500), H, d, 64, mass=True, seed=11)
+    c, tok = made.cache, sum(counts)
+    new = torch.randn((tok, 2 * H * d), device="cuda").to(made.dtype)
+    k_new, v_new = new[:, :H * d].view(tok, H, d), new[:, H * d:].view(tok, H, d)
+    want = [c.k_pages.clone(), c.v_pages.clone(), c.mass.clone()]
+    t0 = 0
+    for r, count in enumerate(counts):
+        for h in range(H):
+            n = int(made.lens_host[r, 1, h])
+            skip = max(0, count - n)                    # tokens without a row
+            rows = made.rows(r, 1, h)[n - (count - skip):]
+            want[0].view(-1, d)[rows] = k_new[t0 + skip:t0 + count, h]
+            want[1].view(-1, d)[rows] = v_new[t0 + skip:t0 + count, h]
+            want[2].view(-1)[rows] = 0
+        t0 += count
+    kv.kv_paged_append(c, kv.Chunk(counts), 1, k_new, v_new)
+    assert kv.kv_check_status(c.status) == 0
+    for a, b in zip((c.k_pages, c.v_pages, c.mass), want):
+        assert torch.equal(_bits(a), _bits(b))
+
+
+@pytest.mark.parametrize("hi,levels", [(20000, 1), (20000, 2), (135000, 1)])
+def test_evict_with_one_weight_for_all_rows(cuda_lib, hi, levels):
+    """Rows loaded without weights all have 0: the first ones stay.  Units by clusters, and past
+    what a cluster holds."""
+    import torch
+    from tests import paged
+    kv = cuda_lib
+    lens = _spread(1, 1, 3, hi - 3000, hi)
+    made = paged.Made(kv, lens, 3, 64, 64, mass=True, seed=12)
+    made.cache.mass.copy_(torch.floor(made.mass0 * levels))
+    into = kv.PagedCache.allocate(1, 1, 3, 3, 64, 7000, 64, made.dtype, mass=True)
+    kept, status = _evict(kv, made, into, [7000, 300, 80], 4, 64, 7000)
+    assert status == 0
+    for h, b in enumerate([7000, 300, 80]):
+        rows = made.rows(0, 0, h)
+        want = paged.evict_unit(made.cache.mass.view(-1)[rows].cpu().tolist(), lens[0][0][h], b, 4, 64)
+        assert kept[h, :b].cpu().tolist() == want
+        assert int(into.lens[0, 0, h]) == b
+
+
 def test_load_reports_rows_that_it_could_not_write(cuda_lib):
     """A page that does not exist holds rows in use: they cannot be written, which is said."""
     import torch
