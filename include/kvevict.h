@@ -393,8 +393,9 @@ kv_status kv_evict_host(const kv_problem *p, const kv_host_plan *plan, const voi
  * zeroing the word: it keeps the first code until kv_check_status(c->status, ...)
  * reads and clears it.  kv_paged_load posts KV_ERR_INVALID_ARG there for rows
  * whose page does not exist, which are not written, and gives a unit that does
- * not fit its table length -1, which the calls after it post.  kv_paged_evict
- * posts to its workspace's status word, which it zeroes first.
+ * not fit its table, or whose rows are not all among total_rows, length -1, which
+ * the calls after it post.  kv_paged_evict posts to its workspace's status word,
+ * which it zeroes first.
  *
  * A workspace serves one call at a time: calls, or graphs of them, that may run
  * side by side need workspaces of their own.

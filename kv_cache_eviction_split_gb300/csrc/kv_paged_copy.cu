@@ -73,11 +73,15 @@ load_kernel(const DevPaged C, const uint4 *__restrict__ k_rows, const uint4 *__r
             long long total_rows) {
     using Part = LanePart<D>;
     const Part p;
+    // whether a unit's rows [a, b) are there and fit its table
+    auto fits = [&](long long a, long long b) {
+        return a >= 0 && a <= b && b <= total_rows && b - a <= C.cap;
+    };
     // lengths: unit u by thread u of the grid
     const long long threads = (long long)gridDim.x * blockDim.x;
     for (long long u = (long long)blockIdx.x * blockDim.x + threadIdx.x; u < C.units; u += threads) {
-        const long long n = offsets[u + 1] - offsets[u];
-        C.lens[u] = n >= 0 && n <= C.cap ? (int)n : -1;
+        const long long a = offsets[u], b = offsets[u + 1];
+        C.lens[u] = fits(a, b) ? (int)(b - a) : -1;
     }
     constexpr int kStep = kWarps * Part::kRows;
     const long long r0 = (long long)blockIdx.x * kLoadRows;
@@ -111,7 +115,7 @@ load_kernel(const DevPaged C, const uint4 *__restrict__ k_rows, const uint4 *__r
                 u1 = offsets[u + 1];
             }
             const long long j = row - u0;
-            if (row >= u1 || j < 0 || u1 - u0 > C.cap) continue;
+            if (row >= u1 || j < 0 || !fits(u0, u1)) continue;
             to[i] = page_row(C, C.table + u * C.max_pages, (int)j);
             if (to[i] < 0 && p.which == 0 && p.ch == 0) post_status(C.status, KV_ERR_INVALID_ARG);
         }

@@ -367,3 +367,20 @@ def test_load_reports_rows_that_it_could_not_write(cuda_lib):
         for a, b in zip((c.k_pages, c.v_pages), want):
             assert torch.equal(_bits(a), _bits(b))
         assert kv.kv_check_status(c.status) == 0
+
+
+def test_load_refuses_units_whose_rows_are_not_there(cuda_lib):
+    """Offsets that run past the packed rows: such a unit gets length -1, and none of its rows."""
+    import torch
+    from tests import paged
+    kv = cuda_lib
+    made = paged.Made(kv, _spread(1, 1, 3, 40, 40), 3, 64, 16, seed=14)
+    c = made.cache
+    want = c.k_pages.clone()
+    x = torch.randn((100, 64), device="cuda").to(made.dtype)
+    want.view(-1, 64)[made.rows(0, 0, 0)] = x[:40]
+    want.view(-1, 64)[made.rows(0, 0, 1)] = x[40:80]
+    kv.kv_paged_load(c, x, x, torch.tensor([0, 40, 80, 120], device="cuda"), 100)
+    torch.cuda.synchronize()
+    assert c.lens.view(-1).tolist() == [40, 40, -1]
+    assert torch.equal(_bits(c.k_pages), _bits(want))
