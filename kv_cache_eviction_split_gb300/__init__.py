@@ -763,6 +763,7 @@ class PagedCache:
     def advance(self, chunk: "Chunk") -> None:
         """Raises every unit's length by its request's new tokens (once a step, before the
         first layer's kv_paged_append)."""
+        _check_requests(self, chunk)
         self.lens.add_(chunk.counts.view(-1, 1, 1))
 
 
@@ -809,10 +810,14 @@ def _token_stride(cache: PagedCache, chunk: Chunk, t, heads: int, name: str) -> 
     return s0 if n > 1 else heads * d
 
 
-def _check_chunk(cache: PagedCache, chunk: Chunk) -> None:
+def _check_requests(cache: PagedCache, chunk: Chunk) -> None:
     if chunk.num_requests != cache.num_requests:
         raise ValueError("the chunk has %d requests, the cache %d"
                          % (chunk.num_requests, cache.num_requests))
+
+
+def _check_chunk(cache: PagedCache, chunk: Chunk) -> None:
+    _check_requests(cache, chunk)
     if chunk._index != cache._index:
         raise ValueError("the chunk is on %s, the cache on %s" % (chunk.cu_dev.device, cache.device))
 
@@ -850,6 +855,7 @@ def kv_paged_load(cache: PagedCache, k_rows, v_rows, offsets_dev, total_rows: in
 
 def kv_paged_attention_workspace_size(cache: PagedCache, chunk: Chunk,
                                       add_mass: bool = False) -> int:
+    _check_requests(cache, chunk)
     n = ctypes.c_size_t()
     _check(load().kv_paged_attention_workspace_size(cache.c, chunk.c, int(add_mass),
                                                     ctypes.byref(n)),

@@ -199,3 +199,15 @@ def test_advance_raises_every_units_length(kv):
     assert c.lens[0].tolist() == [[1, 1], [1, 8], [1, 1]] and c.lens[1].eq(5).all()
     assert np.array_equal(kv.Chunk([1, 0, 5], device="cpu").cu_host, [0, 1, 1, 6])
     assert ctypes.sizeof(kv._KvPaged) == 88
+
+
+def test_a_chunk_of_other_requests_is_refused(kv):
+    """The library reads an offset per request of the cache: a shorter chunk has fewer."""
+    c = _cache(kv)
+    for counts in ([], [5], [1, 2, 3]):
+        bad = kv.Chunk(counts, device="cpu")
+        with pytest.raises(ValueError, match="requests"):
+            kv.kv_paged_attention_workspace_size(c, bad)
+        with pytest.raises(ValueError, match="requests"):
+            c.advance(bad)
+    assert c.lens.eq(0).all()
