@@ -722,6 +722,7 @@ class PagedCache:
         self.page_table, self.lens = page_table, lens
         self.num_requests, self.num_layers, self.num_kv_heads, self.max_pages = page_table.shape
         self.num_q_heads = int(num_q_heads)
+        _check_int32("PagedCache", self.num_q_heads)
         self.num_pages, self.page_size, self.head_dim = k_pages.shape
         self.dtype, self.device = k_pages.dtype, k_pages.device
         self.status = torch.zeros(64, dtype=torch.int32, device=self.device)
@@ -810,6 +811,13 @@ def _token_stride(cache: PagedCache, chunk: Chunk, t, heads: int, name: str) -> 
     return s0 if n > 1 else heads * d
 
 
+def _check_int32(where: str, *values) -> None:
+    """ctypes keeps the low 32 bits of what does not fit."""
+    for x in values:
+        if not -0x80000000 <= x <= 0x7fffffff:
+            raise KvError(KV_ERR_INVALID_ARG, where)
+
+
 def _check_requests(cache: PagedCache, chunk: Chunk) -> None:
     if chunk.num_requests != cache.num_requests:
         raise ValueError("the chunk has %d requests, the cache %d"
@@ -825,6 +833,7 @@ def _check_chunk(cache: PagedCache, chunk: Chunk) -> None:
 def kv_paged_append(cache: PagedCache, chunk: Chunk, layer: int, k_new, v_new, stream=None):
     """New tokens' K and V rows [tokens][kv_heads][head_dim] of one layer into the pages."""
     _check_chunk(cache, chunk)
+    _check_int32("kv_paged_append", layer)
     ks = _token_stride(cache, chunk, k_new, cache.num_kv_heads, "k_new")
     vs = _token_stride(cache, chunk, v_new, cache.num_kv_heads, "v_new")
     _on_current_device(cache, k_new, v_new)
@@ -873,6 +882,7 @@ def kv_paged_attention(cache: PagedCache, chunk: Chunk, layer: int, q, out, work
     import torch
     heads = cache.num_q_heads
     _check_chunk(cache, chunk)
+    _check_int32("kv_paged_attention", layer, window, num_sinks)
     qs = _token_stride(cache, chunk, q, heads, "q")
     os_ = _token_stride(cache, chunk, out, heads, "out")
     if lse is not None and (lse.dtype is not torch.float32 or not lse.is_contiguous() or
@@ -910,6 +920,7 @@ def kv_paged_evict(cache: PagedCache, into: PagedCache, budgets, num_sinks: int,
         raise ValueError("kept: int32 [units][most rows kept]")
     if not workspace.is_contiguous():
         raise ValueError("workspace: contiguous")
+    _check_int32("kv_paged_evict", num_sinks, recent)
     _on_current_device(cache, into.k_pages, budgets, kept, workspace)
     _check(load().kv_paged_evict(cache.c, into.c, _ptr(budgets), int(num_sinks), int(recent),
                                  _ptr(kept), kept.shape[1], _ptr(workspace),

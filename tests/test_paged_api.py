@@ -211,3 +211,47 @@ def test_a_chunk_of_other_requests_is_refused(kv):
         with pytest.raises(ValueError, match="requests"):
             c.advance(bad)
     assert c.lens.eq(0).all()
+
+
+@pytest.mark.parametrize("big", [2 ** 32, 2 ** 32 + 1, -2 ** 32, 2 ** 31, 2 ** 63, 2 ** 70])
+def test_integers_past_32_bits_are_refused(kv, monkeypatch, big):
+    """ctypes would keep their low 32 bits: layer 2^32 is not layer 0."""
+    import torch
+    c, t = _cache(kv), kv.Chunk([1, 5], device="cpu")
+    # as if the tensors were on the GPU, and nothing that could be called there
+    monkeypatch.setattr(kv, "_on_current_device", lambda *tensors: None)
+    monkeypatch.setattr(kv, "_stream", lambda stream: None)
+    calls, real = [], kv.load()
+
+    class Lib:
+        kv_status_string = real.kv_status_string
+
+        def __getattr__(self, name):
+            return lambda *args: calls.append((name, args)) or 0
+
+    monkeypatch.setattr(kv, "_lib", Lib())
+    monkeypatch.setattr(kv, "load", lambda: kv._lib)
+    q, k = (torch.zeros((6, h, 128), dtype=torch.bfloat16) for h in (8, 2))
+    ws = torch.empty(1 << 10, dtype=torch.uint8)
+    kept = torch.zeros((c.num_units, 50), dtype=torch.int32)
+    budgets = torch.zeros(c.num_units, dtype=torch.int32)
+
+    def attend(layer=0, **kw):
+        kv.kv_paged_attention(c, t, layer, q, torch.empty_like(q), ws, **kw)
+
+    def evict(sinks=4, recent=16):
+        kv.kv_paged_evict(c, _cache(kv), budgets, sinks, recent, kept, ws)
+
+    attend()
+    evict()
+    kv.kv_paged_append(c, t, 0, k, k)
+    assert len(calls) == 3
+    for call in (lambda: attend(layer=big), lambda: attend(window=big), lambda: attend(num_sinks=big),
+                 lambda: kv.kv_paged_append(c, t, big, k, k), lambda: evict(sinks=big),
+                 lambda: evict(recent=big)):
+        with pytest.raises(kv.KvError) as e:
+            call()
+        assert e.value.code == kv.KV_ERR_INVALID_ARG
+    assert len(calls) == 3
+    with pytest.raises(kv.KvError):
+        kv.PagedCache(c.k_pages, c.v_pages, c.page_table, c.lens, big)
