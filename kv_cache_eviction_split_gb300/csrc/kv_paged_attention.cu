@@ -181,7 +181,8 @@ bool attend_tiles_fit(const DevPaged &C, const DevChunk &T, const AttendMask &M,
         many += (double)C.H * (rows / kManyRows + 1) * (many_tiles + kManyCost);
         weights += (double)C.H * groups * (rows / 128 + 1 + kManyCost);
     }
-    const double most = 2147483647.0;
+    // the count is rounded up to a whole number of tiles for each CTA
+    const double most = 2147483647.0 - std::max(kFewCtas, kManyCtas);
     return few <= most && many <= most && (!add_mass || weights <= most);
 }
 

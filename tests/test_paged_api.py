@@ -255,3 +255,11 @@ def test_integers_past_32_bits_are_refused(kv, monkeypatch, big):
     assert len(calls) == 3
     with pytest.raises(kv.KvError):
         kv.PagedCache(c.k_pages, c.v_pages, c.page_table, c.lens, big)
+
+
+def test_attention_refuses_tiles_that_only_just_fit_32_bits(kv):
+    """The kernels round the count of tiles up to equal runs, 304 at most: that has to fit too."""
+    lib, c, t = kv.load(), _cache(kv, R=32), kv.Chunk([1] * 32, device="cpu")
+    c._c.max_pages = (1 << 25) - 6           # 64 units of 2^25 - 6 tiles and 5 more each: 2^31 - 64
+    args = [c.c, t.c, 1, 0, 0, 0.1, F, 1024, F, 1024, F, 0, F, 1 << 62, None]
+    assert lib.kv_paged_attention(*args) == kv.KV_ERR_UNSUPPORTED
