@@ -174,8 +174,8 @@ struct AttendWs {
     float *lse2;               // [tokens * Hq]
     void *q_packed;            // [tokens * Hq][d], of the requests the many-rows kernel takes
     // few rows with add_mass: the logits (log2 units, -inf unseen) of every tile of every
-    // unit of the layer, in its span's order
-    float *logits;             // [R * H][ceil(cap / kFewTile)][kFewRows][kFewTile]
+    // unit of the layer, in its span's order; rows: the most of a unit that these kernels take
+    float *logits;             // [R * H][ceil(cap / kFewTile)][rows][kFewTile]
     size_t total;
 };
 AttendWs attend_ws_layout(const DevPaged &C, const DevChunk &T, bool add_mass, void *base);

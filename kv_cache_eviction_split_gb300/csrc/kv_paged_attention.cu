@@ -153,7 +153,7 @@ AttendWs attend_ws_layout(const DevPaged &C, const DevChunk &T, bool add_mass, v
         ws.lse2 = reinterpret_cast<float *>(take((size_t)T.tokens * C.Hq * sizeof(float)));
         ws.q_packed = take(k.many ? (size_t)T.tokens * C.Hq * C.d * 2 : 0);
         ws.logits = reinterpret_cast<float *>(
-            take(k.few_requests ? tiles * kFewRows * kFewTile * sizeof(float) : 0));
+            take(k.few_requests ? tiles * k.max_rows * kFewTile * sizeof(float) : 0));
     }
     ws.total = off;
     return ws;

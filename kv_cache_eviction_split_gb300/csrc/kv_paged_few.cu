@@ -117,6 +117,7 @@ struct FewArgs {
     float *lse2;
     float *logits;             // null without add_mass
     int unit_tiles;            // tiles of the logits to a unit
+    int logit_rows;            // rows of a tile of them
     int blocks;                // kCluster > 0: row blocks to a unit
 };
 
@@ -360,13 +361,13 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
                     __syncwarp();
                 }
                 if (A.logits) {
-                    float *lg = A.logits +
-                                ((long long)v * A.unit_tiles + x) * (kFewRows * kFewTile) + wk + quad;
+                    const long long tile = (long long)v * A.unit_tiles + x;
+                    float *lg = A.logits + tile * A.logit_rows * kFewTile + wk + quad;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            if (nt * 8 + pair + (i & 1) < rows)
+                            if (nt * 8 + pair + (i & 1) < min(rows, A.logit_rows))
                                 lg[(nt * 8 + pair + (i & 1)) * kFewTile + (i >> 1) * 8] = sc[nt][i];
                 }
                 bool up = false;
@@ -670,6 +671,7 @@ __device__ __forceinline__ void add_weights(const DevPaged &C, const DevChunk &T
         if (!few_rows(C, T, U)) continue;
         const FewItem it(C, A.M, U, 0, kFewRows);
         const int x1 = min((int)(end - base), it.span.total);
+        const int rows = min(it.rows, A.logit_rows);
         if (x0 >= x1) continue;
         // what a thread needs of its key in a tile: the rows' logits (-inf past the last or
         // unseen) and the weight so far
@@ -677,10 +679,10 @@ __device__ __forceinline__ void add_weights(const DevPaged &C, const DevChunk &T
         int at = -1;                                 // pool rows are counted in 31 bits
         auto fetch = [&](int x) {
             const int j = it.span.tile(x) * kFewTile + key;
-            const float *src = A.logits + (base + x) * (kFewRows * kFewTile) + key;
+            const float *src = A.logits + (base + x) * A.logit_rows * kFewTile + key;
 #pragma unroll
             for (int row = 0; row < kRows; ++row)
-                lg[row] = row < it.rows ? src[row * kFewTile] : -INFINITY;
+                lg[row] = row < rows ? src[row * kFewTile] : -INFINITY;
             at = j <= it.t_hi ? (int)page_row(C, U.table, j) : -1;
             old = at >= 0 ? C.mass[at] : 0.f;
         };
@@ -802,7 +804,7 @@ cudaError_t launch_attend_few(const DevPaged &C, const DevChunk &T, int layer, c
                               int max_rows, int blocks, const AttendWs &ws, cudaStream_t s) {
     const FewArgs A{layer,      M,         io,      ws.cut,
                     ws.unit_cut, ws.part_ml, ws.part_o, ws.lse2, add_mass ? ws.logits : nullptr,
-                    (C.cap + kFewTile - 1) / kFewTile, blocks};
+                    (C.cap + kFewTile - 1) / kFewTile, max_rows, blocks};
     // short: the largest cluster that leaves every CTA a tile and the GPU in one round
     int cluster = 0;
     if (seen <= kShortRows) {

@@ -263,3 +263,16 @@ def test_attention_refuses_tiles_that_only_just_fit_32_bits(kv):
     c._c.max_pages = (1 << 25) - 6           # 64 units of 2^25 - 6 tiles and 5 more each: 2^31 - 64
     args = [c.c, t.c, 1, 0, 0, 0.1, F, 1024, F, 1024, F, 0, F, 1 << 62, None]
     assert lib.kv_paged_attention(*args) == kv.KV_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("counts,G,rows", [([1] * 64, 4, 4), ([1] * 64, 1, 1), ([1] * 64, 16, 16),
+                                           ([3] * 64, 4, 12), ([1] * 63 + [500], 4, 4)])
+def test_attention_workspace_holds_the_logits_of_the_rows_there_are(kv, counts, G, rows):
+    c = _cache(kv, R=64, L=1, H=8, Hq=8 * G)
+    c._c.max_pages = 131072 // 64
+    t = kv.Chunk(counts, device="cpu")
+    more = kv.kv_paged_attention_workspace_size(c, t, True) - kv.kv_paged_attention_workspace_size(c, t)
+    logits = 64 * 8 * 131072 * rows * 4
+    # beside them the rows' sums and, for a request with more rows, the packed queries
+    beside = t.tokens * 8 * G * (4 + (128 * 2 if max(counts) == 500 else 0))
+    assert logits <= more <= logits + beside + 1024
