@@ -151,8 +151,7 @@ def test_one_token_of_wide_groups(cuda_lib, name):
     _check(made, counts, q, out, lse, 0, window, sinks, mass)
 
 
-# (new tokens, longest unit, weights added): the one-launch form (of 1 GB of rows: a few arrive
-# before a wait for them first looks at its limit), the cut form, the many-rows kernel
+# (new tokens, longest unit, weights added): the one-launch form, the cut form, the many-rows kernel
 EXPIRED = {
     "one_launch": ([1] * 64, 8000, False),
     "one_launch_weights": ([1] * 64, 8000, True),
@@ -165,25 +164,39 @@ EXPIRED = {
 
 @pytest.mark.parametrize("name", EXPIRED)
 def test_a_wait_that_runs_out_is_reported(cuda_lib, name):
-    """With a wait limit of 0, work enough that loads are waited for: the timeout is posted, the
-    calls return, and the next one with the usual limit is right."""
+    """With a wait limit of 0, beside copies that keep the memory busy (a wait sleeps for some
+    microseconds before it first looks at its limit): the timeout is posted, the call returns,
+    and the next one with the usual limit is right."""
+    import torch
     from tests import paged
     from tests.test_gpu_paged_attention import _check
     kv = cuda_lib
     counts, hi, mass = EXPIRED[name]
     made = paged.Made(kv, _spread(len(counts), 1, 4, hi - 300, hi), 16, 128, 64, seed=54, mass=mass)
     q, out = _chunk_inputs(made, counts, 16, False, 54)
+    chunk, c = kv.Chunk(counts), made.cache
+    ws = torch.empty(kv.kv_paged_attention_workspace_size(c, chunk, mass), dtype=torch.uint8,
+                     device="cuda")
+    busy = torch.empty((2, 1 << 30), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
     limit = kv.kv_get_wait_limit_ns()
-    seen = []
+    status = kv.KV_OK
     try:
         kv.kv_set_wait_limit_ns(0)
-        for _ in range(5):
-            seen.append(_run(kv, made, counts, q, out, mass=mass)[1])
+        for _ in range(100):                     # more than half of the calls run into it
+            torch.cuda.synchronize()
+            with torch.cuda.stream(side):
+                for _ in range(3):
+                    busy[0].copy_(busy[1])
+            kv.kv_paged_attention(c, chunk, 0, q, out, ws, add_mass=mass)
+            status = kv.kv_check_status(c.status)
+            if status != kv.KV_OK:
+                break
     finally:
         kv.kv_set_wait_limit_ns(limit)
-    assert set(seen) <= {kv.KV_OK, kv.KV_ERR_TIMEOUT} and kv.KV_ERR_TIMEOUT in seen, seen
+    assert status == kv.KV_ERR_TIMEOUT
     if mass:
-        made.cache.mass.copy_(made.mass0)
+        c.mass.copy_(made.mass0)
     lse, status = _run(kv, made, counts, q, out, mass=mass)
     assert status == 0
     _check(made, counts, q, out, lse, mass=mass)
