@@ -825,7 +825,8 @@ def _check_requests(cache: PagedCache, chunk: Chunk) -> None:
 
 
 def _check_chunk(cache: PagedCache, chunk: Chunk) -> None:
-    _check_requests(cache, chunk)
+    if chunk.num_requests != cache.num_requests:
+        _check_requests(cache, chunk)
     if chunk._index != cache._index:
         raise ValueError("the chunk is on %s, the cache on %s" % (chunk.cu_dev.device, cache.device))
 
@@ -833,7 +834,8 @@ def _check_chunk(cache: PagedCache, chunk: Chunk) -> None:
 def kv_paged_append(cache: PagedCache, chunk: Chunk, layer: int, k_new, v_new, stream=None):
     """New tokens' K and V rows [tokens][kv_heads][head_dim] of one layer into the pages."""
     _check_chunk(cache, chunk)
-    _check_int32("kv_paged_append", layer)
+    if layer >> 31:                              # negative, or past 32 bits
+        _check_int32("kv_paged_append", layer)
     ks = _token_stride(cache, chunk, k_new, cache.num_kv_heads, "k_new")
     vs = _token_stride(cache, chunk, v_new, cache.num_kv_heads, "v_new")
     _on_current_device(cache, k_new, v_new)
@@ -882,7 +884,8 @@ def kv_paged_attention(cache: PagedCache, chunk: Chunk, layer: int, q, out, work
     import torch
     heads = cache.num_q_heads
     _check_chunk(cache, chunk)
-    _check_int32("kv_paged_attention", layer, window, num_sinks)
+    if (layer | window | num_sinks) >> 31:       # one is negative, or past 32 bits
+        _check_int32("kv_paged_attention", layer, window, num_sinks)
     qs = _token_stride(cache, chunk, q, heads, "q")
     os_ = _token_stride(cache, chunk, out, heads, "out")
     if lse is not None and (lse.dtype is not torch.float32 or not lse.is_contiguous() or
