@@ -94,6 +94,7 @@ load_kernel(const DevPaged C, const uint4 *__restrict__ k_rows, const uint4 *__r
         if (offsets[mid] <= first) lo = mid; else hi = mid;
     }
     long long u = lo, u0 = offsets[u], u1 = offsets[u + 1];
+    bool ok = fits(u0, u1), lost = false;
     const uint4 *src = p.which ? v_rows : k_rows;
     uint4 *dst = reinterpret_cast<uint4 *>(p.which ? C.v : C.k);
     for (long long rb = first; rb < r1; rb += kStep * kLoadUnroll) {
@@ -113,11 +114,11 @@ load_kernel(const DevPaged C, const uint4 *__restrict__ k_rows, const uint4 *__r
                 ++u;
                 u0 = u1;
                 u1 = offsets[u + 1];
+                ok = fits(u0, u1);
             }
-            const long long j = row - u0;
-            if (row >= u1 || j < 0 || !fits(u0, u1)) continue;
-            to[i] = page_row(C, C.table + u * C.max_pages, (int)j);
-            if (to[i] < 0 && p.which == 0 && p.ch == 0) post_status(C.status, KV_ERR_INVALID_ARG);
+            if (!ok || row < u0 || row >= u1) continue;
+            to[i] = page_row(C, C.table + u * C.max_pages, (int)(row - u0));
+            lost |= to[i] < 0;
         }
 #pragma unroll
         for (int i = 0; i < kLoadUnroll; ++i) {
@@ -127,6 +128,7 @@ load_kernel(const DevPaged C, const uint4 *__restrict__ k_rows, const uint4 *__r
                 C.mass[to[i]] = mass_rows ? mass_rows[rb + i * kStep] : 0.f;
         }
     }
+    if (lost && p.which == 0 && p.ch == 0) post_status(C.status, KV_ERR_INVALID_ARG);
 }
 
 }  // namespace
