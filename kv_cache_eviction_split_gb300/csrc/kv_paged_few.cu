@@ -362,7 +362,7 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
                 }
                 if (A.logits) {
                     const long long tile = (long long)v * A.unit_tiles + x;
-                    float *lg = A.logits + tile * A.logit_rows * kFewTile + wk + quad;
+                    float *lg = A.logits + tile * (A.logit_rows * kFewTile) + wk + quad;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -679,7 +679,7 @@ __device__ __forceinline__ void add_weights(const DevPaged &C, const DevChunk &T
         int at = -1;                                 // pool rows are counted in 31 bits
         auto fetch = [&](int x) {
             const int j = it.span.tile(x) * kFewTile + key;
-            const float *src = A.logits + (base + x) * A.logit_rows * kFewTile + key;
+            const float *src = A.logits + (base + x) * (A.logit_rows * kFewTile) + key;
 #pragma unroll
             for (int row = 0; row < kRows; ++row)
                 lg[row] = row < rows ? src[row * kFewTile] : -INFINITY;
