@@ -12,7 +12,9 @@ namespace {
 // Merge of the many-rows kernel's cut items.  The CTA that held an item's last tile left
 // its description; block (b, y) merges rows of CTA b's item of every phase.  Partials are
 // added in order: the result does not depend on timing.  A partial that saw nothing
-// (m = -inf) has no output written.
+// (m = -inf) has no output written.  Its inputs are not __restrict__: the kernel before
+// writes them while this one may already run, and loads through restricted pointers need not
+// stay behind the wait for it.
 // ---------------------------------------------------------------------------
 // Up to 256 rows, few partials: kMergeRows rows a warp, their loads together.  One wave of
 // blocks (16 an SM); 14 .. 16 us for 152 cut items of 256 rows, d = 128, 40 MB of partials
@@ -21,8 +23,7 @@ constexpr int kMergeRows = 4;
 template <typename X, int D>
 __global__ void __launch_bounds__(128)
 merge_many_kernel(const DevPaged C, const DevChunk T, int layer, const AttendIo io, float *lse2,
-                  const CutItem *__restrict__ cut, const float2 *__restrict__ part_ml,
-                  const float *__restrict__ part_o, int phases) {
+                  const CutItem *cut, const float2 *part_ml, const float *part_o, int phases) {
     constexpr int kV = D / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
