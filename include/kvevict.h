@@ -475,8 +475,10 @@ kv_status kv_paged_attention_workspace_size(const kv_paged *c, const kv_chunk *t
  * query of the chunk sees are never used, whatever their memory holds (their
  * pages may be gone); rows that one sees must hold finite values.  Products are
  * taken of the stored values and summed in fp32; the softmax weights are rounded
- * once, to the cache's dtype, before they multiply V (to two such parts where
- * few query rows share a head's rows).
+ * once, to the cache's dtype, before they multiply V; to two such parts in requests
+ * of at most 16 query rows a head (new tokens times the group's heads), and without
+ * add_mass of up to 512 where the tables or the window have at most 8192 rows and
+ * the step has few such requests.
  *
  * add_mass != 0 adds to mass of every row j the weights e^(s_j - lse) of the
  * chunk's queries and the group's heads (fp32, in a fixed order: the same call on

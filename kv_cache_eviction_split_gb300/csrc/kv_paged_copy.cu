@@ -4,7 +4,7 @@
 // vectors.  A row pair (K and V) is 2 d / 8 vectors: one warp's load for d = 128,
 // half of one for d = 64, so a warp step moves 512 bytes and addresses are formed
 // once per row.  Measured (d = 128, 8 KV heads): load of 256 units of 1638 rows, 430 MB
-// moved, 69 us (6.2 TB/s; 8 row pairs in flight a lane, 256 rows a CTA); append of 8 tokens
+// moved, 69.6 us (6.2 TB/s; 8 row pairs in flight a lane, 256 rows a CTA); append of 8 tokens
 // 2.2 us on the GPU, the launch itself.
 #include <algorithm>
 

@@ -14,7 +14,7 @@
 // [ (j - t0) G, (j + window - t0) G ), so the mask is two bounds.
 //
 // Measured (2 requests, 301 .. 511 new tokens of 32 query heads over 8 x 13107 .. 32768 rows,
-// d = 128, bf16): 168 us of the call's 447, where the products alone would take 90.  Both
+// d = 128, bf16): 163 us of the call's 442, where the products alone would take 90.  Both
 // operands of a product come from shared memory, as much of its bandwidth as of the tensor
 // cores' time, which the Q tiles' arrival and the rows' lse share.  Without the exponentials
 // 25 us less, with half the products 20 us less, with half the Q traffic the same.  Eight
