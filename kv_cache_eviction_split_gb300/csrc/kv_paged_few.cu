@@ -428,6 +428,10 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
                         mma<E>(o[nt][mt], a, pl[nt][0], pl[nt][1]);
                     }
                 }
+                // The lanes' reads of the stage come before TMA's next writes to it: the arrival
+                // alone does not order the two proxies, and beside other kernels on the SM reads
+                // of V did find the tile that came after.
+                fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[s]);
                 ++cnt;

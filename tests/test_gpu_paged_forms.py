@@ -194,9 +194,58 @@ def test_a_wait_that_runs_out_is_reported(cuda_lib, name):
                 break
     finally:
         kv.kv_set_wait_limit_ns(limit)
+        torch.cuda.synchronize()                 # the copies end before their memory is free
     assert status == kv.KV_ERR_TIMEOUT
     if mass:
         c.mass.copy_(made.mass0)
     lse, status = _run(kv, made, counts, q, out, mass=mass)
     assert status == 0
     _check(made, counts, q, out, lse, mass=mass)
+
+
+# (new tokens, longest unit, weights added)
+BESIDE = {
+    "one_launch": ([1] * 64, 8000, False),
+    "one_launch_weights": ([1] * 64, 8000, True),
+    "one_launch_clusters": ([1] * 8, 8000, False),
+    "row_blocks": ([16] * 16, 1000, False),
+    "cut": ([1] * 8, 30000, False),
+    "cut_weights": ([1, 2] * 8, 30000, True),
+    "many": ([300, 200], 20000, False),
+    "many_weights": ([300, 200], 20000, True),
+}
+
+
+@pytest.mark.parametrize("name", BESIDE)
+def test_other_kernels_on_the_gpu_change_nothing(cuda_lib, name):
+    """Calls beside copies on another stream, which share the SMs, give the bits of a quiet call."""
+    import torch
+    from tests import paged
+    kv = cuda_lib
+    counts, hi, mass = BESIDE[name]
+    made = paged.Made(kv, _spread(len(counts), 1, 4, hi - 300, hi), 16, 128, 64, seed=55, mass=mass)
+    q, out = _chunk_inputs(made, counts, 16, False, 55)
+    chunk, c = kv.Chunk(counts), made.cache
+    ws = torch.empty(kv.kv_paged_attention_workspace_size(c, chunk, mass), dtype=torch.uint8,
+                     device="cuda")
+    lse = torch.empty((sum(counts), 16), device="cuda")
+    busy = torch.empty((2, 1 << 30), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    want = None
+    for i in range(30):
+        out.fill_(-3.0)
+        if mass:
+            c.mass.copy_(made.mass0)
+        torch.cuda.synchronize()
+        if want is not None:
+            with torch.cuda.stream(side):
+                for _ in range(3):
+                    busy[0].copy_(busy[1])
+        kv.kv_paged_attention(c, chunk, 0, q, out, ws, lse=lse, add_mass=mass)
+        assert kv.kv_check_status(c.status) == 0
+        got = [out, lse] + ([c.mass] if mass else [])
+        if want is None:
+            want = [t.clone() for t in got]
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), i
+    torch.cuda.synchronize()                     # the copies end before their memory is free
