@@ -774,6 +774,7 @@ __device__ __forceinline__ void attn_tc_body(const DevProblem P, const CUtensorM
                             in_range(U.kv_row0 + j, kv_rows_total(P), A.status))
                             A.v2[U.kv_row0 + j] = q;
                     }
+                    fence_proxy_async_smem();    // these reads before TMA's next writes
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&v_empty[s]);
                     continue;

@@ -385,8 +385,9 @@ __device__ __forceinline__ void tmem_st_wait() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// Makes this thread's generic-proxy shared-memory writes visible to the async
-// proxy (the tensor core reading them as an MMA operand).
+// Orders this thread's generic-proxy shared-memory accesses with later async-proxy
+// ones: its writes are visible to the tensor core that reads them as an MMA operand,
+// its reads are done before TMA overwrites what they read.
 __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
