@@ -28,7 +28,7 @@
 // Measured (d = 128, bf16, one layer's call).  HBM-bound: 8 requests of 4915 .. 39321 rows
 // in 8 heads each 115 us (6.3 TB/s); 4 heads of 131072 rows, weights added, 67 us of which
 // the tiles 47 (5.7 TB/s) and the finish 12; 16 requests, window 4096 of longer tables,
-// 47 us (5.7 TB/s).  Latency-bound: 8 heads of 1638 rows 6.4 us on the GPU.  As products of
+// 48 us (5.6 TB/s).  Latency-bound: 8 heads of 1638 rows 6.4 us on the GPU.  As products of
 // 128-row tiles in tensor memory the same work would be padded 32 times over.
 #include <algorithm>
 
