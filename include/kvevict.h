@@ -19,6 +19,9 @@
  *                                    optionally a sliding window with visible sinks),
  *                                    accumulating each row's attention weight
  *   kv_paged_evict                   eviction by accumulated attention weight
+ *   kv_rotary, kv_paged_append_rotary  rotary positions, alone or on the way into the pages
+ *   kv_paged_reserve, kv_paged_fork, kv_paged_compact  pages given out, shared between
+ *                                    requests and copied before they are written, moved together
  *
  * Definitions (the pages these steps follow):
  *
@@ -518,6 +521,131 @@ kv_status kv_paged_evict_workspace_size(const kv_paged *src, size_t *bytes);
 kv_status kv_paged_evict(const kv_paged *src, const kv_paged *dst, const int32_t *budgets_dev,
                          int32_t num_sinks, int32_t recent, int32_t *kept, int64_t kept_stride,
                          void *workspace, size_t workspace_bytes, void *stream);
+
+/* -------------------------------------------------------------------------
+ * Rotary positions
+ * -------------------------------------------------------------------------
+ * Pair i (of dims / 2) of a row at position p turns by the angle p * inv_freq[i]:
+ *   (x1, x2) -> factor * (x1 cos - x2 sin, x1 sin + x2 cos)
+ * The pairs are elements (i, i + dims/2), or (2i, 2i+1) if interleaved; elements from
+ * dims on are copied.  Angles are exact to 2^-21 at any position (int32, negative ones
+ * too), products and sums are fp32, a result is rounded once.
+ */
+typedef struct kv_rotation {
+    int32_t dims;              /* elements turned: a multiple of 16, 0 .. head_dim */
+    int32_t interleaved;
+    float factor;              /* of the turned elements; 1 for a plain rotation */
+    const float *inv_freq;     /* device [dims/2] */
+} kv_rotation;
+
+/*
+ * Host helper: inv_freq [dims/2] and the factor.
+ *   KV_ROTARY_NONE    base^(-2i/dims)
+ *   KV_ROTARY_LINEAR  that, divided by scale (position interpolation)
+ *   KV_ROTARY_BASE    with base * scale^(dims/(dims-2)) as the base
+ *   KV_ROTARY_PARTS   by wavelength (YaRN): frequencies that make `fast` turns or more in
+ *                     `context` positions are kept, those of `slow` or fewer are divided by
+ *                     scale, those between are mixed in proportion; factor
+ *                     0.1 ln(scale) + 1
+ * scale >= 1; context, slow and fast are read for KV_ROTARY_PARTS alone.
+ */
+typedef enum kv_rotary_scaling {
+    KV_ROTARY_NONE = 0,
+    KV_ROTARY_LINEAR = 1,
+    KV_ROTARY_BASE = 2,
+    KV_ROTARY_PARTS = 3
+} kv_rotary_scaling;
+kv_status kv_rotary_frequencies(int32_t dims, double base, int32_t scaling, double scale,
+                                double context, double slow, double fast, float *inv_freq,
+                                float *factor);
+
+/*
+ * Rows turned: token t's `heads` rows of head_dim (64 or 128) elements of `dtype` by its
+ * position positions[t] (int32, device).  Row (t, h) begins t * stride + h * head_stride
+ * elements from x, and from out (16-byte aligned, strides multiples of 8; rows of out
+ * must not overlap).  out may be x, with the same strides.  backward != 0 turns the
+ * other way, with the same factor: the gradient of x from that of out.
+ * So [L][H][N][d] keys are N tokens of L*H heads, stride d, head_stride N*d.
+ */
+kv_status kv_rotary(const kv_rotation *rot, const int32_t *positions, int64_t tokens, int32_t heads,
+                    int32_t head_dim, int32_t dtype, const void *x, int64_t x_stride,
+                    int64_t x_head_stride, void *out, int64_t out_stride, int64_t out_head_stride,
+                    int32_t backward, void *stream);
+
+/*
+ * kv_paged_append of rows that are turned first: q [tokens][H_q][d] turned into q_out (which
+ * may be q; strides as in kv_paged_attention; q NULL: no queries), k_new turned into
+ * the pages, v_new copied there, all by positions[token].  row_pos: i32
+ * [num_pages][page_size], or NULL: receives the new rows' positions (the cache's rows
+ * lie at other numbers once some were evicted).
+ */
+kv_status kv_paged_append_rotary(const kv_paged *c, const kv_chunk *t, int32_t layer,
+                                 const kv_rotation *rot, const int32_t *positions, int32_t *row_pos,
+                                 const void *q, int64_t q_stride, void *q_out, int64_t q_out_stride,
+                                 const void *k_new, int64_t k_stride, const void *v_new,
+                                 int64_t v_stride, void *stream);
+
+/*
+ * Positions of a cache's rows, dst_pos i32 [num_pages][page_size] of dst: row i of unit u gets
+ *   p = index[u * stride + i], or index[offsets[u] + i] with offsets (i64 [R*L*H + 1],
+ *   device), or i without an index; with src_pos, the position of row p of the same unit
+ *   of src instead.
+ * After kv_paged_load: the kept indices (sel_idx) and offsets.  After kv_paged_evict: kept,
+ * kept_stride, src and its positions.
+ */
+kv_status kv_paged_place_positions(const kv_paged *dst, int32_t *dst_pos, const kv_paged *src,
+                                   const int32_t *src_pos, const int32_t *index, int64_t stride,
+                                   const int64_t *offsets, void *stream);
+
+/* -------------------------------------------------------------------------
+ * Pages given out, shared and moved together
+ * -------------------------------------------------------------------------
+ * refs i32 [num_pages] (device) counts for every page the table entries in use that name
+ * it: column c of a unit with n rows is in use if c * page_size < n.  A page with
+ * refs 0 is free.  The calls keep refs, the tables and lens in step (the tables are
+ * written: page_table has to be writable memory); what else changes them
+ * (kv_paged_load, kv_paged_evict) is followed by kv_paged_count_refs.  Rows of a shared
+ * page are read by all its units; kv_paged_reserve makes sure that the pages the next
+ * append writes are a unit's own.  (kv_paged_attention's add_mass writes weights of shared
+ * pages too: keep none while pages are shared.)  row_pos as in kv_paged_append_rotary,
+ * or NULL: moves with the pages, as mass does.  Conditions go to the cache's status word.
+ */
+
+/* refs from the tables and lens. */
+kv_status kv_paged_count_refs(const kv_paged *c, int32_t *refs, void *stream);
+
+kv_status kv_paged_reserve_workspace_size(const kv_paged *c, size_t *bytes);
+/*
+ * Room for a step's new tokens in every layer: lens[u] grows by the request's tokens (in place
+ * of the caller's raise), pages are entered for the rows that have none, and a last page that is
+ * part full and shared is copied, the copy taking its place.  The k-th page needed (units
+ * in order, a unit's copy before its new pages) is the k-th lowest free one.  A page
+ * that this call leaves without references is given out from the next call on.
+ * Nothing changes and KV_ERR_BUDGET is posted if there are too few free pages or a
+ * unit would outgrow its table, KV_ERR_INVALID_ARG if a length or last page cannot be.
+ * KV_ERR_BUDGET is returned where the tokens would fill more pages than there are.
+ */
+kv_status kv_paged_reserve(const kv_paged *c, const kv_chunk *t, int32_t *refs, int32_t *row_pos,
+                           void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Every request r goes on from request parents[r] (i32 [R], device): its units take that
+ * request's lengths and table entries as they were before the call, and share its pages.
+ * parents[r] = r leaves it as it is; -1 empties it and gives its pages up.  (Hypotheses of a
+ * beam, several samples of a prompt, requests that have ended.)  Entries past a unit's
+ * last page are left as they were.  A parent outside -1 .. R-1 is posted
+ * (KV_ERR_INVALID_ARG) and its request left as it is; at most 16384 requests.
+ */
+kv_status kv_paged_fork(const kv_paged *c, int32_t *refs, const int32_t *parents, void *stream);
+
+kv_status kv_paged_compact_workspace_size(const kv_paged *c, size_t *bytes);
+/*
+ * Pages in use move to the front of the pools: with n of them in use, the k-th one from page n on
+ * goes to the k-th free page before it, tables and refs with it, and pages n .. num_pages - 1
+ * are free.  live: i32 (device) receives n, or NULL.
+ */
+kv_status kv_paged_compact(const kv_paged *c, int32_t *refs, int32_t *row_pos, int32_t *live,
+                           void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * Synchronises `stream`, then reads and clears the device status word of a

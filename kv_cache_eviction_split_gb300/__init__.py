@@ -10,7 +10,9 @@ Names follow the C ABI: ``kv_score``, ``kv_score_attention``,
 ``kv_score_rescore``, ``kv_make_offsets``, ``kv_select_topk``, ``kv_compact``,
 ``kv_check_status``, ``kv_budgets_pyramid``, ``kv_budgets_ripple``; for the paged
 cache that holds the kept rows while tokens are generated: ``kv_paged_load``,
-``kv_paged_append``, ``kv_paged_attention``, ``kv_paged_evict``.
+``kv_paged_append``, ``kv_paged_attention``, ``kv_paged_evict``; rotary positions
+(``kv_rotary``, ``kv_paged_append_rotary``) and the pages' keeping (``kv_paged_reserve``,
+``kv_paged_fork``, ``kv_paged_compact``).
 """
 from __future__ import annotations
 
@@ -34,7 +36,10 @@ __all__ = ["KvError", "Problem", "load", "build", "kv_score", "kv_score_attentio
            "evict", "KV_SCORE_DROPKV", "KV_SCORE_DROPKV_SQUARED", "KV_SCORE_ATTN_SUM",
            "PagedCache", "Chunk", "kv_paged_append", "kv_paged_load", "kv_paged_attention",
            "kv_paged_attention_workspace_size", "kv_paged_evict",
-           "kv_paged_evict_workspace_size"]
+           "kv_paged_evict_workspace_size", "Rotary", "kv_rotary_frequencies", "kv_rotary",
+           "kv_paged_append_rotary", "kv_paged_place_positions", "kv_paged_count_refs",
+           "kv_paged_reserve", "kv_paged_reserve_workspace_size", "kv_paged_fork",
+           "kv_paged_compact", "kv_paged_compact_workspace_size"]
 
 KV_OK, KV_ERR_INVALID_ARG, KV_ERR_BUDGET, KV_ERR_WORKSPACE, KV_ERR_CUDA, KV_ERR_TIMEOUT, \
     KV_ERR_UNSUPPORTED = range(7)
@@ -42,6 +47,8 @@ KV_OK, KV_ERR_INVALID_ARG, KV_ERR_BUDGET, KV_ERR_WORKSPACE, KV_ERR_CUDA, KV_ERR_
 KV_SCORE_DROPKV, KV_SCORE_DROPKV_SQUARED, KV_SCORE_ATTN_SUM = range(3)
 # kv_paged.dtype
 KV_BF16, KV_FP16 = range(2)
+# kv_rotary_scaling, by the names that kv_rotary_frequencies takes
+_SCALINGS = {"none": 0, "linear": 1, "base": 2, "parts": 3}
 
 EXPORTED_SYMBOLS = ("kv_score_workspace_size", "kv_score", "kv_score_attention",
                     "kv_score_rescore", "kv_make_offsets", "kv_select_workspace_size",
@@ -52,7 +59,11 @@ EXPORTED_SYMBOLS = ("kv_score_workspace_size", "kv_score", "kv_score_attention",
                     "kv_budgets_fraction", "kv_evict_fused", "kv_evict_host_workspace_size",
                     "kv_evict_host", "kv_paged_append", "kv_paged_load",
                     "kv_paged_attention", "kv_paged_attention_workspace_size",
-                    "kv_paged_evict", "kv_paged_evict_workspace_size")
+                    "kv_paged_evict", "kv_paged_evict_workspace_size",
+                    "kv_rotary_frequencies", "kv_rotary", "kv_paged_append_rotary",
+                    "kv_paged_place_positions", "kv_paged_count_refs", "kv_paged_reserve",
+                    "kv_paged_reserve_workspace_size", "kv_paged_fork", "kv_paged_compact",
+                    "kv_paged_compact_workspace_size")
 
 
 class KvError(RuntimeError):
@@ -89,6 +100,11 @@ class _KvPaged(ctypes.Structure):
 class _KvChunk(ctypes.Structure):
     _fields_ = [("tok_offsets_host", ctypes.POINTER(ctypes.c_int64)),
                 ("tok_offsets_dev", ctypes.c_void_p)]
+
+
+class _KvRotation(ctypes.Structure):
+    _fields_ = [("dims", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("factor", ctypes.c_float), ("inv_freq", ctypes.c_void_p)]
 
 
 _lib = None
@@ -135,6 +151,7 @@ def _bind(lib):
         ctypes.c_double
     szp = ctypes.POINTER(ctypes.c_size_t)
     PC, PT = ctypes.POINTER(_KvPaged), ctypes.POINTER(_KvChunk)
+    PR = ctypes.POINTER(_KvRotation)
     sig = {
         "kv_score_workspace_size": [P, szp],
         "kv_score": [P, vp, vp, vp, vp, vp, sz, vp],
@@ -165,6 +182,17 @@ def _bind(lib):
                                vp, sz, vp],
         "kv_paged_evict_workspace_size": [PC, szp],
         "kv_paged_evict": [PC, PC, vp, i32, i32, vp, i64, vp, sz, vp],
+        "kv_rotary_frequencies": [i32, f64, i32, f64, f64, f64, f64, ctypes.POINTER(ctypes.c_float),
+                                  ctypes.POINTER(ctypes.c_float)],
+        "kv_rotary": [PR, vp, i64, i32, i32, i32, vp, i64, i64, vp, i64, i64, i32, vp],
+        "kv_paged_append_rotary": [PC, PT, i32, PR, vp, vp, vp, i64, vp, i64, vp, i64, vp, i64, vp],
+        "kv_paged_place_positions": [PC, vp, PC, vp, vp, i64, vp, vp],
+        "kv_paged_count_refs": [PC, vp, vp],
+        "kv_paged_reserve_workspace_size": [PC, szp],
+        "kv_paged_reserve": [PC, PT, vp, vp, vp, sz, vp],
+        "kv_paged_fork": [PC, vp, vp, vp],
+        "kv_paged_compact_workspace_size": [PC, szp],
+        "kv_paged_compact": [PC, vp, vp, vp, vp, sz, vp],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -697,13 +725,17 @@ class PagedCache:
     page_table        int32 [requests][layers][kv_heads][max_pages]
     lens              int32 [requests][layers][kv_heads]: rows held
     mass              float32 [num_pages][page_size] or None: accumulated attention weights
+    positions         int32 [num_pages][page_size] or None: the rows' positions, where they are not
+                      the rows' numbers (kv_paged_append_rotary, kv_paged_place_positions)
+    refs              int32 [num_pages] or None: table entries in use that name a page
+                      (kv_paged_reserve, kv_paged_fork, kv_paged_compact)
 
-    ``status`` holds the first device-side condition that kv_paged_load, kv_paged_append or
-    kv_paged_attention met (a length or page that cannot be); kv_check_status(cache.status)
-    reads and clears it.
+    ``status`` holds the first device-side condition that a call on the cache met (a length or
+    page that cannot be, too few free pages); kv_check_status(cache.status) reads and clears it.
     """
 
-    def __init__(self, k_pages, v_pages, page_table, lens, num_q_heads: int, mass=None):
+    def __init__(self, k_pages, v_pages, page_table, lens, num_q_heads: int, mass=None,
+                 positions=None, refs=None):
         import torch
         if k_pages.dtype not in (torch.bfloat16, torch.float16) or k_pages.dim() != 3:
             raise ValueError("k_pages: bf16 or fp16 [num_pages][page_size][head_dim]")
@@ -715,10 +747,16 @@ class PagedCache:
             raise ValueError("lens: int32 [requests][layers][kv_heads]")
         if mass is not None and (mass.dtype != torch.float32 or mass.shape != k_pages.shape[:2]):
             raise ValueError("mass: float32 [num_pages][page_size]")
-        for t in (k_pages, v_pages, page_table, lens, mass):
+        if positions is not None and (positions.dtype != torch.int32 or
+                                      positions.shape != k_pages.shape[:2]):
+            raise ValueError("positions: int32 [num_pages][page_size]")
+        if refs is not None and (refs.dtype != torch.int32 or refs.shape != k_pages.shape[:1]):
+            raise ValueError("refs: int32 [num_pages]")
+        for t in (k_pages, v_pages, page_table, lens, mass, positions, refs):
             if t is not None and (not t.is_contiguous() or t.device != k_pages.device):
                 raise ValueError("the cache's tensors are contiguous and on one device")
         self.k_pages, self.v_pages, self.mass = k_pages, v_pages, mass
+        self.positions, self.refs = positions, refs
         self.page_table, self.lens = page_table, lens
         self.num_requests, self.num_layers, self.num_kv_heads, self.max_pages = page_table.shape
         self.num_q_heads = int(num_q_heads)
@@ -738,8 +776,9 @@ class PagedCache:
     @classmethod
     def allocate(cls, num_requests: int, num_layers: int, num_kv_heads: int, num_q_heads: int,
                  head_dim: int, max_rows: int, page_size: int = 64, dtype=None, mass: bool = False,
-                 device="cuda") -> "PagedCache":
-        """An empty cache with pages for `max_rows` rows of every unit, given out in order."""
+                 device="cuda", positions: bool = False, refs: bool = False) -> "PagedCache":
+        """An empty cache with pages for `max_rows` rows of every unit, entered in order.  With
+        refs every page is free: kv_paged_reserve enters others as rows come."""
         import torch
         cols = -(-max(int(max_rows), 1) // page_size)
         pages = max(num_requests * num_layers * num_kv_heads, 1) * cols
@@ -751,7 +790,9 @@ class PagedCache:
                    torch.zeros(pool, dtype=dtype, device=device),
                    torch.arange(count, dtype=torch.int32, device=device).view(*shape, cols),
                    torch.zeros(shape, dtype=torch.int32, device=device), num_q_heads,
-                   torch.zeros(pool[:2], dtype=torch.float32, device=device) if mass else None)
+                   torch.zeros(pool[:2], dtype=torch.float32, device=device) if mass else None,
+                   torch.zeros(pool[:2], dtype=torch.int32, device=device) if positions else None,
+                   torch.zeros(pages, dtype=torch.int32, device=device) if refs else None)
 
     @property
     def c(self):
@@ -929,3 +970,219 @@ def kv_paged_evict(cache: PagedCache, into: PagedCache, budgets, num_sinks: int,
                                  _ptr(kept), kept.shape[1], _ptr(workspace),
                                  workspace.numel() * workspace.element_size(), _stream(stream)),
            "kv_paged_evict")
+
+
+# ---------------------------------------------------------------------------
+# rotary positions
+# ---------------------------------------------------------------------------
+def kv_rotary_frequencies(dims: int, base: float = 10000.0, scaling: str = "none",
+                          scale: float = 1.0, context: float = 0.0, slow: float = 1.0,
+                          fast: float = 32.0):
+    """(inv_freq float32 [dims/2], factor) of rotary positions, scaled for contexts `scale` times
+    as long: "linear" (positions divided), "base" (a larger base), "parts" (by wavelength, for a
+    model of `context` positions)."""
+    if scaling not in _SCALINGS:
+        raise ValueError("scaling: one of %s" % ", ".join(_SCALINGS))
+    _check_int32("kv_rotary_frequencies", dims)
+    out = np.zeros(max(int(dims) // 2, 1), dtype=np.float32)
+    factor = ctypes.c_float()
+    _check(load().kv_rotary_frequencies(dims, base, _SCALINGS[scaling], scale, context, slow, fast,
+                                        out.ctypes.data_as(ctypes.POINTER(ctypes.c_float)),
+                                        ctypes.byref(factor)), "kv_rotary_frequencies")
+    return out, factor.value
+
+
+class Rotary:
+    """Rotary positions: inv_freq float32 [dims/2] on the device; pairs are (i, i + dims/2), or
+    neighbours if `interleaved`; the turned elements are multiplied by `factor`."""
+
+    def __init__(self, inv_freq, factor: float = 1.0, interleaved: bool = False):
+        import torch
+        if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+            raise ValueError("inv_freq: float32 [dims/2]")
+        self.inv_freq, self.factor, self.interleaved = inv_freq, float(factor), bool(interleaved)
+        self.dims = 2 * inv_freq.numel()
+        self._index = inv_freq.get_device()
+        self._c = _KvRotation(self.dims, int(self.interleaved), self.factor, inv_freq.data_ptr())
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def make(cls, dims: int, base: float = 10000.0, interleaved: bool = False, device="cuda",
+             **scaling) -> "Rotary":
+        """From kv_rotary_frequencies' arguments."""
+        import torch
+        inv_freq, factor = kv_rotary_frequencies(dims, base, **scaling)
+        return cls(torch.from_numpy(inv_freq).to(device), factor, interleaved)
+
+
+def _check_positions(positions, tokens: int) -> None:
+    import torch
+    if positions.dtype is not torch.int32 or positions.shape != (tokens,) or \
+            not positions.is_contiguous():
+        raise ValueError("positions: int32 [%d]" % tokens)
+
+
+def kv_rotary(rotary: Rotary, positions, x, out, backward: bool = False, stream=None):
+    """Rows x [tokens][heads][head_dim] (bf16 or fp16, any strides between rows) turned by their
+    tokens' positions (int32 [tokens]) into out, which may be x.  backward: turned the other way,
+    the gradient of x from that of out."""
+    import torch
+    if x.dtype not in (torch.bfloat16, torch.float16) or x.dim() != 3:
+        raise ValueError("x: bf16 or fp16 [tokens][heads][head_dim]")
+    if out.dtype is not x.dtype or out.shape != x.shape:
+        raise ValueError("out: the shape and dtype of x")
+    n, heads, d = x.shape
+    if n == 0 or heads == 0:
+        return
+    for t in (x, out):
+        if t.stride(2) != 1:
+            raise ValueError("x, out: the elements of a row are contiguous")
+    _check_positions(positions, n)
+    index = x.get_device()
+    if index < 0 or index != (_raw or _raw_calls())[0]():
+        raise ValueError("x is on %s, which is not the current CUDA device" % x.device)
+    for t in (out.get_device(), positions.get_device(), rotary._index):
+        if t != index:
+            raise ValueError("a tensor is on another device than x (%s)" % x.device)
+
+    def strides(t):
+        # of a single token or head, any
+        return t.stride(0) if n > 1 else d, t.stride(1) if heads > 1 else d
+
+    code = (_lib or load()).kv_rotary(
+        rotary._ref, positions.data_ptr(), n, heads, d,
+        KV_FP16 if x.dtype is torch.float16 else KV_BF16, x.data_ptr(), *strides(x),
+        out.data_ptr(), *strides(out), int(backward), _stream(stream))
+    if code:
+        raise KvError(code, "kv_rotary")
+
+
+def kv_paged_append_rotary(cache: PagedCache, chunk: Chunk, layer: int, rotary: Rotary, positions, q,
+                           q_out, k_new, v_new, stream=None):
+    """kv_paged_append of rows turned by their tokens' positions (int32 [tokens]): k_new into the
+    pages, q [tokens][q_heads][head_dim] into q_out (which may be q; both None: no queries); v_new is
+    copied.  The rows' positions go to cache.positions, if it keeps them."""
+    _check_chunk(cache, chunk)
+    if layer >> 31:                              # negative, or past 32 bits
+        _check_int32("kv_paged_append_rotary", layer)
+    ks = _token_stride(cache, chunk, k_new, cache.num_kv_heads, "k_new")
+    vs = _token_stride(cache, chunk, v_new, cache.num_kv_heads, "v_new")
+    qs = os_ = 0
+    if q is not None:
+        qs = _token_stride(cache, chunk, q, cache.num_q_heads, "q")
+        os_ = _token_stride(cache, chunk, q_out, cache.num_q_heads, "q_out")
+    _check_positions(positions, chunk.tokens)
+    _on_current_device(cache, k_new, v_new, q, None if q is None else q_out, positions,
+                       rotary.inv_freq)
+    code = (_lib or load()).kv_paged_append_rotary(
+        cache._ref, chunk._ref, layer, rotary._ref, positions.data_ptr(), _ptr(cache.positions),
+        _ptr(q), qs, None if q is None else q_out.data_ptr(), os_, k_new.data_ptr(), ks,
+        v_new.data_ptr(), vs, _stream(stream))
+    if code:
+        raise KvError(code, "kv_paged_append_rotary")
+
+
+def kv_paged_place_positions(cache: PagedCache, index=None, offsets=None,
+                             source: Optional[PagedCache] = None, stream=None):
+    """Positions of every unit's rows: row i of unit u gets index[u][i] (int32 [units][most rows]),
+    or index[offsets[u] + i] (index int32 [rows], offsets int64 [units + 1]: kept indices as
+    kv.evict returns them), or i; with `source`, a cache with positions, that of its row of that
+    number (index: the kept rows of kv_paged_evict)."""
+    import torch
+    if cache.positions is None or (source is not None and source.positions is None):
+        raise ValueError("the cache keeps no positions")
+    stride = 0
+    if index is not None:
+        if index.dtype != torch.int32 or not index.is_contiguous():
+            raise ValueError("index: int32, contiguous")
+        if offsets is None:
+            if index.dim() != 2 or index.shape[0] != cache.num_units:
+                raise ValueError("index: int32 [units][most rows]")
+            stride = index.shape[1]
+    if offsets is not None and (index is None or offsets.dtype != torch.int64 or
+                                offsets.numel() != cache.num_units + 1 or
+                                not offsets.is_contiguous()):
+        raise ValueError("offsets: int64 [units + 1], with an index")
+    if source is not None and index is None:
+        raise ValueError("rows of a source cache are named by an index")
+    _on_current_device(cache, index, offsets, None if source is None else source.k_pages)
+    _check(load().kv_paged_place_positions(
+        cache.c, _ptr(cache.positions), None if source is None else source.c,
+        None if source is None else _ptr(source.positions), _ptr(index), stride, _ptr(offsets),
+        _stream(stream)), "kv_paged_place_positions")
+
+
+# ---------------------------------------------------------------------------
+# pages given out, shared and moved together
+# ---------------------------------------------------------------------------
+def _check_refs(cache: PagedCache) -> None:
+    if cache.refs is None:
+        raise ValueError("the cache keeps no refs")
+
+
+def kv_paged_count_refs(cache: PagedCache, stream=None):
+    """cache.refs from its table and lens: after kv_paged_load or kv_paged_evict."""
+    _check_refs(cache)
+    _on_current_device(cache)
+    _check(load().kv_paged_count_refs(cache.c, cache.refs.data_ptr(), _stream(stream)),
+           "kv_paged_count_refs")
+
+
+def kv_paged_reserve_workspace_size(cache: PagedCache) -> int:
+    n = ctypes.c_size_t()
+    _check(load().kv_paged_reserve_workspace_size(cache.c, ctypes.byref(n)),
+           "kv_paged_reserve_workspace_size")
+    return n.value
+
+
+def kv_paged_reserve(cache: PagedCache, chunk: Chunk, workspace, stream=None):
+    """Room for a step's new tokens, in place of cache.advance: lengths raised, free pages entered,
+    shared last pages copied.  All or nothing: KV_ERR_BUDGET in cache.status if pages lack."""
+    _check_refs(cache)
+    _check_chunk(cache, chunk)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: contiguous")
+    _on_current_device(cache, workspace)
+    code = (_lib or load()).kv_paged_reserve(
+        cache._ref, chunk._ref, cache.refs.data_ptr(), _ptr(cache.positions), workspace.data_ptr(),
+        workspace.nbytes, _stream(stream))
+    if code:
+        raise KvError(code, "kv_paged_reserve")
+
+
+def kv_paged_fork(cache: PagedCache, parents, stream=None):
+    """Every request r goes on from request parents[r] (int32 [requests]), whose pages it shares;
+    r itself: no change; -1: emptied."""
+    import torch
+    _check_refs(cache)
+    if parents.dtype is not torch.int32 or parents.shape != (cache.num_requests,) or \
+            not parents.is_contiguous():
+        raise ValueError("parents: int32 [%d]" % cache.num_requests)
+    _on_current_device(cache, parents)
+    code = (_lib or load()).kv_paged_fork(cache._ref, cache.refs.data_ptr(), parents.data_ptr(),
+                                          _stream(stream))
+    if code:
+        raise KvError(code, "kv_paged_fork")
+
+
+def kv_paged_compact_workspace_size(cache: PagedCache) -> int:
+    n = ctypes.c_size_t()
+    _check(load().kv_paged_compact_workspace_size(cache.c, ctypes.byref(n)),
+           "kv_paged_compact_workspace_size")
+    return n.value
+
+
+def kv_paged_compact(cache: PagedCache, workspace, live=None, stream=None):
+    """Pages in use moved to the front of the pools; live: int32 [1], receives their number."""
+    import torch
+    _check_refs(cache)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: contiguous")
+    if live is not None and (live.dtype is not torch.int32 or live.numel() != 1):
+        raise ValueError("live: int32 [1]")
+    _on_current_device(cache, workspace, live)
+    code = (_lib or load()).kv_paged_compact(
+        cache._ref, cache.refs.data_ptr(), _ptr(cache.positions), _ptr(live), workspace.data_ptr(),
+        workspace.nbytes, _stream(stream))
+    if code:
+        raise KvError(code, "kv_paged_compact")

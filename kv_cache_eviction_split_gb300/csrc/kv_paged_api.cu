@@ -4,6 +4,8 @@
 #include <cmath>
 
 #include "kv_paged.cuh"
+#include "kv_pages.cuh"
+#include "kv_rotary.cuh"
 #include "kv_trace.cuh"
 
 using namespace kvevict;
@@ -82,6 +84,17 @@ kv_status make_chunk(const kv_chunk *t, const DevPaged &C, DevChunk *T) {
 }
 
 bool bad_stride(long long stride, long long least) { return stride < least || stride % 8 != 0; }
+
+kv_status make_rotary(const kv_rotation *r, int d, bool backward, DevRotary *A) {
+    if (!r || r->dims < 0 || r->dims > d) return KV_ERR_INVALID_ARG;
+    if (r->dims % 16 != 0) return KV_ERR_UNSUPPORTED;
+    if (!std::isfinite(r->factor) || (r->dims > 0 && !r->inv_freq)) return KV_ERR_INVALID_ARG;
+    *A = DevRotary{r->dims, r->interleaved != 0, backward, r->factor, r->inv_freq};
+    return KV_OK;
+}
+
+// The counts of a cache's pages.
+bool bad_refs(const DevPaged &C, const int32_t *refs) { return C.units > 0 && bad_ptr(refs); }
 
 }  // namespace
 
@@ -197,6 +210,182 @@ kv_status kv_paged_evict(const kv_paged *src, const kv_paged *dst, const int32_t
         return KV_ERR_CUDA;
     return map_cuda(launch_paged_evict(S, D, budgets_dev, num_sinks, recent, kept, kept_stride,
                                        status, (cudaStream_t)stream));
+}
+
+kv_status kv_rotary_frequencies(int32_t dims, double base, int32_t scaling, double scale,
+                                double context, double slow, double fast, float *inv_freq,
+                                float *factor) {
+    if (dims < 2 || dims % 2 != 0 || !(base > 0) || !std::isfinite(base) || !inv_freq || !factor)
+        return KV_ERR_INVALID_ARG;
+    if (scaling < KV_ROTARY_NONE || scaling > KV_ROTARY_PARTS) return KV_ERR_INVALID_ARG;
+    if (scaling != KV_ROTARY_NONE && (!(scale >= 1) || !std::isfinite(scale)))
+        return KV_ERR_INVALID_ARG;
+    if (scaling == KV_ROTARY_PARTS && (!(context > 0) || !std::isfinite(context) || !(slow >= 0) ||
+                                       !(fast > slow) || !std::isfinite(fast)))
+        return KV_ERR_INVALID_ARG;
+    if (scaling == KV_ROTARY_BASE && dims > 2) base *= std::pow(scale, dims / (dims - 2.0));
+    for (int i = 0; i < dims / 2; ++i) {
+        double w = std::pow(base, -2.0 * i / dims);
+        if (scaling == KV_ROTARY_LINEAR) {
+            w /= scale;
+        } else if (scaling == KV_ROTARY_PARTS) {
+            const double turns = context * w / 6.283185307179586;
+            const double keep = std::min(1.0, std::max(0.0, (turns - slow) / (fast - slow)));
+            w = w * keep + w / scale * (1.0 - keep);
+        }
+        inv_freq[i] = (float)w;
+    }
+    *factor = scaling == KV_ROTARY_PARTS ? (float)(0.1 * std::log(scale) + 1.0) : 1.0f;
+    return KV_OK;
+}
+
+kv_status kv_rotary(const kv_rotation *rot, const int32_t *positions, int64_t tokens, int32_t heads,
+                    int32_t head_dim, int32_t dtype, const void *x, int64_t x_stride,
+                    int64_t x_head_stride, void *out, int64_t out_stride, int64_t out_head_stride,
+                    int32_t backward, void *stream) {
+    KV_API_RANGE();
+    DevRotary A;
+    if (tokens < 0 || heads < 1 || (dtype != KV_BF16 && dtype != KV_FP16)) return KV_ERR_INVALID_ARG;
+    if (head_dim != 64 && head_dim != 128) return KV_ERR_UNSUPPORTED;
+    const kv_status st = make_rotary(rot, head_dim, backward != 0, &A);
+    if (st != KV_OK) return st;
+    // a block's rows are counted in 32 bits
+    if (heads >= (1 << 24) || tokens >= (1LL << 40)) return KV_ERR_UNSUPPORTED;
+    if (tokens == 0) return KV_OK;
+    if (!positions || bad_ptr(x) || bad_ptr(out)) return KV_ERR_INVALID_ARG;
+    for (long long s : {x_stride, x_head_stride, out_stride, out_head_stride})
+        if (s < 0 || s % 8 != 0) return KV_ERR_INVALID_ARG;
+    // rows that lie on one another cannot be written
+    if ((tokens > 1 && out_stride < head_dim) || (heads > 1 && out_head_stride < head_dim))
+        return KV_ERR_INVALID_ARG;
+    if (x == out && (x_stride != out_stride || x_head_stride != out_head_stride))
+        return KV_ERR_INVALID_ARG;
+    const RotaryIo io{static_cast<const uint4 *>(x), x_stride / 8,   x_head_stride / 8,
+                      static_cast<uint4 *>(out),     out_stride / 8, out_head_stride / 8};
+    return map_cuda(launch_rotary(A, tokens, heads, head_dim, dtype, positions, io,
+                                  (cudaStream_t)stream));
+}
+
+kv_status kv_paged_append_rotary(const kv_paged *c, const kv_chunk *t, int32_t layer,
+                                 const kv_rotation *rot, const int32_t *positions, int32_t *row_pos,
+                                 const void *q, int64_t q_stride, void *q_out, int64_t q_out_stride,
+                                 const void *k_new, int64_t k_stride, const void *v_new,
+                                 int64_t v_stride, void *stream) {
+    KV_API_RANGE();
+    DevPaged C;
+    DevChunk T;
+    DevRotary A;
+    kv_status st = make_paged(c, &C);
+    if (st == KV_OK) st = make_chunk(t, C, &T);
+    if (st == KV_OK) st = make_rotary(rot, C.d, false, &A);
+    if (st != KV_OK) return st;
+    if (layer < 0 || layer >= C.L) return KV_ERR_INVALID_ARG;
+    if (C.Hq + 2LL * C.H >= (1 << 24)) return KV_ERR_UNSUPPORTED;
+    if (T.tokens == 0) return KV_OK;
+    const long long row = (long long)C.H * C.d, q_row = (long long)C.Hq * C.d;
+    if (!positions || bad_ptr(k_new) || bad_ptr(v_new) || bad_stride(k_stride, row) ||
+        bad_stride(v_stride, row))
+        return KV_ERR_INVALID_ARG;
+    if (q && (bad_ptr(q) || bad_ptr(q_out) || bad_stride(q_stride, q_row) ||
+              bad_stride(q_out_stride, q_row) || (q == q_out && q_stride != q_out_stride)))
+        return KV_ERR_INVALID_ARG;
+    const AppendIo io{static_cast<const uint4 *>(q),     q_stride / 8,
+                      static_cast<uint4 *>(q_out),       q_out_stride / 8,
+                      static_cast<const uint4 *>(k_new), static_cast<const uint4 *>(v_new),
+                      k_stride / 8,                      v_stride / 8};
+    return map_cuda(launch_append_rotary(C, T, layer, A, positions, row_pos, io,
+                                         (cudaStream_t)stream));
+}
+
+kv_status kv_paged_count_refs(const kv_paged *c, int32_t *refs, void *stream) {
+    KV_API_RANGE();
+    DevPaged C;
+    const kv_status st = make_paged(c, &C);
+    if (st != KV_OK) return st;
+    if (bad_refs(C, refs)) return KV_ERR_INVALID_ARG;
+    if (!refs) return KV_OK;
+    return map_cuda(launch_count_refs(C, refs, (cudaStream_t)stream));
+}
+
+kv_status kv_paged_reserve_workspace_size(const kv_paged *c, size_t *bytes) {
+    DevPaged C;
+    const kv_status st = make_paged(c, &C);
+    if (st != KV_OK) return st;
+    if (!bytes) return KV_ERR_INVALID_ARG;
+    *bytes = reserve_ws_layout(C, nullptr).total;
+    return KV_OK;
+}
+
+kv_status kv_paged_reserve(const kv_paged *c, const kv_chunk *t, int32_t *refs, int32_t *row_pos,
+                           void *workspace, size_t workspace_bytes, void *stream) {
+    KV_API_RANGE();
+    DevPaged C;
+    DevChunk T;
+    kv_status st = make_paged(c, &C);
+    if (st == KV_OK) st = make_chunk(t, C, &T);
+    if (st != KV_OK) return st;
+    if (C.units >= (1 << 28)) return KV_ERR_UNSUPPORTED;
+    if (T.tokens == 0) return KV_OK;
+    if (bad_refs(C, refs) || !aligned16(row_pos) || bad_ptr(workspace)) return KV_ERR_INVALID_ARG;
+    const PagesWs ws = reserve_ws_layout(C, workspace);
+    if (workspace_bytes < ws.total) return KV_ERR_WORKSPACE;
+    // the pages that the tokens fill in any case
+    double least = 0;
+    for (int r = 0; r < C.R; ++r)
+        least += (double)((T.host_off[r + 1] - T.host_off[r]) / C.ps) * C.L * C.H;
+    if (least > (double)C.num_pages) return KV_ERR_BUDGET;
+    return map_cuda(launch_reserve(C, T, refs, row_pos, ws, (cudaStream_t)stream));
+}
+
+kv_status kv_paged_fork(const kv_paged *c, int32_t *refs, const int32_t *parents, void *stream) {
+    KV_API_RANGE();
+    DevPaged C;
+    const kv_status st = make_paged(c, &C);
+    if (st != KV_OK) return st;
+    if (C.R > kForkRequests) return KV_ERR_UNSUPPORTED;
+    if (C.units == 0) return KV_OK;
+    if (bad_refs(C, refs) || !parents) return KV_ERR_INVALID_ARG;
+    return map_cuda(launch_fork(C, refs, parents, (cudaStream_t)stream));
+}
+
+kv_status kv_paged_compact_workspace_size(const kv_paged *c, size_t *bytes) {
+    DevPaged C;
+    const kv_status st = make_paged(c, &C);
+    if (st != KV_OK) return st;
+    if (!bytes) return KV_ERR_INVALID_ARG;
+    *bytes = compact_ws_layout(C, nullptr).total;
+    return KV_OK;
+}
+
+kv_status kv_paged_compact(const kv_paged *c, int32_t *refs, int32_t *row_pos, int32_t *live,
+                           void *workspace, size_t workspace_bytes, void *stream) {
+    KV_API_RANGE();
+    DevPaged C;
+    const kv_status st = make_paged(c, &C);
+    if (st != KV_OK) return st;
+    if (C.units == 0) return KV_OK;
+    if (bad_refs(C, refs) || !aligned16(row_pos) || bad_ptr(workspace)) return KV_ERR_INVALID_ARG;
+    const PagesWs ws = compact_ws_layout(C, workspace);
+    if (workspace_bytes < ws.total) return KV_ERR_WORKSPACE;
+    return map_cuda(launch_compact_pages(C, refs, row_pos, live, ws, (cudaStream_t)stream));
+}
+
+kv_status kv_paged_place_positions(const kv_paged *dst, int32_t *dst_pos, const kv_paged *src,
+                                   const int32_t *src_pos, const int32_t *index, int64_t stride,
+                                   const int64_t *offsets, void *stream) {
+    KV_API_RANGE();
+    DevPaged D, S;
+    kv_status st = make_paged(dst, &D);
+    if (st == KV_OK && src_pos) st = make_paged(src, &S);
+    else S = D;
+    if (st != KV_OK) return st;
+    if (src_pos && (S.R != D.R || S.L != D.L || S.H != D.H || src_pos == dst_pos))
+        return KV_ERR_INVALID_ARG;
+    if (D.units == 0) return KV_OK;
+    if (!dst_pos || stride < 0 || (src_pos && !index) || (offsets && !index))
+        return KV_ERR_INVALID_ARG;
+    return map_cuda(launch_place_positions(D, dst_pos, S, src_pos, index, stride, offsets,
+                                           (cudaStream_t)stream));
 }
 
 }  // extern "C"
