@@ -18,6 +18,8 @@
  *   kv_paged_attention               attention of new tokens over the pages (causal,
  *                                    optionally a sliding window with visible sinks),
  *                                    accumulating each row's attention weight
+ *   kv_paged_attention_scored        the same of scores that are capped or lowered by distance,
+ *                                    masked by position
  *   kv_paged_evict                   eviction by accumulated attention weight
  *   kv_rotary, kv_paged_append_rotary  rotary positions, alone or on the way into the pages
  *   kv_paged_reserve, kv_paged_fork, kv_paged_compact  pages given out, shared between
@@ -497,6 +499,53 @@ kv_status kv_paged_attention(const kv_paged *c, const kv_chunk *t, int32_t layer
                              int64_t q_stride, void *out, int64_t out_stride, float *lse,
                              int32_t add_mass, void *workspace, size_t workspace_bytes,
                              void *stream);
+
+/*
+ * What changes the scores of kv_paged_attention_scored.  Of a query at position p and a row at
+ * position p_j:
+ *   s_j = softmax_scale * q.k_j
+ *   s_j = softcap * tanh(s_j / softcap)                         (softcap > 0)
+ *   s_j = s_j - slopes[head] * |p - p_j|                        (slopes)
+ * A row's position is row_pos's, i32 [num_pages][page_size] beside the pools (as
+ * kv_paged_append_rotary and kv_paged_place_positions leave them), or without it its
+ * number j; a query's position is that of its own cache row t = lens[u] - T_r + i.
+ * Positions are >= 0 and never fall from a unit's row to the next; distances are exact
+ * up to 2^24.
+ * The query sees the rows with
+ *   p_j >= first[token]  (and j > t - window)  or  j < num_sinks,   and
+ *   p_j <= last[token]
+ * (positions, i32 [tokens]; first NULL: from the start; last NULL: up to its own
+ * row.  So first = where a token's document begins keeps documents of a packed prompt
+ * apart, or makes a window of positions; last beyond the token's own position lets the
+ * tokens of a prefix see one another both ways.)  window as in kv_paged_attention;
+ * num_sinks is ignored without a window or first.  A query without a row of its own
+ * (t < 0), or that sees no row, gets out = 0 and lse = -inf.
+ */
+typedef struct kv_scoring {
+    float softcap;             /* 0: none */
+    int32_t window;            /* 0: none */
+    int32_t num_sinks;
+    const float *slopes;       /* f32 [H_q], device, any finite values, or NULL */
+    const int32_t *row_pos;    /* or NULL */
+    const int32_t *first, *last;   /* or NULL */
+} kv_scoring;
+
+kv_status kv_paged_attention_scored_workspace_size(const kv_paged *c, const kv_chunk *t,
+                                                   int32_t add_mass, size_t *bytes);
+
+/*
+ * kv_paged_attention of scores that are changed as above; the other arguments, what is
+ * rounded and how, errors and the status word are that call's.  With first or last, the
+ * rows between the first and the last that any query of a request's chunk sees must
+ * hold finite values, on pages that exist.  lse is of the changed scores.
+ * add_mass: as there, for steps of at most 16 query rows a head in every request
+ * (KV_ERR_UNSUPPORTED otherwise).
+ */
+kv_status kv_paged_attention_scored(const kv_paged *c, const kv_chunk *t, int32_t layer,
+                                    const kv_scoring *f, float softmax_scale, const void *q,
+                                    int64_t q_stride, void *out, int64_t out_stride, float *lse,
+                                    int32_t add_mass, void *workspace, size_t workspace_bytes,
+                                    void *stream);
 
 /* Bytes of workspace kv_paged_evict needs. */
 kv_status kv_paged_evict_workspace_size(const kv_paged *src, size_t *bytes);

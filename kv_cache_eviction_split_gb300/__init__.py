@@ -37,6 +37,7 @@ __all__ = ["KvError", "Problem", "load", "build", "kv_score", "kv_score_attentio
            "PagedCache", "Chunk", "kv_paged_append", "kv_paged_load", "kv_paged_attention",
            "kv_paged_attention_workspace_size", "kv_paged_evict",
            "kv_paged_evict_workspace_size", "Rotary", "kv_rotary_frequencies", "kv_rotary",
+           "kv_paged_attention_scored", "kv_paged_attention_scored_workspace_size",
            "kv_paged_append_rotary", "kv_paged_place_positions", "kv_paged_count_refs",
            "kv_paged_reserve", "kv_paged_reserve_workspace_size", "kv_paged_fork",
            "kv_paged_compact", "kv_paged_compact_workspace_size"]
@@ -60,6 +61,7 @@ EXPORTED_SYMBOLS = ("kv_score_workspace_size", "kv_score", "kv_score_attention",
                     "kv_evict_host", "kv_paged_append", "kv_paged_load",
                     "kv_paged_attention", "kv_paged_attention_workspace_size",
                     "kv_paged_evict", "kv_paged_evict_workspace_size",
+                    "kv_paged_attention_scored", "kv_paged_attention_scored_workspace_size",
                     "kv_rotary_frequencies", "kv_rotary", "kv_paged_append_rotary",
                     "kv_paged_place_positions", "kv_paged_count_refs", "kv_paged_reserve",
                     "kv_paged_reserve_workspace_size", "kv_paged_fork", "kv_paged_compact",
@@ -105,6 +107,13 @@ class _KvChunk(ctypes.Structure):
 class _KvRotation(ctypes.Structure):
     _fields_ = [("dims", ctypes.c_int32), ("interleaved", ctypes.c_int32),
                 ("factor", ctypes.c_float), ("inv_freq", ctypes.c_void_p)]
+
+
+class _KvScoring(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32),
+                ("num_sinks", ctypes.c_int32), ("slopes", ctypes.c_void_p),
+                ("row_pos", ctypes.c_void_p), ("first", ctypes.c_void_p),
+                ("last", ctypes.c_void_p)]
 
 
 _lib = None
@@ -180,6 +189,9 @@ def _bind(lib):
         "kv_paged_attention_workspace_size": [PC, PT, i32, szp],
         "kv_paged_attention": [PC, PT, i32, i32, i32, ctypes.c_float, vp, i64, vp, i64, vp, i32,
                                vp, sz, vp],
+        "kv_paged_attention_scored_workspace_size": [PC, PT, i32, szp],
+        "kv_paged_attention_scored": [PC, PT, i32, ctypes.POINTER(_KvScoring), ctypes.c_float, vp, i64,
+                                      vp, i64, vp, i32, vp, sz, vp],
         "kv_paged_evict_workspace_size": [PC, szp],
         "kv_paged_evict": [PC, PC, vp, i32, i32, vp, i64, vp, sz, vp],
         "kv_rotary_frequencies": [i32, f64, i32, f64, f64, f64, f64, ctypes.POINTER(ctypes.c_float),
@@ -942,6 +954,56 @@ def kv_paged_attention(cache: PagedCache, chunk: Chunk, layer: int, q, out, work
         _stream(stream))
     if code:
         raise KvError(code, "kv_paged_attention")
+
+
+def kv_paged_attention_scored_workspace_size(cache: PagedCache, chunk: Chunk,
+                                             add_mass: bool = False) -> int:
+    _check_requests(cache, chunk)
+    n = ctypes.c_size_t()
+    _check(load().kv_paged_attention_scored_workspace_size(cache.c, chunk.c, int(add_mass),
+                                                           ctypes.byref(n)),
+           "kv_paged_attention_scored_workspace_size")
+    return n.value
+
+
+def kv_paged_attention_scored(cache: PagedCache, chunk: Chunk, layer: int, q, out, workspace,
+                              softcap: float = 0.0, slopes=None, first=None, last=None,
+                              window: int = 0, num_sinks: int = 0,
+                              softmax_scale: Optional[float] = None, lse=None,
+                              add_mass: bool = False, stream=None):
+    """kv_paged_attention of changed scores: softcap * tanh(score / softcap), lowered by
+    slopes[head] (float32 [q_heads]) times the distance of positions.  first, last (int32
+    [tokens]): the first and last positions that a token sees (default: the start, its own row).
+    Positions are cache.positions, or the rows' numbers."""
+    import torch
+    heads = cache.num_q_heads
+    _check_chunk(cache, chunk)
+    if (layer | window | num_sinks) >> 31:       # one is negative, or past 32 bits
+        _check_int32("kv_paged_attention_scored", layer, window, num_sinks)
+    qs = _token_stride(cache, chunk, q, heads, "q")
+    os_ = _token_stride(cache, chunk, out, heads, "out")
+    if lse is not None and (lse.dtype is not torch.float32 or not lse.is_contiguous() or
+                            lse.shape != (chunk.tokens, heads)):
+        raise ValueError("lse: float32 [%d][%d]" % (chunk.tokens, heads))
+    if slopes is not None and (slopes.dtype is not torch.float32 or not slopes.is_contiguous() or
+                               slopes.shape != (heads,)):
+        raise ValueError("slopes: float32 [%d]" % heads)
+    for t in (first, last):
+        if t is not None and (t.dtype is not torch.int32 or not t.is_contiguous() or
+                              t.shape != (chunk.tokens,)):
+            raise ValueError("first, last: int32 [%d]" % chunk.tokens)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: contiguous")
+    _on_current_device(cache, q, out, lse, workspace, slopes, first, last)
+    form = _KvScoring(softcap, window, num_sinks, _ptr(slopes), _ptr(cache.positions), _ptr(first),
+                      _ptr(last))
+    code = (_lib or load()).kv_paged_attention_scored(
+        cache._ref, chunk._ref, layer, ctypes.byref(form),
+        cache._scale if softmax_scale is None else softmax_scale, q.data_ptr(), qs,
+        out.data_ptr(), os_, _ptr(lse), int(add_mass), workspace.data_ptr(), workspace.nbytes,
+        _stream(stream))
+    if code:
+        raise KvError(code, "kv_paged_attention_scored")
 
 
 def kv_paged_evict_workspace_size(cache: PagedCache) -> int:

@@ -162,6 +162,9 @@ __device__ __forceinline__ int part_slot(int cta, bool begun_here) {
     return 2 * cta + (begun_here ? 1 : 0);
 }
 
+struct RowBounds;                // kv_paged_scores.cuh
+struct BlockBounds;
+
 // Workspace of the attention (all offsets 256-byte aligned).
 struct AttendWs {
     CutItem *cut;              // [ctas], a set for each phase; unit -1: no item ends here that
@@ -176,9 +179,15 @@ struct AttendWs {
     // few rows with add_mass: the logits (log2 units, -inf unseen) of every tile of every
     // unit of the layer, in its span's order; rows: the most of a unit that these kernels take
     float *logits;             // [R * H][ceil(cap / kFewTile)][rows][kFewTile]
+    // changed scores: rows that queries see, by position
+    RowBounds *rows;
+    BlockBounds *blocks;
     size_t total;
 };
-AttendWs attend_ws_layout(const DevPaged &C, const DevChunk &T, bool add_mass, void *base);
+AttendWs attend_ws_layout(const DevPaged &C, const DevChunk &T, bool add_mass, void *base,
+                          bool bounds = false);
+// Whether no request has more query rows a head than the few-rows kernels take in any case.
+bool attend_few_only(const DevPaged &C, const DevChunk &T);
 
 struct AttendIo {
     const void *q;

@@ -4,6 +4,7 @@
 #include <cmath>
 
 #include "kv_paged.cuh"
+#include "kv_paged_scores.cuh"
 #include "kv_pages.cuh"
 #include "kv_rotary.cuh"
 #include "kv_trace.cuh"
@@ -178,6 +179,59 @@ kv_status kv_paged_attention(const kv_paged *c, const kv_chunk *t, int32_t layer
     const AttendIo io{q, out, lse, q_stride, out_stride};
     return map_cuda(launch_paged_attention(C, T, layer, M, io, add_mass != 0, ws,
                                            (cudaStream_t)stream));
+}
+
+kv_status kv_paged_attention_scored_workspace_size(const kv_paged *c, const kv_chunk *t,
+                                                   int32_t add_mass, size_t *bytes) {
+    DevPaged C;
+    DevChunk T;
+    const kv_status st = check_attention(c, t, add_mass, &C, &T);
+    if (st != KV_OK) return st;
+    if (!bytes) return KV_ERR_INVALID_ARG;
+    if (add_mass && !attend_few_only(C, T)) return KV_ERR_UNSUPPORTED;
+    *bytes = attend_ws_layout(C, T, add_mass != 0, nullptr, true).total;
+    return KV_OK;
+}
+
+kv_status kv_paged_attention_scored(const kv_paged *c, const kv_chunk *t, int32_t layer,
+                                    const kv_scoring *f, float softmax_scale, const void *q,
+                                    int64_t q_stride, void *out, int64_t out_stride, float *lse,
+                                    int32_t add_mass, void *workspace, size_t workspace_bytes,
+                                    void *stream) {
+    KV_API_RANGE();
+    DevPaged C;
+    DevChunk T;
+    kv_status st = check_attention(c, t, add_mass, &C, &T);
+    if (st != KV_OK) return st;
+    if (!f || layer < 0 || layer >= C.L || f->window < 0 || f->num_sinks < 0)
+        return KV_ERR_INVALID_ARG;
+    if (!(softmax_scale > 0.0f) || !std::isfinite(softmax_scale)) return KV_ERR_INVALID_ARG;
+    if (!(f->softcap >= 0.0f) || !std::isfinite(f->softcap)) return KV_ERR_INVALID_ARG;
+    if (add_mass && !attend_few_only(C, T)) return KV_ERR_UNSUPPORTED;
+    if (T.tokens == 0) return KV_OK;
+    const long long row = (long long)C.Hq * C.d;
+    if (bad_ptr(q) || bad_ptr(out) || !aligned16(lse) || bad_ptr(workspace) ||
+        !aligned16(f->row_pos) || bad_stride(q_stride, row) || bad_stride(out_stride, row))
+        return KV_ERR_INVALID_ARG;
+    const AttendWs ws = attend_ws_layout(C, T, add_mass != 0, workspace, true);
+    if (workspace_bytes < ws.total) return KV_ERR_WORKSPACE;
+    // a window of the table's length or more hides nothing
+    const int w = f->window >= C.cap ? 0 : f->window;
+    const float log2e = 1.4426950408889634f, scale_log2 = softmax_scale * log2e;
+    const AttendMask M{w, w > 0 || f->first ? f->num_sinks : 0, scale_log2};
+    if (!attend_tiles_fit(C, T, M, add_mass != 0)) return KV_ERR_UNSUPPORTED;
+    const AttendIo io{q, out, lse, q_stride, out_stride};
+    if (!(f->softcap > 0.0f) && !f->slopes && !f->first && !f->last)
+        return map_cuda(launch_paged_attention(C, T, layer, M, io, add_mass != 0, ws,
+                                               (cudaStream_t)stream));
+    ScoreForm form{};
+    form.cap2 = f->softcap * log2e;
+    form.cap_u = f->softcap > 0.0f ? 2.0f * scale_log2 / f->softcap : 0.0f;
+    form.slopes = f->slopes;
+    form.pos = f->slopes ? f->row_pos : nullptr;
+    return map_cuda(launch_paged_attention_scored(C, T, layer, M, form,
+                                                  ScoreBounds{f->row_pos, f->first, f->last}, io,
+                                                  add_mass != 0, ws, (cudaStream_t)stream));
 }
 
 kv_status kv_paged_evict_workspace_size(const kv_paged *src, size_t *bytes) {

@@ -4,6 +4,7 @@
 #include <algorithm>
 
 #include "kv_paged_attend.cuh"
+#include "kv_paged_scores.cuh"
 
 namespace kvevict {
 namespace {
@@ -130,7 +131,15 @@ Classes classify(const DevPaged &C, const DevChunk &T, long long seen, bool add_
 }
 }  // namespace
 
-AttendWs attend_ws_layout(const DevPaged &C, const DevChunk &T, bool add_mass, void *base) {
+namespace {
+// Blocks of 128 query rows to a unit.
+int unit_blocks(const DevPaged &C, const DevChunk &T) {
+    return (int)(((long long)T.max_t * C.G + 127) / 128);
+}
+}  // namespace
+
+AttendWs attend_ws_layout(const DevPaged &C, const DevChunk &T, bool add_mass, void *base,
+                          bool bounds) {
     AttendWs ws{};
     char *b = static_cast<char *>(base);
     size_t off = 0;
@@ -155,6 +164,11 @@ AttendWs attend_ws_layout(const DevPaged &C, const DevChunk &T, bool add_mass, v
         ws.q_packed = take(k.many ? (size_t)T.tokens * C.Hq * C.d * 2 : 0);
         ws.logits = reinterpret_cast<float *>(
             take(k.few_requests ? tiles * k.max_rows * kFewTile * sizeof(float) : 0));
+    }
+    if (bounds) {
+        ws.rows = reinterpret_cast<RowBounds *>(take((size_t)T.tokens * C.H * sizeof(RowBounds)));
+        ws.blocks = reinterpret_cast<BlockBounds *>(
+            take((size_t)C.R * C.H * unit_blocks(C, T) * sizeof(BlockBounds)));
     }
     ws.total = off;
     return ws;
@@ -187,22 +201,55 @@ bool attend_tiles_fit(const DevPaged &C, const DevChunk &T, const AttendMask &M,
     return few <= most && many <= most && (!add_mass || weights <= most);
 }
 
-cudaError_t launch_paged_attention(const DevPaged &C, const DevChunk &T0, int layer,
-                                   const AttendMask &M, const AttendIo &io, bool add_mass,
-                                   const AttendWs &ws, cudaStream_t s) {
+bool attend_few_only(const DevPaged &C, const DevChunk &T) {
+    return (long long)T.max_t * C.G <= kFewRows;
+}
+
+namespace {
+// form: null for plain scores.
+cudaError_t attend(const DevPaged &C, const DevChunk &T0, int layer, const AttendMask &M,
+                   const ScoreForm *form, const AttendIo &io, bool add_mass, const AttendWs &ws,
+                   cudaStream_t s) {
     const long long seen = rows_seen(C, T0, M);
     const Classes k = classify(C, T0, seen, add_mass);
     DevChunk T = T0;
     T.few_max = k.few_max;
     cudaError_t e = cudaSuccess;
     if (k.few_requests)
-        e = launch_attend_few(C, T, layer, M, io, add_mass, seen, k.items, k.max_rows, k.blocks, ws,
-                              s);
+        e = form ? launch_attend_few_scored(C, T, layer, M, *form, io, add_mass, seen, k.items,
+                                            k.max_rows, k.blocks, ws, s)
+                 : launch_attend_few(C, T, layer, M, io, add_mass, seen, k.items, k.max_rows,
+                                     k.blocks, ws, s);
     if (e == cudaSuccess && k.many) {
-        e = launch_attend_many(C, T, layer, M, io, ws, s);
+        e = form ? launch_attend_many_scored(C, T, layer, M, *form, io, ws, s)
+                 : launch_attend_many(C, T, layer, M, io, ws, s);
+        // (changed scores: kv_paged_attention_scored refuses add_mass for such steps)
         if (e == cudaSuccess && add_mass) e = launch_many_mass(C, T, layer, M, ws, s);
     }
     return e;
+}
+}  // namespace
+
+cudaError_t launch_paged_attention(const DevPaged &C, const DevChunk &T, int layer,
+                                   const AttendMask &M, const AttendIo &io, bool add_mass,
+                                   const AttendWs &ws, cudaStream_t s) {
+    return attend(C, T, layer, M, nullptr, io, add_mass, ws, s);
+}
+
+cudaError_t launch_paged_attention_scored(const DevPaged &C, const DevChunk &T, int layer,
+                                          const AttendMask &M, const ScoreForm &form0,
+                                          const ScoreBounds &bounds, const AttendIo &io,
+                                          bool add_mass, const AttendWs &ws, cudaStream_t s) {
+    ScoreForm form = form0;
+    if (bounds.first || bounds.last) {
+        form.rows = ws.rows;
+        form.blocks = ws.blocks;
+        form.unit_blocks = unit_blocks(C, T);
+        const cudaError_t e = launch_row_bounds(C, T, layer, M, bounds, ws.rows, ws.blocks,
+                                                form.unit_blocks, s);
+        if (e != cudaSuccess) return e;
+    }
+    return attend(C, T, layer, M, &form, io, add_mass, ws, s);
 }
 
 }  // namespace kvevict
