@@ -217,16 +217,16 @@ kv_status kv_paged_attention_scored(const kv_paged *c, const kv_chunk *t, int32_
     if (workspace_bytes < ws.total) return KV_ERR_WORKSPACE;
     // a window of the table's length or more hides nothing
     const int w = f->window >= C.cap ? 0 : f->window;
-    const float log2e = 1.4426950408889634f, scale_log2 = softmax_scale * log2e;
-    const AttendMask M{w, w > 0 || f->first ? f->num_sinks : 0, scale_log2};
+    const AttendMask M{w, w > 0 || f->first ? f->num_sinks : 0, softmax_scale * kLog2e};
     if (!attend_tiles_fit(C, T, M, add_mass != 0)) return KV_ERR_UNSUPPORTED;
     const AttendIo io{q, out, lse, q_stride, out_stride};
     if (!(f->softcap > 0.0f) && !f->slopes && !f->first && !f->last)
         return map_cuda(launch_paged_attention(C, T, layer, M, io, add_mass != 0, ws,
                                                (cudaStream_t)stream));
     ScoreForm form{};
-    form.cap2 = f->softcap * log2e;
-    form.cap_u = f->softcap > 0.0f ? 2.0f * scale_log2 / f->softcap : 0.0f;
+    if (f->softcap > 0.0f) form.set_cap(f->softcap, softmax_scale);
+    form.slope_s = 1.0f / softmax_scale;
+    form.two_way = f->last != nullptr;
     form.slopes = f->slopes;
     form.pos = f->slopes ? f->row_pos : nullptr;
     return map_cuda(launch_paged_attention_scored(C, T, layer, M, form,

@@ -355,7 +355,9 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) sc[nt][i] = form_logit(A.form, cs, sc[nt][i]);
+                        for (int i = 0; i < 4; ++i)
+                            sc[nt][i] = A.form.cap2 == 0.f ? sc[nt][i] * cs
+                                                           : cap_logit(A.form, sc[nt][i]);
                     if (A.form.slopes) {
                         const int *ps = reinterpret_cast<const int *>(smem + Ly::kPos +
                                                                       s * Ly::kPosStage);

@@ -34,7 +34,7 @@ namespace kvevict {
 
 cudaError_t launch_attend_many(const DevPaged &C, const DevChunk &T, int layer, const AttendMask &M,
                                const AttendIo &io, const AttendWs &ws, cudaStream_t s) {
-    return attend_many<false>(C, T, layer, M, ScoreForm{}, io, ws, s);
+    return attend_many<kPlain>(C, T, layer, M, ScoreForm{}, io, ws, s);
 }
 
 }  // namespace kvevict

@@ -1,6 +1,9 @@
 // kv_paged_many.cuh -- the many-rows attention kernel; kv_paged_many.cu says what it does, and
-// instantiates it for plain scores, kv_paged_many_scored.cu for changed ones (kMod).
+// instantiates it for plain scores, kv_paged_many_scored.cu, _capped.cu and _sloped.cu for changed
+// ones (kForm).
 #pragma once
+#include <type_traits>
+
 #include "kv_paged_attend.cuh"
 #include "kv_paged_scores.cuh"
 
@@ -189,27 +192,62 @@ __device__ __forceinline__ float max32(const float (&v)[32]) {
     return fmaxf(fmax3(b0, b1, b2), b3);
 }
 
-// Logits of a row (128 keys) changed in place: s becomes z, in units of log2.
-__device__ __forceinline__ void change_logits(const ScoreForm &F, float scale_log2,
-                                              float (&s)[4][32]) {
-    if (F.cap2 == 0.f) {
+// cap2 tanh(cap_x s) + add of 2 G logits from s on in place, by an odd polynomial: step by step for
+// all of them, so that none of its chain of products waits for the one before.
+template <int G, int N>
+__device__ __forceinline__ void cap_poly(const float2 (&c2)[N], float2 add, float *s) {
+    float2 x[G], y[G], p[G];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+    for (int g = 0; g < G; ++g) x[g] = make_float2(s[2 * g], s[2 * g + 1]);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) s[c][i] *= scale_log2;
-        return;
+    for (int g = 0; g < G; ++g) y[g] = __fmul2_rn(x[g], x[g]);
+#pragma unroll
+    for (int g = 0; g < G; ++g) p[g] = __ffma2_rn(c2[N - 1], y[g], c2[N - 2]);
+#pragma unroll
+    for (int k = N - 3; k >= 0; --k)
+#pragma unroll
+        for (int g = 0; g < G; ++g) p[g] = __ffma2_rn(p[g], y[g], c2[k]);
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        x[g] = __ffma2_rn(x[g], p[g], add);
+        s[2 * g] = x[g].x;
+        s[2 * g + 1] = x[g].y;
     }
+}
+constexpr int kPolyPairs = 4;
+
+__device__ __forceinline__ float absmax64(const float (&v)[64]) {
+    float a[8];
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int i = 0; i < 32; ++i) s[c][i] = form_logit(F, scale_log2, s[c][i]);
+    for (int i = 0; i < 8; ++i) {
+        a[i] = fmax3(fabsf(v[8 * i]), fabsf(v[8 * i + 1]), fabsf(v[8 * i + 2]));
+        a[i] = fmax3(a[i], fabsf(v[8 * i + 3]), fabsf(v[8 * i + 4]));
+        a[i] = fmax3(a[i], fabsf(v[8 * i + 5]), fabsf(v[8 * i + 6]));
+        a[i] = fmaxf(a[i], fabsf(v[8 * i + 7]));
+    }
+    return fmax3(fmax3(a[0], a[1], a[2]), fmax3(a[3], a[4], a[5]), fmaxf(a[6], a[7]));
+}
+// How a warp takes tanh of logits of up to `most` in its rows: 0 and 1 by ScoreForm's polynomials, 2
+// exactly.  The exact form's two approximate operations a logit (2^x and a reciprocal) come on
+// top of the softmax's own, which fill the unit for them by themselves (4.2 clocks a warp's
+// instruction); the polynomials take 5 and 6 products for two logits (2.1 clocks each) on the
+// units for those.
+__device__ __forceinline__ int cap_tier(const ScoreForm &F, float most) {
+    if (!__any_sync(0xffffffffu, most > F.most4)) return 0;
+    return __any_sync(0xffffffffu, most > F.most5) ? 2 : 1;
 }
 
-template <typename E, int D, bool kMod>
+// kForm: what is changed of the scores, at compile time (with all of it behind branches the code is
+// twice as large, and the row warps wait for instructions: PROMPT).
+constexpr int kPlain = 0, kBounds = 1, kCapped = 2, kSloped = 4;   // kBounds: rows of their own
+
+template <typename E, int D, int kForm>
 __global__ void __launch_bounds__(kThreads, 1)
 many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
             const DevPaged C, const DevChunk T, const ManyArgs A) {
     using Ly = Layout<D>;
+    constexpr bool kMod = kForm != kPlain;
+    constexpr bool kCap = (kForm & kCapped) != 0, kSlope = (kForm & kSloped) != 0;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);   // uniform
     const int lane = threadIdx.x & 31;
@@ -258,7 +296,7 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             mbar_init(&i_full[i], 1);
             mbar_init(&i_empty[i], 3 + 8);    // two loaders, the issuer, eight row warps
         }
-        if constexpr (kMod)
+        if constexpr (kSlope)
             for (int i = 0; i < 4; ++i) mbar_init(&pos_full[i], 4);
         fence_barrier_init();
         prefetch_tensormap(&tm_k);
@@ -312,6 +350,8 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         const uint32_t s_base = tmem + lane_addr + 128 * L;
         const uint32_t o_base = tmem + lane_addr + kOCol + 128 * L;
         const float cs = A.M.scale_log2;
+        // what takes a logit, as it is left before the mask, to units of log2
+        const float zs = kCap ? 1.f : cs;
         int kc = 0, sc = 0, ic = 0;
         [[maybe_unused]] int pc = 0;                      // tiles whose positions were passed on
         // This thread's row of an item.
@@ -320,7 +360,7 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             int t, head, row;          // its query's cache row, query head, row of the unit
             long long tok, prow0;
             RowBounds see;             // kMod: the rows it sees
-            float slope, far;          // kMod: of its head in log2 units; its position, from `ref`
+            float slope, far;          // kMod: of its head, in 1 / zs; its position, from `ref`
             int ref;                   // kMod: the position that distances are counted from
         };
         auto row_of = [&](const Item *w) {
@@ -345,54 +385,59 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                 r.slope = 0.f;
                 r.far = 0.f;
                 r.ref = 0;
-                if (A.form.slopes) {
+                if constexpr (kSlope) {
                     const int t0 = w->n - w->count;
-                    r.ref = A.form.pos ? position_of(C, A.form, U, max(t0, 0)) : 0;
+                    r.ref = A.form.pos ? position_of(C, A.form, U, max(t0, 0)) : max(t0, 0);
                     if (r.valid) {
-                        r.slope = A.form.slopes[r.head] * kLog2e;
-                        r.far = A.form.pos ? (float)(position_of(C, A.form, U, r.t) - r.ref)
-                                           : (float)r.t;
+                        r.slope = A.form.slopes[r.head] * (kCap ? kLog2e : A.form.slope_s);
+                        r.far = (float)((A.form.pos ? position_of(C, A.form, U, r.t) : r.t) - r.ref);
                     }
                 }
             }
             r.any = x0 < min(ns, x1) || max(x0, w->lane[L].a) < min(x1, w->lane[L].b);
             return r;
         };
-        auto load_q = [&](const Row &r, uint4 (&q)[D / 8]) {
-            const uint4 *src = reinterpret_cast<const uint4 *>(
+        // Q rows of the item into shared memory for the products, once those of the item before
+        // are done.  A warp brings its 32 rows together, kQRows rows to a load: a load a row
+        // and thread would touch 32 lines for 512 bytes (8 items of 8 tiles a CTA: QSTORE).
+        constexpr int kQLanes = D / 8, kQRows = 32 / kQLanes, kQLoads = 32 / kQRows;
+        auto bring_q = [&](const Row &r, const Item *w) {
+            const uint4 *mine = reinterpret_cast<const uint4 *>(
                 static_cast<const typename E::T *>(A.io.q) + r.tok * A.io.q_stride +
                 (long long)r.head * D);
+            const int c = lane % kQLanes;
+            uint4 q[kQLoads];
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) q[c] = r.valid ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-        };
-        // Q into shared memory for the products, once those of the item before are done
-        auto store_q = [&](const Row &r, const Item *w, const uint4 (&q)[D / 8]) {
-            uint8_t *qs = smem + Ly::kQ + L * Ly::kOp + rr * 128;
+            for (int k = 0; k < kQLoads; ++k) {
+                const int from = k * kQRows + lane / kQLanes;
+                const uint4 *src = reinterpret_cast<const uint4 *>(__shfl_sync(
+                    0xffffffffu, reinterpret_cast<unsigned long long>(mine), from));
+                const bool valid = __shfl_sync(0xffffffffu, (int)r.valid, from);
+                q[k] = valid ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+            }
+            const bool pack = A.q_packed && w->x0 <= (w->lane[L].ns ? 0 : w->lane[L].a);
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c)
-                *reinterpret_cast<uint4 *>(qs + (c >> 3) * kBlockBytes +
-                                           (((c & 7) ^ (rr & 7)) << 4)) = q[c];
+            for (int k = 0; k < kQLoads; ++k) {
+                const int from = k * kQRows + lane / kQLanes, row = quarter * 32 + from;
+                *reinterpret_cast<uint4 *>(smem + Ly::kQ + L * Ly::kOp + row * 128 +
+                                           (c >> 3) * kBlockBytes + (((c & 7) ^ (row & 7)) << 4)) =
+                    q[k];
+                // the weights' pass takes the rows by TMA; one CTA of a cut item writes them
+                if (pack && row < w->lane[L].rows)
+                    reinterpret_cast<uint4 *>(
+                        static_cast<typename E::T *>(A.q_packed) +
+                        (r.prow0 + w->row0 + L * 128 + row) * D)[c] = q[k];
+            }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_full[L]);
-            if (A.q_packed && r.valid && w->x0 <= (w->lane[L].ns ? 0 : w->lane[L].a)) {
-                // the weights' pass takes the rows by TMA; one CTA of a cut item writes them
-                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<typename E::T *>(A.q_packed) +
-                                                       (r.prow0 + r.row) * D);
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c) dst[c] = q[c];
-            }
         };
         const Item *w = item(0, ok);
         ok = __all_sync(0xffffffffu, ok);
         Row cur{}, nxt{};
         if (ok && w) {
             cur = row_of(w);
-            if (cur.any) {
-                uint4 q[D / 8];
-                load_q(cur, q);
-                store_q(cur, w, q);
-            }
+            if (cur.any) bring_q(cur, w);
         }
         for (int i = 0; ok && w; ++i) {
             const Lane me = w->lane[L], other = w->lane[1 - L];
@@ -403,21 +448,20 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             // Positions of the keys, with slopes: a thread brings one key's of the tile to its
             // lane's four warps.  The page is looked up a tile ahead, the position after the
             // tile's exponentials, so that neither is waited for.
-            [[maybe_unused]] const bool far_keys = kMod && A.form.slopes && A.form.pos;
             [[maybe_unused]] const int32_t *tab = w->table;
             [[maybe_unused]] int page_x = -1, pos_x = -1, next_page = -1, next_pos = 0;
             [[maybe_unused]] const int seen_hi = w->t_hi;
             auto look_up = [&](int x) {
                 const int j = span.tile(x) * kManyTile + rr;
                 page_x = x;
-                next_page = x < x1 && j <= seen_hi ? tab[j >> C.ps_log2] : -1;
+                next_page = A.form.pos && x < x1 && j <= seen_hi ? tab[j >> C.ps_log2] : -1;
             };
             auto fetch = [&]() {
                 const int j = span.tile(page_x) * kManyTile + rr;
                 pos_x = page_x;
                 next_pos = next_page >= 0 && next_page < C.num_pages
                                ? A.form.pos[((long long)next_page << C.ps_log2) + (j & (C.ps - 1))]
-                               : 0;
+                               : j;
             };
             for (int x = x0; x < x1; ++x) {
                 const int key0 = span.tile(x) * kManyTile;
@@ -430,21 +474,20 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                     last <= me.t_lo && (kMod ? key0 >= me.lo_all || last < A.M.sinks
                                              : A.M.window == 0 || key0 > me.t_hi - A.M.window ||
                                                    last < A.M.sinks);
-                if constexpr (kMod)
-                    if (far_keys) {
-                        if (pos_x != x) {
-                            look_up(x);
-                            fetch();
-                        }
-                        ok = __all_sync(0xffffffffu, mbar_wait(&pos_empty[L], (uint32_t)(pc & 1) ^ 1u,
-                                                               s_abort, C.wait_ns));
-                        if (!ok) break;
-                        reinterpret_cast<float *>(smem + Ly::kPos)[L * kManyTile + rr] =
-                            (float)(next_pos - cur.ref);
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&pos_full[L]);
-                        look_up(x + 1);
+                if constexpr (kSlope) {
+                    if (pos_x != x) {
+                        look_up(x);
+                        fetch();
                     }
+                    ok = __all_sync(0xffffffffu, mbar_wait(&pos_empty[L], (uint32_t)(pc & 1) ^ 1u,
+                                                           s_abort, C.wait_ns));
+                    if (!ok) break;
+                    reinterpret_cast<float *>(smem + Ly::kPos)[L * kManyTile + rr] =
+                        (float)(next_pos - cur.ref);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&pos_full[L]);
+                    look_up(x + 1);
+                }
                 if (!full && (L == 0 || !other.sees(x)) &&
                     (last > w->t_hi || (last >= w->sinks && key0 < w->lo))) {
                     // V rows that no query sees may hold anything: 0 weight times NaN.  The
@@ -469,103 +512,256 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                                                        C.wait_ns));
                 if (!ok) break;
                 tc_fence_after();
-                float s[4][32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(s_base + 32 * c, s[c]);
-                tmem_ld_wait();
-#pragma unroll
-                for (int c = 0; c < 4; ++c) reg_fence(s[c]);
-                if constexpr (kMod) {
-                    change_logits(A.form, cs, s);
-                    if (far_keys) {
-                        ok = __all_sync(0xffffffffu, mbar_wait(&pos_full[L], (uint32_t)(pc & 1),
-                                                               s_abort, C.wait_ns));
-                        if (!ok) break;
-                        const float4 *ps =
-                            reinterpret_cast<const float4 *>(smem + Ly::kPos) + L * (kManyTile / 4);
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-#pragma unroll
-                            for (int i = 0; i < 32; i += 4) {
-                                const float4 p = ps[c * 8 + i / 4];
-                                s[c][i] -= cur.slope * fabsf(p.x - cur.far);
-                                s[c][i + 1] -= cur.slope * fabsf(p.y - cur.far);
-                                s[c][i + 2] -= cur.slope * fabsf(p.z - cur.far);
-                                s[c][i + 3] -= cur.slope * fabsf(p.w - cur.far);
-                            }
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&pos_empty[L]);
-                        ++pc;
-                    } else if (A.form.slopes) {
-                        const float d0 = (float)key0 - cur.far;
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                s[c][i] -= cur.slope * fabsf(d0 + (float)(32 * c + i));
-                    }
-                }
-                if (!full) {
+                // the keys of the tile that the row sees, 32 to a word
+                auto seen_keys = [&](int c) {
                     const int lim = (kMod ? cur.see.hi : t) - key0 + 1;
                     const int wlo = kMod ? cur.see.lo - key0
                                          : A.M.window > 0 ? lim - A.M.window : -1;
                     const int sk = A.M.sinks - key0;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const uint32_t see = low_bits(lim - 32 * c) &
-                                             (~low_bits(wlo - 32 * c) | low_bits(sk - 32 * c));
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (!(see >> i & 1u)) s[c][i] = -INFINITY;
-                    }
-                }
-                const float mt =
-                    fmaxf(fmaxf(max32(s[0]), max32(s[1])), fmaxf(max32(s[2]), max32(s[3]))) *
-                    (kMod ? 1.f : cs);
-                const bool up = mt > m + kLazyLog2;
-                if (__any_sync(0xffffffffu, up)) {
-                    const float f = up ? shrink(m, mt) : 1.f;
-                    if (begun) {
-                        // O_L holds the earlier tiles' P V, complete before this S was
+                    return low_bits(lim - 32 * c) &
+                           (~low_bits(wlo - 32 * c) | low_bits(sk - 32 * c));
+                };
+                // a row's new maximum (log2 units): sum and output follow where it is raised
+                auto raise = [&](float mt) {
+                    const bool up = mt > m + kLazyLog2;
+                    if (__any_sync(0xffffffffu, up)) {
+                        const float f = up ? shrink(m, mt) : 1.f;
+                        if (begun) {
+                            // O_L holds the earlier tiles' P V, complete before this S was
 #pragma unroll 1
-                        for (int c = 0; c < D / 16; ++c) {
-                            float o[16];
-                            tmem_ld16(o_base + 16 * c, o);
-                            tmem_ld_wait();
-                            reg_fence(o);
+                            for (int c = 0; c < D / 16; ++c) {
+                                float o[16];
+                                tmem_ld16(o_base + 16 * c, o);
+                                tmem_ld_wait();
+                                reg_fence(o);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] *= f;
-                            tmem_st16(o_base + 16 * c, o);
+                                for (int i = 0; i < 16; ++i) o[i] *= f;
+                                tmem_st16(o_base + 16 * c, o);
+                            }
                         }
+                        l *= f;
+                        if (up) m = mt;
                     }
-                    l *= f;
-                    if (up) m = mt;
-                }
-                begun = true;
-                // nothing seen so far: every p is 0
-                const float nm = m == -INFINITY ? 0.f : E::kShift - m;
-                const float2 cs2 = make_float2(cs, cs), nm2 = make_float2(nm, nm);
+                    begun = true;
+                };
                 float2 sum[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) sum[c] = make_float2(0.f, 0.f);
+                if constexpr (!kMod) {
+                    float s[4][32];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t pw[16];
+                    for (int c = 0; c < 4; ++c) tmem_ld32(s_base + 32 * c, s[c]);
+                    tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        const float2 z = make_float2(s[c][i], s[c][i + 1]);
-                        const float2 e = kMod ? __fadd2_rn(z, nm2) : __ffma2_rn(z, cs2, nm2);
-                        const float2 p = make_float2(ex2_approx(e.x), ex2_approx(e.y));
-                        sum[(i >> 1) & 3] = __fadd2_rn(sum[(i >> 1) & 3], p);
-                        pw[i >> 1] = E::pack(p.x, p.y);
+                    for (int c = 0; c < 4; ++c) reg_fence(s[c]);
+                    if (!full) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const uint32_t see = seen_keys(c);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (!(see >> i & 1u)) s[c][i] = -INFINITY;
+                        }
                     }
-                    tmem_st16u(s_base + 16 * c, pw);
-                    if (c == kPFirst / 32 - 1) {
+                    raise(fmaxf(fmaxf(max32(s[0]), max32(s[1])), fmaxf(max32(s[2]), max32(s[3]))) *
+                          cs);
+                    // nothing seen so far: every p is 0
+                    const float nm = m == -INFINITY ? 0.f : E::kShift - m;
+                    const float2 cs2 = make_float2(cs, cs), nm2 = make_float2(nm, nm);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t pw[16];
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const float2 e =
+                                __ffma2_rn(make_float2(s[c][i], s[c][i + 1]), cs2, nm2);
+                            const float2 p = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+                            sum[(i >> 1) & 3] = __fadd2_rn(sum[(i >> 1) & 3], p);
+                            pw[i >> 1] = E::pack(p.x, p.y);
+                        }
+                        tmem_st16u(s_base + 16 * c, pw);
+                        if (c == kPFirst / 32 - 1) {
+                            tmem_st_wait();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&p_full[L]);
+                        }
+                    }
+                } else {
+                    // Changed scores: the logits stay in tensor memory and come 64 keys at a time, twice,
+                    // in loops.  Unrolled over the 128 keys, what is added here made the row warps
+                    // wait for instructions (INSTR).
+                    struct Half {
+                        uint32_t see[2];
+                        bool none, mixed;          // of all the warp's rows: no key seen, not all
+                    };
+                    auto half_of = [&](int c) {
+                        Half h{{0xffffffffu, 0xffffffffu}, false, false};
+                        if (!full) {
+                            h.see[0] = seen_keys(c);
+                            h.see[1] = seen_keys(c + 1);
+                            h.none = __all_sync(0xffffffffu, (h.see[0] | h.see[1]) == 0u);
+                            h.mixed = !__all_sync(0xffffffffu, (h.see[0] & h.see[1]) == 0xffffffffu);
+                        }
+                        return h;
+                    };
+                    auto load = [&](int c, float (&v)[64]) {
+                        tmem_ld32(s_base + 32 * c, *reinterpret_cast<float(*)[32]>(&v[0]));
+                        tmem_ld32(s_base + 32 * c + 32, *reinterpret_cast<float(*)[32]>(&v[32]));
+                        tmem_ld_wait();
+                        reg_fence(v);
+                    };
+                    auto hide = [&](const Half &h, float (&v)[64], float value) {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            if (!(h.see[i >> 5] >> (i & 31) & 1u)) v[i] = value;
+                    };
+                    // the row's maximum, and with slopes the logits as they enter the softmax
+                    float top = -INFINITY, most = 0.f;
+                    if (kSlope) {
+                        ok = __all_sync(0xffffffffu, mbar_wait(&pos_full[L], (uint32_t)(pc & 1),
+                                                               s_abort, C.wait_ns));
+                        if (!ok) break;
+                    }
+#pragma unroll 1
+                    for (int c = 0; c < 4; c += 2) {
+                        const Half h = half_of(c);
+                        if (h.none) continue;
+                        float v[64];
+                        load(c, v);
+                        if (kCap) {
+                            // what lies behind keys that nobody sees has no say in how tanh is taken
+                            if (h.mixed) hide(h, v, 0.f);
+                            const float am = absmax64(v);
+                            most = fmaxf(most, am);
+                            if (kSlope) {
+                                if (cap_tier(A.form, am) < 2) {
+#pragma unroll
+                                    for (int i = 0; i < 64; i += 2 * kPolyPairs)
+                                        cap_poly<kPolyPairs>(A.form.co5, make_float2(0.f, 0.f), &v[i]);
+                                } else {
+#pragma unroll
+                                    for (int i = 0; i < 64; ++i) v[i] = cap_logit(A.form, v[i]);
+                                }
+                            }
+                        }
+                        if (kSlope) {
+                            const float2 sl = make_float2(cur.slope, cur.slope);
+                            const float2 far = make_float2(-cur.far, -cur.far);
+                            const float4 *ps = reinterpret_cast<const float4 *>(smem + Ly::kPos) +
+                                               L * (kManyTile / 4) + 8 * c;
+                            if (!A.form.two_way) {
+                                // no key behind the query is seen: every distance that counts is
+                                // far - p
+#pragma unroll
+                                for (int i = 0; i < 64; i += 4) {
+                                    const float4 p = ps[i / 4];
+                                    const float2 d0 = __fadd2_rn(make_float2(p.x, p.y), far);
+                                    const float2 d1 = __fadd2_rn(make_float2(p.z, p.w), far);
+                                    const float2 z0 = __ffma2_rn(sl, d0, make_float2(v[i], v[i + 1]));
+                                    const float2 z1 =
+                                        __ffma2_rn(sl, d1, make_float2(v[i + 2], v[i + 3]));
+                                    v[i] = z0.x;
+                                    v[i + 1] = z0.y;
+                                    v[i + 2] = z1.x;
+                                    v[i + 3] = z1.y;
+                                }
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 64; i += 4) {
+                                    const float4 p = ps[i / 4];
+                                    v[i] -= cur.slope * fabsf(p.x - cur.far);
+                                    v[i + 1] -= cur.slope * fabsf(p.y - cur.far);
+                                    v[i + 2] -= cur.slope * fabsf(p.z - cur.far);
+                                    v[i + 3] -= cur.slope * fabsf(p.w - cur.far);
+                                }
+                            }
+                        }
+                        if (h.mixed) hide(h, v, -INFINITY);
+                        top = fmax3(top, max32(*reinterpret_cast<float(*)[32]>(&v[0])),
+                                    max32(*reinterpret_cast<float(*)[32]>(&v[32])));
+                        if (kSlope)
+#pragma unroll
+                            for (int i = 0; i < 64; i += 16)
+                                tmem_st16(s_base + 32 * c + i,
+                                          *reinterpret_cast<float(*)[16]>(&v[i]));
+                    }
+                    int tier = 0;
+                    if (kSlope) {
                         tmem_st_wait();
-                        tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&p_full[L]);
+                        if (lane == 0) mbar_arrive(&pos_empty[L]);
+                        ++pc;
+                    } else if (kCap) {
+                        // without slopes tanh goes with the exponentials: it rises
+                        tier = cap_tier(A.form, most);
+                        float one[2] = {top, top};
+                        if (tier == 0) cap_poly<1>(A.form.co4, make_float2(0.f, 0.f), one);
+                        else if (tier == 1) cap_poly<1>(A.form.co5, make_float2(0.f, 0.f), one);
+                        else one[0] = cap_logit(A.form, top);
+                        if (top != -INFINITY) top = one[0];
                     }
+                    raise(top * zs);
+                    const float nm = m == -INFINITY ? 0.f : E::kShift - m;
+                    const float2 zs2 = make_float2(zs, zs), nm2 = make_float2(nm, nm);
+                    // how: 0 as they are (times zs), 1 and 2 by the polynomials, 3 exactly
+                    auto weights = [&](auto how) {
+#pragma unroll 1
+                        for (int c = 0; c < 4; c += 2) {
+                            const Half h = half_of(c);
+                            uint32_t pw[32];
+                            if (h.none) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) pw[i] = 0u;
+                            } else {
+                                float v[64];
+                                load(c, v);
+                                // eight logits at a time, so that products and exponentials, which
+                                // run on different units, alternate
+                                auto eight = [&](int i, auto mixed) {
+                                    if (how.value == 1) cap_poly<kPolyPairs>(A.form.co4, nm2, &v[i]);
+                                    if (how.value == 2) cap_poly<kPolyPairs>(A.form.co5, nm2, &v[i]);
+#pragma unroll
+                                    for (int j = i; j < i + 2 * kPolyPairs; j += 2) {
+                                        float2 e = make_float2(v[j], v[j + 1]);
+                                        if (how.value == 0) e = __ffma2_rn(e, zs2, nm2);
+                                        if (how.value == 3)
+                                            e = __fadd2_rn(make_float2(cap_logit(A.form, e.x),
+                                                                       cap_logit(A.form, e.y)), nm2);
+                                        float2 p = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+                                        if (mixed.value) {
+                                            if (!(h.see[j >> 5] >> (j & 31) & 1u)) p.x = 0.f;
+                                            if (!(h.see[j >> 5] >> (j & 31) & 2u)) p.y = 0.f;
+                                        }
+                                        sum[(j >> 1) & 3] = __fadd2_rn(sum[(j >> 1) & 3], p);
+                                        pw[j >> 1] = E::pack(p.x, p.y);
+                                    }
+                                };
+                                if (!kSlope && h.mixed) {
+#pragma unroll
+                                    for (int i = 0; i < 64; i += 2 * kPolyPairs)
+                                        eight(i, std::true_type{});
+                                } else {
+#pragma unroll
+                                    for (int i = 0; i < 64; i += 2 * kPolyPairs)
+                                        eight(i, std::false_type{});
+                                }
+                            }
+                            tmem_st32u(s_base + 16 * c, pw);
+                            if (c == 0) {
+                                static_assert(kPFirst == 64, "what the first round writes");
+                                tmem_st_wait();
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(&p_full[L]);
+                            }
+                        }
+                    };
+                    using std::integral_constant;
+                    if (!kCap || kSlope) weights(integral_constant<int, 0>{});
+                    else if (tier == 0) weights(integral_constant<int, 1>{});
+                    else if (tier == 1) weights(integral_constant<int, 2>{});
+                    else weights(integral_constant<int, 3>{});
                 }
                 const float2 a = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
                 l += a.x + a.y;
@@ -574,8 +770,7 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_rest[L]);
                 ++sc;
-                if constexpr (kMod)
-                    if (far_keys) fetch();
+                if constexpr (kSlope) fetch();
             }
             if (!ok) break;
             // ---- the item's end: finished rows, or this run's part of them
@@ -593,11 +788,7 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             nxt.any = false;
             if (w) {
                 nxt = row_of(w);
-                if (nxt.any) {
-                    uint4 q[D / 8];
-                    load_q(nxt, q);
-                    store_q(nxt, w, q);
-                }
+                if (nxt.any) bring_q(nxt, w);
             }
             if (begun) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&o_final[L], (uint32_t)(ic & 1), s_abort,
@@ -883,35 +1074,35 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     if (threadIdx.x < A.phases) A.cut[threadIdx.x * kManyCtas + blockIdx.x] = s_cut[threadIdx.x];
 }
 
-template <typename E, int D, bool kMod>
+template <typename E, int D, int kForm>
 cudaError_t many(const DevPaged &C, const DevChunk &T, const ManyArgs &A, const AttendWs &ws, cudaStream_t s) {
     using Ly = Layout<D>;
     CUtensorMap mk, mv;
     if (!make_tile_map(&mk, C.k, C.num_pages * C.ps, D, C.ps) ||
         !make_tile_map(&mv, C.v, C.num_pages * C.ps, D, C.ps))
         return cudaErrorInvalidValue;
-    constexpr int kSmem = kMod ? Ly::kTotalMod : Ly::kTotal;
-    cudaError_t e = cudaFuncSetAttribute(many_kernel<E, D, kMod>,
+    constexpr int kSmem = kForm & kSloped ? Ly::kTotalMod : Ly::kTotal;
+    cudaError_t e = cudaFuncSetAttribute(many_kernel<E, D, kForm>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e == cudaSuccess)
-        e = launch_dependent(many_kernel<E, D, kMod>, dim3(kManyCtas), kThreads, kSmem, s, mk, mv, C,
+        e = launch_dependent(many_kernel<E, D, kForm>, dim3(kManyCtas), kThreads, kSmem, s, mk, mv, C,
                              T, A);
     if (e == cudaSuccess)
         e = launch_many_merge(C, T, A.layer, A.io, A.lse2, ws, A.phases, s);
     return e;
 }
 
-template <bool kMod>
+template <int kForm>
 cudaError_t attend_many(const DevPaged &C, const DevChunk &T, int layer, const AttendMask &M,
                         const ScoreForm &form, const AttendIo &io, const AttendWs &ws,
                         cudaStream_t s) {
     const ManyArgs A{layer, M, io, ws.cut, ws.part_ml, ws.part_o, ws.lse2, ws.q_packed,
                      many_phases(C), form};
     if (C.dtype == KV_FP16)
-        return C.d == 64 ? many<Fp16, 64, kMod>(C, T, A, ws, s)
-                         : many<Fp16, 128, kMod>(C, T, A, ws, s);
-    return C.d == 64 ? many<Bf16, 64, kMod>(C, T, A, ws, s)
-                     : many<Bf16, 128, kMod>(C, T, A, ws, s);
+        return C.d == 64 ? many<Fp16, 64, kForm>(C, T, A, ws, s)
+                         : many<Fp16, 128, kForm>(C, T, A, ws, s);
+    return C.d == 64 ? many<Bf16, 64, kForm>(C, T, A, ws, s)
+                     : many<Bf16, 128, kForm>(C, T, A, ws, s);
 }
 
 }  // namespace

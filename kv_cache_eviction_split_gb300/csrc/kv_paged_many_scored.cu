@@ -134,7 +134,9 @@ cudaError_t launch_row_bounds(const DevPaged &C, const DevChunk &T, int layer, c
 cudaError_t launch_attend_many_scored(const DevPaged &C, const DevChunk &T, int layer,
                                       const AttendMask &M, const ScoreForm &form, const AttendIo &io,
                                       const AttendWs &ws, cudaStream_t s) {
-    return attend_many<true>(C, T, layer, M, form, io, ws, s);
+    if (form.cap2 != 0.f) return launch_attend_many_capped(C, T, layer, M, form, io, ws, s);
+    if (form.slopes) return launch_attend_many_sloped(C, T, layer, M, form, io, ws, s);
+    return attend_many<kBounds>(C, T, layer, M, form, io, ws, s);
 }
 
 }  // namespace kvevict

@@ -24,17 +24,43 @@ struct BlockBounds {
 constexpr int kNoLo = 0x3fffffff;          // lo of a query that sees nothing
 
 struct ScoreForm {
-    float cap2, cap_u;         // cap log2(e), 0: none; 2 c log2(e) / cap, the exponent of e^2x
+    float cap2;                // cap log2(e), 0: none
+    float cap_u;               // 2 c log2(e) / cap: s to the exponent of e^2x, x = c s / cap
+    float slope_s;             // 1 / c: a slope in units of s
+    int two_way;               // whether a query may see keys behind it
     const float *slopes;       // [Hq], or null
     const int32_t *pos;        // positions of pool rows, or null: a row's number; null without slopes
     const RowBounds *rows;     // [tokens][H], or null: up to the query's own row, and the window
     const BlockBounds *blocks; // [R * H][unit_blocks], with rows
     int unit_blocks;
+    // cap2 tanh(x) = s (c0 + c1 s^2 + ...) with x = cap_x s, for two logits at a time, where |s| is at
+    // most most4 (|x| <= 1/2) and most5 (|x| <= 3/4): fitted in x with the largest error of tanh
+    // least, 1.6e-7 and 2.5e-7 in fp32 (the exact form's 1 has steps of 1.2e-7).  Below 0: never
+    // (powers of cap_x that fp32 has not).
+    float most4, most5;
+    float2 co4[4], co5[5];
+
+    void set_cap(float cap, float scale) {
+        constexpr double k4[4] = {0.9999976754188538, -0.33320656418800354, 0.1314515471458435,
+                                  -0.043372705578804016};
+        constexpr double k5[5] = {0.9999972581863403, -0.33323076367378235, 0.13226093351840973,
+                                  -0.04928047955036163, 0.012318850494921207};
+        const double x = (double)scale / cap, most = (double)cap * kLog2e;
+        cap2 = (float)most;
+        cap_u = (float)(2.0 * x * kLog2e);
+        const bool fits = x >= 1.0 / 4096 && x <= 4096;
+        most4 = fits ? (float)(0.5 / x) : -1.0f;
+        most5 = fits ? (float)(0.75 / x) : -1.0f;
+        double power = x * most;
+        for (int i = 0; i < 5; ++i, power *= x * x) {
+            if (i < 4) co4[i] = make_float2((float)(k4[i] * power), (float)(k4[i] * power));
+            co5[i] = make_float2((float)(k5[i] * power), (float)(k5[i] * power));
+        }
+    }
 };
 
-// z without the distance, in units of log2.
-__device__ __forceinline__ float form_logit(const ScoreForm &F, float scale_log2, float s) {
-    if (F.cap2 == 0.f) return s * scale_log2;
+// Capped, in units of log2.
+__device__ __forceinline__ float cap_logit(const ScoreForm &F, float s) {
     const float e = sm100::ex2_approx(fminf(s * F.cap_u, 64.f));
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
@@ -90,6 +116,12 @@ cudaError_t launch_attend_few_scored(const DevPaged &C, const DevChunk &T, int l
                                      bool add_mass, long long seen, long long items, int max_rows,
                                      int blocks, const AttendWs &ws, cudaStream_t s);
 cudaError_t launch_attend_many_scored(const DevPaged &C, const DevChunk &T, int layer,
+                                      const AttendMask &M, const ScoreForm &form, const AttendIo &io,
+                                      const AttendWs &ws, cudaStream_t s);
+cudaError_t launch_attend_many_capped(const DevPaged &C, const DevChunk &T, int layer,
+                                      const AttendMask &M, const ScoreForm &form, const AttendIo &io,
+                                      const AttendWs &ws, cudaStream_t s);
+cudaError_t launch_attend_many_sloped(const DevPaged &C, const DevChunk &T, int layer,
                                       const AttendMask &M, const ScoreForm &form, const AttendIo &io,
                                       const AttendWs &ws, cudaStream_t s);
 // kv_paged_attention with changed scores (form.rows and form.blocks are filled in).
