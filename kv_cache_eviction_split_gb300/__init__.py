@@ -759,16 +759,10 @@ class PagedCache:
             raise ValueError("lens: int32 [requests][layers][kv_heads]")
         if mass is not None and (mass.dtype != torch.float32 or mass.shape != k_pages.shape[:2]):
             raise ValueError("mass: float32 [num_pages][page_size]")
-        if positions is not None and (positions.dtype != torch.int32 or
-                                      positions.shape != k_pages.shape[:2]):
-            raise ValueError("positions: int32 [num_pages][page_size]")
-        if refs is not None and (refs.dtype != torch.int32 or refs.shape != k_pages.shape[:1]):
-            raise ValueError("refs: int32 [num_pages]")
-        for t in (k_pages, v_pages, page_table, lens, mass, positions, refs):
+        for t in (k_pages, v_pages, page_table, lens, mass):
             if t is not None and (not t.is_contiguous() or t.device != k_pages.device):
                 raise ValueError("the cache's tensors are contiguous and on one device")
         self.k_pages, self.v_pages, self.mass = k_pages, v_pages, mass
-        self.positions, self.refs = positions, refs
         self.page_table, self.lens = page_table, lens
         self.num_requests, self.num_layers, self.num_kv_heads, self.max_pages = page_table.shape
         self.num_q_heads = int(num_q_heads)
@@ -778,6 +772,8 @@ class PagedCache:
         self.status = torch.zeros(64, dtype=torch.int32, device=self.device)
         self._index = k_pages.get_device()          # -1 on the CPU
         self._scale = 1.0 / math.sqrt(self.head_dim)
+        self._f32 = torch.float32
+        self.positions, self.refs = positions, refs
         self._c = _KvPaged(self.num_requests, self.num_layers, self.num_kv_heads, self.num_q_heads,
                            self.head_dim, self.page_size, self.max_pages,
                            KV_FP16 if self.dtype == torch.float16 else KV_BF16, self.num_pages,
@@ -805,6 +801,31 @@ class PagedCache:
                    torch.zeros(pool[:2], dtype=torch.float32, device=device) if mass else None,
                    torch.zeros(pool[:2], dtype=torch.int32, device=device) if positions else None,
                    torch.zeros(pages, dtype=torch.int32, device=device) if refs else None)
+
+    def _beside(self, t, name: str, shape) -> Optional[int]:
+        """The address of an int32 tensor that is kept beside the pages, checked."""
+        if t is not None and (t.dtype != self.lens.dtype or t.shape != shape or
+                              not t.is_contiguous() or t.device != self.device):
+            raise ValueError("%s: int32 %s on the cache's device, contiguous" % (name, list(shape)))
+        return _ptr(t)
+
+    @property
+    def positions(self):
+        return self._positions_tensor
+
+    @positions.setter
+    def positions(self, t):
+        self._positions = self._beside(t, "positions", self.k_pages.shape[:2])
+        self._positions_tensor = t
+
+    @property
+    def refs(self):
+        return self._refs_tensor
+
+    @refs.setter
+    def refs(self, t):
+        self._refs = self._beside(t, "refs", self.k_pages.shape[:1])
+        self._refs_tensor = t
 
     @property
     def c(self):
@@ -975,27 +996,27 @@ def kv_paged_attention_scored(cache: PagedCache, chunk: Chunk, layer: int, q, ou
     slopes[head] (float32 [q_heads]) times the distance of positions.  first, last (int32
     [tokens]): the first and last positions that a token sees (default: the start, its own row).
     Positions are cache.positions, or the rows' numbers."""
-    import torch
     heads = cache.num_q_heads
     _check_chunk(cache, chunk)
     if (layer | window | num_sinks) >> 31:       # one is negative, or past 32 bits
         _check_int32("kv_paged_attention_scored", layer, window, num_sinks)
     qs = _token_stride(cache, chunk, q, heads, "q")
     os_ = _token_stride(cache, chunk, out, heads, "out")
-    if lse is not None and (lse.dtype is not torch.float32 or not lse.is_contiguous() or
+    f32, i32 = cache._f32, chunk.counts.dtype
+    if lse is not None and (lse.dtype is not f32 or not lse.is_contiguous() or
                             lse.shape != (chunk.tokens, heads)):
         raise ValueError("lse: float32 [%d][%d]" % (chunk.tokens, heads))
-    if slopes is not None and (slopes.dtype is not torch.float32 or not slopes.is_contiguous() or
+    if slopes is not None and (slopes.dtype is not f32 or not slopes.is_contiguous() or
                                slopes.shape != (heads,)):
         raise ValueError("slopes: float32 [%d]" % heads)
     for t in (first, last):
-        if t is not None and (t.dtype is not torch.int32 or not t.is_contiguous() or
+        if t is not None and (t.dtype is not i32 or not t.is_contiguous() or
                               t.shape != (chunk.tokens,)):
             raise ValueError("first, last: int32 [%d]" % chunk.tokens)
     if not workspace.is_contiguous():
         raise ValueError("workspace: contiguous")
     _on_current_device(cache, q, out, lse, workspace, slopes, first, last)
-    form = _KvScoring(softcap, window, num_sinks, _ptr(slopes), _ptr(cache.positions), _ptr(first),
+    form = _KvScoring(softcap, window, num_sinks, _ptr(slopes), cache._positions, _ptr(first),
                       _ptr(last))
     code = (_lib or load()).kv_paged_attention_scored(
         cache._ref, chunk._ref, layer, ctypes.byref(form),
@@ -1129,17 +1150,25 @@ def kv_paged_append_rotary(cache: PagedCache, chunk: Chunk, layer: int, rotary: 
         _check_int32("kv_paged_append_rotary", layer)
     ks = _token_stride(cache, chunk, k_new, cache.num_kv_heads, "k_new")
     vs = _token_stride(cache, chunk, v_new, cache.num_kv_heads, "v_new")
-    qs = os_ = 0
-    if q is not None:
+    # (the chunk's counts are int32)
+    if positions.dtype is not chunk.counts.dtype or positions.shape != (chunk.tokens,) or \
+            not positions.is_contiguous():
+        raise ValueError("positions: int32 [%d]" % chunk.tokens)
+    if rotary._index != cache._index:
+        raise ValueError("the frequencies are on %s, the cache on %s" % (rotary.inv_freq.device,
+                                                                         cache.device))
+    if q is None:
+        qp = op = None
+        qs = os_ = 0
+        _on_current_device(cache, k_new, v_new, positions)
+    else:
         qs = _token_stride(cache, chunk, q, cache.num_q_heads, "q")
         os_ = _token_stride(cache, chunk, q_out, cache.num_q_heads, "q_out")
-    _check_positions(positions, chunk.tokens)
-    _on_current_device(cache, k_new, v_new, q, None if q is None else q_out, positions,
-                       rotary.inv_freq)
+        _on_current_device(cache, k_new, v_new, positions, q, q_out)
+        qp, op = q.data_ptr(), q_out.data_ptr()
     code = (_lib or load()).kv_paged_append_rotary(
-        cache._ref, chunk._ref, layer, rotary._ref, positions.data_ptr(), _ptr(cache.positions),
-        _ptr(q), qs, None if q is None else q_out.data_ptr(), os_, k_new.data_ptr(), ks,
-        v_new.data_ptr(), vs, _stream(stream))
+        cache._ref, chunk._ref, layer, rotary._ref, positions.data_ptr(), cache._positions, qp, qs, op,
+        os_, k_new.data_ptr(), ks, v_new.data_ptr(), vs, _stream(stream))
     if code:
         raise KvError(code, "kv_paged_append_rotary")
 
@@ -1206,8 +1235,8 @@ def kv_paged_reserve(cache: PagedCache, chunk: Chunk, workspace, stream=None):
         raise ValueError("workspace: contiguous")
     _on_current_device(cache, workspace)
     code = (_lib or load()).kv_paged_reserve(
-        cache._ref, chunk._ref, cache.refs.data_ptr(), _ptr(cache.positions), workspace.data_ptr(),
-        workspace.nbytes, _stream(stream))
+        cache._ref, chunk._ref, cache._refs, cache._positions, workspace.data_ptr(), workspace.nbytes,
+        _stream(stream))
     if code:
         raise KvError(code, "kv_paged_reserve")
 
@@ -1215,14 +1244,12 @@ def kv_paged_reserve(cache: PagedCache, chunk: Chunk, workspace, stream=None):
 def kv_paged_fork(cache: PagedCache, parents, stream=None):
     """Every request r goes on from request parents[r] (int32 [requests]), whose pages it shares;
     r itself: no change; -1: emptied."""
-    import torch
     _check_refs(cache)
-    if parents.dtype is not torch.int32 or parents.shape != (cache.num_requests,) or \
+    if parents.dtype is not cache.lens.dtype or parents.shape != (cache.num_requests,) or \
             not parents.is_contiguous():
         raise ValueError("parents: int32 [%d]" % cache.num_requests)
     _on_current_device(cache, parents)
-    code = (_lib or load()).kv_paged_fork(cache._ref, cache.refs.data_ptr(), parents.data_ptr(),
-                                          _stream(stream))
+    code = (_lib or load()).kv_paged_fork(cache._ref, cache._refs, parents.data_ptr(), _stream(stream))
     if code:
         raise KvError(code, "kv_paged_fork")
 
@@ -1236,15 +1263,14 @@ def kv_paged_compact_workspace_size(cache: PagedCache) -> int:
 
 def kv_paged_compact(cache: PagedCache, workspace, live=None, stream=None):
     """Pages in use moved to the front of the pools; live: int32 [1], receives their number."""
-    import torch
     _check_refs(cache)
     if not workspace.is_contiguous():
         raise ValueError("workspace: contiguous")
-    if live is not None and (live.dtype is not torch.int32 or live.numel() != 1):
+    if live is not None and (live.dtype is not cache.lens.dtype or live.numel() != 1):
         raise ValueError("live: int32 [1]")
     _on_current_device(cache, workspace, live)
     code = (_lib or load()).kv_paged_compact(
-        cache._ref, cache.refs.data_ptr(), _ptr(cache.positions), _ptr(live), workspace.data_ptr(),
-        workspace.nbytes, _stream(stream))
+        cache._ref, cache._refs, cache._positions, _ptr(live), workspace.data_ptr(), workspace.nbytes,
+        _stream(stream))
     if code:
         raise KvError(code, "kv_paged_compact")

@@ -9,6 +9,8 @@
 // and chains of dependent loads, bound by latency: one cluster of 8 blocks, whose counts meet in
 // distributed shared memory, does it in one launch.  The pages themselves are then copied by all
 // SMs, bound by HBM.
+#include <algorithm>
+
 #include <cooperative_groups.h>
 
 #include "kv_compact.cuh"
@@ -29,18 +31,16 @@ __device__ __forceinline__ int32_t *table_of(const DevPaged &C, long long u) {
     return const_cast<int32_t *>(C.table) + u * C.max_pages;
 }
 
-// Sums of counts over the cluster's threads, in rank and thread order: each thread gets what lies
-// before its own, and the total.  Ends with the cluster in step.
+// Sums of counts over the threads of kCtas blocks (a cluster), in rank and thread order: each thread
+// gets what lies before its own, and the total.  The blocks leave together (leave_cluster).
 template <int N>
 struct ClusterScan {
     int before[N], total[N];
 };
-template <int N>
+template <int kCtas, int N>
 __device__ __forceinline__ ClusterScan<N> cluster_scan(const int (&mine)[N]) {
     __shared__ int s_warp[N][kPlanThreads / 32], s_block[N];
-    cg::cluster_group cl = cg::this_cluster();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int rank = (int)cl.block_rank();
     ClusterScan<N> r;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
@@ -65,28 +65,44 @@ __device__ __forceinline__ ClusterScan<N> cluster_scan(const int (&mine)[N]) {
         s_warp[warp][lane] = x - t;
         if (lane == 31) s_block[warp] = x;
     }
-    cl.sync();
+    if constexpr (kCtas == 1) {
+        __syncthreads();
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-        int base = 0, all = 0;
-#pragma unroll
-        for (int b = 0; b < kPlanCtas; ++b) {
-            const int x = cl.map_shared_rank(s_block, b)[k];
-            if (b < rank) base += x;
-            all += x;
+        for (int k = 0; k < N; ++k) {
+            r.before[k] += s_warp[k][warp];
+            r.total[k] = s_block[k];
         }
-        r.before[k] += base + s_warp[k][warp];
-        r.total[k] = all;
+    } else {
+        cg::cluster_group cl = cg::this_cluster();
+        const int rank = (int)cl.block_rank();
+        cl.sync();
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            int base = 0, all = 0;
+#pragma unroll
+            for (int b = 0; b < kCtas; ++b) {
+                const int x = cl.map_shared_rank(s_block, b)[k];
+                if (b < rank) base += x;
+                all += x;
+            }
+            r.before[k] += base + s_warp[k][warp];
+            r.total[k] = all;
+        }
     }
-    cl.sync();                                   // the sums are read
     return r;
+}
+// No block leaves while another reads its sums.
+template <int kCtas>
+__device__ __forceinline__ void leave_cluster() {
+    if constexpr (kCtas > 1) cg::this_cluster().sync();
 }
 
 // A warp's share of the pages: consecutive, a multiple of 32 (its first page may lie past the end).
+template <int kCtas>
 struct WarpPages {
     long long begin, end;
     __device__ __forceinline__ explicit WarpPages(long long pages) {
-        constexpr int kWarps = kPlanCtas * kPlanThreads / 32;
+        constexpr int kWarps = kCtas * kPlanThreads / 32;
         const long long per = ((pages + kWarps - 1) / kWarps + 31) / 32 * 32;
         const int w = (int)((blockIdx.x * kPlanThreads + threadIdx.x) >> 5);
         begin = min(pages, w * per);
@@ -94,25 +110,25 @@ struct WarpPages {
     }
 };
 
-constexpr int kScanDepth = 4;         // loads of 32 pages in flight a warp
+constexpr int kScanDepth = 8;         // loads of 32 pages in flight a warp
 
 // Walks the warp's pages in order, 32 at a time: f(page, used, mask of the used among the 32, lanes
 // that hold a page).
-template <typename F>
-__device__ __forceinline__ void scan_pages(const WarpPages &W, const int32_t *refs, F f) {
+template <typename W, typename F>
+__device__ __forceinline__ void scan_pages(const W &w, const int32_t *refs, F f) {
     const int lane = threadIdx.x & 31;
-    for (long long p0 = W.begin; p0 < W.end; p0 += 32 * kScanDepth) {
+    for (long long p0 = w.begin; p0 < w.end; p0 += 32 * kScanDepth) {
         int x[kScanDepth];
 #pragma unroll
         for (int i = 0; i < kScanDepth; ++i) {
             const long long p = p0 + 32 * i + lane;
-            x[i] = p < W.end ? refs[p] : 0;
+            x[i] = p < w.end ? refs[p] : 0;
         }
 #pragma unroll
         for (int i = 0; i < kScanDepth; ++i) {
             const long long p = p0 + 32 * i + lane;
-            if (p0 + 32 * i >= W.end) break;
-            const unsigned there = __ballot_sync(0xffffffffu, p < W.end);
+            if (p0 + 32 * i >= w.end) break;
+            const unsigned there = __ballot_sync(0xffffffffu, p < w.end);
             const unsigned used = __ballot_sync(0xffffffffu, x[i] > 0);
             f(p, x[i] > 0, used, there);
         }
@@ -120,121 +136,8 @@ __device__ __forceinline__ void scan_pages(const WarpPages &W, const int32_t *re
 }
 
 // ---------------------------------------------------------------------------
-// Pages for a step's tokens.  A unit of n rows that gets t more needs the pages of rows n .. n + t - 1
-// that it has none for, and one more if its last page is part full and shared: that page is copied
-// and the copy takes its place.  The k-th page needed, units in order, tail first, is the k-th
-// free page.  Nothing changes unless all fit.
-// ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(kPlanThreads, 1)
-reserve_plan_kernel(const DevPaged C, const DevChunk T, int32_t *refs, const PagesWs ws) {
-    constexpr int kAll = kPlanCtas * kPlanThreads;
-    constexpr int kAlone = 4;                    // pages that a unit's thread enters by itself
-    cg::cluster_group cl = cg::this_cluster();
-    const int lane = threadIdx.x & 31;
-    pdl_wait();
-    pdl_trigger();
-    if (blockIdx.x == 0 && threadIdx.x == 0) ws.plan->count = 0;
-    const int units = (int)C.units, chunk = (units + kAll - 1) / kAll;   // units: at most 2^28
-    const int gt = (int)(blockIdx.x * kPlanThreads + threadIdx.x);
-    const int u0 = (int)min((long long)units, (long long)gt * chunk);
-    const int u1 = min(units, u0 + chunk);
-    const int per = C.L * C.H;
-    auto tokens_of = [&](int u) {
-        const int r = u / per;
-        return (int)(T.off[r + 1] - T.off[r]);
-    };
-    // pages needed, free pages, units that cannot be, units longer than their table; the first is
-    // at most num_pages + 2 units (the host has checked the tokens)
-    int mine[4] = {0, 0, 0, 0};
-    for (int u = u0; u < u1; ++u) {
-        const int t = tokens_of(u);
-        int n, need = 0;
-        if (!unit_len(C, u, n)) {
-            mine[2] += 1;
-        } else if (t > C.cap - n) {
-            mine[3] += 1;
-        } else if (t > 0) {
-            const int held = pages_of(C, n);
-            need = 2 * (pages_of(C, n + t) - held);
-            if (n & (C.ps - 1)) {
-                const int page = table_of(C, u)[held - 1];
-                if (!page_ok(C, page)) mine[2] += 1;
-                else if (refs[page] > 1) need += 3;
-            }
-        }
-        ws.need[u] = need;
-        mine[0] += need >> 1;
-    }
-    const WarpPages W(C.num_pages);
-    int free_pages = 0;
-    scan_pages(W, refs, [&](long long, bool, unsigned used, unsigned there) {
-        free_pages += __popc(there & ~used);
-    });
-    if (lane == 0) mine[1] = free_pages;
-    const auto s = cluster_scan(mine);
-    if (s.total[2] > 0 || s.total[3] > 0 || s.total[0] > s.total[1]) {
-        if (gt == 0)
-            post_status(C.status, s.total[2] > 0 ? KV_ERR_INVALID_ARG : KV_ERR_BUDGET);
-        return;                                  // the whole cluster
-    }
-    // the free pages that are given out, in order
-    int rank = __shfl_sync(0xffffffffu, s.before[1], 0);
-    scan_pages(W, refs, [&](long long p, bool is_used, unsigned used, unsigned there) {
-        const unsigned open = there & ~used;
-        const int k = rank + __popc(open & low_bits(lane));
-        if (!is_used && (there >> lane & 1) && k < s.total[0]) ws.list[k] = (int)p;
-        rank += __popc(open);
-    });
-    __threadfence();
-    cl.sync();
-    int k = s.before[0];
-    // units in step over the warp, so that it can help with long runs
-    for (int i = 0; i < chunk; ++i) {
-        const int u = u0 + i;
-        const bool on = u < u1;
-        int want = 0, col = 0;                   // plain pages and the first one's column
-        int32_t *tab = on ? table_of(C, u) : nullptr;
-        if (on) {
-            const int n = C.lens[u], t = tokens_of(u), need = ws.need[u];
-            const int held = pages_of(C, n);
-            if (need & 1) {
-                const int from = tab[held - 1], to = ws.list[k++];
-                tab[held - 1] = to;
-                refs[to] = 1;
-                atomicSub(refs + from, 1);
-                const int at = atomicAdd(&ws.plan->count, 1);
-                ws.src[at] = from;
-                ws.dst[at] = to;
-            }
-            want = (need >> 1) - (need & 1);
-            col = held;
-            C.lens[u] = n + t;
-            if (want <= kAlone)
-                for (int j = 0; j < want; ++j) {
-                    const int page = ws.list[k + j];
-                    tab[col + j] = page;
-                    refs[page] = 1;
-                }
-        }
-        for (unsigned rest = __ballot_sync(0xffffffffu, want > kAlone); rest; rest &= rest - 1) {
-            const int who = __ffs(rest) - 1;
-            const int w = __shfl_sync(0xffffffffu, want, who), c0 = __shfl_sync(0xffffffffu, col, who);
-            const int k0 = __shfl_sync(0xffffffffu, k, who);
-            int32_t *to = reinterpret_cast<int32_t *>(
-                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(tab), who));
-            for (int j = lane; j < w; j += 32) {
-                const int page = ws.list[k0 + j];
-                to[c0 + j] = page;
-                refs[page] = 1;
-            }
-        }
-        k += want;
-    }
-}
-
-// ---------------------------------------------------------------------------
 // Pages copied: K, V, weights and positions of every row.  A piece is 2 KB of a page's K and the
-// same of its V, all in flight in a warp.  Compaction: the tables follow first.
+// same of its V, all in flight in a warp.
 // ---------------------------------------------------------------------------
 constexpr int kPieceVecs = 128;       // 16-byte vectors of K (and of V) in a piece
 
@@ -266,62 +169,200 @@ __device__ __forceinline__ void copy_piece(const DevPaged &C, int32_t *row_pos, 
     }
 }
 
+// ---------------------------------------------------------------------------
+// Pages for a step's tokens.  A unit of n rows that gets t more needs the pages of rows n .. n + t - 1
+// that it has none for, and one more if its last page is part full and shared: that page is copied
+// and the copy takes its place.  The k-th page needed, units in order, tail first, is the k-th
+// free page.  Nothing changes unless all fit.
+//
+// The plan leaves every unit what it needs and the free pages in order; the second kernel, a
+// warp a unit and piece of its copied page, enters and copies them.  (All in the plan's cluster, the
+// tables' entries were a chain of loads more in a kernel of 8 blocks: 14 us for 2048 units
+// and 59000 pages, PLAN_US now.)
+// ---------------------------------------------------------------------------
+// Warp w of `warps`: the units' pages entered and copied.
+__device__ __forceinline__ void enter_pages(const DevPaged &C, const DevChunk &T, int32_t *refs,
+                                            int32_t *row_pos, const PagesWs &ws, long long w,
+                                            long long warps) {
+    const int lane = threadIdx.x & 31, pieces = C.ps * C.d / 8 / kPieceVecs;     // at least one
+    const int per = C.L * C.H;
+    for (long long i = w; i < C.units * pieces; i += warps) {
+        const int u = (int)(i / pieces), piece = (int)(i - (long long)u * pieces);
+        const UnitNeed need = ws.need[u];
+        if (need.from >= 0) copy_piece(C, row_pos, need.from, ws.list[need.at], piece);
+        if (piece) continue;
+        int32_t *tab = table_of(C, u) + need.col;
+        for (int j = lane; j < need.pages; j += 32) {
+            const int page = ws.list[need.at + j];
+            tab[j] = page;
+            refs[page] = 1;
+        }
+        if (lane == 0) {
+            if (need.from >= 0) atomicSub(refs + need.from, 1);
+            const int r = u / per;
+            C.lens[u] += (int)(T.off[r + 1] - T.off[r]);
+        }
+    }
+}
+
 __global__ void __launch_bounds__(kCopyThreads, 4)
-copy_pages_kernel(const DevPaged C, int32_t *row_pos, const PagesWs ws, bool follow) {
+reserve_enter_kernel(const DevPaged C, const DevChunk T, int32_t *refs, int32_t *row_pos,
+                     const PagesWs ws) {
     pdl_wait();
     pdl_trigger();
+    if (ws.plan->count == 0) return;
+    enter_pages(C, T, refs, row_pos, ws, (long long)blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5),
+                (long long)gridDim.x * (kCopyThreads / 32));
+}
+
+// whole (one block): the block enters the pages too.
+template <int kCtas>
+__global__ void __launch_bounds__(kPlanThreads, 1)
+reserve_plan_kernel(const DevPaged C, const DevChunk T, int32_t *refs, int32_t *row_pos,
+                    const PagesWs ws, bool whole) {
+    constexpr int kAll = kCtas * kPlanThreads;
     const int lane = threadIdx.x & 31;
-    const long long warps = (long long)gridDim.x * (kCopyThreads / 32);
-    const long long w0 = (long long)blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5);
-    const int count = ws.plan->count;
-    if (follow && count > 0) {
-        const int live = ws.plan->live;
-        for (long long u = w0; u < C.units; u += warps) {
-            int n;
-            if (!unit_len(C, u, n)) {
-                if (lane == 0) post_status(C.status, KV_ERR_INVALID_ARG);
-                continue;
-            }
-            int32_t *tab = table_of(C, u);
-            const int held = pages_of(C, n);
-            for (int c = lane; c < held; c += 32) {
-                const int page = tab[c];
-                if (!page_ok(C, page)) post_status(C.status, KV_ERR_INVALID_ARG);
-                else if (page >= live) {
-                    // a page without a reference, which a table names all the same, goes nowhere
-                    const int to = ws.list[page];
-                    if (to < 0) post_status(C.status, KV_ERR_INVALID_ARG);
-                    else tab[c] = to;
+    pdl_wait();
+    pdl_trigger();
+    const int units = (int)C.units, chunk = (units + kAll - 1) / kAll;   // units: at most 2^28
+    const int gt = (int)(blockIdx.x * kPlanThreads + threadIdx.x);
+    const int u0 = (int)min((long long)units, (long long)gt * chunk);
+    const int u1 = min(units, u0 + chunk);
+    const int per = C.L * C.H;
+    // pages needed, free pages, units that cannot be, units longer than their table; the first is
+    // at most num_pages + 2 units (the host has checked the tokens)
+    int mine[4] = {0, 0, 0, 0};
+    UnitNeed last{0, 0, -1, 0};
+    for (int u = u0; u < u1; ++u) {
+        const int r = u / per, t = (int)(T.off[r + 1] - T.off[r]);
+        int n;
+        UnitNeed need{0, 0, -1, 0};
+        if (!unit_len(C, u, n)) {
+            mine[2] += 1;
+        } else if (t > C.cap - n) {
+            mine[3] += 1;
+        } else if (t > 0) {
+            need.col = pages_of(C, n);
+            need.pages = pages_of(C, n + t) - need.col;
+            if (n & (C.ps - 1)) {
+                const int page = C.table[(long long)u * C.max_pages + need.col - 1];
+                if (!page_ok(C, page)) {
+                    mine[2] += 1;
+                } else if (refs[page] > 1) {
+                    need.from = page;
+                    need.col -= 1;
+                    need.pages += 1;
                 }
+            }
+        }
+        need.at = mine[0];                       // after the thread's own before it
+        mine[0] += need.pages;
+        last = need;
+        if (chunk > 1) ws.need[u] = need;
+    }
+    const WarpPages<kCtas> W(C.num_pages);
+    int free_pages = 0;
+    scan_pages(W, refs, [&](long long, bool, unsigned used, unsigned there) {
+        free_pages += __popc(there & ~used);
+    });
+    if (lane == 0) mine[1] = free_pages;
+    const auto s = cluster_scan<kCtas>(mine);
+    const bool fits = s.total[2] == 0 && s.total[3] == 0 && s.total[0] <= s.total[1];
+    if (gt == 0) {
+        ws.plan->count = fits ? 1 : 0;
+        if (!fits) post_status(C.status, s.total[2] > 0 ? KV_ERR_INVALID_ARG : KV_ERR_BUDGET);
+    }
+    if (fits) {
+        for (int u = u0; u < u1; ++u) {
+            UnitNeed need = chunk > 1 ? ws.need[u] : last;
+            need.at += s.before[0];
+            ws.need[u] = need;
+        }
+        // the free pages that are given out, in order
+        int rank = __shfl_sync(0xffffffffu, s.before[1], 0);
+        scan_pages(W, refs, [&](long long p, bool is_used, unsigned used, unsigned there) {
+            const unsigned open = there & ~used;
+            const int k = rank + __popc(open & low_bits(lane));
+            if (!is_used && (there >> lane & 1) && k < s.total[0]) ws.list[k] = (int)p;
+            rank += __popc(open);
+        });
+        if (kCtas == 1 && whole) {
+            __syncthreads();
+            enter_pages(C, T, refs, row_pos, ws, threadIdx.x >> 5, kPlanThreads / 32);
+        }
+    }
+    leave_cluster<kCtas>();
+}
+
+// ---------------------------------------------------------------------------
+// Compaction.  With `live` pages in use, the k-th page in use from page `live` on goes to the k-th
+// free page before it.  The plan lists both, the pages to move from the last one on (their
+// number is known to no block while they are listed), so the k-th listed goes to the hole listed
+// k-th from the end.
+// ---------------------------------------------------------------------------
+// Warp w of `warps`: the tables follow their pages, then the pages move, a piece at a time.
+__device__ __forceinline__ void move_pages(const DevPaged &C, int32_t *refs, int32_t *row_pos,
+                                           const PagesWs &ws, int count, int live, long long w,
+                                           long long warps) {
+    const int lane = threadIdx.x & 31;
+    for (long long u = w; u < C.units; u += warps) {
+        int n;
+        if (!unit_len(C, u, n)) {
+            if (lane == 0) post_status(C.status, KV_ERR_INVALID_ARG);
+            continue;
+        }
+        int32_t *tab = table_of(C, u);
+        const int held = pages_of(C, n);
+        for (int c = lane; c < held; c += 32) {
+            const int page = tab[c];
+            if (!page_ok(C, page)) post_status(C.status, KV_ERR_INVALID_ARG);
+            else if (page >= live) {
+                // a page without a reference, which a table names all the same, goes nowhere
+                const int k = ws.list[page];
+                if (k < 0) post_status(C.status, KV_ERR_INVALID_ARG);
+                else tab[c] = ws.dst[count - 1 - k];
             }
         }
     }
     const int pieces = C.ps * C.d / 8 / kPieceVecs;          // at least one
-    for (long long i = w0; i < (long long)count * pieces; i += warps) {
-        const int j = (int)(i / pieces);
-        copy_piece(C, row_pos, ws.src[j], ws.dst[j], (int)(i - (long long)j * pieces));
+    for (long long i = w; i < (long long)count * pieces; i += warps) {
+        const int j = (int)(i / pieces), piece = (int)(i - (long long)j * pieces);
+        const int from = ws.src[j], to = ws.dst[count - 1 - j];
+        copy_piece(C, row_pos, from, to, piece);
+        if (piece == 0 && lane == 0) {
+            refs[to] = refs[from];
+            refs[from] = 0;
+        }
     }
 }
 
-// ---------------------------------------------------------------------------
-// Compaction's plan.  With `live` pages in use, the k-th page in use from page `live` on goes to the
-// k-th free page before it.
-// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(kCopyThreads, 4)
+compact_move_kernel(const DevPaged C, int32_t *refs, int32_t *row_pos, const PagesWs ws) {
+    pdl_wait();
+    pdl_trigger();
+    const int count = ws.plan->count;
+    if (count)
+        move_pages(C, refs, row_pos, ws, count, ws.plan->live,
+                   (long long)blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5),
+                   (long long)gridDim.x * (kCopyThreads / 32));
+}
+
+template <int kCtas>
 __global__ void __launch_bounds__(kPlanThreads, 1)
-compact_plan_kernel(const DevPaged C, int32_t *refs, int32_t *live_out, const PagesWs ws) {
-    cg::cluster_group cl = cg::this_cluster();
+compact_plan_kernel(const DevPaged C, int32_t *refs, int32_t *row_pos, int32_t *live_out,
+                    const PagesWs ws, bool whole) {
     const int lane = threadIdx.x & 31;
     pdl_wait();
     pdl_trigger();
-    const WarpPages W(C.num_pages);
+    if (blockIdx.x == 0 && threadIdx.x == 0) ws.plan->count = 0;
+    const WarpPages<kCtas> W(C.num_pages);
     int in_use = 0;
     scan_pages(W, refs, [&](long long, bool, unsigned used, unsigned) { in_use += __popc(used); });
     const int mine[1] = {lane == 0 ? in_use : 0};
-    const auto s = cluster_scan(mine);
+    const auto s = cluster_scan<kCtas>(mine);
     const int live = s.total[0];
-    const int before = __shfl_sync(0xffffffffu, s.before[0], 0);
-    int at = before;                             // pages in use before the 32 looked at
-    int holes = 0;                               // this warp's free pages before page `live`
+    int at = __shfl_sync(0xffffffffu, s.before[0], 0);       // in use before the 32 looked at
+    int holes = 0;                                           // this warp's free pages before `live`
     scan_pages(W, refs, [&](long long p, bool is_used, unsigned used, unsigned there) {
         const int used_before = at + __popc(used & low_bits(lane));
         if (there >> lane & 1) {
@@ -329,35 +370,25 @@ compact_plan_kernel(const DevPaged C, int32_t *refs, int32_t *live_out, const Pa
                 // as many pages lie before p as are free or in use
                 if (!is_used) ws.dst[(int)p - used_before] = (int)p;
             } else {
-                // counted back from the last page in use: the order of the pages to move
-                if (is_used) ws.src[live - 1 - used_before] = (int)p;
-                ws.list[p] = -1;
+                const int k = live - 1 - used_before;
+                if (is_used) ws.src[k] = (int)p;
+                ws.list[p] = is_used ? k : -1;
             }
         }
         holes += __popc(there & ~used & __ballot_sync(0xffffffffu, p < live));
         at += __popc(used);
     });
-    const int more[1] = {lane == 0 ? holes : 0};
-    __threadfence();
-    const int moved = cluster_scan(more).total[0];
-    // pages are listed from the last one on: the k-th to move is moved - 1 - k
-    for (int k = (int)(blockIdx.x * kPlanThreads + threadIdx.x); k < moved;
-         k += kPlanCtas * kPlanThreads) {
-        const int to = ws.dst[moved - 1 - k], from = ws.src[k];
-        ws.list[from] = to;
-        refs[to] = refs[from];
-        refs[from] = 0;
-    }
-    __threadfence();
-    cl.sync();
-    // the copy takes pairs
-    for (int k = (int)(blockIdx.x * kPlanThreads + threadIdx.x); k < moved;
-         k += kPlanCtas * kPlanThreads)
-        ws.dst[k] = ws.list[ws.src[k]];
+    // (the count's zero came before the cluster's first barrier)
+    if (lane == 0 && holes) atomicAdd(&ws.plan->count, holes);
     if (blockIdx.x == 0 && threadIdx.x == 0) {
-        *ws.plan = PagePlan{moved, live};
+        ws.plan->live = live;
         if (live_out) *live_out = live;
     }
+    if (kCtas == 1 && whole) {
+        __syncthreads();
+        move_pages(C, refs, row_pos, ws, ws.plan->count, live, threadIdx.x >> 5, kPlanThreads / 32);
+    }
+    leave_cluster<kCtas>();
 }
 
 // ---------------------------------------------------------------------------
@@ -491,23 +522,33 @@ PagesWs layout(const DevPaged &C, bool reserve, void *base) {
         off = (off + bytes + 255) / 256 * 256;
         return p;
     };
-    // a reservation copies a page of a unit at most and never more than there are
-    const size_t pages = (size_t)C.num_pages, units = (size_t)C.units;
-    const size_t pairs = reserve && units < pages ? units : pages;
+    const size_t pages = (size_t)C.num_pages;
     ws.plan = reinterpret_cast<PagePlan *>(take(sizeof(PagePlan)));
-    ws.src = reinterpret_cast<int *>(take(pairs * sizeof(int)));
-    ws.dst = reinterpret_cast<int *>(take(pairs * sizeof(int)));
     ws.list = reinterpret_cast<int *>(take(pages * sizeof(int)));
-    if (reserve) ws.need = reinterpret_cast<int *>(take(units * sizeof(int)));
+    if (reserve) {
+        ws.need = reinterpret_cast<UnitNeed *>(take((size_t)C.units * sizeof(UnitNeed)));
+    } else {
+        ws.src = reinterpret_cast<int *>(take(pages * sizeof(int)));
+        ws.dst = reinterpret_cast<int *>(take(pages * sizeof(int)));
+    }
     ws.total = off;
     return ws;
 }
 
-cudaError_t copy_pages(const DevPaged &C, int32_t *row_pos, const PagesWs &ws, bool follow,
-                       cudaStream_t s) {
-    return launch_dependent(copy_pages_kernel, dim3(kCopyCtas), kCopyThreads, 0, s, C, row_pos, ws,
-                            follow);
+// A plan by one block, whose threads meet without a cluster's barrier, where it has few pages and
+// units a thread (PLAN_RULE).
+bool one_block(const DevPaged &C) {
+    return C.num_pages <= 8 * kPlanThreads && C.units <= 2 * kPlanThreads;
 }
+unsigned copy_grid(long long warps) {
+    constexpr int kWarps = kCopyThreads / 32;
+    const long long grid = (warps + kWarps - 1) / kWarps;
+    return (unsigned)std::min<long long>(std::max<long long>(grid, 1), kCopyCtas);
+}
+// The block of such a plan also does what follows, in place of a second launch, where that is a
+// few rounds of its 32 warps.
+constexpr int kWholePieces = 256;
+int page_pieces(const DevPaged &C) { return C.ps * C.d / 8 / kPieceVecs; }
 
 }  // namespace
 
@@ -516,16 +557,39 @@ PagesWs compact_ws_layout(const DevPaged &C, void *base) { return layout(C, fals
 
 cudaError_t launch_reserve(const DevPaged &C, const DevChunk &T, int32_t *refs, int32_t *row_pos,
                            const PagesWs &ws, cudaStream_t s) {
-    const cudaError_t e = launch_cluster_dependent(reserve_plan_kernel, kPlanCtas, dim3(kPlanCtas),
-                                                   kPlanThreads, 0, s, C, T, refs, ws);
-    return e == cudaSuccess ? copy_pages(C, row_pos, ws, false, s) : e;
+    const long long pieces = C.units * page_pieces(C);
+    if (one_block(C)) {
+        const bool whole = pieces <= kWholePieces;
+        const cudaError_t e = launch_dependent(reserve_plan_kernel<1>, dim3(1), kPlanThreads, 0, s, C, T,
+                                               refs, row_pos, ws, whole);
+        if (e != cudaSuccess || whole) return e;
+    } else {
+        const cudaError_t e =
+            launch_cluster_dependent(reserve_plan_kernel<kPlanCtas>, kPlanCtas, dim3(kPlanCtas),
+                                     kPlanThreads, 0, s, C, T, refs, row_pos, ws, false);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_dependent(reserve_enter_kernel, dim3(copy_grid(pieces)), kCopyThreads, 0, s, C, T,
+                            refs, row_pos, ws);
 }
 
 cudaError_t launch_compact_pages(const DevPaged &C, int32_t *refs, int32_t *row_pos, int32_t *live,
                                  const PagesWs &ws, cudaStream_t s) {
-    const cudaError_t e = launch_cluster_dependent(compact_plan_kernel, kPlanCtas, dim3(kPlanCtas),
-                                                   kPlanThreads, 0, s, C, refs, live, ws);
-    return e == cudaSuccess ? copy_pages(C, row_pos, ws, true, s) : e;
+    const long long moved = (C.num_pages + 1) / 2 * page_pieces(C);      // pieces at most
+    const long long work = std::max(moved, C.units);
+    if (one_block(C)) {
+        const bool whole = work <= kWholePieces;
+        const cudaError_t e = launch_dependent(compact_plan_kernel<1>, dim3(1), kPlanThreads, 0, s, C,
+                                               refs, row_pos, live, ws, whole);
+        if (e != cudaSuccess || whole) return e;
+    } else {
+        const cudaError_t e =
+            launch_cluster_dependent(compact_plan_kernel<kPlanCtas>, kPlanCtas, dim3(kPlanCtas),
+                                     kPlanThreads, 0, s, C, refs, row_pos, live, ws, false);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_dependent(compact_move_kernel, dim3(copy_grid(work)), kCopyThreads, 0, s, C, refs,
+                            row_pos, ws);
 }
 
 cudaError_t launch_fork(const DevPaged &C, int32_t *refs, const int32_t *parents, cudaStream_t s) {
@@ -536,7 +600,9 @@ cudaError_t launch_fork(const DevPaged &C, int32_t *refs, const int32_t *parents
     strip = strip > C.max_pages ? C.max_pages : strip;
     const size_t smem = fixed + (size_t)C.R * strip * sizeof(int);
     const cudaError_t e =
-        cudaFuncSetAttribute(fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kForkSmem);
+        smem <= 48 * 1024 ? cudaSuccess
+                          : cudaFuncSetAttribute(
+                                fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kForkSmem);
     return e != cudaSuccess ? e
                             : launch_dependent(fork_kernel, dim3((unsigned)(C.L * C.H)), kForkThreads,
                                                smem, s, C, refs, parents, (int)strip);

@@ -12,18 +12,22 @@ constexpr int kPlanCtas = 8, kPlanThreads = 1024;
 constexpr int kCopyThreads = 256;
 constexpr int kCopyCtas = 8 * 152;
 
-// Pages copied after a plan: src[i] to dst[i].
 struct PagePlan {
-    int count;                 // pages copied
+    int count;                 // compaction: pages moved; reservation: whether all fit
     int live;                  // compaction: pages in use
+};
+// What a unit gets: `pages` pages from list[at] on, entered from column `col` on; the first takes the
+// place of page `from`, whose copy it is (-1: none is copied).
+struct alignas(16) UnitNeed {
+    int at, pages, from, col;
 };
 
 // Workspace of a reservation or compaction (offsets 256-byte aligned).
 struct PagesWs {
     PagePlan *plan;
-    int *src, *dst;            // pages copied; a compaction's pages to move and holes to fill
-    int *list;                 // reservation: free pages; compaction: where a page goes
-    int *need;                 // reservation: pages of a unit, times two, plus 1 if its tail is copied
+    int *list;                 // reservation: free pages; compaction: which to move a page is, or -1
+    UnitNeed *need;            // reservation
+    int *src, *dst;            // compaction: pages to move, holes
     size_t total;
 };
 PagesWs reserve_ws_layout(const DevPaged &C, void *base);

@@ -21,8 +21,77 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMostTokens = 8;        // tokens a block takes together
 constexpr int kMostPairs = 64;        // d / 2
+constexpr int kUnroll = 3;            // units in flight a thread
 
-// Frequencies of the block in turns a position, as 64 bits after the point.
+// x / d for 0 <= x < 2^31 with d's constant from the host.
+struct FastDiv {
+    unsigned mul, shift, d;
+    explicit FastDiv(unsigned n) : d(n) {
+        shift = 0;
+        while ((1ull << shift) < n) ++shift;
+        mul = (unsigned)(((1ull << 32) * ((1ull << shift) - n)) / n + 1);
+    }
+    __device__ __forceinline__ int operator()(int x) const {
+        return (int)((__umulhi((unsigned)x, mul) + (unsigned)x) >> shift);
+    }
+};
+
+// A row's 16 elements of unit i as two vectors, at a and b.  Turned units come first: with
+// halves paired, elements 8 i and dims / 2 + 8 i; the others are neighbours.
+template <bool kInter>
+struct Unit {
+    int a, b;
+    bool turned;
+    __device__ __forceinline__ Unit(int i, int dims) {
+        turned = i * 16 < dims;
+        const bool apart = !kInter && turned;
+        a = apart ? i : 2 * i;
+        b = apart ? i + dims / 16 : 2 * i + 1;
+    }
+};
+
+// Cosines and sines of a token's pairs.  A unit reads four vectors of two pairs each: word w's pairs,
+// which lie a unit apart, so that the threads of a row read side by side.
+struct Angles {
+    float4 cs[4][kMostPairs / 8];
+};
+
+template <typename E, bool kInter>
+__device__ __forceinline__ void turn_unit(uint4 &x, uint4 &y, const Angles &A, int unit) {
+    uint32_t *xw = reinterpret_cast<uint32_t *>(&x), *yw = reinterpret_cast<uint32_t *>(&y);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const float4 c = A.cs[w][unit];        // two pairs: (cos, sin) twice
+        const float2 u = E::unpack(xw[w]), v = E::unpack(yw[w]);
+        if (kInter) {
+            xw[w] = E::pack(u.x * c.x - u.y * c.y, u.x * c.y + u.y * c.x);
+            yw[w] = E::pack(v.x * c.z - v.y * c.w, v.x * c.w + v.y * c.z);
+        } else {
+            xw[w] = E::pack(u.x * c.x - v.x * c.y, u.y * c.z - v.y * c.w);
+            yw[w] = E::pack(u.x * c.y + v.x * c.x, u.y * c.w + v.y * c.z);
+        }
+    }
+}
+
+// The angles of n tokens from t0 on, by all threads.  s_turn: frequencies in turns a position, 64
+// bits after the point.
+template <bool kInter>
+__device__ __forceinline__ void fill_angles(const DevRotary &A, const FastDiv &by_half, int n,
+                                            const int32_t *positions,
+                                            const unsigned long long *s_turn, Angles *s_cs) {
+    const int half = A.dims / 2;
+    for (int i = threadIdx.x; i < n * half; i += kThreads) {
+        const int t = by_half(i), k = i - t * half;
+        const unsigned long long phase = (unsigned long long)(long long)positions[t] * s_turn[k];
+        const float x = (float)(int)(phase >> 32) * 4.656612873077393e-10f;      // half turns
+        float cos, sin;
+        sincospif(x, &sin, &cos);
+        if (A.backward) sin = -sin;
+        const int j = k & 7, w = kInter ? j & 3 : j >> 1, second = kInter ? j >> 2 : j & 1;
+        reinterpret_cast<float2 *>(&s_cs[t].cs[w][k >> 3])[second] =
+            make_float2(cos * A.factor, sin * A.factor);
+    }
+}
 __device__ __forceinline__ void load_turns(const DevRotary &A, unsigned long long *s_turn) {
     const int i = threadIdx.x;
     if (i < A.dims / 2) {
@@ -31,123 +100,74 @@ __device__ __forceinline__ void load_turns(const DevRotary &A, unsigned long lon
         t -= floor(t);
         s_turn[i] = (unsigned long long)(t * 18446744073709551616.0);
     }
-}
-
-// Cosine and sine (times the factor) of position p and frequency `turn`.
-__device__ __forceinline__ float2 turn_of(const DevRotary &A, unsigned long long turn, int p) {
-    const unsigned long long phase = (unsigned long long)(long long)p * turn;
-    const float x = (float)(int)(phase >> 32) * 4.656612873077393e-10f;      // half turns
-    float2 cs;
-    sincospif(x, &cs.y, &cs.x);
-    cs.x *= A.factor;
-    cs.y *= A.factor;
-    return cs;
-}
-
-// A row's 16 elements of unit i as two vectors, at a() and b().  Turned units come first: with
-// halves paired, elements 8 i and dims / 2 + 8 i; the others are neighbours.
-template <bool kInter>
-struct Unit {
-    int a, b, pair;                   // vectors of the row; the first pair
-    bool turned;
-    __device__ __forceinline__ Unit(int i, int dims) {
-        turned = i * 16 < dims;
-        pair = 8 * i;
-        const bool apart = !kInter && turned;
-        a = apart ? i : 2 * i;
-        b = apart ? i + dims / 16 : 2 * i + 1;
-    }
-};
-
-template <typename E, bool kInter>
-__device__ __forceinline__ void turn_unit(uint4 &x, uint4 &y, const float2 *cs) {
-    uint32_t *xw = reinterpret_cast<uint32_t *>(&x), *yw = reinterpret_cast<uint32_t *>(&y);
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        float2 u = E::unpack(xw[w]), v = E::unpack(yw[w]);
-        if (kInter) {
-            const float2 c = cs[w], e = cs[w + 4];
-            u = make_float2(u.x * c.x - u.y * c.y, u.x * c.y + u.y * c.x);
-            v = make_float2(v.x * e.x - v.y * e.y, v.x * e.y + v.y * e.x);
-        } else {
-            const float2 c = cs[2 * w], e = cs[2 * w + 1];
-            const float2 s = u, t = v;
-            u = make_float2(s.x * c.x - t.x * c.y, s.y * e.x - t.y * e.y);
-            v = make_float2(s.x * c.y + t.x * c.x, s.y * e.y + t.y * e.x);
-        }
-        xw[w] = E::pack(u.x, u.y);
-        yw[w] = E::pack(v.x, v.y);
-    }
-}
-
-// The block's loop over groups of tokens: `angles` fills the table of a group and `rows` moves its
-// units.  Two tables, so that one barrier a group is enough.
-template <typename F>
-__device__ __forceinline__ void for_groups(const DevRotary &A, long long tokens, int group,
-                                           const int32_t *positions, F rows) {
-    __shared__ unsigned long long s_turn[kMostPairs];
-    __shared__ float2 s_cs[2][kMostTokens][kMostPairs];
-    const int half = A.dims / 2;
-    load_turns(A, s_turn);
     __syncthreads();
+}
+
+// Rows of a group of tokens, kThreads / (D / 16) at a time: kUnroll of them on their way while the
+// group's angles are taken.  place(row) says where a row of the group comes from, once `prepare` has
+// run where it goes to (null: nowhere), and whether it is turned.  Two tables of angles, and of
+// what `prepare` leaves, so that a barrier a group is enough.
+template <typename E, int D, bool kInter, typename S, typename P, typename T>
+__device__ __forceinline__ void turn_groups(const DevRotary &A, const FastDiv &by_half,
+                                            const FastDiv &by_rows, long long tokens, int group,
+                                            const int32_t *positions, S source, P prepare, T target) {
+    constexpr int kU = D / 16, kSlots = kThreads / kU;
+    __shared__ unsigned long long s_turn[kMostPairs];
+    __shared__ Angles s_cs[2][kMostTokens];
+    load_turns(A, s_turn);
+    const int unit = threadIdx.x % kU, slot = threadIdx.x / kU;
+    const Unit<kInter> u(unit, A.dims);
     int which = 0;
     for (long long t0 = (long long)blockIdx.x * group; t0 < tokens;
          t0 += (long long)gridDim.x * group, which ^= 1) {
-        const int n = (int)min((long long)group, tokens - t0);
-        rows(t0, n, s_cs[which], [&]() {
-            for (int i = threadIdx.x; i < n * half; i += kThreads) {
-                const int t = i / half, k = i - t * half;
-                float2 cs = turn_of(A, s_turn[k], positions[t0 + t]);
-                if (A.backward) cs.y = -cs.y;
-                s_cs[which][t][k] = cs;
+        const int n = (int)min((long long)group, tokens - t0), all = n * (int)by_rows.d;
+        bool ready = false;
+        for (int r0 = slot; r0 < all || !ready; r0 += kSlots * kUnroll) {
+            uint4 a[kUnroll], b[kUnroll];
+#pragma unroll
+            for (int q = 0; q < kUnroll; ++q) {
+                const int row = r0 + q * kSlots;
+                if (row >= all) continue;
+                const int t = by_rows(row);
+                const uint4 *src = source(t0 + t, row - t * (int)by_rows.d);
+                a[q] = src[u.a];
+                b[q] = src[u.b];
             }
-            __syncthreads();
-        });
+            if (!ready) {
+                prepare(t0, n, which);
+                fill_angles<kInter>(A, by_half, n, positions + t0, s_turn, s_cs[which]);
+                __syncthreads();
+                ready = true;
+            }
+#pragma unroll
+            for (int q = 0; q < kUnroll; ++q) {
+                const int row = r0 + q * kSlots;
+                if (row >= all) continue;
+                const int t = by_rows(row);
+                bool turned = u.turned;
+                uint4 *dst = target(t0, t, row - t * (int)by_rows.d, unit, which, turned);
+                if (turned) turn_unit<E, kInter>(a[q], b[q], s_cs[which][t], unit);
+                if (!dst) continue;
+                dst[u.a] = a[q];
+                dst[u.b] = b[q];
+            }
+        }
     }
 }
 
-constexpr int kUnroll = 3;            // units in flight a thread
-
 template <typename E, int D, bool kInter>
 __global__ void __launch_bounds__(kThreads, 4)
-rotary_kernel(const DevRotary A, long long tokens, int heads, int group,
-              const int32_t *positions, const uint4 *x, long long x_tok,
-              long long x_head, uint4 *out, long long out_tok, long long out_head) {
-    constexpr int kU = D / 16;
+rotary_kernel(const DevRotary A, const FastDiv by_half, const FastDiv by_heads, long long tokens,
+              int group, const int32_t *positions, const RotaryIo io) {
     pdl_wait();
     pdl_trigger();
-    for_groups(A, tokens, group, positions,
-               [&](long long t0, int n, const float2 (*cs)[kMostPairs], auto angles) {
-                   const int per = heads * kU, all = n * per;
-                   bool ready = false;
-                   for (int i0 = threadIdx.x; i0 < all || !ready; i0 += kThreads * kUnroll) {
-                       uint4 a[kUnroll], b[kUnroll];
-                       int tk[kUnroll], hd[kUnroll], un[kUnroll];
-#pragma unroll
-                       for (int q = 0; q < kUnroll; ++q) {
-                           const int i = i0 + q * kThreads;
-                           tk[q] = i / per;
-                           hd[q] = (i - tk[q] * per) / kU;
-                           un[q] = i % kU;
-                           if (i >= all) continue;
-                           const Unit<kInter> u(un[q], A.dims);
-                           const uint4 *src = x + (t0 + tk[q]) * x_tok + hd[q] * x_head;
-                           a[q] = src[u.a];
-                           b[q] = src[u.b];
-                       }
-                       if (!ready) angles();
-                       ready = true;
-#pragma unroll
-                       for (int q = 0; q < kUnroll; ++q) {
-                           if (i0 + q * kThreads >= all) continue;
-                           const Unit<kInter> u(un[q], A.dims);
-                           if (u.turned) turn_unit<E, kInter>(a[q], b[q], &cs[tk[q]][u.pair]);
-                           uint4 *dst = out + (t0 + tk[q]) * out_tok + hd[q] * out_head;
-                           dst[u.a] = a[q];
-                           dst[u.b] = b[q];
-                       }
-                   }
-               });
+    turn_groups<E, D, kInter>(
+        A, by_half, by_heads, tokens, group, positions,
+        [&](long long tok, int h) { return io.x + tok * io.x_tok + h * io.x_head; },
+        [](long long, int, int) {},
+        [&](long long t0, int t, int h, int, int, bool &) {
+            return io.out + (t0 + t) * io.out_tok + h * io.out_head;
+        });
 }
 
 // Request of token `tok`, by a warp: 32 offsets at a time.
@@ -163,114 +183,93 @@ __device__ __forceinline__ int request_by_warp(const DevChunk &T, int R, long lo
     return lo;
 }
 
-// Rows of a token: Hq query heads, then H of K, then H of V.
+// Rows of a token: Hq query heads (or none), then H of K, then H of V.
+constexpr int kMostHeads = 32;        // KV heads of a group's tokens whose places fit shared memory
+
 template <typename E, int D, bool kInter>
 __global__ void __launch_bounds__(kThreads, 4)
-append_rotary_kernel(const DevPaged C, const DevChunk T, int layer, const DevRotary A, int group,
+append_rotary_kernel(const DevPaged C, const DevChunk T, int layer, const DevRotary A,
+                     const FastDiv by_half, const FastDiv by_rows, int group,
                      const int32_t *positions, int32_t *row_pos, const AppendIo io) {
-    constexpr int kU = D / 16;
-    __shared__ int s_req[kMostTokens];
+    constexpr int kVecs = D / 8;
+    __shared__ int s_req[2][kMostTokens];
+    __shared__ int s_row[2][kMostTokens][kMostHeads];        // pool rows; -1: nowhere
     pdl_wait();
     pdl_trigger();
     const int Hq = io.q ? C.Hq : 0;
-    for_groups(A, T.tokens, group, positions,
-               [&](long long t0, int n, const float2 (*cs)[kMostPairs], auto angles) {
-                   const int per = (Hq + 2 * C.H) * kU, all = n * per;
-                   bool ready = false;
-                   for (int i0 = threadIdx.x; i0 < all || !ready; i0 += kThreads * kUnroll) {
-                       uint4 a[kUnroll], b[kUnroll];
-                       int tk[kUnroll], hd[kUnroll], un[kUnroll];
-#pragma unroll
-                       for (int q = 0; q < kUnroll; ++q) {
-                           const int i = i0 + q * kThreads;
-                           tk[q] = i / per;
-                           hd[q] = (i - tk[q] * per) / kU;
-                           un[q] = i % kU;
-                           if (i >= all) continue;
-                           const Unit<kInter> u(un[q], A.dims);
-                           const long long tok = t0 + tk[q];
-                           const int h = hd[q] - Hq;
-                           const uint4 *src =
-                               h < 0 ? io.q + tok * io.q_stride + hd[q] * (D / 8)
-                               : h < C.H ? io.k + tok * io.k_stride + h * (D / 8)
-                                         : io.v + tok * io.v_stride + (h - C.H) * (D / 8);
-                           a[q] = src[u.a];
-                           b[q] = src[u.b];
-                       }
-                       if (!ready) {
-                           const int warp = threadIdx.x >> 5;
-                           if (warp < n) {
-                               const int r = request_by_warp(T, C.R, t0 + warp);
-                               if ((threadIdx.x & 31) == 0) s_req[warp] = r;
-                           }
-                           angles();
-                       }
-                       ready = true;
-#pragma unroll
-                       for (int q = 0; q < kUnroll; ++q) {
-                           if (i0 + q * kThreads >= all) continue;
-                           const Unit<kInter> u(un[q], A.dims);
-                           const long long tok = t0 + tk[q];
-                           const int h = hd[q] - Hq;
-                           if (u.turned && h < C.H)
-                               turn_unit<E, kInter>(a[q], b[q], &cs[tk[q]][u.pair]);
-                           uint4 *dst;
-                           if (h < 0) {
-                               dst = io.q_out + tok * io.q_out_stride + hd[q] * (D / 8);
-                           } else {
-                               const int r = s_req[tk[q]], head = h < C.H ? h : h - C.H;
-                               if (tok >= T.off[C.R]) continue;
-                               const long long v = ((long long)r * C.L + layer) * C.H + head;
-                               int len;
-                               const bool ok = unit_len(C, v, len);
-                               const long long j = len - (T.off[r + 1] - tok);
-                               if (ok && j < 0) continue;
-                               const long long row =
-                                   ok ? page_row(C, C.table + v * C.max_pages, (int)j) : -1;
-                               if (row < 0) {
-                                   post_status(C.status, KV_ERR_INVALID_ARG);
-                                   continue;
-                               }
-                               if (h < C.H && un[q] == 0) {
-                                   if (C.mass) C.mass[row] = 0.f;
-                                   if (row_pos) row_pos[row] = positions[tok];
-                               }
-                               dst = static_cast<uint4 *>(h < C.H ? C.k : C.v) + row * (D / 8);
-                           }
-                           dst[u.a] = a[q];
-                           dst[u.b] = b[q];
-                       }
-                   }
-                   // the next group's requests overwrite these
-                   __syncthreads();
-               });
+    // Pool row of token tok's new row of head h, -1 if it has none.
+    auto place = [&](int r, long long tok, int h) {
+        const long long v = ((long long)r * C.L + layer) * C.H + h;
+        int len;
+        const bool ok = unit_len(C, v, len);
+        const long long j = len - (T.off[r + 1] - tok);
+        if (tok >= T.off[C.R] || (ok && j < 0)) return -1;
+        const int row = ok ? (int)page_row(C, C.table + v * C.max_pages, (int)j) : -1;
+        if (row < 0) post_status(C.status, KV_ERR_INVALID_ARG);
+        return row;
+    };
+    turn_groups<E, D, kInter>(
+        A, by_half, by_rows, T.tokens, group, positions,
+        [&](long long tok, int i) {
+            const int h = i - Hq;
+            return h < 0     ? io.q + tok * io.q_stride + i * kVecs
+                   : h < C.H ? io.k + tok * io.k_stride + h * kVecs
+                             : io.v + tok * io.v_stride + (h - C.H) * kVecs;
+        },
+        [&](long long t0, int n, int which) {
+            // a warp a token
+            const int t = threadIdx.x >> 5, lane = threadIdx.x & 31;
+            if (t >= n) return;
+            const int r = request_by_warp(T, C.R, t0 + t);
+            if (lane == 0) s_req[which][t] = r;
+            if (lane < C.H && C.H <= kMostHeads) s_row[which][t][lane] = place(r, t0 + t, lane);
+        },
+        [&](long long t0, int t, int i, int unit, int which, bool &turned) -> uint4 * {
+            const long long tok = t0 + t;
+            const int h = i - Hq;
+            if (h < 0) return io.q_out + tok * io.q_out_stride + i * kVecs;
+            const bool is_k = h < C.H;
+            turned = turned && is_k;
+            const int head = is_k ? h : h - C.H;
+            const int row = C.H <= kMostHeads ? s_row[which][t][head]
+                                              : place(s_req[which][t], tok, head);
+            if (row < 0) return nullptr;
+            if (is_k && unit == 0) {
+                if (C.mass) C.mass[row] = 0.f;
+                if (row_pos) row_pos[row] = positions[tok];
+            }
+            return static_cast<uint4 *>(is_k ? C.k : C.v) + (long long)row * kVecs;
+        });
 }
 
-// Tokens a block takes together: enough units for its threads' first step.
-int group_of(int rows, int d) {
-    const int g = kThreads / (rows * (d / 16));
-    return g < 1 ? 1 : g > kMostTokens ? kMostTokens : g;
+// Tokens a block takes together: as many as give all its threads an angle, fewer where that
+// would leave SMs without a block.
+int group_of(long long tokens, int dims) {
+    const long long g = tokens / kRotarySpread;
+    const int most = dims < 64 ? kMostTokens : 2 * kThreads / dims;
+    return (int)(g < 1 ? 1 : g > most ? most : g);
 }
 unsigned grid_of(long long tokens, int group) {
     const long long n = (tokens + group - 1) / group;
     return (unsigned)(n < kRotaryCtas ? n : kRotaryCtas);
 }
+FastDiv by_half(const DevRotary &A) { return FastDiv(A.dims > 0 ? A.dims / 2 : 1); }
 
 template <typename E, int D, bool kInter>
 cudaError_t rotary(const DevRotary &A, long long tokens, int heads, const int32_t *positions,
                    const RotaryIo &io, cudaStream_t s) {
-    const int group = group_of(heads, D);
-    return launch_dependent(rotary_kernel<E, D, kInter>, dim3(grid_of(tokens, group)), kThreads, 0,
-                            s, A, tokens, heads, group, positions, io.x, io.x_tok, io.x_head,
-                            io.out, io.out_tok, io.out_head);
+    const int group = group_of(tokens, A.dims);
+    return launch_dependent(rotary_kernel<E, D, kInter>, dim3(grid_of(tokens, group)), kThreads, 0, s,
+                            A, by_half(A), FastDiv(heads), tokens, group, positions, io);
 }
 
 template <typename E, int D, bool kInter>
 cudaError_t append(const DevPaged &C, const DevChunk &T, int layer, const DevRotary &A,
                    const int32_t *positions, int32_t *row_pos, const AppendIo &io, cudaStream_t s) {
-    const int group = group_of((io.q ? C.Hq : 0) + 2 * C.H, D);
+    const int group = group_of(T.tokens, A.dims);
     return launch_dependent(append_rotary_kernel<E, D, kInter>, dim3(grid_of(T.tokens, group)),
-                            kThreads, 0, s, C, T, layer, A, group, positions, row_pos, io);
+                            kThreads, 0, s, C, T, layer, A, by_half(A),
+                            FastDiv((io.q ? C.Hq : 0) + 2 * C.H), group, positions, row_pos, io);
 }
 
 }  // namespace

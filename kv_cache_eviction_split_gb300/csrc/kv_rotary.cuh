@@ -28,7 +28,9 @@ struct AppendIo {
     long long k_stride, v_stride;
 };
 
-constexpr long long kRotaryCtas = 152 * 4;
+// Blocks that a step's tokens are spread over before a block takes more than one.
+constexpr long long kRotarySpread = 152 * 2;
+constexpr long long kRotaryCtas = 1 << 20;
 
 cudaError_t launch_rotary(const DevRotary &A, long long tokens, int heads, int d, int dtype,
                           const int32_t *positions, const RotaryIo &io, cudaStream_t s);
