@@ -34,6 +34,13 @@ struct Lane {
     int ns, a, b;
     __device__ __forceinline__ bool sees(int x) const { return x < ns || (x >= a && x < b); }
 };
+// With slopes an item's tiles are taken from the last one on: the nearest keys, whose scores are
+// lowered least, set the maximum, which the other order would raise (and the output with it) at every
+// tile of a steep head (RAISE).  Tile x of a run, as its item counts them:
+template <bool kSlope>
+__device__ __forceinline__ int nth_tile(const TileSpan &span, int x) {
+    return kSlope ? span.total - 1 - x : x;
+}
 // An item and the part of it in this CTA's run, as the scheduler warp writes it.
 struct Item {
     int cta;                   // this CTA, counted on through the phases
@@ -65,10 +72,13 @@ struct Layout {
     static constexpr int kDesc = kFirst + 32;
     static constexpr int kTotal = kDesc + kItems * (int)sizeof(Item);
     static_assert(kTotal + 1024 <= 227 * 1024, "with cut_run's and TMEM's few static words");
-    // kMod: four more barriers and, of each lane, the distances' other end: key positions
+    // kMod: four more barriers, of each lane the distances' other end, key positions, and the
+    // polynomials' coefficients, twice each: of the one that slopes leave room for, or, without
+    // slopes, of both, in the positions' place
     static constexpr int kPosBars = kTotal;
     static constexpr int kPos = (kPosBars + 4 * 8 + 15) / 16 * 16;
-    static constexpr int kTotalMod = kPos + 2 * kManyTile * 4;
+    static constexpr int kCo = kPos + 2 * kManyTile * 4;
+    static constexpr int kTotalMod = kCo + 5 * 8;
     static_assert(kTotalMod + 1024 <= 227 * 1024, "with the static words");
 };
 
@@ -215,6 +225,17 @@ __device__ __forceinline__ void cap_poly(const float2 (&c2)[N], float2 add, floa
     }
 }
 constexpr int kPolyPairs = 4;
+// The coefficients from shared memory into registers, once for a loop: from the constant bank the
+// compiler fetches them anew for every few logits, by moves on the unit that the products need
+// (MOVES).
+template <int N>
+__device__ __forceinline__ void load_coefficients(const uint8_t *from, float2 (&c2)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        asm volatile("ld.volatile.shared.v2.f32 {%0, %1}, [%2];"
+                     : "=f"(c2[i].x), "=f"(c2[i].y)
+                     : "r"(smem_u32(from + 8 * i)));
+}
 
 __device__ __forceinline__ float absmax64(const float (&v)[64]) {
     float a[8];
@@ -302,6 +323,10 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         prefetch_tensormap(&tm_k);
         prefetch_tensormap(&tm_v);
     }
+    uint8_t *s_co = smem + (kSlope ? Ly::kCo : Ly::kPos);      // of the fifth order, the fourth
+    if (kCap && threadIdx.x < (kSlope ? 5 : 9))
+        reinterpret_cast<float2 *>(s_co)[threadIdx.x] =
+            threadIdx.x < 5 ? A.form.co5[threadIdx.x] : A.form.co4[threadIdx.x - 5];
     pdl_wait();
     pdl_trigger();
     const uint32_t tmem = tmem_acquire_all(s_tmem);
@@ -394,7 +419,9 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                     }
                 }
             }
-            r.any = x0 < min(ns, x1) || max(x0, w->lane[L].a) < min(x1, w->lane[L].b);
+            // the run's tiles in the item's count
+            const int y0 = kSlope ? w->span.total - x1 : x0, y1 = kSlope ? w->span.total - x0 : x1;
+            r.any = y0 < min(ns, y1) || max(y0, w->lane[L].a) < min(y1, w->lane[L].b);
             return r;
         };
         // Q rows of the item into shared memory for the products, once those of the item before
@@ -452,21 +479,21 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             [[maybe_unused]] int page_x = -1, pos_x = -1, next_page = -1, next_pos = 0;
             [[maybe_unused]] const int seen_hi = w->t_hi;
             auto look_up = [&](int x) {
-                const int j = span.tile(x) * kManyTile + rr;
+                const int j = span.tile(nth_tile<kSlope>(span, x)) * kManyTile + rr;
                 page_x = x;
                 next_page = A.form.pos && x < x1 && j <= seen_hi ? tab[j >> C.ps_log2] : -1;
             };
             auto fetch = [&]() {
-                const int j = span.tile(page_x) * kManyTile + rr;
+                const int j = span.tile(nth_tile<kSlope>(span, page_x)) * kManyTile + rr;
                 pos_x = page_x;
                 next_pos = next_page >= 0 && next_page < C.num_pages
                                ? A.form.pos[((long long)next_page << C.ps_log2) + (j & (C.ps - 1))]
                                : j;
             };
             for (int x = x0; x < x1; ++x) {
-                const int key0 = span.tile(x) * kManyTile;
-                if (!me.sees(x)) {
-                    kc += other.sees(x);
+                const int key0 = span.tile(nth_tile<kSlope>(span, x)) * kManyTile;
+                if (!me.sees(nth_tile<kSlope>(span, x))) {
+                    kc += other.sees(nth_tile<kSlope>(span, x));
                     continue;
                 }
                 const int last = key0 + kManyTile - 1;
@@ -488,7 +515,7 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                     if (lane == 0) mbar_arrive(&pos_full[L]);
                     look_up(x + 1);
                 }
-                if (!full && (L == 0 || !other.sees(x)) &&
+                if (!full && (L == 0 || !other.sees(nth_tile<kSlope>(span, x))) &&
                     (last > w->t_hi || (last >= w->sinks && key0 < w->lo))) {
                     // V rows that no query sees may hold anything: 0 weight times NaN.  The
                     // first lane of the tile clears them before its P goes to the products.
@@ -636,9 +663,11 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                             most = fmaxf(most, am);
                             if (kSlope) {
                                 if (cap_tier(A.form, am) < 2) {
+                                    float2 co[5];
+                                    load_coefficients(s_co, co);
 #pragma unroll
                                     for (int i = 0; i < 64; i += 2 * kPolyPairs)
-                                        cap_poly<kPolyPairs>(A.form.co5, make_float2(0.f, 0.f), &v[i]);
+                                        cap_poly<kPolyPairs>(co, make_float2(0.f, 0.f), &v[i]);
                                 } else {
 #pragma unroll
                                     for (int i = 0; i < 64; ++i) v[i] = cap_logit(A.form, v[i]);
@@ -695,17 +724,16 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                     } else if (kCap) {
                         // without slopes tanh goes with the exponentials: it rises
                         tier = cap_tier(A.form, most);
-                        float one[2] = {top, top};
-                        if (tier == 0) cap_poly<1>(A.form.co4, make_float2(0.f, 0.f), one);
-                        else if (tier == 1) cap_poly<1>(A.form.co5, make_float2(0.f, 0.f), one);
-                        else one[0] = cap_logit(A.form, top);
-                        if (top != -INFINITY) top = one[0];
+                        if (top != -INFINITY) top = cap_logit(A.form, top);
                     }
                     raise(top * zs);
                     const float nm = m == -INFINITY ? 0.f : E::kShift - m;
                     const float2 zs2 = make_float2(zs, zs), nm2 = make_float2(nm, nm);
                     // how: 0 as they are (times zs), 1 and 2 by the polynomials, 3 exactly
                     auto weights = [&](auto how) {
+                        float2 co[how.value == 2 ? 5 : 4];
+                        if (how.value == 1 || how.value == 2)
+                            load_coefficients(s_co + (how.value == 2 ? 0 : 40), co);
 #pragma unroll 1
                         for (int c = 0; c < 4; c += 2) {
                             const Half h = half_of(c);
@@ -719,8 +747,8 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                                 // eight logits at a time, so that products and exponentials, which
                                 // run on different units, alternate
                                 auto eight = [&](int i, auto mixed) {
-                                    if (how.value == 1) cap_poly<kPolyPairs>(A.form.co4, nm2, &v[i]);
-                                    if (how.value == 2) cap_poly<kPolyPairs>(A.form.co5, nm2, &v[i]);
+                                    if (how.value == 1 || how.value == 2)
+                                        cap_poly<kPolyPairs>(co, nm2, &v[i]);
 #pragma unroll
                                     for (int j = i; j < i + 2 * kPolyPairs; j += 2) {
                                         float2 e = make_float2(v[j], v[j + 1]);
@@ -911,7 +939,7 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                 const int32_t *table = w->table;
                 int base = -1, pg = -1;
                 for (int x = w->x0; x < x1; ++x) {
-                    const int key0 = span.tile(x) * kManyTile, e0 = key0 >> C.ps_log2;
+                    const int key0 = span.tile(nth_tile<kSlope>(span, x)) * kManyTile, e0 = key0 >> C.ps_log2;
                     if ((e0 & ~31) != base) {
                         base = e0 & ~31;
                         pg = base + lane < C.max_pages ? table[base + lane] : -1;
@@ -978,6 +1006,7 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                     };
                     const Lane l0 = lane_of(0), l1 = lane_of(1);
                     const int x0 = uni(w->x0), x1 = uni(w->x1), w_seen = w->t_hi >= 0;
+                    [[maybe_unused]] const int total = uni(w->span.total);
                     __syncwarp();
                     if (el) mbar_arrive(&i_empty[i % kItems]);
                     // Slot x: P V of the lanes' tiles of slot x - 1, then S of tile x.  Their
@@ -988,7 +1017,8 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                     const int slots = uni(w_seen) ? x1 - x0 : 0;
                     for (int i = 0; ok && i < slots + 1; ++i) {
                         const int x = x0 + i;
-                        const bool see[2] = {i < slots && l0.sees(x), i < slots && l1.sees(x)};
+                        const int y = kSlope ? total - 1 - x : x;
+                        const bool see[2] = {i < slots && l0.sees(y), i < slots && l1.sees(y)};
                         const int ks = (kc + i) % Ly::kKSt, vs = (kc + i + 1) % Ly::kVSt;
                         if (i < slots) ok = wait(&k_full[ks], (kc + i) / Ly::kKSt);
                         if (ok && i > 0) ok = wait(&v_full[vs], (kc + i - 1) / Ly::kVSt);
@@ -1081,7 +1111,7 @@ cudaError_t many(const DevPaged &C, const DevChunk &T, const ManyArgs &A, const 
     if (!make_tile_map(&mk, C.k, C.num_pages * C.ps, D, C.ps) ||
         !make_tile_map(&mv, C.v, C.num_pages * C.ps, D, C.ps))
         return cudaErrorInvalidValue;
-    constexpr int kSmem = kForm & kSloped ? Ly::kTotalMod : Ly::kTotal;
+    constexpr int kSmem = kForm & (kSloped | kCapped) ? Ly::kTotalMod : Ly::kTotal;
     cudaError_t e = cudaFuncSetAttribute(many_kernel<E, D, kForm>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e == cudaSuccess)
