@@ -237,16 +237,19 @@ __device__ __forceinline__ void load_coefficients(const uint8_t *from, float2 (&
                      : "r"(smem_u32(from + 8 * i)));
 }
 
-__device__ __forceinline__ float absmax64(const float (&v)[64]) {
-    float a[8];
+template <int N>
+__device__ __forceinline__ float absmax(const float (&v)[N]) {
+    float a[N / 8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < N / 8; ++i) {
         a[i] = fmax3(fabsf(v[8 * i]), fabsf(v[8 * i + 1]), fabsf(v[8 * i + 2]));
         a[i] = fmax3(a[i], fabsf(v[8 * i + 3]), fabsf(v[8 * i + 4]));
         a[i] = fmax3(a[i], fabsf(v[8 * i + 5]), fabsf(v[8 * i + 6]));
         a[i] = fmaxf(a[i], fabsf(v[8 * i + 7]));
     }
-    return fmax3(fmax3(a[0], a[1], a[2]), fmax3(a[3], a[4], a[5]), fmaxf(a[6], a[7]));
+#pragma unroll
+    for (int i = 1; i < N / 8; ++i) a[0] = fmaxf(a[0], a[i]);
+    return a[0];
 }
 // How a warp takes tanh of logits of up to `most` in its rows: 0 and 1 by ScoreForm's polynomials, 2
 // exactly.  The exact form's two approximate operations a logit (2^x and a reciprocal) come on
@@ -615,32 +618,45 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                         }
                     }
                 } else {
-                    // Changed scores: the logits stay in tensor memory and come 64 keys at a time, twice,
-                    // in loops.  Unrolled over the 128 keys, what is added here made the row warps
-                    // wait for instructions (INSTR).
-                    struct Half {
-                        uint32_t see[2];
+                    // Changed scores: the logits stay in tensor memory and come kW keys at a time, twice, in
+                    // loops.  Unrolled over the 128 keys and held in registers, what is added here
+                    // made the row warps wait for instructions: a long cache's chunk, us, held /
+                    // 64 / 32 keys: capped 1391 / 1098 / 1110, with slopes 1081 / 1019 / 1148; a
+                    // packed prompt of short documents, capped 309 / 239 / 219.
+                    constexpr int kW = kCap && !kSlope ? 32 : 64;
+                    struct Part {
+                        uint32_t see[kW / 32];
                         bool none, mixed;          // of all the warp's rows: no key seen, not all
                     };
-                    auto half_of = [&](int c) {
-                        Half h{{0xffffffffu, 0xffffffffu}, false, false};
+                    auto part_of = [&](int c) {
+                        Part h;
+                        h.none = h.mixed = false;
+#pragma unroll
+                        for (int k = 0; k < kW / 32; ++k) h.see[k] = 0xffffffffu;
                         if (!full) {
-                            h.see[0] = seen_keys(c);
-                            h.see[1] = seen_keys(c + 1);
-                            h.none = __all_sync(0xffffffffu, (h.see[0] | h.see[1]) == 0u);
-                            h.mixed = !__all_sync(0xffffffffu, (h.see[0] & h.see[1]) == 0xffffffffu);
+                            uint32_t any = 0u, all = 0xffffffffu;
+#pragma unroll
+                            for (int k = 0; k < kW / 32; ++k) {
+                                h.see[k] = seen_keys(c + k);
+                                any |= h.see[k];
+                                all &= h.see[k];
+                            }
+                            h.none = __all_sync(0xffffffffu, any == 0u);
+                            h.mixed = !__all_sync(0xffffffffu, all == 0xffffffffu);
                         }
                         return h;
                     };
-                    auto load = [&](int c, float (&v)[64]) {
-                        tmem_ld32(s_base + 32 * c, *reinterpret_cast<float(*)[32]>(&v[0]));
-                        tmem_ld32(s_base + 32 * c + 32, *reinterpret_cast<float(*)[32]>(&v[32]));
+                    auto load = [&](int c, float (&v)[kW]) {
+#pragma unroll
+                        for (int k = 0; k < kW / 32; ++k)
+                            tmem_ld32(s_base + 32 * (c + k),
+                                      *reinterpret_cast<float(*)[32]>(&v[32 * k]));
                         tmem_ld_wait();
                         reg_fence(v);
                     };
-                    auto hide = [&](const Half &h, float (&v)[64], float value) {
+                    auto hide = [&](const Part &h, float (&v)[kW], float value) {
 #pragma unroll
-                        for (int i = 0; i < 64; ++i)
+                        for (int i = 0; i < kW; ++i)
                             if (!(h.see[i >> 5] >> (i & 31) & 1u)) v[i] = value;
                     };
                     // the row's maximum, and with slopes the logits as they enter the softmax
@@ -651,26 +667,26 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                         if (!ok) break;
                     }
 #pragma unroll 1
-                    for (int c = 0; c < 4; c += 2) {
-                        const Half h = half_of(c);
+                    for (int c = 0; c < 4; c += kW / 32) {
+                        const Part h = part_of(c);
                         if (h.none) continue;
-                        float v[64];
+                        float v[kW];
                         load(c, v);
                         if (kCap) {
                             // what lies behind keys that nobody sees has no say in how tanh is taken
                             if (h.mixed) hide(h, v, 0.f);
-                            const float am = absmax64(v);
+                            const float am = absmax(v);
                             most = fmaxf(most, am);
                             if (kSlope) {
                                 if (cap_tier(A.form, am) < 2) {
                                     float2 co[5];
                                     load_coefficients(s_co, co);
 #pragma unroll
-                                    for (int i = 0; i < 64; i += 2 * kPolyPairs)
+                                    for (int i = 0; i < kW; i += 2 * kPolyPairs)
                                         cap_poly<kPolyPairs>(co, make_float2(0.f, 0.f), &v[i]);
                                 } else {
 #pragma unroll
-                                    for (int i = 0; i < 64; ++i) v[i] = cap_logit(A.form, v[i]);
+                                    for (int i = 0; i < kW; ++i) v[i] = cap_logit(A.form, v[i]);
                                 }
                             }
                         }
@@ -683,7 +699,7 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                                 // no key behind the query is seen: every distance that counts is
                                 // far - p
 #pragma unroll
-                                for (int i = 0; i < 64; i += 4) {
+                                for (int i = 0; i < kW; i += 4) {
                                     const float4 p = ps[i / 4];
                                     const float2 d0 = __fadd2_rn(make_float2(p.x, p.y), far);
                                     const float2 d1 = __fadd2_rn(make_float2(p.z, p.w), far);
@@ -697,7 +713,7 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                                 }
                             } else {
 #pragma unroll
-                                for (int i = 0; i < 64; i += 4) {
+                                for (int i = 0; i < kW; i += 4) {
                                     const float4 p = ps[i / 4];
                                     v[i] -= cur.slope * fabsf(p.x - cur.far);
                                     v[i + 1] -= cur.slope * fabsf(p.y - cur.far);
@@ -707,11 +723,12 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                             }
                         }
                         if (h.mixed) hide(h, v, -INFINITY);
-                        top = fmax3(top, max32(*reinterpret_cast<float(*)[32]>(&v[0])),
-                                    max32(*reinterpret_cast<float(*)[32]>(&v[32])));
+                        #pragma unroll
+                        for (int k = 0; k < kW; k += 32)
+                            top = fmaxf(top, max32(*reinterpret_cast<float(*)[32]>(&v[k])));
                         if (kSlope)
 #pragma unroll
-                            for (int i = 0; i < 64; i += 16)
+                            for (int i = 0; i < kW; i += 16)
                                 tmem_st16(s_base + 32 * c + i,
                                           *reinterpret_cast<float(*)[16]>(&v[i]));
                     }
@@ -735,14 +752,14 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                         if (how.value == 1 || how.value == 2)
                             load_coefficients(s_co + (how.value == 2 ? 0 : 40), co);
 #pragma unroll 1
-                        for (int c = 0; c < 4; c += 2) {
-                            const Half h = half_of(c);
-                            uint32_t pw[32];
+                        for (int c = 0; c < 4; c += kW / 32) {
+                            const Part h = part_of(c);
+                            uint32_t pw[kW / 2];
                             if (h.none) {
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) pw[i] = 0u;
+                                for (int i = 0; i < kW / 2; ++i) pw[i] = 0u;
                             } else {
-                                float v[64];
+                                float v[kW];
                                 load(c, v);
                                 // eight logits at a time, so that products and exponentials, which
                                 // run on different units, alternate
@@ -767,17 +784,19 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                                 };
                                 if (!kSlope && h.mixed) {
 #pragma unroll
-                                    for (int i = 0; i < 64; i += 2 * kPolyPairs)
+                                    for (int i = 0; i < kW; i += 2 * kPolyPairs)
                                         eight(i, std::true_type{});
                                 } else {
 #pragma unroll
-                                    for (int i = 0; i < 64; i += 2 * kPolyPairs)
+                                    for (int i = 0; i < kW; i += 2 * kPolyPairs)
                                         eight(i, std::false_type{});
                                 }
                             }
-                            tmem_st32u(s_base + 16 * c, pw);
-                            if (c == 0) {
-                                static_assert(kPFirst == 64, "what the first round writes");
+#pragma unroll
+                            for (int k = 0; k < kW / 32; ++k)
+                                tmem_st16u(s_base + 16 * (c + k),
+                                           *reinterpret_cast<uint32_t(*)[16]>(&pw[16 * k]));
+                            if (c + kW / 32 == kPFirst / 32) {
                                 tmem_st_wait();
                                 tc_fence_before();
                                 __syncwarp();
