@@ -427,31 +427,34 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             r.any = y0 < min(ns, y1) || max(y0, w->lane[L].a) < min(y1, w->lane[L].b);
             return r;
         };
-        // Q rows of the item into shared memory for the products, once those of the item before
-        // are done.  A warp brings its 32 rows together, kQRows rows to a load: a load a row
+        // Q rows of an item, fetched, and put into shared memory for the products.  A warp brings its 32 rows together, kQRows rows to a load: a load a row
         // and thread would touch 32 lines for 512 bytes (8 items of 8 tiles a CTA: QSTORE).
         constexpr int kQLanes = D / 8, kQRows = 32 / kQLanes, kQLoads = 32 / kQRows;
-        auto bring_q = [&](const Row &r, const Item *w) {
+        auto load_q = [&](const Row &r, uint4 (&q)[kQLoads]) {
             const uint4 *mine = reinterpret_cast<const uint4 *>(
                 static_cast<const typename E::T *>(A.io.q) + r.tok * A.io.q_stride +
                 (long long)r.head * D);
-            const int c = lane % kQLanes;
-            uint4 q[kQLoads];
 #pragma unroll
             for (int k = 0; k < kQLoads; ++k) {
                 const int from = k * kQRows + lane / kQLanes;
                 const uint4 *src = reinterpret_cast<const uint4 *>(__shfl_sync(
                     0xffffffffu, reinterpret_cast<unsigned long long>(mine), from));
                 const bool valid = __shfl_sync(0xffffffffu, (int)r.valid, from);
-                q[k] = valid ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+                q[k] = valid ? __ldg(src + lane % kQLanes) : make_uint4(0, 0, 0, 0);
             }
+        };
+        // Vector c of row `row` (of the lane) where its Q lies
+        auto q_slot = [&](int row, int c) {
+            return reinterpret_cast<uint4 *>(smem + Ly::kQ + L * Ly::kOp + row * 128 +
+                                             (c >> 3) * kBlockBytes + (((c & 7) ^ (row & 7)) << 4));
+        };
+        auto store_q = [&](const Row &r, const Item *w, const uint4 (&q)[kQLoads]) {
+            const int c = lane % kQLanes;
             const bool pack = A.q_packed && w->x0 <= (w->lane[L].ns ? 0 : w->lane[L].a);
 #pragma unroll
             for (int k = 0; k < kQLoads; ++k) {
-                const int from = k * kQRows + lane / kQLanes, row = quarter * 32 + from;
-                *reinterpret_cast<uint4 *>(smem + Ly::kQ + L * Ly::kOp + row * 128 +
-                                           (c >> 3) * kBlockBytes + (((c & 7) ^ (row & 7)) << 4)) =
-                    q[k];
+                const int row = quarter * 32 + k * kQRows + lane / kQLanes;
+                *q_slot(row, c) = q[k];
                 // the weights' pass takes the rows by TMA; one CTA of a cut item writes them
                 if (pack && row < w->lane[L].rows)
                     reinterpret_cast<uint4 *>(
@@ -462,12 +465,28 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_full[L]);
         };
+        // The warp's 32 rows from where their Q lay, D * 2 bytes each, row by row to dst(row).
+        auto flush = [&](auto dst) {
+            __syncwarp();
+#pragma unroll 4
+            for (int k = 0; k < kQLoads; ++k) {
+                const int row = k * kQRows + lane / kQLanes, c = lane % kQLanes;
+                const uint4 x = *q_slot(quarter * 32 + row, c);
+                uint4 *to = dst(row);
+                if (to) to[c] = x;
+            }
+            __syncwarp();
+        };
         const Item *w = item(0, ok);
         ok = __all_sync(0xffffffffu, ok);
         Row cur{}, nxt{};
         if (ok && w) {
             cur = row_of(w);
-            if (cur.any) bring_q(cur, w);
+            if (cur.any) {
+                uint4 q[kQLoads];
+                load_q(cur, q);
+                store_q(cur, w, q);
+            }
         }
         for (int i = 0; ok && w; ++i) {
             const Lane me = w->lane[L], other = w->lane[1 - L];
@@ -827,15 +846,15 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             // the description is read
             __syncwarp();
             if (lane == 0) mbar_arrive(&i_empty[i % kItems]);
-            // The next item's Q goes to shared memory beside this one's last P V (its last
-            // S is complete), so that S of the next follows at once.
+            // The next item's Q is fetched beside this one's last P V.
             w = item(i + 1, ok);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             nxt.any = false;
+            uint4 q[kQLoads];
             if (w) {
                 nxt = row_of(w);
-                if (nxt.any) bring_q(nxt, w);
+                if (nxt.any) load_q(nxt, q);
             }
             if (begun) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&o_final[L], (uint32_t)(ic & 1), s_abort,
@@ -845,15 +864,13 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                 ++ic;
             }
             const float mm = m - E::kShift;
-            const long long prow =
-                (long long)part_slot(cta, x0 == 0) * kManyRows + L * 128 + rr;
+            const long long prow0 =
+                (long long)part_slot(cta, x0 == 0) * kManyRows + L * 128 + quarter * 32;
+            const long long prow = prow0 + lane;
             const float inv = l > 0.f ? 1.f / l : 0.f;
-            typename E::T *op = static_cast<typename E::T *>(A.io.out) + cur.tok * A.io.out_stride +
-                                (long long)cur.head * D;
-            float *pp = A.part_o + prow * D;
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-                float o[32];
+            // O goes out by way of the rows' Q in shared memory (its last S is complete), so that a
+            // warp writes whole rows: a row a thread touched 32 lines with every store (STORE).
+            auto read_o = [&](int c, float (&o)[32]) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) o[i] = 0.f;
                 if (begun) {
@@ -861,20 +878,44 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                     tmem_ld_wait();
                     reg_fence(o);
                 }
-                if (!cur.valid) continue;
-                if (whole) {
+            };
+            if (whole) {
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    float o[32];
+                    read_o(c, o);
 #pragma unroll
                     for (int i = 0; i < 32; i += 8)
-                        *reinterpret_cast<uint4 *>(op + 32 * c + i) = make_uint4(
+                        *q_slot(rr, 4 * c + i / 8) = make_uint4(
                             E::pack(o[i] * inv, o[i + 1] * inv),
                             E::pack(o[i + 2] * inv, o[i + 3] * inv),
                             E::pack(o[i + 4] * inv, o[i + 5] * inv),
                             E::pack(o[i + 6] * inv, o[i + 7] * inv));
-                } else if (begun) {
+                }
+                typename E::T *op = static_cast<typename E::T *>(A.io.out) +
+                                    cur.tok * A.io.out_stride + (long long)cur.head * D;
+                flush([&](int row) {
+                    uint4 *to = reinterpret_cast<uint4 *>(__shfl_sync(
+                        0xffffffffu, reinterpret_cast<unsigned long long>(op), row));
+                    return __shfl_sync(0xffffffffu, (int)cur.valid, row) ? to : nullptr;
+                });
+            } else if (begun) {
+                // fp32: half the columns at a time
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll 1
+                    for (int c = 0; c < D / 64; ++c) {
+                        float o[32];
+                        read_o(h * (D / 64) + c, o);
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        *reinterpret_cast<float4 *>(pp + 32 * c + i) =
-                            make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                        for (int i = 0; i < 32; i += 4)
+                            *reinterpret_cast<float4 *>(q_slot(rr, 8 * c + i / 4)) =
+                                make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                    }
+                    flush([&](int row) {
+                        uint4 *to = reinterpret_cast<uint4 *>(A.part_o + (prow0 + row) * D + h * (D / 2));
+                        return __shfl_sync(0xffffffffu, (int)cur.valid, row) ? to : nullptr;
+                    });
                 }
             }
             if (begun) {
@@ -882,6 +923,7 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&o_empty[L]);
             }
+            if (nxt.any) store_q(nxt, w, q);
             if (cur.valid) {
                 if (whole) {
                     const float z = row_lse2(mm, l);
