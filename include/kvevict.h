@@ -535,7 +535,8 @@ kv_status kv_paged_attention_scored_workspace_size(const kv_paged *c, const kv_c
 
 /*
  * kv_paged_attention of scores that are changed as above; the other arguments, what is
- * rounded and how, errors and the status word are that call's.  With first or last, the
+ * rounded and how (two parts of a weight here for up to 4096 query rows a head, where that
+ * call has 512), errors and the status word are that call's.  With first or last, the
  * rows between the first and the last that any query of a request's chunk sees must
  * hold finite values, on pages that exist.  lse is of the changed scores.
  * add_mass: as there, for steps of at most 16 query rows a head in every request

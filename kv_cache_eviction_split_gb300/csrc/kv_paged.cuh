@@ -110,6 +110,10 @@ constexpr int kShortRows = 8192;
 //          16 requests 64 rows on 1024 keys 38 / 28 (512 items)
 constexpr int kShortFewRows = 512;
 constexpr int kShortVisits = 8192;
+// With changed scores (the many-rows kernel then takes longer to begin and a tile), in us, this /
+// the many-rows kernel, capped and with slopes, 1 KV head, 4 query heads, d = 64, 1 request:
+//   800 rows on 4096 keys 23 / 56   1200 on 401 14 / 21   1200 on 4096 41 / 40   2400 on 1024 16 / 26
+constexpr int kShortScoredRows = 4096;
 constexpr int kManyTile = 128;     // keys per tile of the tensor-memory kernel
 constexpr int kManyRows = 256;     // query rows per item there: two tiles of 128
 constexpr int kManyCtas = 152;

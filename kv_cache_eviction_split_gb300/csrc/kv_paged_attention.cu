@@ -103,7 +103,7 @@ struct Classes {
     int many;                  // the others
 };
 // seen: most rows of a unit that the step's queries see.
-Classes classify(const DevPaged &C, const DevChunk &T, long long seen, bool add_mass) {
+Classes classify(const DevPaged &C, const DevChunk &T, long long seen, bool add_mass, bool scored) {
     auto with = [&](int few_max) {
         Classes k{};
         k.few_max = few_max;
@@ -123,7 +123,7 @@ Classes classify(const DevPaged &C, const DevChunk &T, long long seen, bool add_
         return k;
     };
     if (seen <= kShortRows && !add_mass) {
-        const Classes k = with(kShortFewRows);
+        const Classes k = with(scored ? kShortScoredRows : kShortFewRows);
         if (k.items <= kFewCtas && k.items * ((seen + kFewTile - 1) / kFewTile) <= kShortVisits)
             return k;
     }
@@ -149,8 +149,9 @@ AttendWs attend_ws_layout(const DevPaged &C, const DevChunk &T, bool add_mass, v
         return p;
     };
     // whatever the window: a call without one needs most
-    const Classes k = classify(C, T, C.cap, add_mass);
-    // the two kernels run one after the other: they share the partials
+    const Classes k = classify(C, T, C.cap, add_mass, false);
+    // the two kernels run one after the other: they share the partials (scored calls take the
+    // many-rows kernel for no more steps than others, which they may turn out to be)
     const bool cut_few = k.few_requests && C.cap > kShortRows;
     const size_t slots = std::max<size_t>(cut_few ? 2 * kFewCtas * (size_t)kFewRows : 0,
                                           k.many ? 2 * (size_t)many_phases(C) * kManyCtas * kManyRows : 0);
@@ -211,7 +212,7 @@ cudaError_t attend(const DevPaged &C, const DevChunk &T0, int layer, const Atten
                    const ScoreForm *form, const AttendIo &io, bool add_mass, const AttendWs &ws,
                    cudaStream_t s) {
     const long long seen = rows_seen(C, T0, M);
-    const Classes k = classify(C, T0, seen, add_mass);
+    const Classes k = classify(C, T0, seen, add_mass, form != nullptr);
     DevChunk T = T0;
     T.few_max = k.few_max;
     cudaError_t e = cudaSuccess;
