@@ -252,13 +252,13 @@ __device__ __forceinline__ float absmax(const float (&v)[N]) {
     return a[0];
 }
 // How a warp takes tanh of logits of up to `most` in its rows: 0 and 1 by ScoreForm's polynomials, 2
-// exactly.  The exact form's two approximate operations a logit (2^x and a reciprocal) come on
+// exactly, 3 so with the series for small ones.  The exact form's two approximate operations a logit (2^x and a reciprocal) come on
 // top of the softmax's own, which fill the unit for them by themselves (4.2 clocks a warp's
 // instruction); the polynomials take 5 and 6 products for two logits (2.1 clocks each) on the
 // units for those.
 __device__ __forceinline__ int cap_tier(const ScoreForm &F, float most) {
     if (!__any_sync(0xffffffffu, most > F.most4)) return 0;
-    return __any_sync(0xffffffffu, most > F.most5) ? 2 : 1;
+    return __any_sync(0xffffffffu, most > F.most5) ? 2 + F.series : 1;
 }
 
 // kForm: what is changed of the scores, at compile time (with all of it behind branches the code is
@@ -703,6 +703,9 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
 #pragma unroll
                                     for (int i = 0; i < kW; i += 2 * kPolyPairs)
                                         cap_poly<kPolyPairs>(co, make_float2(0.f, 0.f), &v[i]);
+                                } else if (!A.form.series) {
+#pragma unroll
+                                    for (int i = 0; i < kW; ++i) v[i] = cap_logit<false>(A.form, v[i]);
                                 } else {
 #pragma unroll
                                     for (int i = 0; i < kW; ++i) v[i] = cap_logit(A.form, v[i]);
@@ -765,7 +768,7 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                     raise(top * zs);
                     const float nm = m == -INFINITY ? 0.f : E::kShift - m;
                     const float2 zs2 = make_float2(zs, zs), nm2 = make_float2(nm, nm);
-                    // how: 0 as they are (times zs), 1 and 2 by the polynomials, 3 exactly
+                    // how: 0 as they are (times zs), 1 and 2 by the polynomials, 3 and 4 exactly
                     auto weights = [&](auto how) {
                         float2 co[how.value == 2 ? 5 : 4];
                         if (how.value == 1 || how.value == 2)
@@ -789,9 +792,12 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                                     for (int j = i; j < i + 2 * kPolyPairs; j += 2) {
                                         float2 e = make_float2(v[j], v[j + 1]);
                                         if (how.value == 0) e = __ffma2_rn(e, zs2, nm2);
-                                        if (how.value == 3)
-                                            e = __fadd2_rn(make_float2(cap_logit(A.form, e.x),
-                                                                       cap_logit(A.form, e.y)), nm2);
+                                        if (how.value >= 3) {
+                                            constexpr bool kSeries = how.value == 4;
+                                            e = __fadd2_rn(make_float2(cap_logit<kSeries>(A.form, e.x),
+                                                                       cap_logit<kSeries>(A.form, e.y)),
+                                                           nm2);
+                                        }
                                         float2 p = make_float2(ex2_approx(e.x), ex2_approx(e.y));
                                         if (mixed.value) {
                                             if (!(h.see[j >> 5] >> (j & 31) & 1u)) p.x = 0.f;
@@ -827,7 +833,8 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                     if (!kCap || kSlope) weights(integral_constant<int, 0>{});
                     else if (tier == 0) weights(integral_constant<int, 1>{});
                     else if (tier == 1) weights(integral_constant<int, 2>{});
-                    else weights(integral_constant<int, 3>{});
+                    else if (tier == 2) weights(integral_constant<int, 3>{});
+                    else weights(integral_constant<int, 4>{});
                 }
                 const float2 a = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
                 l += a.x + a.y;

@@ -3,8 +3,10 @@
 //
 // Of a product s = q.k and softmax scale c, in units of log2:
 //   z = c s, or cap tanh(c s / cap);  z - slope_h |p_q - p_j|
-// tanh(x) = 1 - 2 / (1 + e^2x): two approximate operations, off by a few 2^-23 of cap, which is
-// what counts in an exponent.
+// tanh(x) = 1 - 2 / (1 + e^2x): two approximate operations, off by a few 2^-23 of 1.  For |x| < 1/4,
+// where that is more and more of tanh(x), its series, so that a capped logit is off by a few 2^-21 of
+// itself however large the cap.  (The many-rows kernel goes without it up to a cap of 4096 c, where it
+// would cost a fifth to a half: ScoreForm::series.)
 #pragma once
 #include "kv_paged_attend.cuh"
 
@@ -26,6 +28,8 @@ constexpr int kNoLo = 0x3fffffff;          // lo of a query that sees nothing
 struct ScoreForm {
     float cap2;                // cap log2(e), 0: none
     float cap_u;               // 2 c log2(e) / cap: s to the exponent of e^2x, x = c s / cap
+    float cap_x;               // c / cap: s to x
+    float cap_z;               // c log2(e): s to what it is without a cap
     float slope_s;             // 1 / c: a slope in units of s
     int two_way;               // whether a query may see keys behind it
     const float *slopes;       // [Hq], or null
@@ -38,6 +42,7 @@ struct ScoreForm {
     // least, 1.6e-7 and 2.5e-7 in fp32 (the exact form's 1 has steps of 1.2e-7).  Below 0: never
     // (powers of cap_x that fp32 has not).
     float most4, most5;
+    int series;                // cap beyond 4096 c: the exact form's error, 2^-21 of it, is too much
     float2 co4[4], co5[5];
 
     void set_cap(float cap, float scale) {
@@ -48,9 +53,12 @@ struct ScoreForm {
         const double x = (double)scale / cap, most = (double)cap * kLog2e;
         cap2 = (float)most;
         cap_u = (float)(2.0 * x * kLog2e);
+        cap_x = (float)x;
+        cap_z = (float)((double)scale * kLog2e);
         const bool fits = x >= 1.0 / 4096 && x <= 4096;
         most4 = fits ? (float)(0.5 / x) : -1.0f;
         most5 = fits ? (float)(0.75 / x) : -1.0f;
+        series = x < 1.0 / 4096;
         double power = x * most;
         for (int i = 0; i < 5; ++i, power *= x * x) {
             if (i < 4) co4[i] = make_float2((float)(k4[i] * power), (float)(k4[i] * power));
@@ -59,12 +67,20 @@ struct ScoreForm {
     }
 };
 
-// Capped, in units of log2.
+// Capped, in units of log2.  The series up to x^9: what it leaves out is 9e-9 of tanh(1/4).
+template <bool kSeries = true>
 __device__ __forceinline__ float cap_logit(const ScoreForm &F, float s) {
     const float e = sm100::ex2_approx(fminf(s * F.cap_u, 64.f));
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-    return fmaf(-2.f * F.cap2, r, F.cap2);
+    const float z1 = fmaf(-2.f * F.cap2, r, F.cap2);
+    if (!kSeries) return z1;
+    const float x = s * F.cap_x, x2 = x * x;
+    float t = fmaf(x2, 62.f / 2835, -17.f / 315);
+    t = fmaf(x2, t, 2.f / 15);
+    t = fmaf(x2, t, -1.f / 3);
+    const float z = s * F.cap_z;
+    return fabsf(x) < 0.25f ? fmaf(z * x2, t, z) : z1;
 }
 
 // Rows that query i of a request's chunk sees of unit U.

@@ -28,7 +28,8 @@ def scored_unit(q, K, V, pos, scale, cap=0.0, slopes=None, first=None, last=None
     per row, sum p |v|, and per output the first order of what errors of the logits do to it and to lse.
 
     A logit is off by its d products (2^-23 of the sum of magnitudes each), its 2^x (2^-22 and 2^-22 of
-    itself); capped, by 2^-20 of cap (2^x and the reciprocal to 2^-22 and 2^-23, one fused product);
+    itself); capped, by 2^-20 of cap (2^x and the reciprocal to 2^-22 and 2^-23, one fused product), and with
+    caps beyond 4096 softmax scales by 2^-17 of itself at most (the series, or above a quarter of the cap the same);
     lowered, by 2^-22 of what is taken off (slope log2(e), the product, the difference)."""
     count, G, d = q.shape
     n = K.shape[0]
@@ -48,7 +49,8 @@ def scored_unit(q, K, V, pos, scale, cap=0.0, slopes=None, first=None, last=None
     err = d * 2.0 ** -23 * scale * torch.einsum("igd,jd->gij", q.abs(), K.abs())
     if cap:
         s = cap * torch.tanh(s / cap)
-        err = err + 2.0 ** -20 * cap
+        own = 2.0 ** -17 * s.abs() if cap > 4096 * scale else torch.full_like(s, math.inf)
+        err = err + own.clamp_max(2.0 ** -20 * cap)
     if slopes is not None:
         off = slopes.double()[:, None, None] * (here[:, None] - pos[None]).abs().double()
         s = s - off
