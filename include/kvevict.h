@@ -525,7 +525,8 @@ typedef struct kv_scoring {
     float softcap;             /* 0: none */
     int32_t window;            /* 0: none */
     int32_t num_sinks;
-    const float *slopes;       /* f32 [H_q], device, any finite values, or NULL */
+    const float *slopes;       /* f32 [H_q], device, or NULL; either sign, with slope * distance /
+                                  softmax_scale within float's range */
     const int32_t *row_pos;    /* or NULL */
     const int32_t *first, *last;   /* or NULL */
 } kv_scoring;
@@ -612,8 +613,8 @@ kv_status kv_rotary_frequencies(int32_t dims, double base, int32_t scaling, doub
 /*
  * Rows turned: token t's `heads` rows of head_dim (64 or 128) elements of `dtype` by its
  * position positions[t] (int32, device).  Row (t, h) begins t * stride + h * head_stride
- * elements from x, and from out (16-byte aligned, strides multiples of 8; rows of out
- * must not overlap).  out may be x, with the same strides.  backward != 0 turns the
+ * elements from x, and from out (16-byte aligned, strides multiples of 8; in out a
+ * token's heads lie together, or a head's tokens: KV_ERR_INVALID_ARG otherwise).  out may be x, with the same strides.  backward != 0 turns the
  * other way, with the same factor: the gradient of x from that of out.
  * So [L][H][N][d] keys are N tokens of L*H heads, stride d, head_stride N*d.
  */

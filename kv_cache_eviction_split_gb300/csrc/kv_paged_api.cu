@@ -211,8 +211,12 @@ kv_status kv_paged_attention_scored(const kv_paged *c, const kv_chunk *t, int32_
     if (T.tokens == 0) return KV_OK;
     const long long row = (long long)C.Hq * C.d;
     if (bad_ptr(q) || bad_ptr(out) || !aligned16(lse) || bad_ptr(workspace) ||
-        !aligned16(f->row_pos) || bad_stride(q_stride, row) || bad_stride(out_stride, row))
+        !aligned16(f->row_pos) || bad_stride(q_stride, row) || bad_stride(out_stride, row) ||
+        ((reinterpret_cast<uintptr_t>(f->slopes) | reinterpret_cast<uintptr_t>(f->first) |
+          reinterpret_cast<uintptr_t>(f->last)) & 3))
         return KV_ERR_INVALID_ARG;
+    // slopes are taken in units of q.k
+    if (f->slopes && !std::isfinite(1.0f / softmax_scale)) return KV_ERR_INVALID_ARG;
     const AttendWs ws = attend_ws_layout(C, T, add_mass != 0, workspace, true);
     if (workspace_bytes < ws.total) return KV_ERR_WORKSPACE;
     // a window of the table's length or more hides nothing
@@ -309,8 +313,11 @@ kv_status kv_rotary(const kv_rotation *rot, const int32_t *positions, int64_t to
     if (!positions || bad_ptr(x) || bad_ptr(out)) return KV_ERR_INVALID_ARG;
     for (long long s : {x_stride, x_head_stride, out_stride, out_head_stride})
         if (s < 0 || s % 8 != 0) return KV_ERR_INVALID_ARG;
-    // rows that lie on one another cannot be written
+    // rows that lie on one another cannot be written: a token's heads together, or a head's tokens
     if ((tokens > 1 && out_stride < head_dim) || (heads > 1 && out_head_stride < head_dim))
+        return KV_ERR_INVALID_ARG;
+    if (tokens > 1 && heads > 1 && (out_stride - head_dim) / (heads - 1) < out_head_stride &&
+        (out_head_stride - head_dim) / (tokens - 1) < out_stride)
         return KV_ERR_INVALID_ARG;
     if (x == out && (x_stride != out_stride || x_head_stride != out_head_stride))
         return KV_ERR_INVALID_ARG;

@@ -8,6 +8,9 @@
 // itself however large the cap.  (The many-rows kernel goes without it up to a cap of 4096 c, where it
 // would cost a fifth to a half: ScoreForm::series.)
 #pragma once
+#include <algorithm>
+#include <cfloat>
+
 #include "kv_paged_attend.cuh"
 
 namespace kvevict {
@@ -52,8 +55,9 @@ struct ScoreForm {
                                   -0.04928047955036163, 0.012318850494921207};
         const double x = (double)scale / cap, most = (double)cap * kLog2e;
         cap2 = (float)most;
-        cap_u = (float)(2.0 * x * kLog2e);
-        cap_x = (float)x;
+        // finite, so that a logit of 0 stays 0 with the smallest caps
+        cap_u = (float)std::min(2.0 * x * kLog2e, (double)FLT_MAX);
+        cap_x = (float)std::min(x, (double)FLT_MAX);
         cap_z = (float)((double)scale * kLog2e);
         const bool fits = x >= 1.0 / 4096 && x <= 4096;
         most4 = fits ? (float)(0.5 / x) : -1.0f;

@@ -386,7 +386,9 @@ compact_plan_kernel(const DevPaged C, int32_t *refs, int32_t *row_pos, int32_t *
     }
     if (kCtas == 1 && whole) {
         __syncthreads();
-        move_pages(C, refs, row_pos, ws, ws.plan->count, live, threadIdx.x >> 5, kPlanThreads / 32);
+        const int count = ws.plan->count;
+        if (count)
+            move_pages(C, refs, row_pos, ws, count, live, threadIdx.x >> 5, kPlanThreads / 32);
     }
     leave_cluster<kCtas>();
 }

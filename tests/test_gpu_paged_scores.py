@@ -145,7 +145,7 @@ def test_caps_from_almost_flat_to_almost_none(cuda_lib, kind):
     made = paged.Made(cuda_lib, _spread(len(counts), 1, 2, 300, hi), 8, 128, 64, seed=9, scale=4.0,
                       max_rows=LONG_TABLE if kind == "many" else None)
     q, out = _chunk_inputs(made, counts, 8, False, 9)
-    for cap in (1e-3, 0.5, 20.0, 300.0, 1e4, 1e30):
+    for cap in (1e-43, 1e-3, 0.5, 20.0, 300.0, 1e4, 1e30):
         lse, status = scores.run(cuda_lib, made, counts, q, out, cap=cap, scale=0.25)
         assert status == 0
         scores.check(cuda_lib, made, None, counts, q, out, lse, cap=cap, scale=0.25)

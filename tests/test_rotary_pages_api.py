@@ -47,6 +47,10 @@ def test_rotary_argument_checks(kv):
     inplace[9] = F
     inplace[7] = 1024
     assert lib.kv_rotary(*inplace) == INV                       # other strides than the input's
+    # rows of out on one another: 4 heads 128 apart with tokens 128 .. 504 apart, 10 tokens 512 apart
+    # with heads less than 10 * 512 - 384 apart
+    for strides in ((128, 128), (384, 128), (504, 128), (512, 256), (512, 4728), (1 << 62, 1 << 62)):
+        _each(lib.kv_rotary, [*good[:10], *strides, *good[12:]], [(2, 10, INV)])
     none = list(good)
     none[2] = 0
     assert lib.kv_rotary(*none) == kv.KV_OK
@@ -99,6 +103,64 @@ def test_page_keeping_argument_checks(kv):
     assert lib.kv_paged_reserve(c.c, big.c, F, None, F, 1 << 40, None) == kv.KV_ERR_BUDGET
     c._c.num_requests = 16385
     assert lib.kv_paged_fork(c.c, F, F, None) == kv.KV_ERR_UNSUPPORTED
+
+
+def test_scored_attention_argument_checks(kv):
+    lib, INV, UNS = kv.load(), kv.KV_ERR_INVALID_ARG, kv.KV_ERR_UNSUPPORTED
+    c, t = _cache(kv), kv.Chunk([1, 5], device="cpu")
+    assert not any([kv._KvScoring().softcap, kv._KvScoring().slopes])
+
+    def form(softcap=30.0, window=0, sinks=0, slopes=F, pos=None, first=None, last=None):
+        return ctypes.byref(kv._KvScoring(softcap, window, sinks, slopes, pos, first, last))
+
+    size = kv.kv_paged_attention_scored_workspace_size(c, t)
+    good = [c.c, t.c, 0, form(), 0.1, F, 1024, 2 * F, 1024, None, 0, 3 * F, size, None]
+    _each(lib.kv_paged_attention_scored, good, [
+        (0, None, INV), (1, None, INV), (2, -1, INV), (2, 3, INV), (3, None, INV), (3, form(-1.0), INV),
+        (3, form(math.nan), INV), (3, form(math.inf), INV), (3, form(window=-1), INV), (3, form(sinks=-1), INV),
+        (3, form(slopes=F + 2), INV), (3, form(first=F + 1), INV), (3, form(last=F + 2), INV),
+        (3, form(pos=F + 4), INV), (4, 0.0, INV), (4, -0.1, INV), (4, math.nan, INV), (4, math.inf, INV),
+        (4, 1e-40, INV), (5, None, INV), (5, F + 8, INV), (6, 1016, INV), (6, 1028, INV), (7, None, INV),
+        (7, 2 * F + 2, INV), (8, 512, INV), (9, F + 4, INV), (11, None, INV), (11, F + 8, INV),
+        (12, size - 1, kv.KV_ERR_WORKSPACE)])
+    few = kv.Chunk([4, 1], device="cpu")                        # 16 query rows a head: weights are added
+    assert kv.kv_paged_attention_scored_workspace_size(c, few, True) > 0
+    _each(lib.kv_paged_attention_scored, good, [(10, 1, UNS)])
+    with pytest.raises(kv.KvError) as e:
+        kv.kv_paged_attention_scored_workspace_size(c, t, True)
+    assert e.value.code == UNS
+    bare = kv.PagedCache.allocate(2, 3, 2, 8, 128, 100, 64, c.k_pages.dtype, False, device="cpu")
+    with pytest.raises(kv.KvError) as e:                        # no weights to add to
+        kv.kv_paged_attention_scored_workspace_size(bare, few, True)
+    assert e.value.code == INV
+    none = list(good)
+    none[1] = kv.Chunk([0, 0], device="cpu").c
+    none[5] = none[7] = none[11] = None
+    assert lib.kv_paged_attention_scored(*none) == kv.KV_OK
+    null = ctypes.POINTER(ctypes.c_size_t)()
+    assert lib.kv_paged_attention_scored_workspace_size(c.c, t.c, 0, null) == INV
+
+
+def test_scored_attention_binding_refusals(kv):
+    import torch
+    c, t = _cache(kv, positions=True), kv.Chunk([1, 5], device="cpu")
+    size = kv.kv_paged_attention_scored_workspace_size(c, t)
+    q = torch.zeros((6, 8, 128), dtype=torch.bfloat16)
+    good = dict(cache=c, chunk=t, layer=0, q=q, out=q.clone(), workspace=torch.zeros(size, dtype=torch.uint8))
+    i6 = torch.zeros(6, dtype=torch.int32)
+    for name, value in [
+            ("q", q[:5]), ("q", q.half()), ("out", q[:, :4]), ("lse", torch.zeros((6, 7))),
+            ("lse", torch.zeros((6, 8), dtype=torch.float64)), ("slopes", torch.zeros(7)),
+            ("slopes", torch.zeros(8, dtype=torch.bfloat16)), ("slopes", torch.zeros(16)[::2]),
+            ("first", i6[:5]), ("first", i6.long()), ("last", torch.zeros(12, dtype=torch.int32)[::2]),
+            ("last", i6.float()), ("layer", 1 << 32), ("layer", -(1 << 40)), ("window", 1 << 31),
+            ("num_sinks", -(1 << 33)), ("workspace", torch.zeros((size, 2), dtype=torch.uint8)[:, 0]),
+            ("chunk", kv.Chunk([1], device="cpu"))]:
+        with pytest.raises((ValueError, kv.KvError)) as e:
+            kv.kv_paged_attention_scored(**{**good, name: value})
+        assert "CUDA device" not in str(e.value), name
+    with pytest.raises(ValueError, match="CUDA device"):
+        kv.kv_paged_attention_scored(**good)
 
 
 def test_no_requests_is_a_no_op(kv):
