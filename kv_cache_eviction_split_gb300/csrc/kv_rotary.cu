@@ -12,6 +12,10 @@
 // one turn is an integer product, exact but for the 53 bits of the factor (an angle off by at most
 // p w_i 2^-52, 2^-21 at the last position); fp64 arithmetic per angle would cost as much as the
 // copy does.  Half turns in fp32 (24 bits) then go through sincospif.
+//
+// Measured (d = 128, bf16): 8192 tokens of 32 + 8 + 8 heads into the pages 34 us, 5.9 TB/s, 88% of
+// what a copy reaches; 2047 tokens of 28 heads (dims 64) 6.5 us, where a launch alone is 2.3; one
+// token each of 8 requests 3.5 us.  Three units in flight a thread: two take 35 us, four 34.4 (registers).
 #include "kv_paged_attend.cuh"
 #include "kv_rotary.cuh"
 
@@ -242,12 +246,14 @@ append_rotary_kernel(const DevPaged C, const DevChunk T, int layer, const DevRot
         });
 }
 
-// Tokens a block takes together: as many as give all its threads an angle, fewer where that
-// would leave SMs without a block.
+// Tokens a block takes together: as many as let two blocks an SM take the step at once (a block's
+// start, its frequencies and first loads, costs more than another token does: 1000 tokens of 40
+// heads 4.7 us so, 6.2 with a block a token), and in longer steps as many as give a block's
+// threads two angles each (8192 tokens of 40 heads 27.5 us, 28.0 with 8 a block, 28.3 with an angle each).
 int group_of(long long tokens, int dims) {
-    const long long g = tokens / kRotarySpread;
-    const int most = dims < 64 ? kMostTokens : 2 * kThreads / dims;
-    return (int)(g < 1 ? 1 : g > most ? most : g);
+    const long long g = (tokens + kRotarySpread - 1) / kRotarySpread;
+    if (g <= kMostTokens) return (int)g;
+    return dims < 64 ? kMostTokens : 2 * kThreads / dims;
 }
 unsigned grid_of(long long tokens, int group) {
     const long long n = (tokens + group - 1) / group;

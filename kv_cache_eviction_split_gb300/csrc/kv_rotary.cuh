@@ -28,7 +28,7 @@ struct AppendIo {
     long long k_stride, v_stride;
 };
 
-// Blocks that a step's tokens are spread over before a block takes more than one.
+// Blocks that a step's tokens are spread over before a block takes more than one: two an SM.
 constexpr long long kRotarySpread = 152 * 2;
 constexpr long long kRotaryCtas = 1 << 20;
 
