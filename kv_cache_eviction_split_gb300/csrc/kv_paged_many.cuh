@@ -36,7 +36,7 @@ struct Lane {
 };
 // With slopes an item's tiles are taken from the last one on: the nearest keys, whose scores are
 // lowered least, set the maximum, which the other order would raise (and the output with it) at every
-// tile of a steep head (RAISE).  Tile x of a run, as its item counts them:
+// tile of a steep head, 700 clocks each.  Tile x of a run, as its item counts them:
 template <bool kSlope>
 __device__ __forceinline__ int nth_tile(const TileSpan &span, int x) {
     return kSlope ? span.total - 1 - x : x;
@@ -227,7 +227,7 @@ __device__ __forceinline__ void cap_poly(const float2 (&c2)[N], float2 add, floa
 constexpr int kPolyPairs = 4;
 // The coefficients from shared memory into registers, once for a loop: from the constant bank the
 // compiler fetches them anew for every few logits, by moves on the unit that the products need
-// (MOVES).
+// (126 million of them in a chunk of 2048 tokens over 34816 rows, 31 million so).
 template <int N>
 __device__ __forceinline__ void load_coefficients(const uint8_t *from, float2 (&c2)[N]) {
 #pragma unroll
@@ -252,17 +252,17 @@ __device__ __forceinline__ float absmax(const float (&v)[N]) {
     return a[0];
 }
 // How a warp takes tanh of logits of up to `most` in its rows: 0 and 1 by ScoreForm's polynomials, 2
-// exactly, 3 so with the series for small ones.  The exact form's two approximate operations a logit (2^x and a reciprocal) come on
+// exactly.  The exact form's two approximate operations a logit (2^x and a reciprocal) come on
 // top of the softmax's own, which fill the unit for them by themselves (4.2 clocks a warp's
 // instruction); the polynomials take 5 and 6 products for two logits (2.1 clocks each) on the
 // units for those.
 __device__ __forceinline__ int cap_tier(const ScoreForm &F, float most) {
     if (!__any_sync(0xffffffffu, most > F.most4)) return 0;
-    return __any_sync(0xffffffffu, most > F.most5) ? 2 + F.series : 1;
+    return __any_sync(0xffffffffu, most > F.most5) ? 2 : 1;
 }
 
 // kForm: what is changed of the scores, at compile time (with all of it behind branches the code is
-// twice as large, and the row warps wait for instructions: PROMPT).
+// twice as large, and the row warps wait for instructions: a packed prompt of 8192 tokens, capped, 315 us, 249 apart).
 constexpr int kPlain = 0, kBounds = 1, kCapped = 2, kSloped = 4;   // kBounds: rows of their own
 
 template <typename E, int D, int kForm>
@@ -427,8 +427,9 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             r.any = y0 < min(ns, y1) || max(y0, w->lane[L].a) < min(y1, w->lane[L].b);
             return r;
         };
-        // Q rows of an item, fetched, and put into shared memory for the products.  A warp brings its 32 rows together, kQRows rows to a load: a load a row
-        // and thread would touch 32 lines for 512 bytes (8 items of 8 tiles a CTA: QSTORE).
+        // Q rows of an item, fetched, and put into shared memory for the products.  A warp brings its
+        // 32 rows together, kQRows rows to a load: a load a row and thread would touch 32 lines for
+        // 512 bytes (7 to 10 thousand clocks an item, 3 to 5 so).
         constexpr int kQLanes = D / 8, kQRows = 32 / kQLanes, kQLoads = 32 / kQRows;
         auto load_q = [&](const Row &r, uint4 (&q)[kQLoads]) {
             const uint4 *mine = reinterpret_cast<const uint4 *>(
@@ -703,12 +704,9 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
 #pragma unroll
                                     for (int i = 0; i < kW; i += 2 * kPolyPairs)
                                         cap_poly<kPolyPairs>(co, make_float2(0.f, 0.f), &v[i]);
-                                } else if (!A.form.series) {
-#pragma unroll
-                                    for (int i = 0; i < kW; ++i) v[i] = cap_logit<false>(A.form, v[i]);
                                 } else {
 #pragma unroll
-                                    for (int i = 0; i < kW; ++i) v[i] = cap_logit(A.form, v[i]);
+                                    for (int i = 0; i < kW; ++i) v[i] = cap_logit<false>(A.form, v[i]);
                                 }
                             }
                         }
@@ -763,12 +761,13 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                     } else if (kCap) {
                         // without slopes tanh goes with the exponentials: it rises
                         tier = cap_tier(A.form, most);
-                        if (top != -INFINITY) top = cap_logit(A.form, top);
+                        if (top != -INFINITY)
+                            top = tier < 2 ? cap_poly1(A.form, top) : cap_logit<false>(A.form, top);
                     }
                     raise(top * zs);
                     const float nm = m == -INFINITY ? 0.f : E::kShift - m;
                     const float2 zs2 = make_float2(zs, zs), nm2 = make_float2(nm, nm);
-                    // how: 0 as they are (times zs), 1 and 2 by the polynomials, 3 and 4 exactly
+                    // how: 0 as they are (times zs), 1 and 2 by the polynomials, 3 exactly
                     auto weights = [&](auto how) {
                         float2 co[how.value == 2 ? 5 : 4];
                         if (how.value == 1 || how.value == 2)
@@ -792,12 +791,10 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                                     for (int j = i; j < i + 2 * kPolyPairs; j += 2) {
                                         float2 e = make_float2(v[j], v[j + 1]);
                                         if (how.value == 0) e = __ffma2_rn(e, zs2, nm2);
-                                        if (how.value >= 3) {
-                                            constexpr bool kSeries = how.value == 4;
-                                            e = __fadd2_rn(make_float2(cap_logit<kSeries>(A.form, e.x),
-                                                                       cap_logit<kSeries>(A.form, e.y)),
+                                        if (how.value == 3)
+                                            e = __fadd2_rn(make_float2(cap_logit<false>(A.form, e.x),
+                                                                       cap_logit<false>(A.form, e.y)),
                                                            nm2);
-                                        }
                                         float2 p = make_float2(ex2_approx(e.x), ex2_approx(e.y));
                                         if (mixed.value) {
                                             if (!(h.see[j >> 5] >> (j & 31) & 1u)) p.x = 0.f;
@@ -833,8 +830,7 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                     if (!kCap || kSlope) weights(integral_constant<int, 0>{});
                     else if (tier == 0) weights(integral_constant<int, 1>{});
                     else if (tier == 1) weights(integral_constant<int, 2>{});
-                    else if (tier == 2) weights(integral_constant<int, 3>{});
-                    else weights(integral_constant<int, 4>{});
+                    else weights(integral_constant<int, 3>{});
                 }
                 const float2 a = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
                 l += a.x + a.y;
@@ -876,7 +872,8 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             const long long prow = prow0 + lane;
             const float inv = l > 0.f ? 1.f / l : 0.f;
             // O goes out by way of the rows' Q in shared memory (its last S is complete), so that a
-            // warp writes whole rows: a row a thread touched 32 lines with every store (STORE).
+            // warp writes whole rows: a row a thread touched 32 lines with every store (a packed prompt
+            // of 8192 tokens: 181 us masked and 203 with slopes, 175 and 194 so).
             auto read_o = [&](int c, float (&o)[32]) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) o[i] = 0.f;

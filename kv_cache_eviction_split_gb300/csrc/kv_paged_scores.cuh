@@ -5,11 +5,12 @@
 //   z = c s, or cap tanh(c s / cap);  z - slope_h |p_q - p_j|
 // tanh(x) = 1 - 2 / (1 + e^2x): two approximate operations, off by a few 2^-23 of 1.  For |x| < 1/4,
 // where that is more and more of tanh(x), its series, so that a capped logit is off by a few 2^-21 of
-// itself however large the cap.  (The many-rows kernel goes without it up to a cap of 4096 c, where it
-// would cost a fifth to a half: ScoreForm::series.)
+// itself however large the cap.  (The many-rows kernel takes small ones by polynomials, and goes
+// without the series in the exact form, which it would slow by a fifth to a half.)
 #pragma once
 #include <algorithm>
 #include <cfloat>
+#include <cmath>
 
 #include "kv_paged_attend.cuh"
 
@@ -42,10 +43,8 @@ struct ScoreForm {
     int unit_blocks;
     // cap2 tanh(x) = s (c0 + c1 s^2 + ...) with x = cap_x s, for two logits at a time, where |s| is at
     // most most4 (|x| <= 1/2) and most5 (|x| <= 3/4): fitted in x with the largest error of tanh
-    // least, 1.6e-7 and 2.5e-7 in fp32 (the exact form's 1 has steps of 1.2e-7).  Below 0: never
-    // (powers of cap_x that fp32 has not).
+    // least, 1.6e-7 and 2.5e-7 in fp32 (the exact form's 1 has steps of 1.2e-7).  Below 0: never.
     float most4, most5;
-    int series;                // cap beyond 4096 c: the exact form's error, 2^-21 of it, is too much
     float2 co4[4], co5[5];
 
     void set_cap(float cap, float scale) {
@@ -59,11 +58,13 @@ struct ScoreForm {
         cap_u = (float)std::min(2.0 * x * kLog2e, (double)FLT_MAX);
         cap_x = (float)std::min(x, (double)FLT_MAX);
         cap_z = (float)((double)scale * kLog2e);
-        const bool fits = x >= 1.0 / 4096 && x <= 4096;
-        most4 = fits ? (float)(0.5 / x) : -1.0f;
-        most5 = fits ? (float)(0.75 / x) : -1.0f;
-        series = x < 1.0 / 4096;
+        // caps far above c: smaller x, where the terms that fp32 has not are of no account; and s^2
+        // stays finite
         double power = x * most;
+        auto has = [&](int i) { return power * std::pow(x, 2 * i) > 1e-35; };
+        const double part = has(2) ? 1.0 / 8 : has(1) ? 1.0 / 64 : 1.0 / 4096;
+        most4 = x <= 4096 ? (float)std::min((has(3) ? 0.5 : part) / x, 1e18) : -1.0f;
+        most5 = x <= 4096 ? (float)std::min((has(4) ? 0.75 : has(3) ? 0.25 : part) / x, 1e18) : -1.0f;
         for (int i = 0; i < 5; ++i, power *= x * x) {
             if (i < 4) co4[i] = make_float2((float)(k4[i] * power), (float)(k4[i] * power));
             co5[i] = make_float2((float)(k5[i] * power), (float)(k5[i] * power));
@@ -85,6 +86,15 @@ __device__ __forceinline__ float cap_logit(const ScoreForm &F, float s) {
     t = fmaf(x2, t, -1.f / 3);
     const float z = s * F.cap_z;
     return fabsf(x) < 0.25f ? fmaf(z * x2, t, z) : z1;
+}
+
+// The same of one logit of at most most5 by the polynomial: a shorter chain of operations.
+__device__ __forceinline__ float cap_poly1(const ScoreForm &F, float s) {
+    const float s2 = s * s;
+    float t = F.co5[4].x;
+#pragma unroll
+    for (int i = 3; i >= 0; --i) t = fmaf(t, s2, F.co5[i].x);
+    return t * s;
 }
 
 // Rows that query i of a request's chunk sees of unit U.
