@@ -640,7 +640,8 @@ kv_status kv_paged_append_rotary(const kv_paged *c, const kv_chunk *t, int32_t l
  * Positions of a cache's rows, dst_pos i32 [num_pages][page_size] of dst: row i of unit u gets
  *   p = index[u * stride + i], or index[offsets[u] + i] with offsets (i64 [R*L*H + 1],
  *   device), or i without an index; with src_pos, the position of row p of the same unit
- *   of src instead.
+ *   of src instead.  A unit of more rows than its list has (stride, or the offsets' difference)
+ *   gets those of the list, and KV_ERR_INVALID_ARG is posted.
  * After kv_paged_load: the kept indices (sel_idx) and offsets.  After kv_paged_evict: kept,
  * kept_stride, src and its positions.
  */

@@ -497,6 +497,12 @@ place_positions_kernel(const DevPaged D, int32_t *dst_pos, const DevPaged S, con
         int n;
         bool bad = !unit_len(D, u, n);
         const int32_t *list = index ? index + (offsets ? offsets[u] : u * stride) : nullptr;
+        const long long listed = !index ? n : offsets ? offsets[u + 1] - offsets[u] : stride;
+        if (n > listed) {
+            // more rows than the unit's list names
+            bad = true;
+            n = (int)max(0ll, listed);
+        }
         for (int i = lane; i < n; i += 32) {
             int p = list ? list[i] : i;
             if (src_pos) {

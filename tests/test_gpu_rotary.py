@@ -298,3 +298,19 @@ def test_positions_follow_loads_and_evictions(cuda_lib):
     out[0, 0] = 1 << 20
     kv.kv_paged_place_positions(small, out, source=c)
     assert kv.kv_check_status(small.status) == kv.KV_ERR_INVALID_ARG
+
+
+def test_positions_of_units_with_more_rows_than_their_lists(cuda_lib):
+    """Only what the lists name is read and written."""
+    import torch
+    kv = cuda_lib
+    for offsets in (None, torch.tensor([0, 3, 6], device="cuda")):
+        c = kv.PagedCache.allocate(1, 1, 2, 2, 64, 20, 16, positions=True)
+        c.lens.copy_(torch.tensor([2, 9], dtype=torch.int32).view(1, 1, 2))
+        c.positions.fill_(-7)
+        index = torch.arange(10, 16, dtype=torch.int32, device="cuda")
+        kv.kv_paged_place_positions(c, index.view(2, 3) if offsets is None else index, offsets)
+        assert kv.kv_check_status(c.status) == kv.KV_ERR_INVALID_ARG
+        flat = c.positions.view(2, -1)
+        assert flat[0, :2].tolist() == [10, 11] and flat[1, :3].tolist() == [13, 14, 15]
+        assert (flat[0, 2:] == -7).all() and (flat[1, 3:] == -7).all()
