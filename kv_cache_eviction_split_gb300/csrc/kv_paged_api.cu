@@ -15,6 +15,8 @@ namespace {
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool bad_ptr(const void *p) { return !p || !aligned16(p); }
+// whether an entry begins at p (null: none does)
+inline bool aligned_to(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 kv_status map_cuda(cudaError_t e) { return e == cudaSuccess ? KV_OK : KV_ERR_CUDA; }
 
@@ -89,7 +91,9 @@ bool bad_stride(long long stride, long long least) { return stride < least || st
 kv_status make_rotary(const kv_rotation *r, int d, bool backward, DevRotary *A) {
     if (!r || r->dims < 0 || r->dims > d) return KV_ERR_INVALID_ARG;
     if (r->dims % 16 != 0) return KV_ERR_UNSUPPORTED;
-    if (!std::isfinite(r->factor) || (r->dims > 0 && !r->inv_freq)) return KV_ERR_INVALID_ARG;
+    if (!std::isfinite(r->factor) || (r->dims > 0 && !r->inv_freq) ||
+        !aligned_to(r->inv_freq, 4))
+        return KV_ERR_INVALID_ARG;
     *A = DevRotary{r->dims, r->interleaved != 0, backward, r->factor, r->inv_freq};
     return KV_OK;
 }
@@ -212,8 +216,7 @@ kv_status kv_paged_attention_scored(const kv_paged *c, const kv_chunk *t, int32_
     const long long row = (long long)C.Hq * C.d;
     if (bad_ptr(q) || bad_ptr(out) || !aligned16(lse) || bad_ptr(workspace) ||
         !aligned16(f->row_pos) || bad_stride(q_stride, row) || bad_stride(out_stride, row) ||
-        ((reinterpret_cast<uintptr_t>(f->slopes) | reinterpret_cast<uintptr_t>(f->first) |
-          reinterpret_cast<uintptr_t>(f->last)) & 3))
+        !aligned_to(f->slopes, 4) || !aligned_to(f->first, 4) || !aligned_to(f->last, 4))
         return KV_ERR_INVALID_ARG;
     // slopes are taken in units of q.k
     if (f->slopes && !std::isfinite(1.0f / softmax_scale)) return KV_ERR_INVALID_ARG;
@@ -310,7 +313,8 @@ kv_status kv_rotary(const kv_rotation *rot, const int32_t *positions, int64_t to
     // a block's rows are counted in 32 bits
     if (heads >= (1 << 24) || tokens >= (1LL << 40)) return KV_ERR_UNSUPPORTED;
     if (tokens == 0) return KV_OK;
-    if (!positions || bad_ptr(x) || bad_ptr(out)) return KV_ERR_INVALID_ARG;
+    if (!positions || !aligned_to(positions, 4) || bad_ptr(x) || bad_ptr(out))
+        return KV_ERR_INVALID_ARG;
     for (long long s : {x_stride, x_head_stride, out_stride, out_head_stride})
         if (s < 0 || s % 8 != 0) return KV_ERR_INVALID_ARG;
     // rows that lie on one another cannot be written: a token's heads together, or a head's tokens
@@ -344,8 +348,8 @@ kv_status kv_paged_append_rotary(const kv_paged *c, const kv_chunk *t, int32_t l
     if (C.Hq + 2LL * C.H >= (1 << 24)) return KV_ERR_UNSUPPORTED;
     if (T.tokens == 0) return KV_OK;
     const long long row = (long long)C.H * C.d, q_row = (long long)C.Hq * C.d;
-    if (!positions || bad_ptr(k_new) || bad_ptr(v_new) || bad_stride(k_stride, row) ||
-        bad_stride(v_stride, row))
+    if (!positions || !aligned_to(positions, 4) || !aligned16(row_pos) || bad_ptr(k_new) ||
+        bad_ptr(v_new) || bad_stride(k_stride, row) || bad_stride(v_stride, row))
         return KV_ERR_INVALID_ARG;
     if (q && (bad_ptr(q) || bad_ptr(q_out) || bad_stride(q_stride, q_row) ||
               bad_stride(q_out_stride, q_row) || (q == q_out && q_stride != q_out_stride)))
@@ -405,7 +409,7 @@ kv_status kv_paged_fork(const kv_paged *c, int32_t *refs, const int32_t *parents
     if (st != KV_OK) return st;
     if (C.R > kForkRequests) return KV_ERR_UNSUPPORTED;
     if (C.units == 0) return KV_OK;
-    if (bad_refs(C, refs) || !parents) return KV_ERR_INVALID_ARG;
+    if (bad_refs(C, refs) || !parents || !aligned_to(parents, 4)) return KV_ERR_INVALID_ARG;
     return map_cuda(launch_fork(C, refs, parents, (cudaStream_t)stream));
 }
 
@@ -425,7 +429,8 @@ kv_status kv_paged_compact(const kv_paged *c, int32_t *refs, int32_t *row_pos, i
     const kv_status st = make_paged(c, &C);
     if (st != KV_OK) return st;
     if (C.units == 0) return KV_OK;
-    if (bad_refs(C, refs) || !aligned16(row_pos) || bad_ptr(workspace)) return KV_ERR_INVALID_ARG;
+    if (bad_refs(C, refs) || !aligned16(row_pos) || !aligned_to(live, 4) || bad_ptr(workspace))
+        return KV_ERR_INVALID_ARG;
     const PagesWs ws = compact_ws_layout(C, workspace);
     if (workspace_bytes < ws.total) return KV_ERR_WORKSPACE;
     return map_cuda(launch_compact_pages(C, refs, row_pos, live, ws, (cudaStream_t)stream));
@@ -443,7 +448,8 @@ kv_status kv_paged_place_positions(const kv_paged *dst, int32_t *dst_pos, const 
     if (src_pos && (S.R != D.R || S.L != D.L || S.H != D.H || src_pos == dst_pos))
         return KV_ERR_INVALID_ARG;
     if (D.units == 0) return KV_OK;
-    if (!dst_pos || stride < 0 || (src_pos && !index) || (offsets && !index))
+    if (bad_ptr(dst_pos) || stride < 0 || (src_pos && !index) || (offsets && !index) ||
+        !aligned16(src_pos) || !aligned_to(index, 4) || !aligned_to(offsets, 8))
         return KV_ERR_INVALID_ARG;
     return map_cuda(launch_place_positions(D, dst_pos, S, src_pos, index, stride, offsets,
                                            (cudaStream_t)stream));

@@ -341,6 +341,38 @@ def test_bad_lengths_and_pages_are_reported(cuda_lib, counts, max_rows):
         assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
 
 
+def test_two_steps_at_once(cuda_lib):
+    """Two streams' calls on one cache, each with a workspace of its own, give the bits of one after the other."""
+    import torch
+    from tests import paged, scores
+    from tests.test_gpu_paged_attention import _chunk_inputs, _spread
+    kv = cuda_lib
+    for counts, hi in (([1, 1], 900), ([1, 1], 9000), ([200, 300], 900), ([200, 300], 9000)):
+        made = paged.Made(kv, _spread(2, 2, 4, 300, hi), 16, 128, 64, seed=3)
+        scores.positions_of(made, 3, 3)
+        c, chunk = made.cache, kv.Chunk(counts)
+        q, out = _chunk_inputs(made, counts, 16, False, 3)
+        slopes = 0.1 * torch.rand(16, device="cuda")
+        first = torch.full((sum(counts),), 20, dtype=torch.int32, device="cuda")
+        size = kv.kv_paged_attention_scored_workspace_size(c, chunk)
+
+        def calls(streams):
+            outs = [out.clone() for _ in streams]
+            ws = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in streams]
+            torch.cuda.synchronize()
+            for _ in range(5):
+                for layer, s in enumerate(streams):
+                    kv.kv_paged_attention_scored(c, chunk, layer, q, outs[layer], ws[layer], softcap=20.0,
+                                                 slopes=slopes, first=first, stream=s)
+            torch.cuda.synchronize()
+            assert kv.kv_check_status(c.status) == 0
+            return outs
+
+        one = torch.cuda.Stream()
+        for a, b in zip(calls([one, one]), calls([torch.cuda.Stream(), torch.cuda.Stream()])):
+            assert torch.equal(a, b)
+
+
 def test_a_run_of_the_operators(cuda_lib):
     """A prompt read, two hypotheses that go on from it, tokens for each, one dropped, compaction, more
     tokens: every step's attention is that of rows turned and kept on the host."""

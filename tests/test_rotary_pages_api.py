@@ -39,8 +39,9 @@ def test_rotary_argument_checks(kv):
     good = [rot(), F, 10, 4, 128, 0, F, 512, 128, 2 * F, 512, 128, 0, None]
     _each(lib.kv_rotary, good, [
         (0, None, INV), (0, rot(-16), INV), (0, rot(144), INV), (0, rot(24), UNS), (0, rot(freq=None), INV),
-        (0, rot(factor=math.inf), INV), (0, rot(factor=math.nan), INV), (1, None, INV), (2, -1, INV),
-        (2, 1 << 40, UNS), (3, 0, INV), (3, 1 << 24, UNS), (4, 96, UNS), (5, 2, INV), (6, None, INV),
+        (0, rot(factor=math.inf), INV), (0, rot(factor=math.nan), INV), (0, rot(freq=F + 2), INV),
+        (1, None, INV), (1, F + 2, INV),
+        (2, -1, INV), (2, 1 << 40, UNS), (3, 0, INV), (3, 1 << 24, UNS), (4, 96, UNS), (5, 2, INV), (6, None, INV),
         (6, F + 8, INV), (7, -8, INV), (7, 12, INV), (8, 4, INV), (9, None, INV), (9, F + 2, INV),
         (10, 120, INV), (11, 64, INV)])
     inplace = list(good)
@@ -63,7 +64,8 @@ def test_append_rotary_argument_checks(kv):
     good = [c.c, t.c, 0, ctypes.byref(rot), F, None, F, 1024, 2 * F, 1024, F, 256, F, 256, None]
     _each(lib.kv_paged_append_rotary, good, [
         (0, None, INV), (1, None, INV), (2, 3, INV), (2, -1, INV), (3, None, INV), (4, None, INV),
-        (6, F + 4, INV), (7, 1016, INV), (7, 1028, INV), (8, None, INV), (8, F + 8, INV), (9, 1000, INV),
+        (4, F + 1, INV), (5, F + 4, INV), (6, F + 4, INV), (7, 1016, INV),
+        (7, 1028, INV), (8, None, INV), (8, F + 8, INV), (9, 1000, INV),
         (10, None, INV), (11, 248, INV), (12, F + 2, INV), (13, 260, INV)])
     rot.dims = 144
     assert lib.kv_paged_append_rotary(*good) == INV
@@ -86,14 +88,15 @@ def test_page_keeping_argument_checks(kv):
            (4, F + 8, INV), (5, ws - 1, kv.KV_ERR_WORKSPACE)])
     ws = kv.kv_paged_compact_workspace_size(c)
     _each(lib.kv_paged_compact, [c.c, F, None, None, F, ws, None],
-          [(0, None, INV), (1, None, INV), (1, F + 4, INV), (2, F + 4, INV), (4, None, INV),
+          [(0, None, INV), (1, None, INV), (1, F + 4, INV), (2, F + 4, INV), (3, F + 2, INV), (4, None, INV),
            (5, ws - 1, kv.KV_ERR_WORKSPACE)])
-    _each(lib.kv_paged_fork, [c.c, F, F, None], [(0, None, INV), (1, None, INV), (1, F + 4, INV), (2, None, INV)])
+    _each(lib.kv_paged_fork, [c.c, F, F, None], [(0, None, INV), (1, None, INV), (1, F + 4, INV), (2, None, INV),
+                                                  (2, F + 2, INV)])
     _each(lib.kv_paged_count_refs, [c.c, F, None], [(0, None, INV), (1, None, INV), (1, F + 4, INV)])
     d = _cache(kv)
     _each(lib.kv_paged_place_positions, [c.c, F, d.c, 2 * F, F, 50, None, None],
           [(0, None, INV), (1, None, INV), (2, None, INV), (2, _cache(kv, H=4).c, INV), (3, F, INV), (4, None, INV),
-           (5, -1, INV)])
+           (5, -1, INV), (1, F + 4, INV), (3, 2 * F + 4, INV), (4, F + 2, INV), (6, F + 4, INV)])
     assert lib.kv_paged_place_positions(c.c, F, None, None, None, 0, F, None) == INV
     for name in ("kv_paged_reserve_workspace_size", "kv_paged_compact_workspace_size"):
         assert getattr(lib, name)(None, ctypes.byref(ctypes.c_size_t())) == INV
