@@ -184,16 +184,20 @@ __device__ __forceinline__ void copy_piece(const DevPaged &C, int32_t *row_pos, 
 // tables' entries were a chain of loads more in a kernel of 8 blocks: 14.3 us for 2048 units
 // and 59000 pages, 11.5 now, without the copies.)
 // ---------------------------------------------------------------------------
-// Warp w of `warps`: the units' pages entered and copied.
+// Warp w of `warps`: the units' pages entered and copied, `run` pieces of a page by a warp.
 __device__ __forceinline__ void enter_pages(const DevPaged &C, const DevChunk &T, int32_t *refs,
-                                            int32_t *row_pos, const PagesWs &ws, long long w,
-                                            long long warps) {
+                                            int32_t *row_pos, const PagesWs &ws, int run,
+                                            long long w, long long warps) {
     const int lane = threadIdx.x & 31, pieces = C.ps * C.d / 8 / kPieceVecs;     // at least one
-    const int per = C.L * C.H;
-    for (long long i = w; i < C.units * pieces; i += warps) {
-        const int u = (int)(i / pieces), piece = (int)(i - (long long)u * pieces);
+    const int per = C.L * C.H, runs = (pieces + run - 1) / run;
+    for (long long i = w; i < C.units * runs; i += warps) {
+        const int u = (int)(i / runs), piece = (int)(i - (long long)u * runs) * run;
         const UnitNeed need = ws.need[u];
-        if (need.from >= 0) copy_piece(C, row_pos, need.from, ws.list[need.at], piece);
+        if (need.from >= 0) {
+            const int to = ws.list[need.at];
+            for (int k = piece; k < min(pieces, piece + run); ++k)
+                copy_piece(C, row_pos, need.from, to, k);
+        }
         if (piece) continue;
         int32_t *tab = table_of(C, u) + need.col;
         for (int j = lane; j < need.pages; j += 32) {
@@ -211,11 +215,11 @@ __device__ __forceinline__ void enter_pages(const DevPaged &C, const DevChunk &T
 
 __global__ void __launch_bounds__(kCopyThreads, 4)
 reserve_enter_kernel(const DevPaged C, const DevChunk T, int32_t *refs, int32_t *row_pos,
-                     const PagesWs ws) {
+                     const PagesWs ws, int run) {
     pdl_wait();
     pdl_trigger();
     if (ws.plan->count == 0) return;
-    enter_pages(C, T, refs, row_pos, ws, (long long)blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5),
+    enter_pages(C, T, refs, row_pos, ws, run, (long long)blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5),
                 (long long)gridDim.x * (kCopyThreads / 32));
 }
 
@@ -292,7 +296,7 @@ reserve_plan_kernel(const DevPaged C, const DevChunk T, int32_t *refs, int32_t *
         });
         if (kCtas == 1 && whole) {
             __syncthreads();
-            enter_pages(C, T, refs, row_pos, ws, threadIdx.x >> 5, kPlanThreads / 32);
+            enter_pages(C, T, refs, row_pos, ws, 1, threadIdx.x >> 5, kPlanThreads / 32);
         }
     }
     leave_cluster<kCtas>();
@@ -584,8 +588,11 @@ cudaError_t launch_reserve(const DevPaged &C, const DevChunk &T, int32_t *refs, 
                                      kPlanThreads, 0, s, C, T, refs, row_pos, ws, false);
         if (e != cudaSuccess) return e;
     }
-    return launch_dependent(reserve_enter_kernel, dim3(copy_grid(pieces)), kCopyThreads, 0, s, C, T,
-                            refs, row_pos, ws);
+    // four pieces a warp where all warps have one: what a unit needs is then looked up once for them
+    // (2048 units with pages of 16 pieces: 29 us with the fork and the plan, 32 a piece at a time)
+    const int run = pieces > kCopyCtas * (kCopyThreads / 32) ? 4 : 1;
+    return launch_dependent(reserve_enter_kernel, dim3(copy_grid((pieces + run - 1) / run)), kCopyThreads,
+                            0, s, C, T, refs, row_pos, ws, run);
 }
 
 cudaError_t launch_compact_pages(const DevPaged &C, int32_t *refs, int32_t *row_pos, int32_t *live,
