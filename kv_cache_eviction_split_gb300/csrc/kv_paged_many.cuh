@@ -710,7 +710,11 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                                         cap_poly<kPolyPairs>(co, make_float2(0.f, 0.f), &v[i]);
                                 } else {
 #pragma unroll
-                                    for (int i = 0; i < kW; ++i) v[i] = cap_logit<false>(A.form, v[i]);
+                                    for (int i = 0; i < kW; i += 2) {
+                                        const float2 z = cap_pair(A.form, make_float2(v[i], v[i + 1]));
+                                        v[i] = z.x;
+                                        v[i + 1] = z.y;
+                                    }
                                 }
                             }
                         }
@@ -766,7 +770,7 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                         // without slopes tanh goes with the exponentials: it rises
                         tier = cap_tier(A.form, most);
                         if (top != -INFINITY)
-                            top = tier < 2 ? cap_poly1(A.form, top) : cap_logit<false>(A.form, top);
+                            top = tier < 2 ? cap_poly1(A.form, top) : cap_pair(A.form, make_float2(top, top)).x;
                     }
                     raise(top * zs);
                     const float nm = m == -INFINITY ? 0.f : E::kShift - m;
@@ -796,9 +800,7 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                                         float2 e = make_float2(v[j], v[j + 1]);
                                         if (how.value == 0) e = __ffma2_rn(e, zs2, nm2);
                                         if (how.value == 3)
-                                            e = __fadd2_rn(make_float2(cap_logit<false>(A.form, e.x),
-                                                                       cap_logit<false>(A.form, e.y)),
-                                                           nm2);
+                                            e = __fadd2_rn(cap_pair(A.form, e), nm2);
                                         float2 p = make_float2(ex2_approx(e.x), ex2_approx(e.y));
                                         if (mixed.value) {
                                             if (!(h.see[j >> 5] >> (j & 31) & 1u)) p.x = 0.f;

@@ -72,20 +72,30 @@ struct ScoreForm {
     }
 };
 
+__device__ __forceinline__ float rcp_approx(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 // Capped, in units of log2.  The series up to x^9: what it leaves out is 9e-9 of tanh(1/4).
-template <bool kSeries = true>
 __device__ __forceinline__ float cap_logit(const ScoreForm &F, float s) {
     const float e = sm100::ex2_approx(fminf(s * F.cap_u, 64.f));
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-    const float z1 = fmaf(-2.f * F.cap2, r, F.cap2);
-    if (!kSeries) return z1;
+    const float z1 = fmaf(-2.f * F.cap2, rcp_approx(1.f + e), F.cap2);
     const float x = s * F.cap_x, x2 = x * x;
     float t = fmaf(x2, 62.f / 2835, -17.f / 315);
     t = fmaf(x2, t, 2.f / 15);
     t = fmaf(x2, t, -1.f / 3);
     const float z = s * F.cap_z;
     return fabsf(x) < 0.25f ? fmaf(z * x2, t, z) : z1;
+}
+
+// Two logits without the series, by one reciprocal of both denominators: three products on units
+// that have time for them save one of five operations on the one that has none.
+__device__ __forceinline__ float2 cap_pair(const ScoreForm &F, float2 s) {
+    const float a = 1.f + sm100::ex2_approx(fminf(s.x * F.cap_u, 60.f));
+    const float b = 1.f + sm100::ex2_approx(fminf(s.y * F.cap_u, 60.f));
+    const float r = rcp_approx(a * b);
+    return make_float2(fmaf(-2.f * F.cap2, r * b, F.cap2), fmaf(-2.f * F.cap2, r * a, F.cap2));
 }
 
 // The same of one logit of at most most5 by the polynomial: a shorter chain of operations.

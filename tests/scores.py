@@ -28,7 +28,8 @@ def scored_unit(q, K, V, pos, scale, cap=0.0, slopes=None, first=None, last=None
     per row, sum p |v|, and per output the first order of what errors of the logits do to it and to lse.
 
     A logit is off by its d products (2^-23 of the sum of magnitudes each), its 2^x (2^-22 and 2^-22 of
-    itself); capped, by 2^-20 of cap (2^x and the reciprocal to 2^-22 and 2^-23, one fused product), and with
+    itself); capped, by 2^-20 of cap (2^x to 2^-22, which counts a quarter, a reciprocal to
+    2^-23 of two factors with three roundings, one fused product: 6.5 2^-23), and with
     caps beyond 4096 softmax scales by 2^-17 of itself at most (a polynomial whose first coefficient is 2.8e-6 off,
     or the series; above a quarter of the cap the same);
     lowered, by 2^-22 of what is taken off (slope log2(e), the product, the difference)."""
