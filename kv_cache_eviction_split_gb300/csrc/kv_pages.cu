@@ -10,7 +10,7 @@
 // distributed shared memory, does it in one launch.  The pages themselves are then copied by all
 // SMs, bound by HBM.
 //
-// Measured (us, cold caches): 8 hypotheses of 256 units and 59000 pages fork 5, plan 11.5, enter and
+// Measured (us, cold caches): 8 hypotheses of 256 units and 59000 pages fork 6, plan 13, enter and
 // copy up to 2048 pages of 32 KB 19; a compaction of 1.3 GB plans in 14.7 and moves at 6.3 TB/s, 93% of
 // what a copy reaches.
 #include <algorithm>
