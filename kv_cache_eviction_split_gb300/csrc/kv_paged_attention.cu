@@ -17,9 +17,12 @@ namespace {
 // writes them while this one may already run, and loads through restricted pointers need not
 // stay behind the wait for it.
 // ---------------------------------------------------------------------------
-// Up to 256 rows, few partials: kMergeRows rows a warp, their loads together.  One wave of
-// blocks (16 an SM); 14 .. 16 us for 152 cut items of 256 rows, d = 128, 40 MB of partials
-// (18 us with a block for every phase's slot, most of them empty).
+// Up to 256 rows, few partials: kMergeRows rows a warp, their loads together; 14 us for 152 cut
+// items of 256 rows, d = 128, 40 MB of partials (18 us with a block for every phase's slot, most of
+// them empty).  Whole calls, us, with the first two partials behind the maxima and 4 rows / beside
+// them and 4 / 2 / 1 / 8 rows: 2048 tokens over 34816 rows 702 / 699 / 695 / 694 / 707; 8192 tokens
+// in 5 documents, capped, 212 / 210 / 209 / 209 / 215; 2 x 511 tokens with weights, 16 units, 430 / 427 /
+// 436 / 442.
 constexpr int kMergeRows = 4;
 template <typename X, int D>
 __global__ void __launch_bounds__(128)
@@ -47,27 +50,44 @@ merge_many_kernel(const DevPaged C, const DevChunk T, int layer, const AttendIo 
 #pragma unroll
             for (int i = 0; i < kV; ++i) acc[r][i] = 0.f;
         }
-        for (int p = 0; p < parts; ++p)
-#pragma unroll
-            for (int r = 0; r < kMergeRows; ++r) m[r] = fmaxf(m[r], part_ml[slot_row(p, r)].x);
-#pragma unroll 2
-        for (int p = 0; p < parts; ++p)
+        auto fetch = [&](int p, float2 (&ml)[kMergeRows], float (&x)[kMergeRows][kV]) {
 #pragma unroll
             for (int r = 0; r < kMergeRows; ++r) {
                 const long long at = slot_row(p, r);
-                const float2 ml = part_ml[at];
-                const float f = shrink(ml.x, m[r]);
-                l[r] += ml.y * f;
-                float x[kV];
+                ml[r] = part_ml[at];
                 if constexpr (kV == 4)
-                    *reinterpret_cast<float4 *>(x) =
+                    *reinterpret_cast<float4 *>(x[r]) =
                         *reinterpret_cast<const float4 *>(part_o + at * D + lane * kV);
                 else
-                    *reinterpret_cast<float2 *>(x) =
+                    *reinterpret_cast<float2 *>(x[r]) =
                         *reinterpret_cast<const float2 *>(part_o + at * D + lane * kV);
-#pragma unroll
-                for (int i = 0; i < kV; ++i) acc[r][i] += f == 0.f ? 0.f : x[i] * f;
             }
+        };
+        auto add = [&](const float2 (&ml)[kMergeRows], const float (&x)[kMergeRows][kV]) {
+#pragma unroll
+            for (int r = 0; r < kMergeRows; ++r) {
+                const float f = shrink(ml[r].x, m[r]);
+                l[r] += ml[r].y * f;
+#pragma unroll
+                for (int i = 0; i < kV; ++i) acc[r][i] += f == 0.f ? 0.f : x[r][i] * f;
+            }
+        };
+        // a cut item has two parts at least: theirs come beside the maxima
+        float2 ml0[kMergeRows], ml1[kMergeRows];
+        float o0[kMergeRows][kV], o1[kMergeRows][kV];
+        fetch(0, ml0, o0);
+        fetch(1, ml1, o1);
+#pragma unroll
+        for (int r = 0; r < kMergeRows; ++r) m[r] = fmaxf(ml0[r].x, ml1[r].x);
+        for (int p = 2; p < parts; ++p)
+#pragma unroll
+            for (int r = 0; r < kMergeRows; ++r) m[r] = fmaxf(m[r], part_ml[slot_row(p, r)].x);
+        add(ml0, o0);
+        add(ml1, o1);
+        for (int p = 2; p < parts; ++p) {
+            fetch(p, ml0, o0);
+            add(ml0, o0);
+        }
 #pragma unroll
         for (int r = 0; r < kMergeRows; ++r)
             if (row0 + r < it.rows)
