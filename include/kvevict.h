@@ -478,7 +478,8 @@ kv_status kv_paged_attention_workspace_size(const kv_paged *c, const kv_chunk *t
  * from one token to the next (multiples of 8); rows of tokens past the last
  * request's are not touched.  lse: f32 [tokens][H_q], or NULL.  Rows that no
  * query of the chunk sees are never used, whatever their memory holds (their
- * pages may be gone); rows that one sees must hold finite values.  Products are
+ * pages may be gone); rows that one sees must hold finite values.  (NaN in a query, or
+ * in a key that it sees, makes the query's out and lse NaN, and no other's.)  Products are
  * taken of the stored values and summed in fp32; the softmax weights are rounded
  * once, to the cache's dtype, before they multiply V; to two such parts in requests
  * of at most 16 query rows a head (new tokens times the group's heads), and without

@@ -278,9 +278,10 @@ __device__ __forceinline__ void cut_units(int units, int phases, long long rows,
     __syncthreads();
 }
 
-// log2 of a row's softmax sum from its maximum (log2 units) and sum.
+// log2 of a row's softmax sum from its maximum (log2 units) and sum.  A sum is 0 where nothing is seen,
+// and NaN, as are then lse and output, where a logit was.
 __device__ __forceinline__ float row_lse2(float m, float l) {
-    return l > 0.f ? m + __log2f(l) : -INFINITY;
+    return l == 0.f ? -INFINITY : m + __log2f(l);
 }
 
 // Writes a merged row of an item (a warp, D / 32 elements of the sum a lane).
@@ -293,7 +294,7 @@ __device__ __forceinline__ void store_merged(const DevPaged &C, const DevChunk &
     const UnitRows U = unit_rows(C, T, layer, it.unit);
     const long long tok = U.tok0 + (it.row0 + row) / C.G;
     const int head = U.h * C.G + (it.row0 + row) % C.G;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
     typename X::T *op = static_cast<typename X::T *>(io.out) + tok * io.out_stride +
                         (long long)head * D + lane * kV;
     static_assert(kV == 2 || kV == 4, "two or four elements a lane");

@@ -549,7 +549,7 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
                             const int row = it.row0 + r2;
                             const long long tok = U.tok0 + row / C.G;
                             const int head = U.h * C.G + row % C.G;
-                            const float inv = ll > 0.f ? 1.f / ll : 0.f;
+                            const float inv = ll == 0.f ? 0.f : 1.f / ll;
                             typename E::T *op = static_cast<typename E::T *>(A.io.out) +
                                                 tok * A.io.out_stride + (long long)head * D + quad;
 #pragma unroll
@@ -622,7 +622,7 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
             const long long tok = U.tok0 + row / C.G;
             const int head = U.h * C.G + row % C.G;
             static_cast<typename E::T *>(A.io.out)[tok * A.io.out_stride + (long long)head * D + e] =
-                E::one(ll > 0.f ? acc / ll : 0.f);
+                E::one(ll == 0.f ? 0.f : acc / ll);
             if (e == 0) {
                 const float z = row_lse2(mm, ll);
                 if (A.io.lse) A.io.lse[tok * C.Hq + head] = z * kLn2;

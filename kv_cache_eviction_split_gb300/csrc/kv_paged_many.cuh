@@ -876,7 +876,7 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             const long long prow0 =
                 (long long)part_slot(cta, x0 == 0) * kManyRows + L * 128 + quarter * 32;
             const long long prow = prow0 + lane;
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
             // O goes out by way of the rows' Q in shared memory (its last S is complete), so that a
             // warp writes whole rows: a row a thread touched 32 lines with every store (a packed prompt
             // of 8192 tokens: 181 us masked and 203 with slopes, 175 and 194 so).
