@@ -798,6 +798,10 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
 #pragma unroll
                                     for (int j = i; j < i + 2 * kPolyPairs; j += 2) {
                                         float2 e = make_float2(v[j], v[j + 1]);
+                                        if (how.value == 3 && mixed.value) {
+                                            if (!(h.see[j >> 5] >> (j & 31) & 1u)) e.x = 0.f;
+                                            if (!(h.see[j >> 5] >> (j & 31) & 2u)) e.y = 0.f;
+                                        }
                                         if (how.value == 0) e = __ffma2_rn(e, zs2, nm2);
                                         if (how.value == 3)
                                             e = __fadd2_rn(cap_pair(A.form, e), nm2);

@@ -77,9 +77,15 @@ __device__ __forceinline__ float rcp_approx(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+// The smaller of two, NaN if one is: fminf would make a bound of a logit of NaN.
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 // Capped, in units of log2.  The series up to x^9: what it leaves out is 9e-9 of tanh(1/4).
 __device__ __forceinline__ float cap_logit(const ScoreForm &F, float s) {
-    const float e = sm100::ex2_approx(fminf(s * F.cap_u, 64.f));
+    const float e = sm100::ex2_approx(min_nan(s * F.cap_u, 64.f));
     const float z1 = fmaf(-2.f * F.cap2, rcp_approx(1.f + e), F.cap2);
     const float x = s * F.cap_x, x2 = x * x;
     float t = fmaf(x2, 62.f / 2835, -17.f / 315);
@@ -90,10 +96,11 @@ __device__ __forceinline__ float cap_logit(const ScoreForm &F, float s) {
 }
 
 // Two logits without the series, by one reciprocal of both denominators: three products on units
-// that have time for them save one of five operations on the one that has none.
+// that have time for them save one of five operations on the one that has none.  NaN in one makes both
+// NaN: logits behind keys that the row does not see are set to something else before.
 __device__ __forceinline__ float2 cap_pair(const ScoreForm &F, float2 s) {
-    const float a = 1.f + sm100::ex2_approx(fminf(s.x * F.cap_u, 60.f));
-    const float b = 1.f + sm100::ex2_approx(fminf(s.y * F.cap_u, 60.f));
+    const float a = 1.f + sm100::ex2_approx(min_nan(s.x * F.cap_u, 60.f));
+    const float b = 1.f + sm100::ex2_approx(min_nan(s.y * F.cap_u, 60.f));
     const float r = rcp_approx(a * b);
     return make_float2(fmaf(-2.f * F.cap2, r * b, F.cap2), fmaf(-2.f * F.cap2, r * a, F.cap2));
 }

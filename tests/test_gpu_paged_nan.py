@@ -16,11 +16,18 @@ FORMS = {
     "many": (4, 32, 128, 32, "bf16", [200, 1, 0, 151], 211, 700, 700),
     "many_fp16": (8, 32, 64, 64, "fp16", [140, 257], 300, 1300, 1300),
 }
+# cap 200: below half of it; cap 2: far above it (softmax scales 1 / sqrt(d) and 1)
 CHANGES = {
     "plain": {},
     "slopes": dict(slopes=True),
     "docs": dict(docs=True),
     "docs_slopes": dict(docs=True, slopes=True),
+    "cap": dict(cap=200.0),
+    "cap_exact": dict(cap=2.0, scale=1.0),
+    "both": dict(cap=200.0, slopes=True),
+    "both_exact": dict(cap=2.0, scale=1.0, slopes=True),
+    "docs_cap": dict(docs=True, cap=200.0),
+    "docs_cap_exact": dict(docs=True, cap=2.0, scale=1.0),
 }
 
 
