@@ -621,10 +621,9 @@ cudaError_t launch_fork(const DevPaged &C, int32_t *refs, const int32_t *parents
     strip = strip > kForkThreads ? kForkThreads : strip;
     strip = strip > C.max_pages ? C.max_pages : strip;
     const size_t smem = fixed + (size_t)C.R * strip * sizeof(int);
-    const cudaError_t e =
-        smem <= 48 * 1024 ? cudaSuccess
-                          : cudaFuncSetAttribute(
-                                fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kForkSmem);
+    // (a block has 48 KB unasked, of which its static word takes a part)
+    const cudaError_t e = cudaFuncSetAttribute(
+        fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kForkSmem);
     return e != cudaSuccess ? e
                             : launch_dependent(fork_kernel, dim3((unsigned)(C.L * C.H)), kForkThreads,
                                                smem, s, C, refs, parents, (int)strip);
