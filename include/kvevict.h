@@ -427,7 +427,8 @@ typedef struct kv_paged {
     float *mass;
     const int32_t *page_table;
     int32_t *lens;
-    int32_t *status;           /* the cache's status word, device memory, 0 when it is made */
+    int32_t *status;           /* the cache's status word, device memory, 0 when it is made; read
+                                  by kv_check_status (it holds more than the code) */
 } kv_paged;
 
 /* The new tokens of a step, packed: request r's are [tok_offsets[r], tok_offsets[r+1])
@@ -676,7 +677,14 @@ kv_status kv_paged_reserve_workspace_size(const kv_paged *c, size_t *bytes);
  * that this call leaves without references is given out from the next call on.
  * Nothing changes and KV_ERR_BUDGET is posted if there are too few free pages or a
  * unit would outgrow its table, KV_ERR_INVALID_ARG if a length or last page cannot be.
- * KV_ERR_BUDGET is returned where the tokens would fill more pages than there are.
+ * The step's calls that are queued behind it then change nothing in the cache either:
+ * kv_paged_append and kv_paged_append_rotary write no rows, and attention adds no
+ * weights (what it returns for that step has no meaning), until a reservation fits or
+ * kv_check_status has read the status word.  So a step can be given again once
+ * there are pages.  A step that is queued behind a failed one without a look at the status
+ * may still fit, and goes on from the rows that are there.
+ * KV_ERR_BUDGET is returned where the tokens would fill more pages than there are: queue
+ * nothing of the step then.
  */
 kv_status kv_paged_reserve(const kv_paged *c, const kv_chunk *t, int32_t *refs, int32_t *row_pos,
                            void *workspace, size_t workspace_bytes, void *stream);

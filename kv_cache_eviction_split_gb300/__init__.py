@@ -1228,7 +1228,8 @@ def kv_paged_reserve_workspace_size(cache: PagedCache) -> int:
 
 def kv_paged_reserve(cache: PagedCache, chunk: Chunk, workspace, stream=None):
     """Room for a step's new tokens, in place of cache.advance: lengths raised, free pages entered,
-    shared last pages copied.  All or nothing: KV_ERR_BUDGET in cache.status if pages lack."""
+    shared last pages copied.  All or nothing: KV_ERR_BUDGET in cache.status if pages lack, and the appends
+    and weights of the step that are queued behind it then leave the cache as it is."""
     _check_refs(cache)
     _check_chunk(cache, chunk)
     if not workspace.is_contiguous():

@@ -433,7 +433,7 @@ kv_status kv_check_status(void *workspace, void *stream, int32_t *device_status)
     if (cudaMemcpy(&word, workspace, sizeof word, cudaMemcpyDeviceToHost) != cudaSuccess)
         return KV_ERR_CUDA;
     if (word != 0 && cudaMemset(workspace, 0, sizeof word) != cudaSuccess) return KV_ERR_CUDA;
-    *device_status = word;
+    *device_status = word & kStatusCode;
     return KV_OK;
 }
 

@@ -187,6 +187,9 @@ cudaError_t launch_fused(const DevProblem &P, const __nv_bfloat16 *q, const __nv
                          long long total_rows, float *scores, int32_t *sel, __nv_bfloat16 *kout,
                          __nv_bfloat16 *vout, const ScoreWs &ws, cudaStream_t s);
 
+// A status word: the first code posted, in its low bits; and in a paged cache's, whether the last
+// reservation of pages failed (kv_paged.cuh).
+constexpr int kStatusCode = 0xffff, kStatusNoRows = 1 << 16;
 __device__ inline void post_status(int *status, int code) {
     atomicCAS(status, 0, code);
 }

@@ -46,6 +46,12 @@ __device__ __forceinline__ bool unit_len(const DevPaged &C, long long u, int &n)
     return ok;
 }
 
+// Whether the last reservation failed: the step's tokens have no rows then, and those where they
+// would be are earlier ones, which what was queued behind the reservation leaves alone.
+__device__ __forceinline__ bool without_rows(const DevPaged &C) {
+    return (*static_cast<volatile const int *>(C.status) & kStatusNoRows) != 0;
+}
+
 // Pool row of cache row j of the unit whose table is `tab`; -1 if its page does not exist.
 __device__ __forceinline__ long long page_row(const DevPaged &C, const int32_t *tab, int j) {
     const int page = tab[j >> C.ps_log2];

@@ -45,8 +45,9 @@ append_kernel(const DevPaged C, const DevChunk T, int layer, const uint4 *__rest
     const int h = (int)(i - tok * C.H);
     const uint4 *src = p.which ? v_new + tok * v_stride : k_new + tok * k_stride;
     const uint4 val = ld_nc(src + h * Part::kVecs + p.ch);
+    const bool none = without_rows(C);
     const int r = request_of(T, C.R, tok);
-    if (tok >= T.off[C.R]) return;
+    if (tok >= T.off[C.R] || none) return;
     const long long u = ((long long)r * C.L + layer) * C.H + h;
     int n;
     const bool ok = unit_len(C, u, n);

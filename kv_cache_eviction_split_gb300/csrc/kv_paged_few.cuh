@@ -709,6 +709,7 @@ __device__ __forceinline__ void add_weights(const DevPaged &C, const DevChunk &T
     constexpr int kK = kFinishThreads / kFewRows, kTiles = kFinishThreads / kFewTile;
     __shared__ float sm_m[kK][kFewRows], sm_l[kK][kFewRows], sm_z[kFewRows];
     const int key = threadIdx.x % kFewTile, group = threadIdx.x / kFewTile;
+    const bool none = without_rows(C);
     for (long long t = t0; t < t1;) {
         const int v = (int)(t / A.unit_tiles);
         const long long base = (long long)v * A.unit_tiles, end = min(t1, base + A.unit_tiles);
@@ -774,7 +775,7 @@ __device__ __forceinline__ void add_weights(const DevPaged &C, const DevChunk &T
                 seen |= see;
                 acc += see ? ex2_approx(lg[row] - sm_z[row]) : 0.f;
             }
-            if (seen && at >= 0) C.mass[at] = old + acc;
+            if (seen && at >= 0 && !none) C.mass[at] = old + acc;
             x += kTiles;
             if (x < x1) fetch(x);
         }

@@ -175,6 +175,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
         const float cs = A.M.scale_log2;
         const float2 cs2 = make_float2(cs, cs);
+        const bool adds = par == 0 && !without_rows(C);
         int rc = 0, summed = 0;
         for (int i = 0;; ++i) {
             const Item *w = item(i, ok);
@@ -203,7 +204,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                     : (int)min((long long)rows, max(0ll, ((long long)key0 + A.M.window - t0) * G));
             // the key's weight so far is looked up beside the first steps: its page here, its
             // value after the first
-            const int page = par == 0 && held && r_lo < r_hi ? table[j >> C.ps_log2] : -1;
+            const int page = adds && held && r_lo < r_hi ? table[j >> C.ps_log2] : -1;
             float *to = nullptr;
             float acc = 0.f, old = 0.f;
             auto find = [&]() {

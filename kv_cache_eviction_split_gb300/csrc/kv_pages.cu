@@ -177,7 +177,8 @@ __device__ __forceinline__ void copy_piece(const DevPaged &C, int32_t *row_pos, 
 // Pages for a step's tokens.  A unit of n rows that gets t more needs the pages of rows n .. n + t - 1
 // that it has none for, and one more if its last page is part full and shared: that page is copied
 // and the copy takes its place.  The k-th page needed, units in order, tail first, is the k-th
-// free page.  Nothing changes unless all fit.
+// free page.  Nothing changes unless all fit; what the step has queued behind the call then finds a
+// mark in the status word and writes nothing either (without_rows).
 //
 // The plan leaves every unit what it needs and the free pages in order; the second kernel, a
 // warp a unit and piece of its copied page, enters and copies them.  (All in the plan's cluster, the
@@ -278,7 +279,12 @@ reserve_plan_kernel(const DevPaged C, const DevChunk T, int32_t *refs, int32_t *
     const bool fits = s.total[2] == 0 && s.total[3] == 0 && s.total[0] <= s.total[1];
     if (gt == 0) {
         ws.plan->count = fits ? 1 : 0;
-        if (!fits) post_status(C.status, s.total[2] > 0 ? KV_ERR_INVALID_ARG : KV_ERR_BUDGET);
+        if (fits) {
+            atomicAnd(C.status, ~kStatusNoRows);
+        } else {
+            post_status(C.status, s.total[2] > 0 ? KV_ERR_INVALID_ARG : KV_ERR_BUDGET);
+            atomicOr(C.status, kStatusNoRows);
+        }
     }
     if (fits) {
         for (int u = u0; u < u1; ++u) {

@@ -201,13 +201,14 @@ append_rotary_kernel(const DevPaged C, const DevChunk T, int layer, const DevRot
     pdl_wait();
     pdl_trigger();
     const int Hq = io.q ? C.Hq : 0;
+    const bool none = without_rows(C);
     // Pool row of token tok's new row of head h, -1 if it has none.
     auto place = [&](int r, long long tok, int h) {
         const long long v = ((long long)r * C.L + layer) * C.H + h;
         int len;
         const bool ok = unit_len(C, v, len);
         const long long j = len - (T.off[r + 1] - tok);
-        if (tok >= T.off[C.R] || (ok && j < 0)) return -1;
+        if (tok >= T.off[C.R] || (ok && j < 0) || none) return -1;
         const int row = ok ? (int)page_row(C, C.table + v * C.max_pages, (int)j) : -1;
         if (row < 0) post_status(C.status, KV_ERR_INVALID_ARG);
         return row;
