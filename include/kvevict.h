@@ -703,7 +703,7 @@ kv_status kv_paged_compact_workspace_size(const kv_paged *c, size_t *bytes);
 /*
  * Pages in use move to the front of the pools: with n of them in use, the k-th one from page n on
  * goes to the k-th free page before it, tables and refs with it, and pages n .. num_pages - 1
- * are free.  live: i32 (device) receives n, or NULL.
+ * are free.  live: i32 (device) receives n (0 without requests), or NULL.
  */
 kv_status kv_paged_compact(const kv_paged *c, int32_t *refs, int32_t *row_pos, int32_t *live,
                            void *workspace, size_t workspace_bytes, void *stream);

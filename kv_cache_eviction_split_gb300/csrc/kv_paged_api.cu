@@ -428,9 +428,10 @@ kv_status kv_paged_compact(const kv_paged *c, int32_t *refs, int32_t *row_pos, i
     DevPaged C;
     const kv_status st = make_paged(c, &C);
     if (st != KV_OK) return st;
-    if (C.units == 0) return KV_OK;
-    if (bad_refs(C, refs) || !aligned16(row_pos) || !aligned_to(live, 4) || bad_ptr(workspace))
-        return KV_ERR_INVALID_ARG;
+    if (!aligned_to(live, 4)) return KV_ERR_INVALID_ARG;
+    if (C.units == 0)
+        return !live ? KV_OK : map_cuda(cudaMemsetAsync(live, 0, sizeof(int32_t), (cudaStream_t)stream));
+    if (bad_refs(C, refs) || !aligned16(row_pos) || bad_ptr(workspace)) return KV_ERR_INVALID_ARG;
     const PagesWs ws = compact_ws_layout(C, workspace);
     if (workspace_bytes < ws.total) return KV_ERR_WORKSPACE;
     return map_cuda(launch_compact_pages(C, refs, row_pos, live, ws, (cudaStream_t)stream));
