@@ -581,8 +581,9 @@ kv_status kv_paged_evict(const kv_paged *src, const kv_paged *dst, const int32_t
  * Pair i (of dims / 2) of a row at position p turns by the angle p * inv_freq[i]:
  *   (x1, x2) -> factor * (x1 cos - x2 sin, x1 sin + x2 cos)
  * The pairs are elements (i, i + dims/2), or (2i, 2i+1) if interleaved; elements from
- * dims on are copied.  Angles are exact to 2^-21 at any position (int32, negative ones
- * too), products and sums are fp32, a result is rounded once.
+ * dims on are copied.  An angle is off by at most 2^-52 |p inv_freq[i]| + 2^-23 (2^-20 at
+ * any position for frequencies up to 1), with positions of int32, negative ones too, and
+ * finite frequencies; products and sums are fp32, a result is rounded once.
  */
 typedef struct kv_rotation {
     int32_t dims;              /* elements turned: a multiple of 16, 0 .. head_dim */

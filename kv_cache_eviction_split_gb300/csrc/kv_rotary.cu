@@ -10,8 +10,8 @@
 // p w_i in fp32 would be off by 0.06 at a position of a million: the angle is kept in turns,
 // as 64 bits after the point.  w_i / 2 pi is taken once a block in fp64 and p times it modulo
 // one turn is an integer product, exact but for the 53 bits of the factor (an angle off by at most
-// p w_i 2^-52, 2^-21 at the last position); fp64 arithmetic per angle would cost as much as the
-// copy does.  Half turns in fp32 (24 bits) then go through sincospif.
+// p w_i 2^-52, 2^-21 at the last position for w_i = 1); fp64 arithmetic per angle would cost as much as
+// the copy does.  Half turns in fp32 (24 bits: 2^-23 of an angle) then go through sincospif.
 //
 // Measured (d = 128, bf16): 8192 tokens of 32 + 8 + 8 heads into the pages 34 us, 5.9 TB/s, 88% of
 // what a copy reaches; 2047 tokens of 28 heads (dims 64) 6.5 us, where a launch alone is 2.3; one
