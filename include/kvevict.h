@@ -597,11 +597,15 @@ typedef struct kv_rotation {
  *   KV_ROTARY_NONE    base^(-2i/dims)
  *   KV_ROTARY_LINEAR  that, divided by scale (position interpolation)
  *   KV_ROTARY_BASE    with base * scale^(dims/(dims-2)) as the base
- *   KV_ROTARY_PARTS   by wavelength (YaRN): frequencies that make `fast` turns or more in
- *                     `context` positions are kept, those of `slow` or fewer are divided by
- *                     scale, those between are mixed in proportion; factor
+ *   KV_ROTARY_PARTS   by wavelength: frequencies that make `fast` turns or more in `context`
+ *                     positions are kept, those of `slow` or fewer are divided by
+ *                     scale, those between are mixed in proportion to their turns; factor
  *                     0.1 ln(scale) + 1
  * scale >= 1; context, slow and fast are read for KV_ROTARY_PARTS alone.
+ * KV_ROTARY_PARTS is the formula of the YaRN paper.  Its published implementations mix in
+ * proportion to a pair's index instead (up to 2.3 times another frequency at dims 128, scale 8):
+ * models trained with those, or with a mix by turns and factor 1, need their own inv_freq
+ * or factor in kv_rotation.
  */
 typedef enum kv_rotary_scaling {
     KV_ROTARY_NONE = 0,

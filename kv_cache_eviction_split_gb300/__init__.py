@@ -1063,7 +1063,8 @@ def kv_rotary_frequencies(dims: int, base: float = 10000.0, scaling: str = "none
                           fast: float = 32.0):
     """(inv_freq float32 [dims/2], factor) of rotary positions, scaled for contexts `scale` times
     as long: "linear" (positions divided), "base" (a larger base), "parts" (by wavelength, for a
-    model of `context` positions)."""
+    model of `context` positions; mixed in proportion to the turns, where some models' own
+    frequencies are in proportion to the pair's index: those go to Rotary as they are)."""
     if scaling not in _SCALINGS:
         raise ValueError("scaling: one of %s" % ", ".join(_SCALINGS))
     _check_int32("kv_rotary_frequencies", dims)
