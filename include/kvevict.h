@@ -512,7 +512,8 @@ kv_status kv_paged_attention(const kv_paged *c, const kv_chunk *t, int32_t layer
  * kv_paged_append_rotary and kv_paged_place_positions leave them), or without it its
  * number j; a query's position is that of its own cache row t = lens[u] - T_r + i.
  * Positions are >= 0 and never fall from a unit's row to the next; distances are exact
- * up to 2^24.
+ * up to 2^24 where the positions of a request's new tokens span no more than that (past
+ * either, rounded to 24 bits of the distance, or of the span).
  * The query sees the rows with
  *   p_j >= first[token]  (and j > t - window)  or  j < num_sinks,   and
  *   p_j <= last[token]

@@ -393,7 +393,8 @@ many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             long long tok, prow0;
             RowBounds see;             // kMod: the rows it sees
             float slope, far;          // kMod: of its head, in 1 / zs; its position, from `ref`
-            int ref;                   // kMod: the position that distances are counted from
+            int ref;                   // kMod: the position that distances are counted from, the
+                                       // first query's: keys before it lie further off than it
         };
         auto row_of = [&](const Item *w) {
             Row r;
