@@ -1158,6 +1158,8 @@ def kv_paged_append_rotary(cache: PagedCache, chunk: Chunk, layer: int, rotary: 
     if rotary._index != cache._index:
         raise ValueError("the frequencies are on %s, the cache on %s" % (rotary.inv_freq.device,
                                                                          cache.device))
+    if (q is None) is not (q_out is None):
+        raise ValueError("q and q_out: both, or neither")
     if q is None:
         qp = op = None
         qs = os_ = 0
