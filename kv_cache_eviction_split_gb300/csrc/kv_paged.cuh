@@ -119,6 +119,8 @@ constexpr int kShortVisits = 8192;
 // With changed scores (the many-rows kernel then takes longer to begin and a tile), in us, this /
 // the many-rows kernel, capped and with slopes, 1 KV head, 4 query heads, d = 64, 1 request:
 //   800 rows on 4096 keys 23 / 56   1200 on 401 14 / 21   1200 on 4096 41 / 40   2400 on 1024 16 / 26
+// (A step with more such items than the above allows has its requests of over kFewRows rows in the
+// many-rows kernel, those of up to kShortFewRows too.)
 constexpr int kShortScoredRows = 4096;
 constexpr int kManyTile = 128;     // keys per tile of the tensor-memory kernel
 constexpr int kManyRows = 256;     // query rows per item there: two tiles of 128

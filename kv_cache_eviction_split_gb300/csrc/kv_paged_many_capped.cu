@@ -2,8 +2,8 @@
 //
 // Bound by the row warps: the cap's polynomial and the exponentials in turn (ScoreForm, cap_tier).  32 query
 // heads on 8, d = 128, bf16: a prompt of 8192 tokens in 5 documents 212 us (masked alone 174), 2048 tokens
-// over 34816 rows 1180 us, 0.96 PFLOP/s (plain 699); saturated, with the exact form, 286 and 1640; with
-// slopes too 264 and 1500.
+// over 34816 rows 1180 us, 0.96 PFLOP/s (plain 699); saturated, with the exact form, 285 and 1600; with
+// slopes too 261 and 1510.
 #include "kv_paged_many.cuh"
 
 namespace kvevict {

@@ -410,7 +410,8 @@ compact_plan_kernel(const DevPaged C, int32_t *refs, int32_t *row_pos, int32_t *
 // ---------------------------------------------------------------------------
 // Requests go on from others' caches.  A block takes one (layer, head) of all requests, so that it
 // alone reads and writes their entries and lengths: a strip of columns of every request into
-// shared memory, then out to the requests that go on from another.
+// shared memory, then out to the requests that go on from another.  8 hypotheses of 256 units of 1638 rows
+// 3.1 us replayed, 64 of them 9.8; 1000 requests of one (layer, head), one block's work, 58.
 // ---------------------------------------------------------------------------
 constexpr int kForkThreads = 256;
 constexpr int kForkSmem = 192 * 1024;
@@ -474,7 +475,8 @@ fork_kernel(const DevPaged C, int32_t *refs, const int32_t *parents, int strip) 
     }
 }
 
-// Table entries in use, counted: a warp a unit.
+// Table entries in use, counted: a warp a unit, 32 entries a step.  Bound by latency: 256 units of 1638 rows
+// 3.1 us with the zeroing, 2048 of them 3.4; 16 units of 131072 rows, 64 steps each, 16.
 __global__ void __launch_bounds__(256) count_refs_kernel(const DevPaged C, int32_t *refs) {
     pdl_wait();
     pdl_trigger();
@@ -495,7 +497,10 @@ __global__ void __launch_bounds__(256) count_refs_kernel(const DevPaged C, int32
     }
 }
 
-// Positions of every unit's rows: a warp a unit.
+// Positions of every unit's rows: a warp a unit, 32 rows a step, each step a chain of list, table and
+// (with a source) position before its store.  Bound by that latency, once after a load or an eviction: 256 units of
+// 1638 rows by their lists 14.3 us, 2048 of them 14.8 (27 MB); 112 units of 6553 rows 51, of a source's rows 93;
+// 16 of 131072 rows 990.  Long units would want several warps each.
 __global__ void __launch_bounds__(256)
 place_positions_kernel(const DevPaged D, int32_t *dst_pos, const DevPaged S, const int32_t *src_pos,
                        const int32_t *index, long long stride, const int64_t *offsets) {
